@@ -76,8 +76,10 @@ typedef enum {
   LP_ERR_DEVICE_TIMEOUT = 7,       /* device: a pipeline wait ran past its limit */
   LP_ERR_CUDA = 8,                 /* a CUDA runtime call failed */
   LP_ERR_REPLAY_TOO_MANY_IDS = 9,  /* device: a keep-mask row kept more than 64 ids (row fails closed) */
-  LP_ERR_BOUNDS = 10               /* device, bounds-checked builds only: an index failed its check and
+  LP_ERR_BOUNDS = 10,              /* device, bounds-checked builds only: an index failed its check and
                                       the access was skipped (see lp_debug_bounds_build) */
+  LP_ERR_TOKEN_OUT_OF_RANGE = 11,  /* device: an embedding id not in {-1} U [0, vocab_real) */
+  LP_ERR_SEQ_OFFSETS = 12          /* device: cu_seqlens does not ascend from 0 to T */
 } lp_status;
 
 typedef enum {
@@ -87,7 +89,10 @@ typedef enum {
   LP_OP_BACKWARD = 3,
   LP_OP_TOP_P_REPLAY_DENSE_MASK = 4,
   LP_OP_BACKWARD_FROM_LOGITS = 5,  /* needs no workspace */
-  LP_OP_FORWARD_HOST = 6
+  LP_OP_FORWARD_HOST = 6,
+  LP_OP_EMBEDDING_BACKWARD = 7,
+  LP_OP_POLICY_LOSS = 8,           /* sized by lp_loss_workspace_size */
+  LP_OP_PREFERENCE_LOSS = 9        /* sized by lp_loss_workspace_size */
 } lp_op;
 
 /* Element type of an output buffer whose type the caller chooses. */
@@ -375,6 +380,222 @@ LP_API lp_status lp_merge_shard_stats(const float* shard_stats, int64_t T, const
  * Needs no workspace. */
 LP_API lp_status lp_sum_partials(const float* const* parts, int32_t n_parts, int64_t count, void* out,
                                  lp_dtype out_dtype, lp_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * The two neighbours of the linear-logp operator in a training step. The pages have no
+ * counterpart to these entry points: they name the framework around the operator, whose
+ * embedding makes the hidden states (and, where it shares the head's table, adds its
+ * gradient into the very dW that lp_backward_ex fills) and whose policy or preference loss
+ * turns logp and entropy into the grad_logp and grad_entropy that lp_backward takes.
+ * --------------------------------------------------------------------------------- */
+
+/* Embedding lookup with scaling: Y[t] = scale * W[ids[t]], the product in fp32, then rounded to
+ * Y's type (an exact copy when scale = 1 and the types agree).
+ *   ids      int32 [T] global ids: [0, vocab_real), or -1 for an unused position
+ *   W        host array [n_shards] of device pointers, shard k [V_k, H] row-major of type
+ *            w_dtype (NULL allowed for a shard without real ids), H % 8 == 0
+ *   scale    finite
+ *   Y        [T, H] of type y_dtype with row stride ld_y elements (ld_y >= H; rows must
+ *            start on a 16-byte boundary). Must not overlap W.
+ * The row of an unused position is zero, and so is, in a rank-local partition, the row of
+ * another rank's id (the ranks' results then add up to the whole lookup). An id outside
+ * {-1} U [0, vocab_real) records LP_ERR_TOKEN_OUT_OF_RANGE and gives a zero row. Needs no
+ * workspace. */
+LP_API lp_status lp_embedding(const int32_t* ids, int64_t T, int64_t H, const void* const* W, lp_dtype w_dtype,
+                              const lp_vocab_partition* part, float scale, void* Y, int64_t ld_y, lp_dtype y_dtype,
+                              lp_stream_t stream);
+
+/* Output options of lp_embedding_backward.
+ *   dw_dtype    LP_DTYPE_F32, or LP_DTYPE_BF16 (the fp32 result rounded once)
+ *   accumulate  0: dW[k] is overwritten, rows no position names with zeros; 1: the gradient
+ *               is added to what the named rows hold (one fp32 add per element after the
+ *               sum; the other rows are neither read nor written). Accumulation needs fp32
+ *               dW: with a table tied to the head, lp_backward_ex fills dW first and this
+ *               call adds to it. */
+typedef struct {
+  int32_t dw_dtype;
+  int32_t accumulate;
+} lp_embedding_options;
+
+/* Gradient of lp_embedding with respect to the table:
+ *   dW[v] = scale * sum of dY[t] over the positions t with ids[t] = v.
+ * The sum is in fp32 and its order is fixed: the positions are sorted by id, equal ids by
+ * position; sums of up to 32 positions are taken in ascending order, longer ones in
+ * pieces that are joined in ascending order. The result is bitwise the same from run to
+ * run (it depends on where an id's positions fall in the sorted batch, so a row's bits may
+ * differ between batches that share it, unlike the forward's).
+ *   dY       [T, H] of type dy_dtype, row stride ld_dy elements (ld_dy >= H; rows must
+ *            start on a 16-byte boundary); rows of unused positions are not read
+ *   dW       host array [n_shards] of device pointers, shard k [V_k, H] (NULL allowed for an
+ *            empty shard); the rows of padded ids get zeros, or are left when accumulating
+ *   opts     NULL means {LP_DTYPE_F32, 0}
+ * Ids follow the rules of lp_embedding. T = 0 writes zeros (nothing when accumulating).
+ * Workspace: lp_workspace_size(LP_OP_EMBEDDING_BACKWARD, T, H, part). */
+LP_API lp_status lp_embedding_backward(const int32_t* ids, int64_t T, int64_t H, const void* dY, int64_t ld_dy,
+                                       lp_dtype dy_dtype, const lp_vocab_partition* part, float scale,
+                                       void* const* dW, const lp_embedding_options* opts, void* workspace,
+                                       size_t ws_bytes, lp_stream_t stream);
+
+/* Bytes of device scratch of lp_policy_loss (LP_OP_POLICY_LOSS) or lp_preference_loss
+ * (LP_OP_PREFERENCE_LOSS; n_seqs = 2 * n_pairs). 0 for invalid arguments. */
+LP_API size_t lp_loss_workspace_size(lp_op op, int64_t T, int64_t n_seqs);
+
+/* How token terms are weighted into the loss; n_i = kept tokens of sequence i, S = the
+ * number of sequences with n_i > 0. */
+typedef enum {
+  LP_AGG_TOKEN_MEAN = 0,          /* w_t = 1 / sum_i n_i */
+  LP_AGG_SEQ_MEAN_TOKEN_MEAN = 1, /* w_t = 1 / (S n_i) */
+  LP_AGG_SEQ_MEAN_TOKEN_SUM = 2   /* w_t = 1 / S */
+} lp_aggregation;
+
+/* Estimators of the divergence from the reference policy, x = ref_logp - logp. */
+typedef enum {
+  LP_KL_K1 = 0, /* -x */
+  LP_KL_K2 = 1, /* x^2 / 2 */
+  LP_KL_K3 = 2  /* e^x - x - 1 */
+} lp_kl;
+
+/* Inputs of lp_policy_loss: fp32 device arrays of one value per token.
+ *   logp        of the policy being trained
+ *   old_logp    of the policy that sampled the tokens
+ *   ref_logp    of the reference policy; NULL only when kl_coef = 0
+ *   entropy     NULL only when entropy_coef = 0
+ *   advantages  [T], or [n_seqs] with options.adv_per_seq
+ *   mask        uint8 [T], nonzero = the token counts; NULL keeps every token. What the
+ *               other arrays hold where the mask is zero (NaN, infinities) has no effect.
+ *   cu_seqlens  int32 [n_seqs + 1] token offsets of packed sequences, ascending from 0 to
+ *               T (a sequence may be empty); NULL only for the token mean with one
+ *               advantage per token
+ *   upstream    device fp32 [1], the gradient of what follows with respect to the loss;
+ *               NULL means 1 */
+typedef struct {
+  const float* logp;
+  const float* old_logp;
+  const float* ref_logp;
+  const float* entropy;
+  const float* advantages;
+  const uint8_t* mask;
+  const int32_t* cu_seqlens;
+  const float* upstream;
+  int64_t n_seqs;
+} lp_policy_inputs;
+
+/* Options of lp_policy_loss.
+ *   clip_low, clip_high  the ratio is clipped to [1 - clip_low, 1 + clip_high]; 0 <= clip_low
+ *                        <= 1, clip_high >= 0
+ *   dual_clip            0 for none, else c > 1: with a negative advantage the ratio is also
+ *                        clipped to c
+ *   denominator          0, or > 0: replaces sum_i n_i (token mean) or S (sequence means),
+ *                        for a mean over more tokens than this call holds (micro-batches,
+ *                        ranks)
+ *   aggregation          lp_aggregation
+ *   kl_kind              lp_kl
+ *   adv_per_seq          1: advantages are one per sequence */
+typedef struct {
+  float clip_low;
+  float clip_high;
+  float dual_clip;
+  float kl_coef;
+  float entropy_coef;
+  float denominator;
+  int32_t aggregation;
+  int32_t kl_kind;
+  int32_t adv_per_seq;
+} lp_policy_options;
+
+#define LP_POLICY_METRICS 6
+#define LP_PREFERENCE_METRICS 5
+
+/* Outputs of lp_policy_loss, device arrays; any may be NULL (at least one must not be).
+ *   metrics       fp32 [6]: the loss, then the sums over kept tokens, weighted by w_t, of
+ *                 the policy term, the KL estimate (0 without ref_logp), the entropy (0
+ *                 without it), 1[clipped] and the ratio
+ *   counts        int64 [2]: kept tokens, and sequences with at least one (0 without
+ *                 cu_seqlens)
+ *   grad_logp     fp32 [T]: upstream * d loss / d logp
+ *   grad_entropy  fp32 [T]: upstream * d loss / d entropy; needs entropy */
+typedef struct {
+  float* metrics;
+  int64_t* counts;
+  float* grad_logp;
+  float* grad_entropy;
+} lp_policy_outputs;
+
+/* Clipped policy loss with a KL and an entropy term, and its gradient, in one call. With
+ * A the advantage, r = e^(logp - old_logp), [lo, hi] = [1 - clip_low, 1 + clip_high]:
+ *   clipped = (A > 0 and r > hi) or (A < 0 and r < lo) or (dual_clip and A < 0 and r > c)
+ *   l_t     = -A rc + kl_coef kl - entropy_coef entropy,  rc = r, or where clipped the bound it passed
+ *   loss    = sum over kept tokens of w_t l_t
+ *   grad_logp    = upstream w_t ((clipped ? 0 : -r A) + kl_coef dkl/dlogp)
+ *   grad_entropy = -upstream w_t entropy_coef
+ * (-A rc is max(-A r, -A clip(r)), lowered to -c A by the dual clip.) Tokens that are not
+ * kept get zero gradients; a batch that keeps none has loss 0. A kept token whose inputs
+ * are not finite makes the loss, and its own gradient, what fp32 arithmetic gives.
+ * Offsets that do not ascend from 0 to T record LP_ERR_SEQ_OFFSETS; metrics are then NaN
+ * and gradients zero. Sums have a fixed order: results are bitwise the same from run to
+ * run. Workspace: lp_loss_workspace_size(LP_OP_POLICY_LOSS, T, n_seqs). T = 0 gives loss 0. */
+LP_API lp_status lp_policy_loss(int64_t T, const lp_policy_inputs* in, const lp_policy_options* opts,
+                                const lp_policy_outputs* out, void* workspace, size_t ws_bytes, lp_stream_t stream);
+
+/* The function of a pair's margin h that lp_preference_loss averages; b = beta, e = label_smoothing. */
+typedef enum {
+  LP_PREF_SIGMOID = 0, /* -(1 - e) log sigmoid(b h) - e log sigmoid(-b h) */
+  LP_PREF_HINGE = 1,   /* max(0, 1 - b h) */
+  LP_PREF_IPO = 2      /* (h - 1 / (2 b))^2 */
+} lp_preference;
+
+/* Inputs of lp_preference_loss: as lp_policy_inputs. Sequences 2p and 2p + 1 are the chosen
+ * and the rejected answer of pair p; cu_seqlens int32 [2 n_pairs + 1] is required.
+ * ref_logp NULL means a reference-free loss (0 everywhere). */
+typedef struct {
+  const float* logp;
+  const float* ref_logp;
+  const uint8_t* mask;
+  const int32_t* cu_seqlens;
+  const float* upstream;
+  int64_t n_pairs;
+} lp_preference_inputs;
+
+/* Options of lp_preference_loss.
+ *   beta               > 0
+ *   label_smoothing    in [0, 1), for LP_PREF_SIGMOID only (else 0)
+ *   margin             subtracted from every h
+ *   denominator        0, or > 0: replaces the number of counted pairs
+ *   kind               lp_preference
+ *   length_normalised  1: sums over a sequence are divided by its kept tokens */
+typedef struct {
+  float beta;
+  float label_smoothing;
+  float margin;
+  float denominator;
+  int32_t kind;
+  int32_t length_normalised;
+} lp_preference_options;
+
+/* Outputs of lp_preference_loss, device arrays; any may be NULL (at least one must not be).
+ *   metrics    fp32 [5]: the loss, then means over the counted pairs of 1[h > 0], beta h,
+ *              beta s_chosen, beta s_rejected
+ *   counts     int64 [1]: counted pairs
+ *   margins    fp32 [n_pairs]: h (0 for a pair that is not counted)
+ *   grad_logp  fp32 [T]: upstream * d loss / d logp */
+typedef struct {
+  float* metrics;
+  int64_t* counts;
+  float* margins;
+  float* grad_logp;
+} lp_preference_outputs;
+
+/* Preference loss over pairs of answers, and its gradient, in one call. Per sequence
+ * s = sum over kept tokens of (logp - ref_logp) (divided by their number when
+ * length_normalised); per pair h = s_chosen - s_rejected - margin; the loss is the mean of
+ * the chosen function of h over the counted pairs, those both of whose answers keep a
+ * token. Pairs that are not counted, and tokens that are not kept, get zero gradients;
+ * with no counted pair the loss is 0. Offsets and determinism as lp_policy_loss (with wrong
+ * offsets the margins are undefined).
+ * Workspace: lp_loss_workspace_size(LP_OP_PREFERENCE_LOSS, T, 2 * n_pairs). */
+LP_API lp_status lp_preference_loss(int64_t T, const lp_preference_inputs* in, const lp_preference_options* opts,
+                                    const lp_preference_outputs* out, void* workspace, size_t ws_bytes,
+                                    lp_stream_t stream);
 
 /* Synchronises `stream`, returns the first device-side error recorded on the
  * current device since the last call (LP_OK if none) and clears it. */

@@ -45,6 +45,8 @@ STATUS_NAMES = {
     8: "LP_ERR_CUDA",
     9: "LP_ERR_REPLAY_TOO_MANY_IDS",
     10: "LP_ERR_BOUNDS",
+    11: "LP_ERR_TOKEN_OUT_OF_RANGE",
+    12: "LP_ERR_SEQ_OFFSETS",
 }
 
 LP_OP_FORWARD = 0
@@ -54,6 +56,15 @@ LP_OP_BACKWARD = 3
 LP_OP_TOP_P_REPLAY_DENSE_MASK = 4
 LP_OP_BACKWARD_FROM_LOGITS = 5
 LP_OP_FORWARD_HOST = 6
+LP_OP_EMBEDDING_BACKWARD = 7
+LP_OP_POLICY_LOSS = 8
+LP_OP_PREFERENCE_LOSS = 9
+
+LP_AGGREGATIONS = {"token_mean": 0, "seq_mean_token_mean": 1, "seq_mean_token_sum": 2}
+LP_KL_KINDS = {"k1": 0, "k2": 1, "k3": 2}
+LP_PREFERENCES = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+POLICY_METRICS = ("loss", "policy", "kl", "entropy", "clip_fraction", "ratio")
+PREFERENCE_METRICS = ("loss", "accuracy", "margin", "chosen_reward", "rejected_reward")
 
 LP_DTYPE_F32 = 0
 LP_DTYPE_BF16 = 1
@@ -64,7 +75,9 @@ EXPORTED = ("lp_workspace_size", "lp_forward", "lp_forward_noalloc", "lp_forward
             "lp_top_p_replay", "lp_top_p_replay_from_logits", "lp_top_p_replay_dense_mask", "lp_backward",
             "lp_backward_ex", "lp_backward_from_logits", "lp_get_device_error", "lp_selftest_wait_timeout",
             "lp_selftest_bounds", "lp_debug_bounds_build", "lp_device_supported", "lp_status_string",
-            "lp_build_id", "lp_merge_shard_stats", "lp_sum_partials", "lp_set_wait_limit")
+            "lp_build_id", "lp_merge_shard_stats", "lp_sum_partials", "lp_set_wait_limit",
+            "lp_embedding", "lp_embedding_backward", "lp_loss_workspace_size", "lp_policy_loss",
+            "lp_preference_loss")
 
 
 class LPError(RuntimeError):
@@ -106,6 +119,39 @@ class _Outputs(ctypes.Structure):
 
 class _BackwardOptions(ctypes.Structure):
     _fields_ = [("dx_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("dw_dtype", ctypes.c_int32)]
+
+
+class _EmbeddingOptions(ctypes.Structure):
+    _fields_ = [("dw_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class _PolicyInputs(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("logp", "old_logp", "ref_logp", "entropy", "advantages", "mask",
+                                               "cu_seqlens", "upstream")] + [("n_seqs", ctypes.c_int64)]
+
+
+class _PolicyOptions(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_float) for k in ("clip_low", "clip_high", "dual_clip", "kl_coef", "entropy_coef",
+                                               "denominator")]
+                + [(k, ctypes.c_int32) for k in ("aggregation", "kl_kind", "adv_per_seq")])
+
+
+class _PolicyOutputs(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("metrics", "counts", "grad_logp", "grad_entropy")]
+
+
+class _PreferenceInputs(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("logp", "ref_logp", "mask", "cu_seqlens", "upstream")] + [
+        ("n_pairs", ctypes.c_int64)]
+
+
+class _PreferenceOptions(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_float) for k in ("beta", "label_smoothing", "margin", "denominator")]
+                + [(k, ctypes.c_int32) for k in ("kind", "length_normalised")])
+
+
+class _PreferenceOutputs(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("metrics", "counts", "margins", "grad_logp")]
 
 
 _lib = None
@@ -152,6 +198,14 @@ def lib() -> ctypes.CDLL:
     L.lp_forward_host.argtypes = [vp, i64, i64, P(vp), P(vp), P(_Partition), vp, f32, P(_Outputs), vp, sz, vp]
     L.lp_merge_shard_stats.argtypes = [vp, i64, P(_Partition), vp, P(_Outputs), vp]
     L.lp_sum_partials.argtypes = [P(vp), i32, i64, vp, ctypes.c_int, vp]
+    L.lp_embedding.argtypes = [vp, i64, i64, P(vp), ctypes.c_int, P(_Partition), f32, vp, i64, ctypes.c_int, vp]
+    L.lp_embedding_backward.argtypes = [vp, i64, i64, vp, i64, ctypes.c_int, P(_Partition), f32, P(vp),
+                                        P(_EmbeddingOptions), vp, sz, vp]
+    L.lp_loss_workspace_size.argtypes = [ctypes.c_int, i64, i64]
+    L.lp_loss_workspace_size.restype = sz
+    L.lp_policy_loss.argtypes = [i64, P(_PolicyInputs), P(_PolicyOptions), P(_PolicyOutputs), vp, sz, vp]
+    L.lp_preference_loss.argtypes = [i64, P(_PreferenceInputs), P(_PreferenceOptions), P(_PreferenceOutputs), vp, sz,
+                                     vp]
     L.lp_get_device_error.argtypes = [vp]
     L.lp_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     L.lp_set_wait_limit.argtypes = [ctypes.c_uint64]
@@ -164,7 +218,8 @@ def lib() -> ctypes.CDLL:
                  "lp_top_p_replay_from_logits", "lp_top_p_replay_dense_mask",
                  "lp_backward", "lp_backward_ex", "lp_backward_from_logits", "lp_forward_host", "lp_get_device_error",
                  "lp_selftest_wait_timeout", "lp_selftest_bounds", "lp_debug_bounds_build", "lp_device_supported",
-                 "lp_merge_shard_stats", "lp_sum_partials", "lp_set_wait_limit"):
+                 "lp_merge_shard_stats", "lp_sum_partials", "lp_set_wait_limit", "lp_embedding",
+                 "lp_embedding_backward", "lp_policy_loss", "lp_preference_loss"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -729,3 +784,233 @@ def lp_sum_partials(parts: Sequence[torch.Tensor], out_dtype=torch.float32,
                                    _LP_DTYPES[out_dtype], _stream(parts[0].device))
     _raise(st, "lp_sum_partials")
     return out
+
+
+# ------------------------------------------------------------------ embedding
+
+def _rows(t: torch.Tensor, name: str, dtype, T: int, H: int) -> int:
+    """Checks a [T, H] matrix whose rows are contiguous; returns its row stride in elements."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
+        raise TypeError(f"{name} must be a 2-D CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _shape(t, name, (T, H))
+    if t.stride(1) != 1 and t.numel():
+        raise ValueError(f"{name} must have unit column stride")
+    # the stride of a lone row has no meaning; what torch reports for it may not be a multiple of 16 bytes
+    return t.stride(0) if T > 1 else (H + 7) // 8 * 8
+
+
+def _table(W, part, name: str, dtypes) -> Tuple[list, int, torch.dtype]:
+    """The shards of a [V, H] table: (list, H, dtype)."""
+    n = len(part.ranges)
+    if len(W) != n:
+        raise ValueError(f"{name} must have one entry per shard ({n})")
+    given = [w for w in W if w is not None]
+    if not given:
+        raise ValueError(f"{name} holds no shard")
+    H, dtype = given[0].shape[-1], given[0].dtype
+    if dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
+    for k, (w, (s, e)) in enumerate(zip(W, part.ranges)):
+        if w is None:
+            if e > s and s < part.vocab_real:
+                raise ValueError(f"{name}[{k}] is None")
+            continue
+        _check(w, f"{name}[{k}]", dtype, 2)
+        _shape(w, f"{name}[{k}]", (e - s, H))
+    return list(W), H, dtype
+
+
+def lp_embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: float = 1.0, out_dtype=None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Embedding lookup: row t is scale * W[ids[t]] in fp32, as ``out_dtype`` (default: the
+    table's type). ids int32 [T] global ids, -1 = unused (a zero row); W[k] bf16 or fp32
+    [V_k, H]. ``out`` may be a [T, H] view with a row stride that is a multiple of 16 bytes."""
+    _check(ids, "ids", torch.int32, 1)
+    W, H, dtype = _table(W, part, "W", _LP_DTYPES)
+    out_dtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    if out_dtype not in _LP_DTYPES:
+        raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+    T = ids.shape[0]
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=ids.device)
+        ld = H
+    else:
+        ld = _rows(out, "out", out_dtype, T, H)
+    for w in W:
+        if w is not None:
+            _same_device(ids, w)
+    _same_device(ids, out)
+    cp, _keep = _c_partition(part)
+    with torch.cuda.device(ids.device):
+        st = lib().lp_embedding(ids.data_ptr(), T, H, _ptr_array(W), _LP_DTYPES[dtype], ctypes.byref(cp), float(scale),
+                                out.data_ptr(), ld, _LP_DTYPES[out_dtype], _stream(ids.device))
+    _raise(st, "lp_embedding")
+    return out
+
+
+def lp_embedding_backward(ids: torch.Tensor, dY: torch.Tensor, part, scale: float = 1.0, dw_dtype=torch.float32,
+                          accumulate: bool = False, dW=None, workspace: Optional[torch.Tensor] = None) -> list:
+    """Gradient of lp_embedding with respect to the table: dW[v] = scale * the sum of dY[t] over the
+    positions with ids[t] = v, one [V_k, H] tensor per shard (None for an empty one). dY bf16 or fp32
+    [T, H] (a row stride that is a multiple of 16 bytes is fine). ``accumulate`` adds into the
+    caller's fp32 ``dW`` (for example the dW of lp_backward_ex, for a table tied to the head)."""
+    _check(ids, "ids", torch.int32, 1)
+    T = ids.shape[0]
+    if not isinstance(dY, torch.Tensor) or dY.dim() != 2 or dY.dtype not in _LP_DTYPES:
+        raise TypeError("dY must be a 2-D fp32 or bf16 tensor")
+    H = dY.shape[1]
+    ld = _rows(dY, "dY", dY.dtype, T, H)
+    _same_device(ids, dY)
+    if dw_dtype not in _LP_DTYPES:
+        raise TypeError("dw_dtype must be torch.float32 or torch.bfloat16")
+    if accumulate and dw_dtype != torch.float32:
+        raise ValueError("accumulation needs fp32 dW")
+    if accumulate and dW is None:
+        raise ValueError("accumulate=True adds into the caller's dW: pass it")
+    n = len(part.ranges)
+    widths = [e - s for s, e in part.ranges]
+    if dW is None:
+        dW = [torch.empty((w, H), dtype=dw_dtype, device=ids.device) if w else None for w in widths]
+    else:
+        dW = _shard_list(dW, n, "dW", dw_dtype, 2, True)
+        for k, (t, w) in enumerate(zip(dW, widths)):
+            if w and (t is None or tuple(t.shape) != (w, H)):
+                raise ValueError(f"dW[{k}] must be {dw_dtype} [{w}, {H}]")
+            if t is not None:
+                _same_device(ids, t)
+    cp, _keep = _c_partition(part)
+    opts = _EmbeddingOptions(_LP_DTYPES[dw_dtype], 1 if accumulate else 0)
+    L = lib()
+    with torch.cuda.device(ids.device):
+        need = int(L.lp_workspace_size(LP_OP_EMBEDDING_BACKWARD, T, H, ctypes.byref(cp)))
+        ws, wsb = _workspace(need, ids.device, workspace)
+        st = L.lp_embedding_backward(ids.data_ptr(), T, H, dY.data_ptr(), ld, _LP_DTYPES[dY.dtype], ctypes.byref(cp),
+                                     float(scale), _ptr_array(dW), ctypes.byref(opts), _ptr(ws), wsb,
+                                     _stream(ids.device))
+    _raise(st, "lp_embedding_backward")
+    return dW
+
+
+# ------------------------------------------------------------------ losses
+
+def _per_token(t: Optional[torch.Tensor], name: str, n: int, like: torch.Tensor, dtype=torch.float32):
+    if t is None:
+        return
+    _check(t, name, dtype, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    _same_device(like, t)
+
+
+def _mask(mask: Optional[torch.Tensor], T: int, like: torch.Tensor):
+    if mask is not None and isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    _per_token(mask, "mask", T, like, torch.uint8)
+    return mask
+
+
+def _upstream(u: Optional[torch.Tensor], like: torch.Tensor):
+    if u is not None:
+        if not (isinstance(u, torch.Tensor) and u.is_cuda and u.dtype == torch.float32 and u.numel() == 1):
+            raise TypeError("upstream must be an fp32 CUDA tensor of one element")
+        _same_device(like, u)
+
+
+def lp_loss_workspace_size(op: int, T: int, n_seqs: int) -> int:
+    return int(lib().lp_loss_workspace_size(int(op), int(T), int(n_seqs)))
+
+
+def lp_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                   ref_logp: Optional[torch.Tensor] = None, entropy: Optional[torch.Tensor] = None,
+                   mask: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                   clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0, kl_coef: float = 0.0,
+                   kl_kind: str = "k3", entropy_coef: float = 0.0, aggregation: str = "token_mean",
+                   denominator: float = 0.0, upstream: Optional[torch.Tensor] = None, grads: bool = True,
+                   metrics: bool = True, workspace: Optional[torch.Tensor] = None,
+                   adv_per_seq: Optional[bool] = None) -> dict:
+    """Clipped policy loss with a KL term (``ref_logp``, ``kl_coef``, ``kl_kind`` k1 / k2 / k3) and an
+    entropy bonus, with its gradients. fp32 [T] per token; ``advantages`` [T], or one per sequence of
+    ``cu_seqlens`` (int32 [S + 1]; where S = T they are per token unless ``adv_per_seq``); ``mask`` bool or uint8 [T], zero = the token does not count.
+    ``aggregation``: token_mean, seq_mean_token_mean or seq_mean_token_sum; ``denominator`` replaces
+    the number of tokens (sequences) of the mean; ``upstream`` (fp32, one element, on the GPU)
+    multiplies the gradients. Returns loss (0-D), metrics [6] (POLICY_METRICS), counts int64 [2] (kept
+    tokens, counted sequences), grad_logp and, when entropy is given, grad_entropy."""
+    _check(logp, "logp", torch.float32, 1)
+    T = logp.shape[0]
+    _per_token(old_logp, "old_logp", T, logp)
+    _per_token(ref_logp, "ref_logp", T, logp)
+    _per_token(entropy, "entropy", T, logp)
+    mask = _mask(mask, T, logp)
+    S = 0
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
+        _same_device(logp, cu_seqlens)
+        S = cu_seqlens.shape[0] - 1
+        if S < 0:
+            raise ValueError("cu_seqlens must have n_seqs + 1 entries")
+    _check(advantages, "advantages", torch.float32, 1)
+    _same_device(logp, advantages)
+    per_seq = advantages.shape[0] != T if adv_per_seq is None else bool(adv_per_seq)
+    if (per_seq and cu_seqlens is None) or advantages.shape[0] != (S if per_seq else T):
+        raise ValueError("advantages must have one entry per token, or one per sequence of cu_seqlens")
+    if aggregation not in LP_AGGREGATIONS or kl_kind not in LP_KL_KINDS:
+        raise ValueError(f"aggregation is one of {tuple(LP_AGGREGATIONS)}, kl_kind of {tuple(LP_KL_KINDS)}")
+    _upstream(upstream, logp)
+    dev = logp.device
+    m = torch.empty(len(POLICY_METRICS), dtype=torch.float32, device=dev) if metrics else None
+    c = torch.empty(2, dtype=torch.int64, device=dev) if metrics else None
+    g = torch.empty(T, dtype=torch.float32, device=dev) if grads else None
+    ge = torch.empty(T, dtype=torch.float32, device=dev) if grads and entropy is not None else None
+    ci = _PolicyInputs(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(entropy), _ptr(advantages), _ptr(mask),
+                       _ptr(cu_seqlens), _ptr(upstream), S)
+    co = _PolicyOptions(clip_low, clip_high, dual_clip, kl_coef, entropy_coef, denominator,
+                        LP_AGGREGATIONS[aggregation], LP_KL_KINDS[kl_kind], 1 if per_seq else 0)
+    cr = _PolicyOutputs(_ptr(m), _ptr(c), _ptr(g), _ptr(ge))
+    L = lib()
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(int(L.lp_loss_workspace_size(LP_OP_POLICY_LOSS, T, S)), dev, workspace)
+        st = L.lp_policy_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb, _stream(dev))
+    _raise(st, "lp_policy_loss")
+    return {"loss": None if m is None else m[0], "metrics": m, "counts": c, "grad_logp": g, "grad_entropy": ge}
+
+
+def lp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
+                       mask: Optional[torch.Tensor] = None, beta: float = 0.1, kind: str = "sigmoid",
+                       label_smoothing: float = 0.0, length_normalised: bool = False, margin: float = 0.0,
+                       denominator: float = 0.0, upstream: Optional[torch.Tensor] = None, grads: bool = True,
+                       metrics: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Preference loss over pairs of answers with its gradient: sequences 2p and 2p + 1 of
+    ``cu_seqlens`` (int32 [2 P + 1]) are the chosen and the rejected answer of pair p. logp and
+    ref_logp fp32 [T] (None: a reference-free loss), mask bool or uint8 [T]. ``kind``: sigmoid, hinge or
+    ipo. Returns loss (0-D), metrics [5] (PREFERENCE_METRICS), counts int64 [1] (counted pairs), margins
+    [P] and grad_logp."""
+    _check(logp, "logp", torch.float32, 1)
+    T = logp.shape[0]
+    _per_token(ref_logp, "ref_logp", T, logp)
+    mask = _mask(mask, T, logp)
+    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    _same_device(logp, cu_seqlens)
+    if cu_seqlens.shape[0] % 2 != 1:
+        raise ValueError("cu_seqlens must have 2 * n_pairs + 1 entries")
+    P = cu_seqlens.shape[0] // 2
+    if kind not in LP_PREFERENCES:
+        raise ValueError(f"kind is one of {tuple(LP_PREFERENCES)}")
+    _upstream(upstream, logp)
+    dev = logp.device
+    m = torch.empty(len(PREFERENCE_METRICS), dtype=torch.float32, device=dev) if metrics else None
+    c = torch.empty(1, dtype=torch.int64, device=dev) if metrics else None
+    h = torch.empty(P, dtype=torch.float32, device=dev) if metrics else None
+    g = torch.empty(T, dtype=torch.float32, device=dev) if grads else None
+    ci = _PreferenceInputs(_ptr(logp), _ptr(ref_logp), _ptr(mask), _ptr(cu_seqlens), _ptr(upstream), P)
+    co = _PreferenceOptions(beta, label_smoothing, margin, denominator, LP_PREFERENCES[kind],
+                            1 if length_normalised else 0)
+    cr = _PreferenceOutputs(_ptr(m), _ptr(c), _ptr(h), _ptr(g))
+    L = lib()
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(int(L.lp_loss_workspace_size(LP_OP_PREFERENCE_LOSS, T, 2 * P)), dev, workspace)
+        st = L.lp_preference_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb,
+                                  _stream(dev))
+    _raise(st, "lp_preference_loss")
+    return {"loss": None if m is None else m[0], "metrics": m, "counts": c, "margins": h, "grad_logp": g}

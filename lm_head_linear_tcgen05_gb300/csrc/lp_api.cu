@@ -131,6 +131,14 @@ lp_status device_copy_stream(DeviceState* st) {
 
 }  // namespace
 
+// The current device's error word, for the translation units that launch kernels themselves.
+lp_status device_error_word(unsigned int** err) {
+  DeviceState* st = nullptr;
+  const lp_status s = device_state(&st);
+  if (s == LP_OK) *err = st->err;
+  return s;
+}
+
 uint64_t wait_limit_ns() { return g_wait_limit.load(std::memory_order_relaxed); }
 
 // bf16 row-major matrix [rows, inner] with row stride ld elements, boxes of
@@ -245,6 +253,8 @@ const char* lp_status_string(lp_status s) {
     case LP_ERR_CUDA: return "LP_ERR_CUDA: a CUDA runtime call failed";
     case LP_ERR_REPLAY_TOO_MANY_IDS: return "LP_ERR_REPLAY_TOO_MANY_IDS: a keep-mask row keeps more than 64 ids";
     case LP_ERR_BOUNDS: return "LP_ERR_BOUNDS: a device bounds check failed (bounds-checked build)";
+    case LP_ERR_TOKEN_OUT_OF_RANGE: return "LP_ERR_TOKEN_OUT_OF_RANGE: an embedding id is neither -1 nor in [0, vocab_real)";
+    case LP_ERR_SEQ_OFFSETS: return "LP_ERR_SEQ_OFFSETS: cu_seqlens does not ascend from 0 to T";
   }
   return "unknown lp_status";
 }
@@ -265,6 +275,10 @@ size_t lp_workspace_size(lp_op op, int64_t T, int64_t H, const lp_vocab_partitio
     case LP_OP_BACKWARD: return valid_hidden(H) ? backward_ws_bytes(T, H, sh) : 0;
     case LP_OP_BACKWARD_FROM_LOGITS: return 0;
     case LP_OP_FORWARD_HOST: return valid_hidden(H) ? host_layout(T, H, sh).total : 0;
+    case LP_OP_EMBEDDING_BACKWARD:
+      return valid_hidden(H) && T > 0 ? embedding_backward_ws_bytes(T, H, sh.end[sh.n - 1] - sh.start[0]) : 0;
+    case LP_OP_POLICY_LOSS:
+    case LP_OP_PREFERENCE_LOSS: return 0;  // lp_loss_workspace_size
   }
   return 0;
 }

@@ -227,6 +227,82 @@ struct BackwardArgs {
   int num_sms;
 };
 
+// ------------------------------------------------------------ embedding
+struct EmbeddingParams {
+  const int32_t* ids;
+  const void* W[LP_MAX_SHARDS];
+  void* Y;
+  int64_t ld_y;
+  int64_t shard_start[LP_MAX_SHARDS];
+  int64_t real[LP_MAX_SHARDS];
+  int64_t vocab_real;
+  int32_t n_shards;
+  int32_t T;
+  int32_t H;
+  float scale;
+  unsigned int* err;
+};
+
+// Gradient of the table. Rows are counted locally: row r of the call is id lo + r, r < width.
+struct EmbeddingGradParams {
+  const int32_t* ids;
+  const void* dY;
+  int64_t ld_dy;
+  void* dW[LP_MAX_SHARDS];
+  int64_t row_start[LP_MAX_SHARDS + 1];  // first local row of each shard; [n_shards] = width
+  int64_t lo;                            // id of local row 0
+  int64_t vocab_real;
+  int32_t n_shards;
+  int32_t T;
+  int32_t H;
+  int32_t key_bits;                      // bits of the sort key (a local row, or width: no row)
+  int32_t accumulate;
+  float scale;
+  unsigned int* err;
+  uint2* sorted[2];                      // (local row, position), ping-pong; the last pass fills [0]
+  float* partials;                       // [chunks][2][H]: pieces of runs longer than a chunk
+  int32_t* joins;                        // [0] their number, then their first chunks
+  uint32_t* present;                     // bit per local row: some position names it (overwriting only)
+};
+
+size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width);
+void embedding_backward_carve(EmbeddingGradParams* p, void* workspace, int64_t width);
+cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16, cudaStream_t s);
+cudaError_t launch_embedding_backward(const EmbeddingGradParams& p, bool dy_bf16, bool dw_bf16, cudaStream_t s);
+
+// ------------------------------------------------------------ losses
+struct PolicyParams {
+  lp_policy_inputs in;
+  lp_policy_outputs out;
+  float lo, hi, dual;                    // ratio bounds; dual 0 = none
+  float kl_coef, entropy_coef, denominator;
+  int32_t aggregation, kl_kind, adv_per_seq;
+  int32_t T, n_seqs;
+  void* workspace;
+  unsigned int* err;
+};
+
+struct PreferenceParams {
+  lp_preference_inputs in;
+  lp_preference_outputs out;
+  float beta, smoothing, margin, denominator;
+  int32_t kind, length_normalised;
+  int32_t T, n_pairs;
+  void* workspace;
+  unsigned int* err;
+};
+
+size_t policy_ws_bytes(int64_t T, int64_t n_seqs);
+size_t preference_ws_bytes(int64_t T, int64_t n_seqs);
+cudaError_t launch_policy_loss(const PolicyParams& p, cudaStream_t s);
+cudaError_t launch_preference_loss(const PreferenceParams& p, cudaStream_t s);
+
+// Argument checks and per-device state shared by the translation units of the C ABI.
+lp_status check_partition(const lp_vocab_partition* part, Shards* sh);
+bool valid_rows(int64_t T);
+bool valid_hidden(int64_t H);
+lp_status device_error_word(unsigned int** err);
+
 size_t backward_ws_bytes(int64_t T, int64_t H, const Shards& sh);
 lp_status run_backward(const BackwardArgs& a, const Shards& sh, cudaStream_t s);
 

@@ -1,0 +1,232 @@
+"""lp_embedding and lp_embedding_backward on the GPU against the fp64 oracle.
+
+The lookup is compared bit for bit with the fp32 product. The gradient of an id with n positions is
+a sum of n fp32 values in some order, then one product: each element may be off by (n + 1) 2^-24 of
+the sum of the magnitudes (and half a bf16 step where it is stored in bf16)."""
+import numpy as np
+import pytest
+
+from lp_util import dev_i32
+from oracle import train
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lp():
+    from lm_head_linear_tcgen05_gb300 import _build
+    _build.build()
+    import lm_head_linear_tcgen05_gb300 as mod
+    import torch
+    assert mod.lp_device_supported()
+    torch.cuda.set_device(0)
+    return mod
+
+
+def _part(lp, real, bounds, local=False):
+    return lp.VocabPartition(real, bounds[-1] if not local else max(bounds[-1], real),
+                             tuple((bounds[i], bounds[i + 1]) for i in range(len(bounds) - 1)), local=local)
+
+
+def _rand(shape, dtype, seed):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.empty(shape, dtype=dtype, device="cuda").normal_(generator=g)
+
+
+def _dtype(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+PARTS = [(1000, [0, 1000]), (997, [0, 200, 200, 600, 1024]), (513, [0, 8, 16, 500, 501, 513, 513, 513, 513])]
+
+
+@pytest.mark.parametrize("table", ["bf16", "f32"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,part", [(1, 8, 0), (3, 264, 1), (257, 1032, 2), (64, 4096, 0), (1000, 72, 1)])
+def test_lookup(lp, table, out, T, H, part):
+    import torch
+    real, bounds = PARTS[part]
+    rs = np.random.RandomState(T + H)
+    ids = rs.randint(-1, real, T)
+    ids[0] = real - 1
+    W = [_rand((b - a, H), _dtype(table), 7 + a) if b > a else None for a, b in zip(bounds[:-1], bounds[1:])]
+    for scale in (1.0, 0.37, -64.0):
+        y = lp.lp_embedding(dev_i32(ids), W, _part(lp, real, bounds), scale=scale, out_dtype=_dtype(out))
+        full = torch.cat([w for w in W if w is not None]).float()
+        at = torch.from_numpy(np.maximum(ids, 0)).cuda()
+        want = torch.where(torch.from_numpy(ids >= 0).cuda()[:, None],
+                           full[at] * torch.tensor(scale, dtype=torch.float32, device="cuda"), 0.0).to(_dtype(out))
+        assert torch.equal(y, want)
+        oracle = train.embedding(ids, full.double().cpu().numpy(), 0, float(np.float32(scale)))
+        # half an ulp of the output type, and of fp32 before it
+        half = (2.0 ** -8 if out == "bf16" else 2.0 ** -24) + 2.0 ** -24
+        assert np.all(np.abs(y.double().cpu().numpy() - oracle) <= np.abs(oracle) * half * 1.001 + 1e-38)
+    assert lp.lp_get_device_error() == 0
+
+
+def test_lookup_rank_local_strided_and_refused_ids(lp):
+    import torch
+    real, H = 1000, 136
+    full = _rand((real, H), torch.bfloat16, 1)
+    ids = dev_i32(np.array([0, 399, 400, 699, 700, 999, -1]))
+    lo = lp.lp_embedding(ids, [full[:400].contiguous()], _part(lp, real, [0, 400], local=True))
+    mid = lp.lp_embedding(ids, [full[400:700].contiguous()], _part(lp, real, [400, 700], local=True))
+    hi = lp.lp_embedding(ids, [full[700:].contiguous()], _part(lp, real, [700, 1000], local=True))
+    whole = lp.lp_embedding(ids, [full], _part(lp, real, [0, 1000]))
+    assert torch.equal(lo + mid + hi, whole) and torch.count_nonzero(lo[2:]) == 0
+    assert lp.lp_get_device_error() == 0
+    # a view with a longer row stride; what lies between the rows is left alone
+    buf = torch.full((7, H + 24), 5.0, dtype=torch.bfloat16, device="cuda")
+    lp.lp_embedding(ids, [full], _part(lp, real, [0, 1000]), out=buf[:, 8:8 + H])
+    assert torch.equal(buf[:, 8:8 + H], whole)
+    assert bool((buf[:, :8] == 5).all()) and bool((buf[:, 8 + H:] == 5).all())
+    for bad in (1000, -2, 2 ** 31 - 1, -2 ** 31):
+        y = lp.lp_embedding(dev_i32(np.array([5, bad])), [full], _part(lp, real, [0, 1000]))
+        assert torch.equal(y[0], full[5]) and torch.count_nonzero(y[1]) == 0
+        assert lp.lp_get_device_error() == 11
+    # NaN and infinities of the table come through
+    full[3, 0], full[3, 1] = float("nan"), float("inf")
+    y = lp.lp_embedding(dev_i32([3]), [full], _part(lp, real, [0, 1000]), scale=2.0)
+    assert bool(y[0, 0].isnan()) and bool(y[0, 1].isinf())
+    assert lp.lp_embedding(dev_i32(np.zeros(0)), [full], _part(lp, real, [0, 1000])).shape == (0, H)
+    assert lp.lp_get_device_error() == 0
+
+
+def _ids(kind, T, real, rs):
+    ids = np.minimum((real ** rs.rand(T)).astype(np.int64) - 1, real - 1)
+    if kind == "hot":
+        ids[rs.rand(T) < 0.8] = real // 2
+    elif kind == "one":
+        ids[:] = real - 1
+    elif kind == "distinct":
+        ids = rs.permutation(max(real, T))[:T] % real
+    elif kind == "unused":
+        ids[:] = -1
+    elif kind == "runs":                              # lengths around the 32-position chunk, and far above
+        ids = np.repeat(np.arange(real), np.resize([1, 31, 32, 33, 64, 65, 2, 30, 97, 5], real))[:T]
+        ids = rs.permutation(np.resize(ids, T))
+    ids[rs.rand(T) < 0.1] = -1
+    return ids
+
+
+def _check_gradient(got, bf16, want, mag, n):
+    got = got.double().cpu().numpy()
+    bound = (n[:, None] + 1) * 2.0 ** -24 * mag * 1.01
+    if bf16:
+        bound = bound + (np.abs(want) + bound) * 2.0 ** -8
+    assert np.all(np.abs(got - want) <= bound + 1e-38)
+    assert np.all(got[n == 0] == 0)
+
+
+@pytest.mark.parametrize("grad,dw", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
+@pytest.mark.parametrize("kind", ["zipf", "hot", "one", "distinct", "unused", "runs"])
+@pytest.mark.parametrize("T,H,part", [(1, 8, 0), (31, 264, 1), (33, 256, 2), (1000, 136, 1), (4099, 72, 0)])
+def test_gradient(lp, grad, dw, kind, T, H, part):
+    import torch
+    real, bounds = PARTS[part]
+    rs = np.random.RandomState(T * 7 + H)
+    ids = _ids(kind, T, real, rs)
+    dY = _rand((T, H), _dtype(grad), 3)
+    out = lp.lp_embedding_backward(dev_i32(ids), dY, _part(lp, real, bounds), scale=0.75, dw_dtype=_dtype(dw))
+    host = dY.double().cpu().numpy()
+    want, mag, n = train.embedding_backward(ids, host, 0, bounds[-1], 0.75)
+    got = torch.cat([g for g in out if g is not None])
+    _check_gradient(got, dw == "bf16", want, mag, n)
+    again = lp.lp_embedding_backward(dev_i32(ids), dY, _part(lp, real, bounds), scale=0.75, dw_dtype=_dtype(dw))
+    assert all(a is None or torch.equal(a, b) for a, b in zip(out, again))
+    assert lp.lp_get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", ["zipf", "hot", "runs"])
+def test_gradient_accumulates_one_add_per_element(lp, kind):
+    import torch
+    real, bounds = PARTS[1]
+    T, H = 3001, 136
+    ids = _ids(kind, T, real, np.random.RandomState(9))
+    dY = _rand((T, H), torch.bfloat16, 5)
+    part = _part(lp, real, bounds)
+    fresh = lp.lp_embedding_backward(dev_i32(ids), dY, part, scale=3.0)
+    held = [_rand((b - a, H), torch.float32, 11 + a) if b > a else None for a, b in zip(bounds[:-1], bounds[1:])]
+    before = [None if h is None else h.clone() for h in held]
+    lp.lp_embedding_backward(dev_i32(ids), dY, part, scale=3.0, accumulate=True, dW=held)
+    for h, b, f in zip(held, before, fresh):
+        assert h is None or torch.equal(h, b + f)
+    # an empty batch: zeros, or nothing when accumulating
+    none, dY0 = dev_i32(np.zeros(0)), torch.empty((0, H), dtype=torch.bfloat16, device="cuda")
+    lp.lp_embedding_backward(none, dY0, part, accumulate=True, dW=held)
+    assert all(h is None or torch.equal(h, b + f) for h, b, f in zip(held, before, fresh))
+    assert all(z is None or torch.count_nonzero(z) == 0 for z in lp.lp_embedding_backward(none, dY0, part, dW=held))
+
+
+def test_gradient_rank_local_strided_and_refused_ids(lp):
+    import torch
+    real, T, H = 1000, 777, 200
+    rs = np.random.RandomState(2)
+    ids = _ids("hot", T, real, rs)
+    buf = _rand((T, H + 40), torch.bfloat16, 4)
+    dY = buf[:, 16:16 + H]
+    whole = lp.lp_embedding_backward(dev_i32(ids), dY, _part(lp, real, [0, 400, 1000]))
+    want, mag, n = train.embedding_backward(ids, dY.double().cpu().numpy(), 0, real, 1.0)
+    _check_gradient(torch.cat(whole), False, want, mag, n)
+    a = lp.lp_embedding_backward(dev_i32(ids), dY, _part(lp, real, [0, 400], local=True))
+    b = lp.lp_embedding_backward(dev_i32(ids), dY, _part(lp, real, [400, 1000], local=True))
+    for got, lo, hi in ((a[0], 0, 400), (b[0], 400, 1000)):
+        _check_gradient(got, False, want[lo:hi], mag[lo:hi], n[lo:hi])
+    assert lp.lp_get_device_error() == 0
+    # a refused id takes no part; a NaN stays in its own row, and an unused position's is never read
+    bad = ids.copy()
+    bad[5], bad[6] = real, -7
+    got = lp.lp_embedding_backward(dev_i32(bad), dY, _part(lp, real, [0, 400, 1000]))
+    assert lp.lp_get_device_error() == 11
+    want, mag, n = train.embedding_backward(np.where((bad < 0) | (bad >= real), -1, bad), dY.double().cpu().numpy(), 0,
+                                            real, 1.0)
+    _check_gradient(torch.cat(got), False, want, mag, n)
+    ids[:] = np.arange(T)
+    ids[10] = -1
+    nan = dY.contiguous()
+    nan[10], nan[11] = float("nan"), float("nan")
+    got = torch.cat(lp.lp_embedding_backward(dev_i32(ids), nan, _part(lp, real, [0, 400, 1000])))
+    assert bool(got[11].isnan().all()) and int(got.isnan().any(dim=1).sum()) == 1
+    assert lp.lp_get_device_error() == 0
+
+
+def test_gradient_is_the_transpose_of_the_lookup(lp):
+    """<lookup(V), dY> = <V, gradient(dY)> for any V: on integers, where fp32 is exact."""
+    import torch
+    real, T, H = 300, 2000, 64
+    rs = np.random.RandomState(8)
+    ids = dev_i32(_ids("hot", T, real, rs))
+    V = torch.from_numpy(rs.randint(-3, 4, (real, H)).astype(np.float32)).cuda()
+    dY = torch.from_numpy(rs.randint(-3, 4, (T, H)).astype(np.float32)).cuda()
+    part = _part(lp, real, [0, real])
+    y = lp.lp_embedding(ids, [V], part, scale=2.0)
+    g = lp.lp_embedding_backward(ids, dY, part, scale=2.0)[0]
+    assert float((y.double() * dY.double()).sum()) == float((V.double() * g.double()).sum())
+
+
+def test_streams_and_graph(lp):
+    """The calls run on the caller's stream and can be captured."""
+    import torch
+    real, T, H = 500, 600, 128
+    part = _part(lp, real, [0, real])
+    ids = dev_i32(_ids("hot", T, real, np.random.RandomState(3)))
+    W, dY = _rand((real, H), torch.bfloat16, 1), _rand((T, H), torch.bfloat16, 2)
+    y0, g0 = lp.lp_embedding(ids, [W], part), lp.lp_embedding_backward(ids, dY, part)[0]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        y1, g1 = lp.lp_embedding(ids, [W], part), lp.lp_embedding_backward(ids, dY, part)[0]
+    s.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(g0, g1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y2, g2 = lp.lp_embedding(ids, [W], part), lp.lp_embedding_backward(ids, dY, part)[0]
+    for _ in range(3):
+        y2.zero_()
+        g2.fill_(7.0)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y0, y2) and torch.equal(g0, g2)
