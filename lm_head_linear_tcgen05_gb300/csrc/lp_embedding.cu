@@ -6,16 +6,16 @@
 // the bits depend on the order the hardware ran them in, so the positions are sorted by id
 // first (stably: equal ids stay in ascending position) and every row of dW is then written by
 // one owner that adds its positions in that order:
-//   sort_kernel     LSD radix sort of (local row, position), up to 9 bits a pass, in one CTA;
+//   sort_kernel     LSD radix sort of (local row, position), up to 9 bits a pass, in one cluster;
 //                   an unused or foreign position gets the key `width` and sorts last. It also
 //                   marks the rows that some position names.
-//   segment_kernel  one warp per (chunk of 32 sorted positions, 256 columns). A run of equal
-//                   rows of at most 32 positions is summed by the warp whose chunk it starts in,
-//                   which follows it into the next chunk; a longer run is summed in pieces, one
-//                   per chunk it touches, that go to the workspace. Which of the two holds is
+//   segment_kernel  four warps per (chunk of 32 sorted positions, 256 columns). A run of equal
+//                   rows of at most 32 positions is summed by the warp in whose quarter of a
+//                   chunk it begins, which follows it as far as it goes; a longer run is summed
+//                   in pieces, one per chunk it touches, that go to the workspace. Which of the two holds is
 //                   decided from the 96 keys around the chunk, so every warp reaches it alone.
 //                   When overwriting, further CTAs write zeros to the rows nobody names.
-//   join_kernel     adds the pieces of each long run in ascending order: 32 warps take
+//   join_kernel     adds the pieces of each long run in ascending order: 16 warps take
 //                   consecutive groups of pieces, whose sums are added in ascending order.
 #include <cuda_bf16.h>
 
@@ -131,63 +131,106 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 9;
 constexpr int kMaxBins = 1 << kMaxDigit;
 static_assert(kMaxBins == kSortThreads, "a thread per bin");
+#ifndef LP_SORT_CLUSTER
+#define LP_SORT_CLUSTER 8
+#endif
+constexpr int kSortCtas = LP_SORT_CLUSTER;
+constexpr int kSortAhead = 4;  // loads in flight per lane
+// positions of a CTA below which fewer CTAs sort: their barriers cost more than they save
+constexpr int64_t kSortMinPerCta = 512;
 
-// sort key of position t: its local row, or `width`
-__device__ __forceinline__ uint32_t position_key(const EmbeddingGradParams& p, int64_t t, uint32_t width, bool report) {
-  const int id = __ldg(p.ids + t);
-  if (id < 0 || int64_t(id) >= p.vocab_real) {
-    if (report && id != -1) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
-    return width;
-  }
-  const int64_t r = int64_t(id) - p.lo;
-  return r >= 0 && r < int64_t(width) ? uint32_t(r) : width;
+__device__ __forceinline__ uint32_t ld_cluster(const void* local, uint32_t cta) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(local, cta)) : "memory");
+  return v;
 }
 
+// sort key of the id at one position: its local row, or `width`
+__device__ __forceinline__ uint32_t position_key(const EmbeddingGradParams& p, int id, uint32_t width) {
+  const int64_t r = int64_t(id) - p.lo;
+  return id >= 0 && int64_t(id) < p.vocab_real && r >= 0 && r < int64_t(width) ? uint32_t(r) : width;
+}
+
+// One cluster. Each pass: every warp counts the digits of its stretch of positions, the CTAs
+// exchange their totals through distributed shared memory, and every warp walks its stretch
+// again, in order, writing each position where its digit's count says.
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ EmbeddingGradParams p) {
   __shared__ uint32_t hist[kSortWarps][kMaxBins];
+  __shared__ uint32_t totals[kMaxBins];
   __shared__ uint32_t warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t cta = blockIdx.x, ctas = gridDim.x;  // one cluster: the block index is the rank
   const uint32_t width = uint32_t(p.row_start[p.n_shards]);
   const int passes = (p.key_bits + kMaxDigit - 1) / kMaxDigit;
   const int bits = (p.key_bits + passes - 1) / passes;
   const uint32_t bins = 1u << bits;
-  const int64_t T = p.T;
-  const int64_t per_warp = ((T + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-  const int64_t begin = min(T, warp * per_warp), end = min(T, begin + per_warp);
-  if (tid == 0) p.joins[0] = 0;
+  const int64_t T = p.T, warps = int64_t(ctas) * kSortWarps;
+  const int64_t per_warp = ((T + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t begin = min(T, (int64_t(cta) * kSortWarps + warp) * per_warp), end = min(T, begin + per_warp);
+  grid_launch_dependents();
+  if (cta == 0 && tid == 0) *p.n_joins = 0;
   if (!p.accumulate) {
     const uint32_t words = (width + 31) / 32;
-    for (uint32_t i = tid; i < words; i += kSortThreads) p.present[i] = 0u;
-    __syncthreads();
+    for (uint32_t i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) p.present[i] = 0u;
+    cluster_sync();
   }
   for (int pass = 0; pass < passes; ++pass) {
     // passes alternate so that the last one fills sorted[0]
     const uint2* src = p.sorted[(passes - pass) & 1];
     uint2* dst = p.sorted[(passes - 1 - pass) & 1];
     const int shift = pass * bits;
-    for (int i = tid; i < kSortWarps * kMaxBins; i += kSortThreads) (&hist[0][0])[i] = 0u;
+    for (int w = 0; w < kSortWarps; ++w) hist[w][tid] = 0u;
     __syncthreads();
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-      const int64_t i = i0 + lane;
-      uint32_t key = 0, digit = kMaxBins;
-      if (i < end) {
-        key = pass == 0 ? position_key(p, i, width, true) : src[i].x;
-        digit = (key >> shift) & (bins - 1);
-        if (pass == 0 && !p.accumulate && key < width) atomicOr(p.present + (key >> 5), 1u << (key & 31));
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
+      uint32_t key[kSortAhead];
+#pragma unroll
+      for (int u = 0; u < kSortAhead; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        key[u] = 0u;
+        if (i < end) key[u] = pass == 0 ? uint32_t(__ldg(p.ids + i)) : __ldcg(src + i).x;
       }
-      const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-      if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
-      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < kSortAhead; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        if (i0 + 32 * u >= end) break;
+        uint32_t digit = kMaxBins;
+        if (i < end) {
+          uint32_t k = key[u];
+          if (pass == 0) {
+            const int id = int(k);
+            k = position_key(p, id, width);
+            if (id < -1 || int64_t(id) >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+            if (!p.accumulate && k < width) {
+              const uint32_t bit = 1u << (k & 31);
+              if ((__ldcg(p.present + (k >> 5)) & bit) == 0u) atomicOr(p.present + (k >> 5), bit);
+            }
+          }
+          digit = (k >> shift) & (bins - 1);
+        }
+        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
+        __syncwarp();
+      }
     }
     __syncthreads();
-    // exclusive prefix over (bin, warp): a thread per bin
-    uint32_t total = 0;
+    // a thread per bin: exclusive prefix over the CTA's warps, then over the CTAs, then over the bins
+    uint32_t mine = 0;
     for (int w = 0; w < kSortWarps; ++w) {
       const uint32_t x = hist[w][tid];
-      hist[w][tid] = total;
-      total += x;
+      hist[w][tid] = mine;
+      mine += x;
     }
-    uint32_t incl = total;
+    totals[tid] = mine;
+    cluster_sync();
+    uint32_t all = 0, before_me = 0, of_cta[kSortCtas];
+#pragma unroll
+    for (uint32_t c = 0; c < kSortCtas; ++c) of_cta[c] = c < ctas ? ld_cluster(totals + tid, c) : 0u;
+#pragma unroll
+    for (uint32_t c = 0; c < kSortCtas; ++c) {
+      if (c < cta) before_me += of_cta[c];
+      all += of_cta[c];
+    }
+    uint32_t incl = all;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
@@ -195,33 +238,41 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    uint32_t base = incl - total;
+    uint32_t base = incl - all + before_me;
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
     for (int w = 0; w < kSortWarps; ++w) hist[w][tid] += base;
     __syncthreads();
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-      const int64_t i = i0 + lane;
-      uint2 e = make_uint2(0u, uint32_t(i));
-      uint32_t digit = kMaxBins;
-      if (i < end) {
-        if (pass == 0)
-          e.x = position_key(p, i, width, false);
-        else
-          e = src[i];
-        digit = (e.x >> shift) & (bins - 1);
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
+      uint2 e[kSortAhead];
+#pragma unroll
+      for (int u = 0; u < kSortAhead; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        e[u] = make_uint2(0u, uint32_t(i));
+        if (i < end) {
+          if (pass == 0)
+            e[u].x = position_key(p, __ldg(p.ids + i), width);
+          else
+            e[u] = __ldcg(src + i);
+        }
       }
-      const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-      const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
-      uint32_t at = 0;
-      if (i < end) at = hist[warp][digit] + before;
-      __syncwarp();
-      if (i < end) {
-        if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e;
-        if (before == 0) hist[warp][digit] += uint32_t(__popc(peers));
+#pragma unroll
+      for (int u = 0; u < kSortAhead; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        if (i0 + 32 * u >= end) break;
+        const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : uint32_t(kMaxBins);
+        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
+        uint32_t at = 0;
+        if (i < end) at = hist[warp][digit] + before;
+        __syncwarp();
+        if (i < end) {
+          if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
+          if (before == 0) hist[warp][digit] += uint32_t(__popc(peers));
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-    __syncthreads();
+    cluster_sync();  // the pass's output and the totals' readers
   }
 }
 
@@ -229,6 +280,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
 
 constexpr int kChunk = 32;  // sorted positions of a warp
 constexpr int kSegWarps = 4;
+#ifndef LP_SEG_PARTS
+#define LP_SEG_PARTS 4
+#endif
+constexpr int kParts = LP_SEG_PARTS;     // warps that share a chunk's columns
+constexpr int kPart = kChunk / kParts;   // positions in which a warp's runs begin
 
 // the row of dW with local index r: its base pointer's element offset, in the shard that holds it
 __device__ __forceinline__ void* dw_row(const EmbeddingGradParams& p, uint32_t r, int64_t* off) {
@@ -311,9 +367,26 @@ __device__ __forceinline__ void sum_runs(const EmbeddingGradParams& p, const uin
     finish8<WB>(p, cur, col, acc);
 }
 
+__device__ __forceinline__ float4 add4(const float4 a, const float4 b) {
+  return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+
 // piece `slot` (0: of the run the chunk begins in, 1: of the run it ends in) of a chunk
 __device__ __forceinline__ float* piece_of(const EmbeddingGradParams& p, int64_t chunk, int slot) {
   return p.partials + (chunk * 2 + slot) * p.H;
+}
+
+// the last of the chunks [lo, hi] whose first position has `key`; chunk lo has, and those that have
+// come first. 32 probes a step.
+__device__ __forceinline__ int64_t last_chunk_of(const EmbeddingGradParams& p, uint32_t key, int64_t lo, int64_t hi) {
+  const int lane = threadIdx.x & 31;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+    const bool has = at <= hi && p.sorted[0][at * kChunk].x == key;
+    lo += __popc(__ballot_sync(0xffffffffu, has)) * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
 }
 
 template <bool DB, bool WB>
@@ -321,6 +394,8 @@ __global__ void __launch_bounds__(kSegWarps * 32) segment_kernel(const __grid_co
                                                                  int seg_ctas) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t width = uint32_t(p.row_start[p.n_shards]);
+  grid_launch_dependents();
+  grid_dependency_wait();
   if (int(blockIdx.x) >= seg_ctas) {  // zeros: 32 rows a CTA
     const uint32_t word = blockIdx.x - seg_ctas;
     const uint32_t present = p.present[word];
@@ -338,8 +413,9 @@ __global__ void __launch_bounds__(kSegWarps * 32) segment_kernel(const __grid_co
   }
   const int slabs = (p.H + kSlab - 1) / kSlab;
   const int64_t unit = int64_t(blockIdx.x) * kSegWarps + warp;
-  const int64_t chunk = unit / slabs, p0 = chunk * kChunk;
+  const int64_t chunk = unit / (slabs * kParts), p0 = chunk * kChunk;
   const int slab = int(unit % slabs), col = slab * kSlab + lane * 8;
+  const int begin = int(unit / slabs % kParts) * kPart;  // this warp's part of the chunk
   const int64_t T = p.T;
   if (p0 >= T) return;
   const uint2 none = make_uint2(width, 0u);
@@ -349,77 +425,85 @@ __global__ void __launch_bounds__(kSegWarps * 32) segment_kernel(const __grid_co
   const uint32_t first = __shfl_sync(0xffffffffu, own.x, 0), last = __shfl_sync(0xffffffffu, own.x, 31);
   if (first >= width) return;  // only unused positions from here on
   const uint32_t eq_prev = __ballot_sync(0xffffffffu, prev == first);
-  const uint32_t eq_own = __ballot_sync(0xffffffffu, own.x == first);
-  const uint32_t eq_last = __ballot_sync(0xffffffffu, own.x == last);
+  const int n_first = __popc(__ballot_sync(0xffffffffu, own.x == first));
+  const int n_last = __popc(__ballot_sync(0xffffffffu, own.x == last));
   const int next_last = __popc(__ballot_sync(0xffffffffu, next.x == last));
   const int valid = __popc(__ballot_sync(0xffffffffu, own.x < width));
-  int q0 = 0;
-  if (eq_prev != 0u) {  // the chunk begins inside a run
-    const int b = __popc(eq_own);
-    if (__popc(eq_prev) + b + (b == 32 ? next_last : 0) > kChunk)
-      sum_runs<DB, WB>(p, own, next, 0, b, col, piece_of(p, chunk, 0));
-    q0 = b;
-  }
-  if (q0 >= valid) return;
-  int q1 = valid;
+  const uint32_t left = __shfl_up_sync(0xffffffffu, own.x, 1);
+  const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 ? eq_prev == 0u : own.x != left);
+  // a long run the chunk begins inside
+  if (eq_prev != 0u && begin == 0 && __popc(eq_prev) + n_first + (n_first == 32 ? next_last : 0) > kChunk)
+    sum_runs<DB, WB>(p, own, next, 0, n_first, col, piece_of(p, chunk, 0));
+  if (eq_prev != 0u && n_first == 32) return;
+  int limit = valid, stop = valid;  // the last short run begins before limit and ends at stop
   if (valid == 32) {
-    const int b = __popc(eq_last);
-    if (b + next_last > kChunk) {  // ends inside a long run that starts here
-      sum_runs<DB, WB>(p, own, next, 32 - b, 32, col, piece_of(p, chunk, 1));
-      q1 = 32 - b;
-      if (slab == 0 && lane == 0) p.joins[1 + atomicAdd(p.joins, 1)] = int32_t(chunk);
-    } else {
-      q1 = 32 + next_last;
+    stop = 32 + next_last;
+    if (n_last + next_last > kChunk) {  // a long run that begins here and goes on
+      limit = stop = 32 - n_last;
+      if (limit / kPart * kPart == begin) {
+        sum_runs<DB, WB>(p, own, next, limit, 32, col, piece_of(p, chunk, 1));
+        if (slab == 0) {
+          const int64_t end = last_chunk_of(p, last, chunk + 1, (T + kChunk - 1) / kChunk - 1);
+          if (lane == 0) p.joins[atomicAdd(p.n_joins, 1)] = make_int4(int(chunk), int(end - chunk) + 1, int(last), 0);
+        }
+      }
     }
   }
-  if (q0 < q1) sum_runs<DB, WB>(p, own, next, q0, q1, col, nullptr);
+  // the short runs that begin in this warp's part
+  const uint32_t here = starts & ~((1u << begin) - 1u);
+  if (here == 0u || __ffs(here) - 1 >= min(begin + kPart, limit)) return;
+  const uint32_t after = begin + kPart < 32 ? starts & ~((1u << (begin + kPart)) - 1u) : 0u;
+  const int q1 = after != 0u && __ffs(after) - 1 < limit ? __ffs(after) - 1 : stop;
+  sum_runs<DB, WB>(p, own, next, __ffs(here) - 1, q1, col, nullptr);
 }
 
-constexpr int kJoinWarps = 32;
-constexpr int kJoinCtas = 304;
+constexpr int kJoinWarps = 16;
+constexpr int kJoinCols = 128;   // columns of a CTA: 4 a lane
+constexpr int kJoinAhead = 8;    // pieces in flight per lane
+constexpr int kJoinCtas = 608;
 
 template <bool WB>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ EmbeddingGradParams p) {
-  __shared__ float part[kJoinWarps][32];
+  __shared__ float4 part[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t chunks = (int64_t(p.T) + kChunk - 1) / kChunk;
-  const int n_runs = p.joins[0], slabs = (p.H + 31) / 32;
+  grid_dependency_wait();
+  const int n_runs = *p.n_joins, slabs = (p.H + kJoinCols - 1) / kJoinCols;
   for (int64_t item = blockIdx.x; item < int64_t(n_runs) * slabs; item += gridDim.x) {
-    const int64_t c0 = p.joins[1 + item / slabs];
-    const int col = int(item % slabs) * 32 + lane;
-    const uint32_t key = p.sorted[0][c0 * kChunk + kChunk - 1].x;
-    // the last chunk whose first position belongs to the run (c0 + 1 does)
-    int64_t lo = c0 + 1, hi = chunks - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) / 2;
-      if (p.sorted[0][mid * kChunk].x == key)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const int64_t n = lo - c0 + 1, per = (n + kJoinWarps - 1) / kJoinWarps;
+    const int4 run = p.joins[item / slabs];  // first chunk, pieces, row
+    const int64_t c0 = run.x, n = run.y, per = (n + kJoinWarps - 1) / kJoinWarps;
+    const uint32_t key = uint32_t(run.z);
+    const int col = int(item % slabs) * kJoinCols + lane * 4;
     const int64_t a = min(n, warp * per), b = min(n, a + per);
-    float s = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < p.H) {
-      for (int64_t i = a; i < b; ++i) {
-        const float x = piece_of(p, c0 + i, i == 0 ? 1 : 0)[col];
-        s = i == a ? x : __fadd_rn(s, x);
+      for (int64_t i0 = a; i0 < b; i0 += kJoinAhead) {
+        float4 x[kJoinAhead];
+#pragma unroll
+        for (int u = 0; u < kJoinAhead; ++u)
+          if (i0 + u < b)
+            x[u] = __ldcg(reinterpret_cast<const float4*>(piece_of(p, c0 + i0 + u, i0 + u == 0 ? 1 : 0) + col));
+#pragma unroll
+        for (int u = 0; u < kJoinAhead; ++u)
+          if (i0 + u < b) s = i0 + u == a ? x[u] : add4(s, x[u]);
       }
     }
     part[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && col < p.H) {
-      float sum = part[0][lane];
-      for (int w = 1; w < kJoinWarps && w * per < n; ++w) sum = __fadd_rn(sum, part[w][lane]);
-      sum = __fmul_rn(sum, p.scale);
+      float4 sum = part[0][lane];
+      for (int w = 1; w < kJoinWarps && w * per < n; ++w) sum = add4(sum, part[w][lane]);
+      const float f[4] = {__fmul_rn(sum.x, p.scale), __fmul_rn(sum.y, p.scale), __fmul_rn(sum.z, p.scale),
+                          __fmul_rn(sum.w, p.scale)};
       int64_t off = 0;
       void* base = dw_row(p, key, &off);
-      if (in_bounds(base != nullptr, p.err)) {
+      if (in_bounds(base != nullptr && col + 4 <= p.H, p.err)) {
         if constexpr (WB) {
-          static_cast<__nv_bfloat16*>(base)[off + col] = __float2bfloat16_rn(sum);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + off + col) =
+              make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
         } else {
-          float* q = static_cast<float*>(base) + off + col;
-          *q = p.accumulate ? __fadd_rn(*q, sum) : sum;
+          float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + off + col);
+          const float4 v = make_float4(f[0], f[1], f[2], f[3]);
+          *q = p.accumulate ? add4(*q, v) : v;
         }
       }
     }
@@ -431,13 +515,47 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int64_t chunk_count(int64_t T) { return (T + kChunk - 1) / kChunk; }
 
+cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
+  int ctas = kSortCtas;
+  while (ctas > 1 && p.T < ctas * kSortMinPerCta) ctas /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas), 1, 1);
+  cfg.blockDim = dim3(kSortThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_kernel, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 template <bool DB, bool WB>
-void launch_sums(const EmbeddingGradParams& p, cudaStream_t s) {
+cudaError_t launch_sums(const EmbeddingGradParams& p, cudaStream_t s) {
   const int64_t slabs = (p.H + kSlab - 1) / kSlab;
-  const int64_t seg = (chunk_count(p.T) * slabs + kSegWarps - 1) / kSegWarps;
+  const int64_t seg = (chunk_count(p.T) * kParts * slabs + kSegWarps - 1) / kSegWarps;
   const int64_t zero = p.accumulate ? 0 : (p.row_start[p.n_shards] + 31) / 32;
-  segment_kernel<DB, WB><<<unsigned(seg + zero), kSegWarps * 32, 0, s>>>(p, int(seg));
-  if (p.T > kChunk) join_kernel<WB><<<kJoinCtas, kJoinWarps * 32, 0, s>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(unsigned(seg + zero), 1, 1);
+  cfg.blockDim = dim3(kSegWarps * 32, 1, 1);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, segment_kernel<DB, WB>, p, int(seg));
+  if (e == cudaSuccess && p.T > kChunk) {
+    cfg.gridDim = dim3(kJoinCtas, 1, 1);
+    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+    e = cudaLaunchKernelEx(&cfg, join_kernel<WB>, p);
+  }
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 }  // namespace
@@ -458,7 +576,7 @@ cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16,
 
 size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width) {
   const size_t chunks = size_t(chunk_count(T));
-  return 2 * up256(size_t(T) * sizeof(uint2)) + up256((1 + chunks) * sizeof(int32_t)) +
+  return 2 * up256(size_t(T) * sizeof(uint2)) + up256(sizeof(int4)) + up256(chunks * sizeof(int4)) +
          up256(size_t((width + 31) / 32) * sizeof(uint32_t)) + (T > kChunk ? chunks * 2 * size_t(H) * sizeof(float) : 0);
 }
 
@@ -468,8 +586,10 @@ void embedding_backward_carve(EmbeddingGradParams* p, void* workspace, int64_t w
     p->sorted[i] = reinterpret_cast<uint2*>(w);
     w += up256(size_t(p->T) * sizeof(uint2));
   }
-  p->joins = reinterpret_cast<int32_t*>(w);
-  w += up256((1 + size_t(chunk_count(p->T))) * sizeof(int32_t));
+  p->n_joins = reinterpret_cast<int32_t*>(w);
+  w += up256(sizeof(int4));
+  p->joins = reinterpret_cast<int4*>(w);
+  w += up256(size_t(chunk_count(p->T)) * sizeof(int4));
   p->present = reinterpret_cast<uint32_t*>(w);
   w += up256(size_t((width + 31) / 32) * sizeof(uint32_t));
   p->partials = reinterpret_cast<float*>(w);
@@ -477,16 +597,10 @@ void embedding_backward_carve(EmbeddingGradParams* p, void* workspace, int64_t w
 
 cudaError_t launch_embedding_backward(const EmbeddingGradParams& p, bool dy_bf16, bool dw_bf16, cudaStream_t s) {
   if (p.row_start[p.n_shards] == 0) return cudaSuccess;  // no rows at all
-  sort_kernel<<<1, kSortThreads, 0, s>>>(p);
-  if (dy_bf16 && dw_bf16)
-    launch_sums<true, true>(p, s);
-  else if (dy_bf16)
-    launch_sums<true, false>(p, s);
-  else if (dw_bf16)
-    launch_sums<false, true>(p, s);
-  else
-    launch_sums<false, false>(p, s);
-  return cudaGetLastError();
+  cudaError_t e = launch_sort(p, s);
+  if (e != cudaSuccess) return e;
+  if (dy_bf16) return dw_bf16 ? launch_sums<true, true>(p, s) : launch_sums<true, false>(p, s);
+  return dw_bf16 ? launch_sums<false, true>(p, s) : launch_sums<false, false>(p, s);
 }
 
 }  // namespace lp

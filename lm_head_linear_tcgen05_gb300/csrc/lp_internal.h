@@ -261,7 +261,8 @@ struct EmbeddingGradParams {
   unsigned int* err;
   uint2* sorted[2];                      // (local row, position), ping-pong; the last pass fills [0]
   float* partials;                       // [chunks][2][H]: pieces of runs longer than a chunk
-  int32_t* joins;                        // [0] their number, then their first chunks
+  int32_t* n_joins;                      // number of such runs
+  int4* joins;                           // their first chunk, number of pieces and row
   uint32_t* present;                     // bit per local row: some position names it (overwriting only)
 };
 
