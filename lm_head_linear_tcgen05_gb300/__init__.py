@@ -12,7 +12,9 @@ functions works but the first call raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
@@ -787,6 +789,31 @@ def lp_sum_partials(parts: Sequence[torch.Tensor], out_dtype=torch.float32,
 
 
 # ------------------------------------------------------------------ embedding
+# These calls can be as short as a launch, so what surrounds the launch is kept short too: the
+# device is switched only when it is not the current one, the stream is read as a raw handle, and
+# a partition's C form is made once per partition value.
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(dev: torch.device):
+    return _SAME_DEVICE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(dev: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+_cached_partition = functools.lru_cache(maxsize=64)(_c_partition)
+
+
+def _partition_ref(part):
+    """A pointer to the C form of ``part`` for a call (which only reads it)."""
+    try:
+        return ctypes.byref(_cached_partition(part)[0])
+    except TypeError:                       # not hashable: ranges given as a list
+        return ctypes.byref(_c_partition(part)[0])
+
 
 def _rows(t: torch.Tensor, name: str, dtype, T: int, H: int) -> int:
     """Checks a [T, H] matrix whose rows are contiguous; returns its row stride in elements."""
@@ -842,10 +869,10 @@ def lp_embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: floa
         if w is not None:
             _same_device(ids, w)
     _same_device(ids, out)
-    cp, _keep = _c_partition(part)
-    with torch.cuda.device(ids.device):
-        st = lib().lp_embedding(ids.data_ptr(), T, H, _ptr_array(W), _LP_DTYPES[dtype], ctypes.byref(cp), float(scale),
-                                out.data_ptr(), ld, _LP_DTYPES[out_dtype], _stream(ids.device))
+    dev = ids.device
+    with _on(dev):
+        st = lib().lp_embedding(ids.data_ptr(), T, H, _ptr_array(W), _LP_DTYPES[dtype], _partition_ref(part), scale,
+                                out.data_ptr(), ld, _LP_DTYPES[out_dtype], _raw_stream(dev))
     _raise(st, "lp_embedding")
     return out
 
@@ -880,42 +907,42 @@ def lp_embedding_backward(ids: torch.Tensor, dY: torch.Tensor, part, scale: floa
                 raise ValueError(f"dW[{k}] must be {dw_dtype} [{w}, {H}]")
             if t is not None:
                 _same_device(ids, t)
-    cp, _keep = _c_partition(part)
+    cp = _partition_ref(part)
     opts = _EmbeddingOptions(_LP_DTYPES[dw_dtype], 1 if accumulate else 0)
-    L = lib()
-    with torch.cuda.device(ids.device):
-        need = int(L.lp_workspace_size(LP_OP_EMBEDDING_BACKWARD, T, H, ctypes.byref(cp)))
-        ws, wsb = _workspace(need, ids.device, workspace)
-        st = L.lp_embedding_backward(ids.data_ptr(), T, H, dY.data_ptr(), ld, _LP_DTYPES[dY.dtype], ctypes.byref(cp),
-                                     float(scale), _ptr_array(dW), ctypes.byref(opts), _ptr(ws), wsb,
-                                     _stream(ids.device))
+    L, dev = lib(), ids.device
+    with _on(dev):
+        ws, wsb = _workspace(L.lp_workspace_size(LP_OP_EMBEDDING_BACKWARD, T, H, cp), dev, workspace)
+        st = L.lp_embedding_backward(ids.data_ptr(), T, H, dY.data_ptr(), ld, _LP_DTYPES[dY.dtype], cp, scale,
+                                     _ptr_array(dW), ctypes.byref(opts), _ptr(ws), wsb, _raw_stream(dev))
     _raise(st, "lp_embedding_backward")
     return dW
 
 
 # ------------------------------------------------------------------ losses
 
-def _per_token(t: Optional[torch.Tensor], name: str, n: int, like: torch.Tensor, dtype=torch.float32):
-    if t is None:
-        return
-    _check(t, name, dtype, 1)
-    if t.shape[0] != n:
+def _vector(t, name: str, dtype, n: Optional[int], device: int) -> int:
+    """Checks a contiguous 1-D CUDA tensor of n entries on GPU ``device``; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.dim() == 1
+            and t.is_contiguous() and (n is None or t.shape[0] == n)):
+        _check(t, name, dtype, 1)
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    _same_device(like, t)
+    return t.data_ptr()
 
 
-def _mask(mask: Optional[torch.Tensor], T: int, like: torch.Tensor):
-    if mask is not None and isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
-        mask = mask.view(torch.uint8)
-    _per_token(mask, "mask", T, like, torch.uint8)
-    return mask
+def _mask_bytes(mask, T: int, device: int) -> Optional[int]:
+    if mask is None:
+        return None
+    return _vector(mask, "mask", torch.bool if getattr(mask, "dtype", None) is torch.bool else torch.uint8, T, device)
 
 
-def _upstream(u: Optional[torch.Tensor], like: torch.Tensor):
-    if u is not None:
-        if not (isinstance(u, torch.Tensor) and u.is_cuda and u.dtype == torch.float32 and u.numel() == 1):
-            raise TypeError("upstream must be an fp32 CUDA tensor of one element")
-        _same_device(like, u)
+def _upstream(u: Optional[torch.Tensor], device: int) -> Optional[int]:
+    if u is None:
+        return None
+    if not (isinstance(u, torch.Tensor) and u.dtype is torch.float32 and u.numel() == 1 and u.get_device() == device):
+        raise TypeError(f"upstream must be an fp32 tensor of one element on cuda:{device}")
+    return u.data_ptr()
 
 
 def lp_loss_workspace_size(op: int, T: int, n_seqs: int) -> int:
@@ -938,40 +965,34 @@ def lp_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch
     multiplies the gradients. Returns loss (0-D), metrics [6] (POLICY_METRICS), counts int64 [2] (kept
     tokens, counted sequences), grad_logp and, when entropy is given, grad_entropy."""
     _check(logp, "logp", torch.float32, 1)
-    T = logp.shape[0]
-    _per_token(old_logp, "old_logp", T, logp)
-    _per_token(ref_logp, "ref_logp", T, logp)
-    _per_token(entropy, "entropy", T, logp)
-    mask = _mask(mask, T, logp)
+    T, d, f32 = logp.shape[0], logp.get_device(), torch.float32
     S = 0
     if cu_seqlens is not None:
-        _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
-        _same_device(logp, cu_seqlens)
+        cu = _vector(cu_seqlens, "cu_seqlens", torch.int32, None, d)
         S = cu_seqlens.shape[0] - 1
         if S < 0:
             raise ValueError("cu_seqlens must have n_seqs + 1 entries")
-    _check(advantages, "advantages", torch.float32, 1)
-    _same_device(logp, advantages)
-    per_seq = advantages.shape[0] != T if adv_per_seq is None else bool(adv_per_seq)
-    if (per_seq and cu_seqlens is None) or advantages.shape[0] != (S if per_seq else T):
+    per_seq = len(advantages) != T if adv_per_seq is None else bool(adv_per_seq)
+    if (per_seq and cu_seqlens is None) or len(advantages) != (S if per_seq else T):
         raise ValueError("advantages must have one entry per token, or one per sequence of cu_seqlens")
     if aggregation not in LP_AGGREGATIONS or kl_kind not in LP_KL_KINDS:
         raise ValueError(f"aggregation is one of {tuple(LP_AGGREGATIONS)}, kl_kind of {tuple(LP_KL_KINDS)}")
-    _upstream(upstream, logp)
-    dev = logp.device
-    m = torch.empty(len(POLICY_METRICS), dtype=torch.float32, device=dev) if metrics else None
-    c = torch.empty(2, dtype=torch.int64, device=dev) if metrics else None
-    g = torch.empty(T, dtype=torch.float32, device=dev) if grads else None
-    ge = torch.empty(T, dtype=torch.float32, device=dev) if grads and entropy is not None else None
-    ci = _PolicyInputs(_ptr(logp), _ptr(old_logp), _ptr(ref_logp), _ptr(entropy), _ptr(advantages), _ptr(mask),
-                       _ptr(cu_seqlens), _ptr(upstream), S)
+    ci = _PolicyInputs(logp.data_ptr(), _vector(old_logp, "old_logp", f32, T, d),
+                       None if ref_logp is None else _vector(ref_logp, "ref_logp", f32, T, d),
+                       None if entropy is None else _vector(entropy, "entropy", f32, T, d),
+                       _vector(advantages, "advantages", f32, None, d), _mask_bytes(mask, T, d),
+                       None if cu_seqlens is None else cu, _upstream(upstream, d), S)
     co = _PolicyOptions(clip_low, clip_high, dual_clip, kl_coef, entropy_coef, denominator,
                         LP_AGGREGATIONS[aggregation], LP_KL_KINDS[kl_kind], 1 if per_seq else 0)
+    dev, L = logp.device, lib()
+    m = torch.empty(len(POLICY_METRICS), dtype=f32, device=dev) if metrics else None
+    c = torch.empty(2, dtype=torch.int64, device=dev) if metrics else None
+    g = torch.empty_like(logp) if grads else None
+    ge = torch.empty_like(logp) if grads and entropy is not None else None
     cr = _PolicyOutputs(_ptr(m), _ptr(c), _ptr(g), _ptr(ge))
-    L = lib()
-    with torch.cuda.device(dev):
-        ws, wsb = _workspace(int(L.lp_loss_workspace_size(LP_OP_POLICY_LOSS, T, S)), dev, workspace)
-        st = L.lp_policy_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb, _stream(dev))
+    with _on(dev):
+        ws, wsb = _workspace(L.lp_loss_workspace_size(LP_OP_POLICY_LOSS, T, S), dev, workspace)
+        st = L.lp_policy_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb, _raw_stream(dev))
     _raise(st, "lp_policy_loss")
     return {"loss": None if m is None else m[0], "metrics": m, "counts": c, "grad_logp": g, "grad_entropy": ge}
 
@@ -987,30 +1008,26 @@ def lp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp: O
     ipo. Returns loss (0-D), metrics [5] (PREFERENCE_METRICS), counts int64 [1] (counted pairs), margins
     [P] and grad_logp."""
     _check(logp, "logp", torch.float32, 1)
-    T = logp.shape[0]
-    _per_token(ref_logp, "ref_logp", T, logp)
-    mask = _mask(mask, T, logp)
-    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    _same_device(logp, cu_seqlens)
+    T, d, f32 = logp.shape[0], logp.get_device(), torch.float32
+    cu = _vector(cu_seqlens, "cu_seqlens", torch.int32, None, d)
     if cu_seqlens.shape[0] % 2 != 1:
         raise ValueError("cu_seqlens must have 2 * n_pairs + 1 entries")
     P = cu_seqlens.shape[0] // 2
     if kind not in LP_PREFERENCES:
         raise ValueError(f"kind is one of {tuple(LP_PREFERENCES)}")
-    _upstream(upstream, logp)
-    dev = logp.device
-    m = torch.empty(len(PREFERENCE_METRICS), dtype=torch.float32, device=dev) if metrics else None
-    c = torch.empty(1, dtype=torch.int64, device=dev) if metrics else None
-    h = torch.empty(P, dtype=torch.float32, device=dev) if metrics else None
-    g = torch.empty(T, dtype=torch.float32, device=dev) if grads else None
-    ci = _PreferenceInputs(_ptr(logp), _ptr(ref_logp), _ptr(mask), _ptr(cu_seqlens), _ptr(upstream), P)
+    ci = _PreferenceInputs(logp.data_ptr(), None if ref_logp is None else _vector(ref_logp, "ref_logp", f32, T, d),
+                           _mask_bytes(mask, T, d), cu, _upstream(upstream, d), P)
     co = _PreferenceOptions(beta, label_smoothing, margin, denominator, LP_PREFERENCES[kind],
                             1 if length_normalised else 0)
+    dev, L = logp.device, lib()
+    m = torch.empty(len(PREFERENCE_METRICS), dtype=f32, device=dev) if metrics else None
+    c = torch.empty(1, dtype=torch.int64, device=dev) if metrics else None
+    h = torch.empty(P, dtype=f32, device=dev) if metrics else None
+    g = torch.empty_like(logp) if grads else None
     cr = _PreferenceOutputs(_ptr(m), _ptr(c), _ptr(h), _ptr(g))
-    L = lib()
-    with torch.cuda.device(dev):
-        ws, wsb = _workspace(int(L.lp_loss_workspace_size(LP_OP_PREFERENCE_LOSS, T, 2 * P)), dev, workspace)
+    with _on(dev):
+        ws, wsb = _workspace(L.lp_loss_workspace_size(LP_OP_PREFERENCE_LOSS, T, 2 * P), dev, workspace)
         st = L.lp_preference_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb,
-                                  _stream(dev))
+                                  _raw_stream(dev))
     _raise(st, "lp_preference_loss")
     return {"loss": None if m is None else m[0], "metrics": m, "counts": c, "margins": h, "grad_logp": g}

@@ -27,6 +27,9 @@ namespace lp {
 namespace {
 
 constexpr int kSlab = 256;  // columns of a warp: 8 a lane
+#ifndef LP_LOOKUP_FEW
+#define LP_LOOKUP_FEW (4 * 64 * 152)
+#endif
 
 // 8 consecutive elements of a row as raw 16-byte loads
 template <bool BF16>
@@ -95,33 +98,44 @@ __device__ __forceinline__ void put8(void* base, int64_t off, const float (&f)[8
 
 constexpr int kLookupWarps = 4;
 
-template <bool WB, bool YB>
-__global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __grid_constant__ EmbeddingParams p) {
-  const int lane = threadIdx.x & 31;
-  const int slabs = (p.H + kSlab - 1) / kSlab;
-  const int64_t unit = int64_t(blockIdx.x) * kLookupWarps + (threadIdx.x >> 5);
-  const int64_t t = unit / slabs;
-  const int col = int(unit % slabs) * kSlab + lane * 8;
-  if (t >= p.T) return;
-  const int id = __ldg(p.ids + t);
-  if ((id < -1 || int64_t(id) >= p.vocab_real) && lane == 0) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
-  const void* W = nullptr;
-  int64_t row = 0;
-  for (int k = 0; k < p.n_shards; ++k) {
-    const int64_t r = int64_t(id) - p.shard_start[k];
-    if (id >= 0 && r >= 0 && r < p.real[k]) {
-      W = p.W[k];
-      row = r;
-    }
-  }
+// A CTA takes `rows` consecutive rows (ROWS of a warp at a time, their loads in flight together)
+// by kLookupWarps * 32 lanes of 8 columns.
+template <bool WB, bool YB, int ROWS>
+__global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __grid_constant__ EmbeddingParams p,
+                                                                      int warps_per_row) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = int(blockIdx.y * warps_per_row + (warp & (warps_per_row - 1))) * kSlab + lane * 8;
+  const int rows = kLookupWarps / warps_per_row;  // rows of the CTA at a time
+  const int t0 = int(blockIdx.x) * rows * ROWS + warp / warps_per_row;
+  int id[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) id[r] = t0 + r * rows < p.T ? __ldg(p.ids + t0 + r * rows) : -1;
   if (col >= p.H || !in_bounds(p.H <= p.ld_y, p.err)) return;
-  float f[8];
-  widen8<WB>(W != nullptr ? load8<WB>(W, row * p.H + col) : zero8<WB>(), f);
-  if (W != nullptr) {
+  Vec8<WB> v[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const void* W = nullptr;
+    int row = 0;
+    for (int k = 0; k < p.n_shards; ++k) {
+      const int at = id[r] - p.shard_start[k];  // a negative id stays negative or wraps past every shard
+      if (id[r] >= 0 && at >= 0 && at < p.real[k]) {
+        W = p.W[k];
+        row = at;
+      }
+    }
+    v[r] = W != nullptr ? load8<WB>(W, int64_t(row) * p.H + col) : zero8<WB>();
+    if ((id[r] < -1 || id[r] >= p.vocab_real) && col == 0) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int t = t0 + r * rows;
+    if (t >= p.T) break;
+    float f[8];
+    widen8<WB>(v[r], f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], p.scale);
+    put8<YB>(p.Y, int64_t(t) * p.ld_y + col, f);
   }
-  put8<YB>(p.Y, t * p.ld_y + col, f);
 }
 
 // ------------------------------------------------------------------ gradient: sort
@@ -134,10 +148,30 @@ static_assert(kMaxBins == kSortThreads, "a thread per bin");
 #ifndef LP_SORT_CLUSTER
 #define LP_SORT_CLUSTER 8
 #endif
+#ifndef LP_SORT_BALLOT
+#define LP_SORT_BALLOT 0
+#endif
+#ifndef LP_SORT_MIN
+#define LP_SORT_MIN 512
+#endif
 constexpr int kSortCtas = LP_SORT_CLUSTER;
 constexpr int kSortAhead = 4;  // loads in flight per lane
 // positions of a CTA below which fewer CTAs sort: their barriers cost more than they save
-constexpr int64_t kSortMinPerCta = 512;
+constexpr int64_t kSortMinPerCta = LP_SORT_MIN;
+
+// lanes whose digit (of `bits` bits; bit `bits` set: no position) equals this lane's
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits) {
+#if LP_SORT_BALLOT
+  uint32_t peers = 0xffffffffu;
+  for (int b = 0; b <= bits; ++b) {
+    const uint32_t set = __ballot_sync(0xffffffffu, (digit >> b) & 1u);
+    peers &= ((digit >> b) & 1u) ? set : ~set;
+  }
+  return peers;
+#else
+  return __match_any_sync(0xffffffffu, digit);
+#endif
+}
 
 __device__ __forceinline__ uint32_t ld_cluster(const void* local, uint32_t cta) {
   uint32_t v;
@@ -172,7 +206,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   if (!p.accumulate) {
     const uint32_t words = (width + 31) / 32;
     for (uint32_t i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) p.present[i] = 0u;
-    cluster_sync();
   }
   for (int pass = 0; pass < passes; ++pass) {
     // passes alternate so that the last one fills sorted[0]
@@ -193,21 +226,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
       for (int u = 0; u < kSortAhead; ++u) {
         const int64_t i = i0 + 32 * u + lane;
         if (i0 + 32 * u >= end) break;
-        uint32_t digit = kMaxBins;
+        uint32_t digit = bins;
         if (i < end) {
           uint32_t k = key[u];
           if (pass == 0) {
             const int id = int(k);
             k = position_key(p, id, width);
             if (id < -1 || int64_t(id) >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
-            if (!p.accumulate && k < width) {
-              const uint32_t bit = 1u << (k & 31);
-              if ((__ldcg(p.present + (k >> 5)) & bit) == 0u) atomicOr(p.present + (k >> 5), bit);
-            }
           }
           digit = (k >> shift) & (bins - 1);
         }
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        const uint32_t peers = same_digit(digit, bits);
         if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
         __syncwarp();
       }
@@ -259,9 +288,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
       for (int u = 0; u < kSortAhead; ++u) {
         const int64_t i = i0 + 32 * u + lane;
         if (i0 + 32 * u >= end) break;
-        const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : uint32_t(kMaxBins);
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
+        const uint32_t peers = same_digit(digit, bits);
         const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
+        if (pass == 0 && !p.accumulate) {  // a lane whose first peer has its row leaves the mark to it
+          const uint32_t of_first = __shfl_sync(0xffffffffu, e[u].x, __ffs(peers) - 1);
+          if (i < end && e[u].x < width && (before == 0 || e[u].x != of_first))
+            atomicOr(p.present + (e[u].x >> 5), 1u << (e[u].x & 31));
+        }
         uint32_t at = 0;
         if (i < end) at = hist[warp][digit] + before;
         __syncwarp();
@@ -411,11 +445,11 @@ __global__ void __launch_bounds__(kSegWarps * 32) segment_kernel(const __grid_co
     }
     return;
   }
-  const int slabs = (p.H + kSlab - 1) / kSlab;
-  const int64_t unit = int64_t(blockIdx.x) * kSegWarps + warp;
-  const int64_t chunk = unit / (slabs * kParts), p0 = chunk * kChunk;
-  const int slab = int(unit % slabs), col = slab * kSlab + lane * 8;
-  const int begin = int(unit / slabs % kParts) * kPart;  // this warp's part of the chunk
+  const uint32_t slabs = uint32_t(p.H + kSlab - 1) / kSlab;
+  const uint32_t unit = blockIdx.x * kSegWarps + warp, piece = unit / slabs;
+  const int64_t chunk = piece / kParts, p0 = chunk * kChunk;
+  const int slab = int(unit - piece * slabs), col = slab * kSlab + lane * 8;
+  const int begin = int(piece % kParts) * kPart;  // this warp's part of the chunk
   const int64_t T = p.T;
   if (p0 >= T) return;
   const uint2 none = make_uint2(width, 0u);
@@ -529,6 +563,9 @@ cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+#if LP_SORT_CLUSTER > 8
+  cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+#endif
   const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_kernel, p);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
@@ -560,18 +597,26 @@ cudaError_t launch_sums(const EmbeddingGradParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16, cudaStream_t s) {
-  const int64_t units = int64_t(p.T) * ((p.H + kSlab - 1) / kSlab);
-  const unsigned grid = unsigned((units + kLookupWarps - 1) / kLookupWarps);
-  if (w_bf16 && y_bf16)
-    embedding_kernel<true, true><<<grid, kLookupWarps * 32, 0, s>>>(p);
-  else if (w_bf16)
-    embedding_kernel<true, false><<<grid, kLookupWarps * 32, 0, s>>>(p);
-  else if (y_bf16)
-    embedding_kernel<false, true><<<grid, kLookupWarps * 32, 0, s>>>(p);
+namespace {
+
+template <bool WB, bool YB>
+cudaError_t launch_lookup(const EmbeddingParams& p, cudaStream_t s) {
+  const int slabs = (p.H + kSlab - 1) / kSlab;
+  const int per_row = slabs % 4 == 0 ? 4 : slabs % 2 == 0 ? 2 : 1, rows = kLookupWarps / per_row;
+  const unsigned y = unsigned((slabs + per_row - 1) / per_row);
+  // four rows a warp once that leaves every SM its full 64 warps; below, rows come one a warp
+  if (int64_t(p.T) * slabs >= LP_LOOKUP_FEW)
+    embedding_kernel<WB, YB, 4><<<dim3(unsigned((p.T + rows * 4 - 1) / (rows * 4)), y), kLookupWarps * 32, 0, s>>>(p, per_row);
   else
-    embedding_kernel<false, false><<<grid, kLookupWarps * 32, 0, s>>>(p);
+    embedding_kernel<WB, YB, 1><<<dim3(unsigned((p.T + rows - 1) / rows), y), kLookupWarps * 32, 0, s>>>(p, per_row);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16, cudaStream_t s) {
+  if (w_bf16) return y_bf16 ? launch_lookup<true, true>(p, s) : launch_lookup<true, false>(p, s);
+  return y_bf16 ? launch_lookup<false, true>(p, s) : launch_lookup<false, false>(p, s);
 }
 
 size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width) {

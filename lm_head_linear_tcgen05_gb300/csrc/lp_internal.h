@@ -233,9 +233,9 @@ struct EmbeddingParams {
   const void* W[LP_MAX_SHARDS];
   void* Y;
   int64_t ld_y;
-  int64_t shard_start[LP_MAX_SHARDS];
-  int64_t real[LP_MAX_SHARDS];
-  int64_t vocab_real;
+  int32_t shard_start[LP_MAX_SHARDS];    // ids fit 32 bits (check_partition)
+  int32_t real[LP_MAX_SHARDS];
+  int32_t vocab_real;
   int32_t n_shards;
   int32_t T;
   int32_t H;
@@ -278,6 +278,7 @@ struct PolicyParams {
   float lo, hi, dual;                    // ratio bounds; dual 0 = none
   float kl_coef, entropy_coef, denominator;
   int32_t aggregation, kl_kind, adv_per_seq;
+  int32_t vec;                           // every per-token array allows 16-byte accesses
   int32_t T, n_seqs;
   void* workspace;
   unsigned int* err;
@@ -288,6 +289,7 @@ struct PreferenceParams {
   lp_preference_outputs out;
   float beta, smoothing, margin, denominator;
   int32_t kind, length_normalised;
+  int32_t vec;                           // the mask and the gradient allow 4- and 16-byte accesses
   int32_t T, n_pairs;
   void* workspace;
   unsigned int* err;

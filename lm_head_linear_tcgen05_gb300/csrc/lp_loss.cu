@@ -1,20 +1,23 @@
 // lp_loss.cu - the clipped policy loss and the preference loss, each with its gradient.
 //
-// Both are sums over tokens whose weights need a sum over all of them first (the kept tokens,
-// the counted sequences or pairs), so each runs as a few passes over the tokens:
-//   policy       count_kernel        kept tokens of every block of 4096
-//                policy_stat_kernel  kept tokens of every sequence (whole blocks plus the two
-//                                    ragged ends), totals
-//                policy_kernel       every token's term, gradients, partial sums
-//                policy_final_kernel the metrics
-//   preference   pref_sum_kernel     log-ratio sums of 256-token tiles; a sequence inside one tile
-//                                    is finished here
-//                pref_pair_kernel    sequences from their tiles, the pair's function and slope,
-//                                    partial sums
-//                pref_grad_kernel    gradients; its first CTA also writes the metrics
-// Token terms and the sums of a thread or warp are fp32; partial sums are added in fp64. All
-// sums have an order fixed by T and the offsets, never by timing. Everything the offsets index
-// is clamped to [0, T], so wrong offsets give LP_ERR_SEQ_OFFSETS and never a stray access.
+// Both are sums over tokens whose weights need a sum over all of them first (the kept tokens, the
+// counted sequences or pairs), so each runs in stages over the tokens:
+//   policy       count   kept tokens of every block of 512
+//                stat    kept tokens of every sequence (whole blocks plus the two ragged ends), totals
+//                tokens  every token's term, gradients, partial sums
+//                final   the metrics
+//   preference   sum     log-ratio sums of 256-token tiles; a sequence inside one tile is finished here
+//                pair    sequences from their tiles, the pair's function and slope, partial sums
+//                grad    gradients; the first CTA also writes the metrics
+// A stage is a device function over (CTA, number of CTAs). Long batches launch a kernel per stage
+// (the policy's last stage is run by the CTA that finishes the tokens last). Short ones are bound by
+// what a launch and its dependencies cost, so one cluster runs all stages with its hardware barrier
+// between them.
+// Token terms and the sums of a thread, warp or CTA are fp32. Sums over tiles and pairs carry their
+// rounding along in a second fp32 (fp64 additions issue at a thirty-second of the fp32 rate here:
+// with them the pair stage took 19 us instead of 6 for 1024 pairs).
+// All sums have an order fixed by T and the offsets, never by timing. Everything the offsets index is
+// clamped to [0, T], so wrong offsets give LP_ERR_SEQ_OFFSETS and never a stray access.
 #include "lp_device.cuh"
 
 namespace lp {
@@ -23,82 +26,130 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCountBlock = 4096;  // tokens of a count
-constexpr int kStatCtas = 304;     // most CTAs of the per-sequence and per-pair passes
-constexpr int kTokenTile = 1024;   // tokens of a CTA and step, four a thread
-constexpr int kTokenCtas = 1216;   // most CTAs of the token passes
-constexpr int kPrefTile = 256;     // tokens of a warp, eight a lane
+constexpr int kCountBlock = 512;            // tokens of a count: 16 a lane
+constexpr int kStatCtas = 304;              // most CTAs of the per-sequence and per-pair stages
+constexpr int kTokenTile = 4 * kThreads;    // tokens of a CTA and step, four a thread
+#ifndef LP_TOKEN_MIN
+#define LP_TOKEN_MIN 3
+#endif
+#ifndef LP_TOKEN_CTAS
+#define LP_TOKEN_CTAS 456
+#endif
+constexpr int kTokenCtas = LP_TOKEN_CTAS;             // most CTAs of the token stages
+constexpr int kPrefTile = 256;              // tokens of a warp, eight a lane
+constexpr int kCluster = 8;                 // CTAs of the one-launch form
+#ifndef LP_LOSS_FUSED_T
+#define LP_LOSS_FUSED_T 16384
+#endif
+constexpr int64_t kFusedTokens = LP_LOSS_FUSED_T;  // batches up to this long run in one launch
+constexpr int64_t kFusedSeqs = 16384;              // of up to this many sequences
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// what the CTAs of a per-sequence pass report
-struct Totals {
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// What a CTA of a per-sequence stage reports.
+struct __align__(16) Totals {
   long long kept;
   int seqs;
   int bad;  // offsets out of order
 };
 
+// Workspace written by an earlier stage is read past the L1, which another SM's writes do not
+// reach within a launch.
+__device__ __forceinline__ Totals read_totals(const Totals* t) {
+  const int4 v = __ldcg(reinterpret_cast<const int4*>(t));
+  return Totals{(long long)(uint64_t(uint32_t(v.x)) | (uint64_t(uint32_t(v.y)) << 32)), v.z, v.w};
+}
+
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
-
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
-
-// Sum over the CTA of a value per thread, in a fixed order; every thread gets it.
 template <typename V>
-__device__ __forceinline__ V cta_sum(V v, V* scratch) {
-  v = warp_sum(v);
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// A sum with the rounding errors of its additions, found exactly by the two-sum of Knuth.
+struct __align__(8) Pair32 {
+  float hi, lo;
+  __device__ __forceinline__ float value() const { return __fadd_rn(hi, lo); }
+};
+
+__device__ __forceinline__ Pair32 add(const Pair32 a, const Pair32 b) {
+  const float s = __fadd_rn(a.hi, b.hi);
+  if (!isfinite(s)) return Pair32{s, 0.f};
+  const float t = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+  return Pair32{s, __fadd_rn(e, __fadd_rn(a.lo, b.lo))};
+}
+
+__device__ __forceinline__ Pair32 add(const Pair32 a, float b) { return add(a, Pair32{b, 0.f}); }
+
+__device__ __forceinline__ Pair32 warp_add(Pair32 v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1)
+    v = add(v, Pair32{__shfl_xor_sync(0xffffffffu, v.hi, off), __shfl_xor_sync(0xffffffffu, v.lo, off)});
+  return v;
+}
+
+// Sums over the CTA of N values per warp (lane 0's), in the order of the warps; thread i gets the
+// i-th.
+__device__ __forceinline__ float add(float a, float b) { return __fadd_rn(a, b); }
+
+template <int N, typename V>
+__device__ __forceinline__ V cta_sums(const V (&v)[N], V (&scratch)[kWarps][N]) {
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) scratch[threadIdx.x >> 5][i] = v[i];
   __syncthreads();
-  V s = scratch[0];
-  for (int w = 1; w < kWarps; ++w) s += scratch[w];
+  V s{};
+  if (threadIdx.x < N) {
+    s = scratch[0][threadIdx.x];
+#pragma unroll 1
+    for (int w = 1; w < kWarps; ++w) s = add(s, scratch[w][threadIdx.x]);
+  }
   return s;
 }
 
-// Totals over the n CTAs of an earlier pass, added by all threads of this CTA.
-__device__ __forceinline__ Totals add_totals(const Totals* t, int n) {
-  __shared__ long long kept[kWarps];
-  __shared__ int seqs[kWarps], bad[kWarps];
-  long long k = 0;
-  int s = 0, b = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    k += t[i].kept;
-    s += t[i].seqs;
-    b |= t[i].bad;
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) k += __shfl_xor_sync(0xffffffffu, k, off);
-  s = warp_sum_int(s);
-  b = __reduce_or_sync(0xffffffffu, b);
-  if ((threadIdx.x & 31) == 0) {
-    kept[threadIdx.x >> 5] = k;
-    seqs[threadIdx.x >> 5] = s;
-    bad[threadIdx.x >> 5] = b;
-  }
+// Totals of the CTA from one per warp; every thread gets them.
+__device__ __forceinline__ Totals cta_totals(Totals t) {
+  __shared__ Totals part[kWarps];
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
   __syncthreads();
   Totals r{0, 0, 0};
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
-    r.kept += kept[w];
-    r.seqs += seqs[w];
-    r.bad |= bad[w];
+    r.kept += part[w].kept;
+    r.seqs += part[w].seqs;
+    r.bad |= part[w].bad;
   }
-  __syncthreads();
   return r;
 }
 
-// index of the sequence that holds token t: the number of ends at or before t (empty sequences
-// are passed over), at most n - 1 whatever the offsets hold
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int t) {
-  int lo = 0, hi = n - 1;
+// Totals over the n CTAs of an earlier stage; every thread gets them.
+__device__ __forceinline__ Totals add_totals(const Totals* totals, int n) {
+  Totals t{0, 0, 0};
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Totals o = read_totals(totals + i);
+    t.kept += o.kept;
+    t.seqs += o.seqs;
+    t.bad |= o.bad;
+  }
+  t.kept = warp_sum(t.kept);
+  t.seqs = warp_sum_int(t.seqs);
+  t.bad = __reduce_or_sync(0xffffffffu, t.bad);
+  return cta_totals(t);
+}
+
+// ------------------------------------------------------------------ sequences
+
+// Index of the sequence that holds token t: the number of ends at or before t among the first
+// hi (empty sequences are passed over), searched in [lo, hi].
+__device__ __forceinline__ int sequence_in(const int32_t* cu, int lo, int hi, int t) {
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(cu + mid + 1) <= t)
@@ -109,7 +160,19 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int t) {
   return lo;
 }
 
-// offsets of sequence s, clamped to [0, T] and in order; *bad is raised when they were not
+// The same over all n sequences by a warp for one token: 32 probes a step. At most n - 1 whatever
+// the offsets hold.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int n, int t) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, i = lo + (int(threadIdx.x & 31) + 1) * step - 1;
+    lo += __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(cu + i + 1) <= t)) * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+// Offsets of sequence s, clamped to [0, T] and in order; *bad is raised when they were not.
 __device__ __forceinline__ void sequence_range(const int32_t* cu, int n, int T, int s, int* a, int* b, int* bad) {
   const int x = __ldg(cu + s), y = __ldg(cu + s + 1);
   if (x < 0 || y < x || y > T || (s == 0 && x != 0) || (s == n - 1 && y != T)) *bad = 1;
@@ -117,27 +180,88 @@ __device__ __forceinline__ void sequence_range(const int32_t* cu, int n, int T, 
   *b = min(max(y, *a), T);
 }
 
-__device__ __forceinline__ bool kept(const uint8_t* mask, int64_t t) { return mask == nullptr || __ldg(mask + t) != 0; }
+// nonzero bytes of a word
+__device__ __forceinline__ int nonzero4(uint32_t w) { return __popc(__vsetne4(w, 0u)); }
 
-// kept tokens of [a, b) counted by one warp
+// Kept tokens of [a, b), b - a < 2^31, counted by one warp: 16-byte loads between the edges.
 __device__ __forceinline__ int count_kept(const uint8_t* mask, int a, int b) {
+  const int lane = threadIdx.x & 31;
   int c = 0;
-  for (int t = a + int(threadIdx.x & 31); t < b; t += 32) c += __ldg(mask + t) != 0;
+  const int head = min(b - a, int((16 - (reinterpret_cast<uintptr_t>(mask + a) & 15)) & 15));
+  if (lane < head) c += __ldg(mask + a + lane) != 0;
+  const int v0 = a + head, vecs = (b - v0) / 16;
+  for (int i = lane; i < vecs; i += 32) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(mask + v0) + i);
+    c += nonzero4(v.x) + nonzero4(v.y) + nonzero4(v.z) + nonzero4(v.w);
+  }
+  const int t0 = v0 + vecs * 16;
+  if (t0 + lane < b) c += __ldg(mask + t0 + lane) != 0;
   return warp_sum_int(c);
 }
 
+// Four consecutive tokens t, t + 1, ... of an fp32 array (the first n of them exist): one load when
+// the array is 16-byte aligned.
+__device__ __forceinline__ void load4(const float* base, int64_t t, int n, bool vec, float (&f)[4]) {
+  if (vec && n == 4) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(base + t));
+    f[0] = v.x;
+    f[1] = v.y;
+    f[2] = v.z;
+    f[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < n ? __ldg(base + t + i) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store4(float* base, int64_t t, int n, bool vec, const float (&f)[4]) {
+  if (vec && n == 4) {
+    *reinterpret_cast<float4*>(base + t) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) base[t + i] = f[i];
+  }
+}
+
+// Byte i: the mask of token t + i, 0 when it does not exist.
+__device__ __forceinline__ uint32_t load_mask4(const uint8_t* mask, int64_t t, int n, bool vec) {
+  if (vec && n == 4 && mask != nullptr) return __ldg(reinterpret_cast<const uint32_t*>(mask + t));
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) w |= uint32_t(mask != nullptr ? __ldg(mask + t + i) : 1u) << (8 * i);
+  return w;
+}
+
+__device__ __forceinline__ bool mask_bit(uint32_t w, int i) { return ((w >> (8 * i)) & 0xffu) != 0u; }
+
+// The sequences of a warp's 128 tokens [w0, w0 + 128), followed by one lane over its four.
+struct SeqCursor {
+  int seq, last;  // of the current token, of the warp's last
+  int next;       // where seq ends
+  __device__ __forceinline__ void start(const int32_t* cu, int n, int64_t w0, int T) {
+    seq = sequence_of(cu, n, int(w0));
+    next = __ldg(cu + seq + 1);
+    last = int64_t(next) >= min(w0 + 128, int64_t(T)) ? seq : sequence_of(cu, n, int(min(w0 + 127, int64_t(T) - 1)));
+  }
+  __device__ __forceinline__ void find(const int32_t* cu, int64_t t) {
+    seq = sequence_in(cu, seq, last, int(t));
+    next = __ldg(cu + seq + 1);
+  }
+};
+
 // ------------------------------------------------------------------ policy
+
+constexpr int kPolicySums = 5;
 
 struct PolicyWs {
   int32_t* block_kept;  // [ceil(T / kCountBlock)]
   int32_t* seq_kept;    // [n_seqs]
   Totals* totals;       // [kStatCtas]
-  float* sums;          // [kTokenCtas][5]
+  float* sums;          // [kTokenCtas][kPolicySums]
+  uint32_t* done;       // CTAs that have finished their tokens
 };
-
-constexpr int kPolicySums = 5;
-
-__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 PolicyWs policy_carve(void* workspace, int64_t T, int64_t n_seqs, size_t* bytes) {
   char* w = static_cast<char*>(workspace);
@@ -152,40 +276,32 @@ PolicyWs policy_carve(void* workspace, int64_t T, int64_t n_seqs, size_t* bytes)
   r.seq_kept = reinterpret_cast<int32_t*>(take(size_t(n_seqs) * 4));
   r.totals = reinterpret_cast<Totals*>(take(kStatCtas * sizeof(Totals)));
   r.sums = reinterpret_cast<float*>(take(size_t(kTokenCtas) * kPolicySums * 4));
+  r.done = reinterpret_cast<uint32_t*>(take(4));
   *bytes = off;
   return r;
 }
 
-// kept tokens of each block of kCountBlock, a warp per 512 of them
-__global__ void __launch_bounds__(kThreads) count_kernel(const uint8_t* mask, int T, int32_t* block_kept) {
-  __shared__ int part[kWarps];
-  const int64_t b0 = int64_t(blockIdx.x) * kCountBlock;
-  const int warp = threadIdx.x >> 5;
-  constexpr int kPer = kCountBlock / kWarps;
-  const int a = int(min(int64_t(T), b0 + warp * kPer)), b = int(min(int64_t(T), b0 + (warp + 1) * kPer));
-  const int c = count_kept(mask, a, b);
-  if ((threadIdx.x & 31) == 0) part[warp] = c;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int s = 0;
-    for (int w = 0; w < kWarps; ++w) s += part[w];
-    block_kept[blockIdx.x] = s;
+// kept tokens of each block of kCountBlock, a warp per block
+__device__ __forceinline__ void policy_count(const PolicyParams& p, const PolicyWs& ws, int cta, int ctas) {
+  const int64_t blocks = ceil_div(p.T, kCountBlock);
+  for (int64_t i = int64_t(cta) * kWarps + (threadIdx.x >> 5); i < blocks; i += int64_t(ctas) * kWarps) {
+    const int c = count_kept(p.in.mask, int(i * kCountBlock), int(min(int64_t(p.T), (i + 1) * kCountBlock)));
+    if ((threadIdx.x & 31) == 0) ws.block_kept[i] = c;
   }
 }
 
-__global__ void __launch_bounds__(kThreads) policy_stat_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws) {
-  __shared__ Totals part[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int gw = int(blockIdx.x) * kWarps + warp, n_warps = int(gridDim.x) * kWarps;
+__device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyWs& ws, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  const int gw = cta * kWarps + int(threadIdx.x >> 5), n_warps = ctas * kWarps;
   const uint8_t* mask = p.in.mask;
   Totals t{0, 0, 0};
   if (p.n_seqs == 0) {
     if (mask == nullptr) {
       t.kept = gw == 0 ? p.T : 0;
     } else {
-      const int blocks = int(ceil_div(p.T, kCountBlock));
+      const int64_t blocks = ceil_div(p.T, kCountBlock);
       int c = 0;
-      for (int i = gw * 32 + lane; i < blocks; i += n_warps * 32) c += ws.block_kept[i];
+      for (int64_t i = int64_t(gw) * 32 + lane; i < blocks; i += int64_t(n_warps) * 32) c += __ldcg(ws.block_kept + i);
       t.kept = warp_sum_int(c);
     }
   } else {
@@ -197,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) policy_stat_kernel(const __grid_cons
         const int b0 = int(ceil_div(a, kCountBlock)), b1 = b / kCountBlock;  // whole blocks [b0, b1)
         if (b0 < b1) {
           int c = 0;
-          for (int i = b0 + lane; i < b1; i += 32) c += ws.block_kept[i];
+          for (int i = b0 + lane; i < b1; i += 32) c += __ldcg(ws.block_kept + i);
           n = warp_sum_int(c) + count_kept(mask, a, b0 * kCountBlock) + count_kept(mask, b1 * kCountBlock, b);
         } else {
           n = count_kept(mask, a, b);
@@ -208,24 +324,22 @@ __global__ void __launch_bounds__(kThreads) policy_stat_kernel(const __grid_cons
       t.seqs += n > 0;
     }
   }
-  if (lane == 0) part[warp] = t;
-  __syncthreads();
+  t = cta_totals(t);
   if (threadIdx.x == 0) {
-    Totals r{0, 0, 0};
-    for (int w = 0; w < kWarps; ++w) {
-      r.kept += part[w].kept;
-      r.seqs += part[w].seqs;
-      r.bad |= part[w].bad;
-    }
-    if (r.bad) record_error(p.err, LP_ERR_SEQ_OFFSETS);
-    ws.totals[blockIdx.x] = r;
+    if (t.bad) record_error(p.err, LP_ERR_SEQ_OFFSETS);
+    ws.totals[cta] = t;
+    if (cta == 0) *ws.done = 0u;
   }
 }
 
-// e^x - 1 - x. Near 0 both e^x - 1 and x are far larger than their difference, so there it is
-// summed as x^2 / 2 + x^3 / 6 + ...: 9 terms leave less than 2^-26 of it at |x| <= 1.
-__device__ __forceinline__ float exp_minus_linear(float x) {
-  if (fabsf(x) > 1.f) return expm1f(x) - x;
+// e^x - 1 - x, and e^x - 1 in *em1. Near 0 both e^x - 1 and x are far larger than their
+// difference, so there it is summed as x^2 / 2 + x^3 / 6 + ... + x^11 / 11!, whose rest at |x| <= 1
+// is below 2^-27 of it, and e^x - 1 is x plus that sum.
+__device__ __forceinline__ float exp_minus_linear(float x, float* em1) {
+  if (!(fabsf(x) <= 1.f)) {
+    *em1 = expm1f(x);
+    return *em1 - x;
+  }
   float s = 1.f / 39916800.f;  // 1 / 11!
   s = fmaf(s, x, 1.f / 3628800.f);
   s = fmaf(s, x, 1.f / 362880.f);
@@ -236,112 +350,132 @@ __device__ __forceinline__ float exp_minus_linear(float x) {
   s = fmaf(s, x, 1.f / 24.f);
   s = fmaf(s, x, 1.f / 6.f);
   s = fmaf(s, x, 0.5f);
-  return s * x * x;
+  s *= x * x;
+  *em1 = x + s;
+  return s;
 }
 
-struct TokenTerm {
-  float policy, kl, clipped, ratio, grad;
+constexpr int kNoKl = -1;
+
+// What one lane loads for its four tokens.
+struct Tokens {
+  float logp[4], old[4], ref[4], ent[4], adv[4];
+  uint32_t mask;
 };
 
-__device__ __forceinline__ TokenTerm token_term(const PolicyParams& p, float logp, float old, float ref, float A) {
-  const float r = expf(__fsub_rn(logp, old));
-  float rc = r;
-  bool clipped = false;
-  if (A > 0.f && r > p.hi) {
-    rc = p.hi;
-    clipped = true;
-  } else if (A < 0.f && r < p.lo) {
-    rc = p.lo;
-    clipped = true;
-  } else if (p.dual != 0.f && A < 0.f && r > p.dual) {
-    rc = p.dual;
-    clipped = true;
-  }
-  TokenTerm t;
-  t.policy = -__fmul_rn(rc, A);
-  t.ratio = r;
-  t.clipped = clipped ? 1.f : 0.f;
-  t.grad = clipped ? 0.f : -__fmul_rn(r, A);
-  t.kl = 0.f;
-  if (p.in.ref_logp != nullptr) {
-    const float x = __fsub_rn(ref, logp);
-    float d;
-    if (p.kl_kind == LP_KL_K1) {
-      t.kl = -x;
-      d = 1.f;
-    } else if (p.kl_kind == LP_KL_K2) {
-      t.kl = 0.5f * x * x;
-      d = -x;
-    } else {
-      t.kl = exp_minus_linear(x);
-      d = -expm1f(x);
-    }
-    if (p.kl_coef != 0.f) t.grad = __fmaf_rn(p.kl_coef, d, t.grad);
-  }
-  return t;
+template <int KL>
+__device__ __forceinline__ void load_tokens(const PolicyParams& p, int64_t t0, int n, Tokens* k) {
+  const bool vec = p.vec != 0;
+  k->mask = load_mask4(p.in.mask, t0, n, vec);
+  load4(p.in.logp, t0, n, vec, k->logp);
+  load4(p.in.old_logp, t0, n, vec, k->old);
+  if (KL != kNoKl) load4(p.in.ref_logp, t0, n, vec, k->ref);
+  if (p.in.entropy != nullptr) load4(p.in.entropy, t0, n, vec, k->ent);
+  if (!p.adv_per_seq) load4(p.in.advantages, t0, n, vec, k->adv);
 }
 
-__global__ void __launch_bounds__(kThreads) policy_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws,
-                                                          int stat_ctas) {
-  __shared__ float scratch[kWarps];
+// KL: the estimator, or kNoKl without a reference. BY_SEQ: weights or advantages go by sequence.
+// A lane loads its next four tokens before it works on the present ones. A token that is not kept
+// is worked on as zeros of weight zero, so that no lane leaves the others' path.
+template <int KL, bool BY_SEQ>
+__device__ __forceinline__ void policy_tokens(const PolicyParams& p, const PolicyWs& ws, int cta, int ctas,
+                                              int stat_ctas, bool wait) {
+  __shared__ float scratch[kWarps][kPolicySums];
+  const int lane = threadIdx.x & 31;
+  const int64_t step = int64_t(ctas) * kTokenTile, T = p.T;
+  int64_t w0 = int64_t(cta) * kTokenTile + int64_t(threadIdx.x & ~31) * 4;  // the warp's 128 tokens
+  auto lanes = [&](int64_t w) { return int(max(int64_t(0), min(int64_t(4), T - w - 4 * lane))); };
+  Tokens cur;
+  load_tokens<KL>(p, w0 + 4 * lane, lanes(w0), &cur);
+  if (wait) grid_dependency_wait();  // only what the call's earlier kernels write has to wait
   const Totals tot = add_totals(ws.totals, stat_ctas);
-  const bool token_mean = p.aggregation == LP_AGG_TOKEN_MEAN;
-  const bool seq_token_mean = p.aggregation == LP_AGG_SEQ_MEAN_TOKEN_MEAN;
-  const float own = token_mean ? float(tot.kept) : float(tot.seqs);
+  const bool seq_token_mean = p.aggregation == LP_AGG_SEQ_MEAN_TOKEN_MEAN, vec = p.vec != 0;
+  const float own = p.aggregation == LP_AGG_TOKEN_MEAN ? float(tot.kept) : float(tot.seqs);
   const float denom = p.denominator > 0.f ? p.denominator : own;
-  const float w_all = denom > 0.f ? __fdiv_rn(1.f, denom) : 0.f;
+  const float w_all = denom > 0.f && !tot.bad ? __fdiv_rn(1.f, denom) : 0.f;
   const float up = p.in.upstream != nullptr ? __ldg(p.in.upstream) : 1.f;
-  const bool by_seq = seq_token_mean || p.adv_per_seq;
+  const int32_t* cu = p.in.cu_seqlens;
   float sum[kPolicySums] = {0.f, 0.f, 0.f, 0.f, 0.f};
-  const int tiles = int(ceil_div(p.T, kTokenTile));
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t t0 = int64_t(tile) * kTokenTile + int(threadIdx.x) * 4;
-    if (t0 >= p.T) continue;
-    int seq = by_seq ? sequence_of(p.in.cu_seqlens, p.n_seqs, int(t0)) : 0;
-    for (int64_t t = t0; t < min(t0 + 4, int64_t(p.T)); ++t) {
-      float g = 0.f, ge = 0.f;
-      if (!tot.bad && kept(p.in.mask, t)) {
-        if (by_seq && __ldg(p.in.cu_seqlens + seq + 1) <= t)
-          seq = sequence_of(p.in.cu_seqlens, p.n_seqs, int(t));
-        const float A = __ldg(p.in.advantages + (p.adv_per_seq ? int64_t(seq) : t));
-        const float w = seq_token_mean ? __fdiv_rn(1.f, __fmul_rn(float(ws.seq_kept[seq]), denom)) : w_all;
-        const float ref = p.in.ref_logp != nullptr ? __ldg(p.in.ref_logp + t) : 0.f;
-        const TokenTerm k = token_term(p, __ldg(p.in.logp + t), __ldg(p.in.old_logp + t), ref, A);
-        sum[0] = __fmaf_rn(w, k.policy, sum[0]);
-        sum[1] = __fmaf_rn(w, k.kl, sum[1]);
-        if (p.in.entropy != nullptr) sum[2] = __fmaf_rn(w, __ldg(p.in.entropy + t), sum[2]);
-        sum[3] = __fmaf_rn(w, k.clipped, sum[3]);
-        sum[4] = __fmaf_rn(w, k.ratio, sum[4]);
-        g = __fmul_rn(up, __fmul_rn(w, k.grad));
-        ge = -__fmul_rn(up, __fmul_rn(w, p.entropy_coef));
-      }
-      if (p.out.grad_logp != nullptr) p.out.grad_logp[t] = g;
-      if (p.out.grad_entropy != nullptr) p.out.grad_entropy[t] = ge;
+  for (; w0 < T; w0 += step) {
+    const int64_t t0 = w0 + 4 * lane;
+    const int n = lanes(w0);
+    Tokens next;
+    if (w0 + step < T) load_tokens<KL>(p, t0 + step, lanes(w0 + step), &next);
+    SeqCursor at{0, 0, 0};
+    float w_seq = w_all, a_seq = 0.f;
+    auto enter = [&](int64_t t) {
+      at.find(cu, t);
+      if (seq_token_mean) w_seq = tot.bad ? 0.f : __fdiv_rn(1.f, __fmul_rn(float(__ldcg(ws.seq_kept + at.seq)), denom));
+      if (p.adv_per_seq) a_seq = __ldg(p.in.advantages + at.seq);
+    };
+    if (BY_SEQ) {
+      at.start(cu, p.n_seqs, w0, p.T);
+      enter(min(t0, T - 1));
     }
+    float g[4], ge[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool keep = mask_bit(cur.mask, i) && !tot.bad;
+      if (BY_SEQ && keep && t0 + i >= at.next) enter(t0 + i);
+      const float w = keep ? w_seq : 0.f;
+      const float logp = keep ? cur.logp[i] : 0.f, old = keep ? cur.old[i] : 0.f;
+      const float A = keep ? (BY_SEQ && p.adv_per_seq ? a_seq : cur.adv[i]) : 0.f;
+      const float r = expf(__fsub_rn(logp, old));
+      const bool neg = A < 0.f, high = A > 0.f && r > p.hi, low = neg && r < p.lo;
+      const bool dual = neg && p.dual != 0.f && r > p.dual, clipped = high || low || dual;
+      const float rc = high ? p.hi : low ? p.lo : dual ? p.dual : r;
+      float slope = clipped ? 0.f : -__fmul_rn(r, A);
+      sum[0] = __fmaf_rn(w, -__fmul_rn(rc, A), sum[0]);
+      if (KL != kNoKl) {
+        const float x = __fsub_rn(keep ? cur.ref[i] : 0.f, logp);
+        float kl, d;  // the estimate and its derivative in logp
+        if (KL == LP_KL_K1) {
+          kl = -x;
+          d = 1.f;
+        } else if (KL == LP_KL_K2) {
+          kl = 0.5f * x * x;
+          d = -x;
+        } else {
+          kl = exp_minus_linear(x, &d);
+          d = -d;
+        }
+        sum[1] = __fmaf_rn(w, kl, sum[1]);
+        if (p.kl_coef != 0.f) slope = __fmaf_rn(p.kl_coef, d, slope);
+      }
+      if (p.in.entropy != nullptr) sum[2] = __fmaf_rn(w, keep ? cur.ent[i] : 0.f, sum[2]);
+      sum[3] = __fadd_rn(sum[3], clipped ? w : 0.f);
+      sum[4] = __fmaf_rn(w, r, sum[4]);
+      g[i] = keep ? __fmul_rn(up, __fmul_rn(w, slope)) : 0.f;
+      ge[i] = keep ? -__fmul_rn(up, __fmul_rn(w, p.entropy_coef)) : 0.f;
+    }
+    if (p.out.grad_logp != nullptr) store4(p.out.grad_logp, t0, n, vec, g);
+    if (p.out.grad_entropy != nullptr) store4(p.out.grad_entropy, t0, n, vec, ge);
+    cur = next;
   }
-  for (int i = 0; i < kPolicySums; ++i) {
-    const float s = cta_sum(sum[i], scratch);
-    if (threadIdx.x == 0) ws.sums[blockIdx.x * kPolicySums + i] = s;
-  }
+#pragma unroll
+  for (int i = 0; i < kPolicySums; ++i) sum[i] = warp_sum(sum[i]);
+  const float s = cta_sums(sum, scratch);
+  if (threadIdx.x < kPolicySums) ws.sums[cta * kPolicySums + threadIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(kThreads) policy_final_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws,
-                                                                int stat_ctas, int token_ctas) {
-  __shared__ double scratch[kWarps];
+__device__ __forceinline__ void policy_final(const PolicyParams& p, const PolicyWs& ws, int stat_ctas, int token_ctas) {
+  __shared__ Pair32 m[kPolicySums];
   const Totals tot = add_totals(ws.totals, stat_ctas);
-  double m[kPolicySums];
-  for (int i = 0; i < kPolicySums; ++i) {
-    double s = 0.0;
-    for (int b = threadIdx.x; b < token_ctas; b += kThreads) s += double(ws.sums[b * kPolicySums + i]);
-    m[i] = cta_sum(s, scratch);
+  const int lane = threadIdx.x & 31, i = threadIdx.x >> 5;
+  if (i < kPolicySums) {  // a warp per sum
+    Pair32 v{0.f, 0.f};
+    for (int b = lane; b < token_ctas; b += 32) v = add(v, __ldcg(ws.sums + b * kPolicySums + i));
+    v = warp_add(v);
+    if (lane == 0) m[i] = v;
   }
+  __syncthreads();
   if (threadIdx.x != 0) return;
   if (p.out.metrics != nullptr) {
-    const double kl = p.kl_coef != 0.f ? double(p.kl_coef) * m[1] : 0.0;
-    const double ent = p.entropy_coef != 0.f ? double(p.entropy_coef) * m[2] : 0.0;
-    const double nan = double(NAN);
-    p.out.metrics[0] = float(tot.bad ? nan : m[0] + kl - ent);
-    for (int i = 0; i < kPolicySums; ++i) p.out.metrics[1 + i] = float(tot.bad ? nan : m[i]);
+    Pair32 loss = m[0];
+    if (p.kl_coef != 0.f) loss = add(loss, __fmul_rn(p.kl_coef, m[1].value()));
+    if (p.entropy_coef != 0.f) loss = add(loss, -__fmul_rn(p.entropy_coef, m[2].value()));
+    p.out.metrics[0] = tot.bad ? NAN : loss.value();
+    for (int k = 0; k < kPolicySums; ++k) p.out.metrics[1 + k] = tot.bad ? NAN : m[k].value();
   }
   if (p.out.counts != nullptr) {
     p.out.counts[0] = tot.kept;
@@ -349,24 +483,67 @@ __global__ void __launch_bounds__(kThreads) policy_final_kernel(const __grid_con
   }
 }
 
+__global__ void __launch_bounds__(kThreads) policy_count_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws) {
+  grid_launch_dependents();
+  policy_count(p, ws, blockIdx.x, gridDim.x);
+}
+
+__global__ void __launch_bounds__(kThreads) policy_stat_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  policy_stat(p, ws, blockIdx.x, gridDim.x);
+}
+
+template <int KL, bool BY_SEQ>
+__global__ void __launch_bounds__(kThreads, LP_TOKEN_MIN)
+    policy_token_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws, int stat_ctas) {
+  __shared__ bool is_last;
+  policy_tokens<KL, BY_SEQ>(p, ws, blockIdx.x, gridDim.x, stat_ctas, true);
+  // the CTA that finishes last adds the partial sums, in the order of the CTAs
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) is_last = atomicAdd(ws.done, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  policy_final(p, ws, stat_ctas, gridDim.x);
+}
+
+template <int KL, bool BY_SEQ>
+__global__ void __launch_bounds__(kThreads) policy_cluster_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws) {
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  if (p.in.mask != nullptr) {
+    policy_count(p, ws, cta, ctas);
+    cluster_sync();
+  }
+  policy_stat(p, ws, cta, ctas);
+  cluster_sync();
+  policy_tokens<KL, BY_SEQ>(p, ws, cta, ctas, ctas, false);
+  cluster_sync();
+  if (cta == 0) policy_final(p, ws, ctas, ctas);
+}
+
 // ------------------------------------------------------------------ preference
 
 // log-ratio sum and kept tokens of (part of) a sequence
-struct Piece {
+struct __align__(8) Piece {
   float sum;
   int n;
 };
 
-struct PairSums {
-  double v[LP_PREFERENCE_METRICS];
-};
+__device__ __forceinline__ Piece read_piece(const Piece* c) {
+  const int2 v = __ldcg(reinterpret_cast<const int2*>(c));
+  return Piece{__int_as_float(v.x), v.y};
+}
+
+constexpr int kPrefSums = LP_PREFERENCE_METRICS;
 
 struct PrefWs {
-  Piece* pieces;    // [tiles][2]: of the sequence a tile begins in, of the one it ends in
-  Piece* whole;     // [2 n_pairs]: of the sequences that lie within one tile
-  float* slope;     // [2 n_pairs]: d (sum of pair losses) / d logp of a kept token
-  Totals* totals;   // [kStatCtas], seqs = counted pairs
-  PairSums* sums;   // [kStatCtas]
+  Piece* pieces;   // [tiles][2]: of the sequence a tile begins in, of the one it ends in
+  Piece* whole;    // [2 n_pairs]: of the sequences that lie within one tile
+  float* slope;    // [2 n_pairs]: d (sum of pair losses) / d logp of a kept token
+  Totals* totals;  // [kStatCtas], seqs = counted pairs
+  Pair32* sums;    // [kStatCtas][kPrefSums]
 };
 
 PrefWs pref_carve(void* workspace, int64_t T, int64_t n_seqs, size_t* bytes) {
@@ -382,42 +559,38 @@ PrefWs pref_carve(void* workspace, int64_t T, int64_t n_seqs, size_t* bytes) {
   r.whole = reinterpret_cast<Piece*>(take(size_t(n_seqs) * sizeof(Piece)));
   r.slope = reinterpret_cast<float*>(take(size_t(n_seqs) * 4));
   r.totals = reinterpret_cast<Totals*>(take(kStatCtas * sizeof(Totals)));
-  r.sums = reinterpret_cast<PairSums*>(take(kStatCtas * sizeof(PairSums)));
+  r.sums = reinterpret_cast<Pair32*>(take(size_t(kStatCtas) * kPrefSums * 8));
   *bytes = off;
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) pref_sum_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
+__device__ __forceinline__ void pref_sum_tile(const PreferenceParams& p, const PrefWs& ws, int64_t tile) {
   const int lane = threadIdx.x & 31;
-  const int64_t tile = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t t0 = tile * kPrefTile;
-  if (t0 >= p.T) return;
   const int n = 2 * p.n_pairs, a = int(t0), b = int(min(t0 + kPrefTile, int64_t(p.T)));
-  float x[8];
-  uint32_t keep = 0;  // bit i: token a + 32 i + lane is kept
+  float x[8], ref[8];
+  uint8_t keep[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int t = a + 32 * i + lane;
-    x[i] = 0.f;
-    if (t < b && kept(p.in.mask, t)) {
-      keep |= 1u << i;
-      const float ref = p.in.ref_logp != nullptr ? __ldg(p.in.ref_logp + t) : 0.f;
-      x[i] = __fsub_rn(__ldg(p.in.logp + t), ref);
-    }
+    keep[i] = t < b ? (p.in.mask != nullptr ? __ldg(p.in.mask + t) : uint8_t(1)) : uint8_t(0);
+    x[i] = t < b ? __ldg(p.in.logp + t) : 0.f;
+    ref[i] = t < b && p.in.ref_logp != nullptr ? __ldg(p.in.ref_logp + t) : 0.f;
   }
-  // the sequences of the tile, each found by a search, so that runs of empty ones cost nothing
-  // and offsets out of order end the walk
+  // the sequences of the tile; empty ones are passed over by a search, and offsets out of order end
+  // the walk
+  int s = sequence_of(p.in.cu_seqlens, n, a);
   for (int at = a; at < b;) {
-    const int s = sequence_of(p.in.cu_seqlens, n, at);
     const int s0 = __ldg(p.in.cu_seqlens + s), s1 = __ldg(p.in.cu_seqlens + s + 1);
+    const int s2 = s + 2 <= n ? __ldg(p.in.cu_seqlens + s + 2) : s1;
     if (s1 <= at) break;
     const int to = min(s1, b);
     Piece c{0.f, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = a + 32 * i + lane;
-      if (t >= at && t < to && ((keep >> i) & 1u)) {
-        c.sum = __fadd_rn(c.sum, x[i]);
+      if (t >= at && t < to && keep[i] != 0) {
+        c.sum = __fadd_rn(c.sum, __fsub_rn(x[i], ref[i]));
         ++c.n;
       }
     }
@@ -430,58 +603,94 @@ __global__ void __launch_bounds__(kThreads) pref_sum_kernel(const __grid_constan
         ws.pieces[tile * 2 + (s0 < a ? 0 : 1)] = c;
     }
     at = to;
+    if (at < b) s = s2 > at ? s + 1 : sequence_of(p.in.cu_seqlens, n, at);  // usually the one after
   }
 }
 
-// sum and kept tokens of sequence s, by one warp
-__device__ __forceinline__ void sequence_sum(const PreferenceParams& p, const PrefWs& ws, int s, double* sum, int* n,
-                                             int* bad) {
+__device__ __forceinline__ void pref_sum(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas) {
+  const int64_t tiles = ceil_div(p.T, kPrefTile);
+  for (int64_t tile = int64_t(cta) * kWarps + (threadIdx.x >> 5); tile < tiles; tile += int64_t(ctas) * kWarps)
+    pref_sum_tile(p, ws, tile);
+}
+
+// Sums and kept tokens of the sequences that the lanes of a warp hold, one each, over tiles [first,
+// last] (none when last < first). Up to kPrefSerial tiles are added by the lane itself; a longer
+// sequence by the whole warp, 32 tiles at a time.
+constexpr int kPrefSerial = 8;
+
+__device__ __forceinline__ void sequence_sums(const PrefWs& ws, int s, int first, int last, Pair32* sum, int* n) {
   const int lane = threadIdx.x & 31;
-  int a, b;
-  sequence_range(p.in.cu_seqlens, 2 * p.n_pairs, p.T, s, &a, &b, bad);
-  *sum = 0.0;
-  *n = 0;
-  if (a == b) return;
-  const int first = a / kPrefTile, last = (b - 1) / kPrefTile;
-  if (first == last) {
-    // beginning and ending on the tile's own edges counts as within it
-    const Piece c = ws.whole[s];
-    *sum = double(c.sum);
-    *n = c.n;
-    return;
-  }
-  double v = 0.0;
+  Pair32 v{0.f, 0.f};
   int k = 0;
-  for (int tile = first + lane; tile <= last; tile += 32) {
-    const Piece c = ws.pieces[int64_t(tile) * 2 + (tile == first ? 1 : 0)];
-    v += double(c.sum);
-    k += c.n;
+  if (first == last) {  // beginning and ending on the tile's own edges counts as within it
+    const Piece c = read_piece(ws.whole + s);
+    v.hi = c.sum;
+    k = c.n;
+  } else if (first < last && last - first < kPrefSerial) {
+    Piece c[kPrefSerial];
+#pragma unroll
+    for (int i = 0; i < kPrefSerial; ++i)
+      c[i] = first + i <= last ? read_piece(ws.pieces + int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) : Piece{0.f, 0};
+#pragma unroll
+    for (int i = 0; i < kPrefSerial; ++i) {
+      v = add(v, c[i].sum);
+      k += c[i].n;
+    }
   }
-  *sum = warp_sum(v);
-  *n = warp_sum_int(k);
+  for (uint32_t left = __ballot_sync(0xffffffffu, last - first >= kPrefSerial); left != 0u; left &= left - 1u) {
+    const int who = __ffs(left) - 1, f = __shfl_sync(0xffffffffu, first, who), l = __shfl_sync(0xffffffffu, last, who);
+    Pair32 w{0.f, 0.f};
+    int m = 0;
+    for (int tile = f + lane; tile <= l; tile += 32) {
+      const Piece c = read_piece(ws.pieces + int64_t(tile) * 2 + (tile == f ? 1 : 0));
+      w = add(w, c.sum);
+      m += c.n;
+    }
+    w = warp_add(w);
+    m = warp_sum_int(m);
+    if (lane == who) {
+      v = w;
+      k = m;
+    }
+  }
+  *sum = v;
+  *n = k;
 }
 
-__global__ void __launch_bounds__(kThreads) pref_pair_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
-  __shared__ Totals part[kWarps];
-  __shared__ PairSums sums[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// A lane per pair.
+__device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, bool wait) {
+  __shared__ Pair32 scratch[kWarps][kPrefSums];
+  const int lane = threadIdx.x & 31, n_seqs = 2 * p.n_pairs;
   Totals t{0, 0, 0};
-  PairSums m;
-  for (int i = 0; i < LP_PREFERENCE_METRICS; ++i) m.v[i] = 0.0;
-  for (int pair = int(blockIdx.x) * kWarps + warp; pair < p.n_pairs; pair += int(gridDim.x) * kWarps) {
-    double sc, sr;
+  Pair32 m[kPrefSums] = {};
+  for (int64_t base = (int64_t(cta) * kWarps + (threadIdx.x >> 5)) * 32; base < p.n_pairs;
+       base += int64_t(ctas) * kWarps * 32) {
+    const int pair = int(base) + lane;
+    const bool live = pair < p.n_pairs;
+    int first[2] = {0, 0}, last[2] = {-1, -1};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int a = 0, b = 0;
+      if (live) sequence_range(p.in.cu_seqlens, n_seqs, p.T, 2 * pair + i, &a, &b, &t.bad);
+      if (a < b) {
+        first[i] = a / kPrefTile;
+        last[i] = (b - 1) / kPrefTile;
+      }
+    }
+    if (wait) grid_dependency_wait();  // the offsets are the caller's, the tiles the kernel's before
+    Pair32 sc, sr;
     int nc, nr;
-    sequence_sum(p, ws, 2 * pair, &sc, &nc, &t.bad);
-    sequence_sum(p, ws, 2 * pair + 1, &sr, &nr, &t.bad);
-    if (lane != 0) continue;
+    sequence_sums(ws, 2 * pair, first[0], last[0], &sc, &nc);
+    sequence_sums(ws, 2 * pair + 1, first[1], last[1], &sr, &nr);
+    if (!live) continue;
     const bool counted = nc > 0 && nr > 0;
     float h = 0.f, slope = 0.f;
     if (counted) {
       if (p.length_normalised) {
-        sc /= double(nc);
-        sr /= double(nr);
+        sc = Pair32{__fdiv_rn(sc.value(), float(nc)), 0.f};
+        sr = Pair32{__fdiv_rn(sr.value(), float(nr)), 0.f};
       }
-      h = float(sc - sr - double(p.margin));
+      h = add(add(sc, Pair32{-sr.hi, -sr.lo}), -p.margin).value();
       const float x = p.beta * h;
       float loss;
       if (p.kind == LP_PREF_SIGMOID) {
@@ -501,69 +710,131 @@ __global__ void __launch_bounds__(kThreads) pref_pair_kernel(const __grid_consta
         slope = 2.f * gap;
       }
       ++t.seqs;
-      m.v[0] += double(loss);
-      m.v[1] += h > 0.f ? 1.0 : 0.0;
-      m.v[2] += double(x);
-      m.v[3] += double(p.beta) * sc;
-      m.v[4] += double(p.beta) * sr;
+      m[0] = add(m[0], loss);
+      m[1] = add(m[1], h > 0.f ? 1.f : 0.f);
+      m[2] = add(m[2], x);
+      m[3] = add(m[3], p.beta * sc.value());
+      m[4] = add(m[4], p.beta * sr.value());
     }
     ws.slope[2 * pair] = p.length_normalised && counted ? slope / float(nc) : slope;
     ws.slope[2 * pair + 1] = p.length_normalised && counted ? -slope / float(nr) : -slope;
     if (p.out.margins != nullptr) p.out.margins[pair] = h;
   }
-  if (lane == 0) {
-    part[warp] = t;
-    sums[warp] = m;
+  if (wait) grid_dependency_wait();
+  t.seqs = warp_sum_int(t.seqs);
+  t.bad = __reduce_or_sync(0xffffffffu, t.bad);
+#pragma unroll
+  for (int i = 0; i < kPrefSums; ++i) m[i] = warp_add(m[i]);
+  t = cta_totals(t);
+  const Pair32 sum = cta_sums(m, scratch);
+  if (threadIdx.x < kPrefSums) ws.sums[cta * kPrefSums + threadIdx.x] = sum;
+  if (threadIdx.x == 0) {
+    if (t.bad) record_error(p.err, LP_ERR_SEQ_OFFSETS);
+    ws.totals[cta] = t;
   }
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int w = 1; w < kWarps; ++w) {
-    t.seqs += part[w].seqs;
-    t.bad |= part[w].bad;
-    for (int i = 0; i < LP_PREFERENCE_METRICS; ++i) m.v[i] += sums[w].v[i];
+}
+
+__device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, int pair_ctas) {
+  const Totals tot = add_totals(ws.totals, pair_ctas);
+  const float denom = p.denominator > 0.f ? p.denominator : float(tot.seqs);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (cta == 0 && warp < kPrefSums) {  // a warp per metric
+    Pair32 v{0.f, 0.f};
+    for (int b = lane; b < pair_ctas; b += 32) {
+      const float2 o = __ldcg(reinterpret_cast<const float2*>(ws.sums + b * kPrefSums + warp));
+      v = add(v, Pair32{o.x, o.y});
+    }
+    v = warp_add(v);
+    if (lane == 0 && p.out.metrics != nullptr)
+      p.out.metrics[warp] = tot.bad ? NAN : denom > 0.f ? __fdiv_rn(v.value(), denom) : 0.f;
   }
-  if (t.bad) record_error(p.err, LP_ERR_SEQ_OFFSETS);
-  ws.totals[blockIdx.x] = t;
-  ws.sums[blockIdx.x] = m;
+  if (cta == 0 && threadIdx.x == 0 && p.out.counts != nullptr) p.out.counts[0] = tot.seqs;
+  if (p.out.grad_logp == nullptr) return;
+  const float scale = denom > 0.f ? __fdiv_rn(p.in.upstream != nullptr ? __ldg(p.in.upstream) : 1.f, denom) : 0.f;
+  const int32_t* cu = p.in.cu_seqlens;
+  const bool vec = p.vec != 0;
+  const int64_t tiles = ceil_div(p.T, kTokenTile);
+  for (int64_t tile = cta; tile < tiles; tile += ctas) {
+    const int64_t w0 = tile * kTokenTile + int64_t(threadIdx.x & ~31) * 4;  // the warp's 128 tokens
+    if (w0 >= p.T) continue;
+    const int64_t t0 = w0 + int64_t(threadIdx.x & 31) * 4;
+    const int n = int(max(int64_t(0), min(int64_t(4), p.T - t0)));
+    const uint32_t mask = load_mask4(p.in.mask, t0, n, vec);
+    SeqCursor at;
+    at.start(cu, 2 * p.n_pairs, w0, p.T);
+    float c = 0.f, g[4];
+    auto enter = [&](int64_t t) {
+      at.find(cu, t);
+      const float slope = __ldcg(ws.slope + at.seq);
+      c = slope == 0.f ? 0.f : __fmul_rn(slope, scale);
+    };
+    enter(min(t0, int64_t(p.T) - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool keep = mask_bit(mask, i) && !tot.bad;
+      if (keep && t0 + i >= at.next) enter(t0 + i);
+      g[i] = keep ? c : 0.f;
+    }
+    store4(p.out.grad_logp, t0, n, vec, g);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) pref_sum_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
+  grid_launch_dependents();
+  pref_sum(p, ws, blockIdx.x, gridDim.x);
+}
+
+__global__ void __launch_bounds__(kThreads) pref_pair_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
+  grid_launch_dependents();
+  pref_pair(p, ws, blockIdx.x, gridDim.x, true);
 }
 
 __global__ void __launch_bounds__(kThreads) pref_grad_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws,
                                                              int pair_ctas) {
-  __shared__ double scratch[kWarps];
-  const Totals tot = add_totals(ws.totals, pair_ctas);
-  const float denom = p.denominator > 0.f ? p.denominator : float(tot.seqs);
-  if (blockIdx.x == 0) {
-    for (int i = 0; i < LP_PREFERENCE_METRICS; ++i) {
-      double s = 0.0;
-      for (int b = threadIdx.x; b < pair_ctas; b += kThreads) s += ws.sums[b].v[i];
-      s = cta_sum(s, scratch);
-      if (threadIdx.x == 0 && p.out.metrics != nullptr)
-        p.out.metrics[i] = tot.bad ? NAN : denom > 0.f ? float(s / double(denom)) : 0.f;
-    }
-    if (threadIdx.x == 0 && p.out.counts != nullptr) p.out.counts[0] = tot.seqs;
-  }
-  if (p.out.grad_logp == nullptr) return;
-  const float scale = denom > 0.f ? __fdiv_rn(p.in.upstream != nullptr ? __ldg(p.in.upstream) : 1.f, denom) : 0.f;
-  const int n = 2 * p.n_pairs, tiles = int(ceil_div(p.T, kTokenTile));
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t t0 = int64_t(tile) * kTokenTile + int(threadIdx.x) * 4;
-    if (t0 >= p.T) continue;
-    int seq = sequence_of(p.in.cu_seqlens, n, int(t0));
-    for (int64_t t = t0; t < min(t0 + 4, int64_t(p.T)); ++t) {
-      float g = 0.f;
-      if (!tot.bad && kept(p.in.mask, t)) {
-        if (__ldg(p.in.cu_seqlens + seq + 1) <= t) seq = sequence_of(p.in.cu_seqlens, n, int(t));
-        const float c = ws.slope[seq];
-        g = c == 0.f ? 0.f : __fmul_rn(c, scale);
-      }
-      p.out.grad_logp[t] = g;
-    }
-  }
+  grid_dependency_wait();
+  pref_grad(p, ws, blockIdx.x, gridDim.x, pair_ctas);
 }
 
-int stat_ctas(int64_t items) { return int(ceil_div(items, kWarps) < kStatCtas ? ceil_div(items, kWarps) : kStatCtas); }
+__global__ void __launch_bounds__(kThreads) pref_cluster_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  pref_sum(p, ws, cta, ctas);
+  cluster_sync();
+  pref_pair(p, ws, cta, ctas, false);
+  cluster_sync();
+  pref_grad(p, ws, cta, ctas, ctas);
+}
 
-int token_ctas(int64_t T) { return int(ceil_div(T, kTokenTile) < kTokenCtas ? ceil_div(T, kTokenTile) : kTokenCtas); }
+// ------------------------------------------------------------------ launches
+
+int at_most(int64_t n, int most) { return int(n < 1 ? 1 : n < most ? n : most); }
+
+bool one_launch(int64_t T, int64_t n_seqs) { return T <= kFusedTokens && n_seqs <= kFusedSeqs; }
+
+// `grid` CTAs of kThreads; as one cluster, or as the programmatic dependent of the kernel before it
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int grid, bool cluster, bool dependent, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (cluster) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(grid);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster || dependent ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
 
@@ -579,27 +850,59 @@ size_t preference_ws_bytes(int64_t T, int64_t n_seqs) {
   return bytes;
 }
 
-cudaError_t launch_policy_loss(const PolicyParams& p, cudaStream_t s) {
-  size_t bytes = 0;
-  const PolicyWs ws = policy_carve(p.workspace, p.T, p.n_seqs, &bytes);
+namespace {
+
+template <int KL, bool BY_SEQ>
+cudaError_t launch_policy(const PolicyParams& p, const PolicyWs& ws, cudaStream_t s) {
+  if (one_launch(p.T, p.n_seqs))
+    return launch(policy_cluster_kernel<KL, BY_SEQ>, at_most(ceil_div(p.T, kTokenTile), kCluster), true, false, s, p, ws);
   const int64_t blocks = ceil_div(p.T, kCountBlock);
-  if (p.in.mask != nullptr) count_kernel<<<unsigned(blocks), kThreads, 0, s>>>(p.in.mask, p.T, ws.block_kept);
-  const int st = stat_ctas(p.n_seqs > 0 ? p.n_seqs : ceil_div(blocks, 32));
-  policy_stat_kernel<<<st, kThreads, 0, s>>>(p, ws);
-  const int tok = token_ctas(p.T);
-  policy_kernel<<<tok, kThreads, 0, s>>>(p, ws, st);
-  policy_final_kernel<<<1, kThreads, 0, s>>>(p, ws, st, tok);
-  return cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  if (p.in.mask != nullptr)
+    e = launch(policy_count_kernel, at_most(ceil_div(blocks, kWarps), 1 << 30), false, false, s, p, ws);
+  const int stat = at_most(ceil_div(p.n_seqs > 0 ? int64_t(p.n_seqs) : ceil_div(blocks, 32), kWarps), kStatCtas);
+  if (e == cudaSuccess) e = launch(policy_stat_kernel, stat, false, p.in.mask != nullptr, s, p, ws);
+  if (e == cudaSuccess)
+    e = launch(policy_token_kernel<KL, BY_SEQ>, at_most(ceil_div(p.T, kTokenTile), kTokenCtas), false, true, s, p, ws,
+               stat);
+  return e;
 }
 
-cudaError_t launch_preference_loss(const PreferenceParams& p, cudaStream_t s) {
+template <int KL>
+cudaError_t launch_policy(const PolicyParams& p, const PolicyWs& ws, cudaStream_t s) {
+  const bool by_seq = p.aggregation == LP_AGG_SEQ_MEAN_TOKEN_MEAN || p.adv_per_seq;
+  return by_seq ? launch_policy<KL, true>(p, ws, s) : launch_policy<KL, false>(p, ws, s);
+}
+
+}  // namespace
+
+cudaError_t launch_policy_loss(const PolicyParams& params, cudaStream_t s) {
+  PolicyParams p = params;
+  size_t bytes = 0;
+  const PolicyWs ws = policy_carve(p.workspace, p.T, p.n_seqs, &bytes);
+  p.vec = aligned_to(p.in.logp, 16) && aligned_to(p.in.old_logp, 16) && aligned_to(p.in.ref_logp, 16) &&
+          aligned_to(p.in.entropy, 16) && (p.adv_per_seq || aligned_to(p.in.advantages, 16)) &&
+          aligned_to(p.in.mask, 4) && aligned_to(p.out.grad_logp, 16) && aligned_to(p.out.grad_entropy, 16);
+  if (p.in.ref_logp == nullptr) return launch_policy<kNoKl>(p, ws, s);
+  if (p.kl_kind == LP_KL_K1) return launch_policy<LP_KL_K1>(p, ws, s);
+  if (p.kl_kind == LP_KL_K2) return launch_policy<LP_KL_K2>(p, ws, s);
+  return launch_policy<LP_KL_K3>(p, ws, s);
+}
+
+cudaError_t launch_preference_loss(const PreferenceParams& params, cudaStream_t s) {
+  PreferenceParams p = params;
   size_t bytes = 0;
   const PrefWs ws = pref_carve(p.workspace, p.T, 2 * int64_t(p.n_pairs), &bytes);
-  pref_sum_kernel<<<unsigned(ceil_div(p.T, kPrefTile * kWarps)), kThreads, 0, s>>>(p, ws);
-  const int st = stat_ctas(p.n_pairs);
-  pref_pair_kernel<<<st, kThreads, 0, s>>>(p, ws);
-  pref_grad_kernel<<<token_ctas(p.T), kThreads, 0, s>>>(p, ws, st);
-  return cudaGetLastError();
+  p.vec = aligned_to(p.in.mask, 4) && aligned_to(p.out.grad_logp, 16);
+  if (one_launch(p.T, 2 * int64_t(p.n_pairs)))
+    return launch(pref_cluster_kernel, at_most(ceil_div(p.T, kTokenTile), kCluster), true, false, s, p, ws);
+  const int pair = at_most(ceil_div(p.n_pairs, kThreads), kStatCtas);
+  cudaError_t e =
+      launch(pref_sum_kernel, at_most(ceil_div(p.T, kPrefTile * kWarps), 1 << 30), false, false, s, p, ws);
+  if (e == cudaSuccess) e = launch(pref_pair_kernel, pair, false, true, s, p, ws);
+  if (e == cudaSuccess)
+    e = launch(pref_grad_kernel, at_most(ceil_div(p.T, kTokenTile), kTokenCtas), false, true, s, p, ws, pair);
+  return e;
 }
 
 }  // namespace lp

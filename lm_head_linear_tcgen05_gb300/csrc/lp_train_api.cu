@@ -24,6 +24,9 @@ lp_status check_rows(const void* base, int64_t H, int64_t ld, int32_t dtype) {
   return LP_OK;
 }
 
+// warps' shares of the work are counted in 32-bit integers on the device
+bool countable(int64_t T, int64_t H) { return T * ((H + 255) / 256) <= int64_t(INT32_MAX); }
+
 bool finite_at_least(float x, float lo) { return std::isfinite(x) && x >= lo; }
 
 }  // namespace
@@ -35,7 +38,7 @@ lp_status lp_embedding(const int32_t* ids, int64_t T, int64_t H, const void* con
                        lp_stream_t stream) {
   Shards sh;
   if (check_partition(part, &sh) != LP_OK) return LP_ERR_INVALID_ARG;
-  if (!valid_rows(T) || !valid_hidden(H) || !std::isfinite(scale)) return LP_ERR_INVALID_ARG;
+  if (!valid_rows(T) || !valid_hidden(H) || !countable(T, H) || !std::isfinite(scale)) return LP_ERR_INVALID_ARG;
   if (!known_dtype(w_dtype) || !known_dtype(y_dtype)) return LP_ERR_INVALID_ARG;
   if (T == 0) return LP_OK;
   if (ids == nullptr || W == nullptr) return LP_ERR_INVALID_ARG;
@@ -52,12 +55,12 @@ lp_status lp_embedding(const int32_t* ids, int64_t T, int64_t H, const void* con
   p.ids = ids;
   for (int k = 0; k < sh.n; ++k) {
     p.W[k] = W[k];
-    p.shard_start[k] = sh.start[k];
-    p.real[k] = sh.real[k];
+    p.shard_start[k] = int32_t(sh.start[k]);
+    p.real[k] = int32_t(sh.real[k]);
   }
   p.Y = Y;
   p.ld_y = ld_y;
-  p.vocab_real = sh.vocab_real;
+  p.vocab_real = int32_t(sh.vocab_real);
   p.n_shards = sh.n;
   p.T = int32_t(T);
   p.H = int32_t(H);
@@ -74,7 +77,8 @@ lp_status lp_embedding_backward(const int32_t* ids, int64_t T, int64_t H, const 
                                 lp_stream_t stream) {
   Shards sh;
   if (check_partition(part, &sh) != LP_OK) return LP_ERR_INVALID_ARG;
-  if (!valid_rows(T) || !valid_hidden(H) || !std::isfinite(scale) || dW == nullptr) return LP_ERR_INVALID_ARG;
+  if (!valid_rows(T) || !valid_hidden(H) || !countable(T, H) || !std::isfinite(scale) || dW == nullptr)
+    return LP_ERR_INVALID_ARG;
   const int32_t dw_dtype = opts != nullptr ? opts->dw_dtype : int32_t(LP_DTYPE_F32);
   const int32_t accumulate = opts != nullptr ? opts->accumulate : 0;
   if (!known_dtype(dy_dtype) || !known_dtype(dw_dtype) || (accumulate != 0 && accumulate != 1) ||
