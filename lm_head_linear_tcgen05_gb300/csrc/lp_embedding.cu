@@ -15,9 +15,11 @@
 //                   in pieces, one per chunk it touches, that go to the workspace. Which of the two holds is
 //                   decided from the 96 keys around the chunk, so every warp reaches it alone.
 //                   When overwriting, further CTAs write zeros to the rows nobody names.
-//   join_kernel     adds the pieces of each long run in ascending order: 16 warps take
-//                   consecutive groups of pieces, whose sums are added in ascending order.
+//   join_kernel     adds the pieces of each long run in ascending order: groups of lanes take
+//                   consecutive pieces, and their sums are added in the order of the groups.
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "lp_device.cuh"
 #include "lp_f32x2.cuh"
@@ -27,11 +29,8 @@ namespace lp {
 namespace {
 
 constexpr int kSlab = 256;  // columns of a warp: 8 a lane
-#ifndef LP_LOOKUP_FEW
-#define LP_LOOKUP_FEW (4 * 64 * 152)
-#endif
 
-// 8 consecutive elements of a row as raw 16-byte loads
+// 8 consecutive elements of a row as loaded: 16 bytes of bf16, 32 of fp32
 template <bool BF16>
 struct Vec8 {
   uint4 a;
@@ -41,15 +40,24 @@ struct Vec8<false> {
   uint4 a, b;
 };
 
+// fp32: one 32-byte access when the rows are 32-byte aligned (`wide`), else two of 16, each of which
+// leaves half of every sector it touches to the other
 template <bool BF16>
-__device__ __forceinline__ Vec8<BF16> load8(const void* base, int64_t off) {
+__device__ __forceinline__ Vec8<BF16> load8(const void* base, int64_t off, bool wide) {
   Vec8<BF16> v;
   if constexpr (BF16) {
     v.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off));
   } else {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + off);
-    v.a = __ldg(q);
-    v.b = __ldg(q + 1);
+    if (wide) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y), "=r"(v.b.z),
+                     "=r"(v.b.w)
+                   : "l"(q));
+    } else {
+      v.a = __ldcg(q);
+      v.b = __ldcg(q + 1);
+    }
   }
   return v;
 }
@@ -83,14 +91,22 @@ __device__ __forceinline__ void widen8(const Vec8<BF16>& v, float (&f)[8]) {
 
 // store 8 consecutive elements, rounding each once to bf16 when BF16
 template <bool BF16>
-__device__ __forceinline__ void put8(void* base, int64_t off, const float (&f)[8]) {
+__device__ __forceinline__ void put8(void* base, int64_t off, const float (&f)[8], bool wide) {
   if constexpr (BF16) {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off) = make_uint4(
         cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
   } else {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + off);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    float* q = static_cast<float*>(base) + off;
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "r"(__float_as_uint(f[0])),
+                   "r"(__float_as_uint(f[1])), "r"(__float_as_uint(f[2])), "r"(__float_as_uint(f[3])),
+                   "r"(__float_as_uint(f[4])), "r"(__float_as_uint(f[5])), "r"(__float_as_uint(f[6])),
+                   "r"(__float_as_uint(f[7]))
+                   : "memory");
+    } else {
+      reinterpret_cast<float4*>(q)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(q)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   }
 }
 
@@ -123,7 +139,7 @@ __global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __gr
         row = at;
       }
     }
-    v[r] = W != nullptr ? load8<WB>(W, int64_t(row) * p.H + col) : zero8<WB>();
+    v[r] = W != nullptr ? load8<WB>(W, int64_t(row) * p.H + col, p.wide_w != 0) : zero8<WB>();
     if ((id[r] < -1 || id[r] >= p.vocab_real) && col == 0) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
   }
 #pragma unroll
@@ -134,44 +150,37 @@ __global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __gr
     widen8<WB>(v[r], f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], p.scale);
-    put8<YB>(p.Y, int64_t(t) * p.ld_y + col, f);
+    put8<YB>(p.Y, int64_t(t) * p.ld_y + col, f, p.wide_y != 0);
   }
 }
 
 // ------------------------------------------------------------------ gradient: sort
+
+// the row of dW with local index r: the base pointer of the shard that holds it, the element offset
+__device__ __forceinline__ void* dw_row(const EmbeddingGradParams& p, uint32_t r, int64_t* off) {
+  void* base = nullptr;
+  for (int k = 0; k < p.n_shards; ++k)
+    if (r >= p.row_start[k] && r < p.row_start[k + 1]) {
+      base = p.dW[k];
+      *off = int64_t(r - p.row_start[k]) * p.H;
+    }
+  return base;
+}
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigit = 9;
 constexpr int kMaxBins = 1 << kMaxDigit;
 static_assert(kMaxBins == kSortThreads, "a thread per bin");
-#ifndef LP_SORT_CLUSTER
-#define LP_SORT_CLUSTER 8
-#endif
-#ifndef LP_SORT_BALLOT
-#define LP_SORT_BALLOT 0
-#endif
-#ifndef LP_SORT_MIN
-#define LP_SORT_MIN 512
-#endif
-constexpr int kSortCtas = LP_SORT_CLUSTER;
+constexpr int kSortCtas = 16;  // most CTAs of the sorting cluster
 constexpr int kSortAhead = 4;  // loads in flight per lane
-// positions of a CTA below which fewer CTAs sort: their barriers cost more than they save
-constexpr int64_t kSortMinPerCta = LP_SORT_MIN;
-
-// lanes whose digit (of `bits` bits; bit `bits` set: no position) equals this lane's
-__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits) {
-#if LP_SORT_BALLOT
-  uint32_t peers = 0xffffffffu;
-  for (int b = 0; b <= bits; ++b) {
-    const uint32_t set = __ballot_sync(0xffffffffu, (digit >> b) & 1u);
-    peers &= ((digit >> b) & 1u) ? set : ~set;
-  }
-  return peers;
-#else
-  return __match_any_sync(0xffffffffu, digit);
-#endif
-}
+// Positions of a CTA below which half the CTAs sort: up to 8 (the portable cluster size) their
+// barriers and exchanges cost more than they save below 512, 16 pay from 1024 on (T = 16384 over
+// 151936 ids, whole call at H = 8: 38.1 us with 8, 35.6 with 16; T = 8192: 32.0 and 31.7).
+constexpr int64_t kSortMinPerCta = 512;
+constexpr int64_t kSortMinPerCta16 = 1024;
+// Zeros written while one cluster sorts (see launch_sort).
+constexpr int64_t kEarlyBytes = int64_t(48) << 20;
 
 __device__ __forceinline__ uint32_t ld_cluster(const void* local, uint32_t cta) {
   uint32_t v;
@@ -182,19 +191,46 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* local, uint32_t cta) 
 // sort key of the id at one position: its local row, or `width`
 __device__ __forceinline__ uint32_t position_key(const EmbeddingGradParams& p, int id, uint32_t width) {
   const int64_t r = int64_t(id) - p.lo;
-  return id >= 0 && int64_t(id) < p.vocab_real && r >= 0 && r < int64_t(width) ? uint32_t(r) : width;
+  return id >= 0 && id < p.vocab_real && r >= 0 && r < int64_t(width) ? uint32_t(r) : width;
 }
 
-// One cluster. Each pass: every warp counts the digits of its stretch of positions, the CTAs
-// exchange their totals through distributed shared memory, and every warp walks its stretch
-// again, in order, writing each position where its digit's count says.
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ EmbeddingGradParams p) {
+// Writes zeros to the rows of [r0, r0 + 32) whose bit in `skip` is clear, by all warps of a CTA.
+template <int WARPS>
+__device__ __forceinline__ void zero_rows(const EmbeddingGradParams& p, uint32_t r0, uint32_t skip) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vecs = p.H * (p.dw_bf16 ? 2 : 4) / 16;           // 16-byte pieces of a row
+  const int per = vecs < 32 ? 32 / vecs : 1;                 // rows of a warp at a time
+  const int row = vecs < 32 ? lane / vecs : 0, first = vecs < 32 ? lane % vecs : lane;
+  if (row >= per) return;
+  for (int i = warp * per + row; i < 32; i += WARPS * per) {
+    const uint32_t r = r0 + i;
+    if (((skip >> i) & 1u) != 0u || r >= p.row_start[p.n_shards]) continue;
+    int64_t off = 0;
+    char* base = static_cast<char*>(dw_row(p, r, &off));
+    if (base == nullptr) continue;
+    uint4* q = reinterpret_cast<uint4*>(base + off * (p.dw_bf16 ? 2 : 4));
+    for (int c = first; c < vecs; c += 32) q[c] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// The first cluster sorts. Each pass: every warp counts the digits of its stretch of positions, the
+// CTAs exchange their totals through distributed shared memory, and every warp walks its stretch
+// again, in order, writing each position where its digit's count says. The other clusters, when
+// overwriting, meanwhile write the zeros of the first rows.
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ EmbeddingGradParams p, int sort_ctas) {
+  if (int(blockIdx.x) >= sort_ctas) {  // the first rows' zeros, while one cluster sorts
+    grid_launch_dependents();
+    for (uint32_t word = blockIdx.x - sort_ctas; word < p.early_words; word += gridDim.x - sort_ctas)
+      zero_rows<kSortWarps>(p, word * 32, 0u);
+    return;
+  }
   __shared__ uint32_t hist[kSortWarps][kMaxBins];
   __shared__ uint32_t totals[kMaxBins];
+  __shared__ uint32_t bin_base[kMaxBins];
   __shared__ uint32_t warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t cta = blockIdx.x, ctas = gridDim.x;  // one cluster: the block index is the rank
-  const uint32_t width = uint32_t(p.row_start[p.n_shards]);
+  const uint32_t cta = blockIdx.x, ctas = sort_ctas;  // the first cluster: the block index is the rank
+  const uint32_t width = p.row_start[p.n_shards];
   const int passes = (p.key_bits + kMaxDigit - 1) / kMaxDigit;
   const int bits = (p.key_bits + passes - 1) / passes;
   const uint32_t bins = 1u << bits;
@@ -202,7 +238,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   const int64_t per_warp = ((T + warps - 1) / warps + 31) / 32 * 32;
   const int64_t begin = min(T, (int64_t(cta) * kSortWarps + warp) * per_warp), end = min(T, begin + per_warp);
   grid_launch_dependents();
-  if (cta == 0 && tid == 0) *p.n_joins = 0;
+  if (cta == 0 && tid < 2) p.n_joins[tid] = 0;
   if (!p.accumulate) {
     const uint32_t words = (width + 31) / 32;
     for (uint32_t i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) p.present[i] = 0u;
@@ -232,11 +268,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
           if (pass == 0) {
             const int id = int(k);
             k = position_key(p, id, width);
-            if (id < -1 || int64_t(id) >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+            if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
           }
           digit = (k >> shift) & (bins - 1);
         }
-        const uint32_t peers = same_digit(digit, bits);
+        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
         if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
         __syncwarp();
       }
@@ -269,7 +305,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     __syncthreads();
     uint32_t base = incl - all + before_me;
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
-    for (int w = 0; w < kSortWarps; ++w) hist[w][tid] += base;
+    bin_base[tid] = base;
     __syncthreads();
     for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
       uint2 e[kSortAhead];
@@ -289,7 +325,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
         const int64_t i = i0 + 32 * u + lane;
         if (i0 + 32 * u >= end) break;
         const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
-        const uint32_t peers = same_digit(digit, bits);
+        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
         const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
         if (pass == 0 && !p.accumulate) {  // a lane whose first peer has its row leaves the mark to it
           const uint32_t of_first = __shfl_sync(0xffffffffu, e[u].x, __ffs(peers) - 1);
@@ -297,7 +333,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
             atomicOr(p.present + (e[u].x >> 5), 1u << (e[u].x & 31));
         }
         uint32_t at = 0;
-        if (i < end) at = hist[warp][digit] + before;
+        if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
         __syncwarp();
         if (i < end) {
           if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
@@ -314,47 +350,28 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
 
 constexpr int kChunk = 32;  // sorted positions of a warp
 constexpr int kSegWarps = 4;
-#ifndef LP_SEG_PARTS
-#define LP_SEG_PARTS 4
-#endif
-constexpr int kParts = LP_SEG_PARTS;     // warps that share a chunk's columns
+constexpr int kParts = 4;               // warps that share a chunk's columns
 constexpr int kPart = kChunk / kParts;   // positions in which a warp's runs begin
-
-// the row of dW with local index r: its base pointer's element offset, in the shard that holds it
-__device__ __forceinline__ void* dw_row(const EmbeddingGradParams& p, uint32_t r, int64_t* off) {
-  void* base = nullptr;
-  for (int k = 0; k < p.n_shards; ++k)
-    if (int64_t(r) >= p.row_start[k] && int64_t(r) < p.row_start[k + 1]) {
-      base = p.dW[k];
-      *off = (int64_t(r) - p.row_start[k]) * p.H;
-    }
-  return base;
-}
 
 // dW[r][col..col+7] = or += scale * acc
 template <bool WB>
 __device__ __forceinline__ void finish8(const EmbeddingGradParams& p, uint32_t r, int col, const float (&acc)[8]) {
   int64_t off = 0;
   void* base = dw_row(p, r, &off);
-  if (!in_bounds(base != nullptr && col + 8 <= p.H, p.err)) return;
+  if (base == nullptr || !in_bounds(col + 8 <= p.H, p.err)) return;
+  const bool wide = p.wide_dw != 0;
   float f[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(acc[i], p.scale);
   if constexpr (!WB) {
     if (p.accumulate) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off + col);
-      const float4 a = q[0], b = q[1];
-      f[0] = __fadd_rn(a.x, f[0]);
-      f[1] = __fadd_rn(a.y, f[1]);
-      f[2] = __fadd_rn(a.z, f[2]);
-      f[3] = __fadd_rn(a.w, f[3]);
-      f[4] = __fadd_rn(b.x, f[4]);
-      f[5] = __fadd_rn(b.y, f[5]);
-      f[6] = __fadd_rn(b.z, f[6]);
-      f[7] = __fadd_rn(b.w, f[7]);
+      float old[8];
+      widen8<false>(load8<false>(base, off + col, wide), old);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(old[i], f[i]);
     }
   }
-  put8<WB>(base, off + col, f);
+  put8<WB>(base, off + col, f, wide);
 }
 
 // sum of the rows of positions [q0, q1) of the 64 sorted entries own | next, run by run;
@@ -362,30 +379,32 @@ __device__ __forceinline__ void finish8(const EmbeddingGradParams& p, uint32_t r
 template <bool DB, bool WB>
 __device__ __forceinline__ void sum_runs(const EmbeddingGradParams& p, const uint2 own, const uint2 next, int q0, int q1,
                                          int col, float* piece) {
-  constexpr int kAhead = DB ? 8 : 4;  // rows in flight
+  constexpr int kAhead = 4;  // rows in flight
   const bool live = col < p.H;
   float acc[8];
   uint32_t cur = 0xffffffffu;
+#pragma unroll 1
   for (int q = q0; q < q1; q += kAhead) {
     Vec8<DB> v[kAhead];
-    uint32_t key[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = q + u;
+      const uint32_t t0 = __shfl_sync(0xffffffffu, own.y, at & 31), t1 = __shfl_sync(0xffffffffu, next.y, at & 31);
+      const int64_t t = at < 32 ? t0 : t1;
+      if (at < q1 && live && in_bounds(t < p.T && p.H <= p.ld_dy, p.err))
+        v[u] = load8<DB>(p.dY, t * p.ld_dy + col, p.wide_dy != 0);
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int at = q + u;
       const uint32_t k0 = __shfl_sync(0xffffffffu, own.x, at & 31), k1 = __shfl_sync(0xffffffffu, next.x, at & 31);
-      const uint32_t t0 = __shfl_sync(0xffffffffu, own.y, at & 31), t1 = __shfl_sync(0xffffffffu, next.y, at & 31);
-      key[u] = at < 32 ? k0 : k1;
-      const int64_t t = at < 32 ? t0 : t1;
-      if (at < q1 && live && in_bounds(t < p.T && p.H <= p.ld_dy, p.err)) v[u] = load8<DB>(p.dY, t * p.ld_dy + col);
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (q + u >= q1) break;
+      const uint32_t key = at < 32 ? k0 : k1;
+      if (at >= q1) break;
       float f[8];
       widen8<DB>(v[u], f);
-      if (key[u] != cur) {
+      if (key != cur) {
         if (cur != 0xffffffffu && live) finish8<WB>(p, cur, col, acc);
-        cur = key[u];
+        cur = key;
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = f[i];
       } else {
@@ -396,7 +415,7 @@ __device__ __forceinline__ void sum_runs(const EmbeddingGradParams& p, const uin
   }
   if (cur == 0xffffffffu || !live) return;
   if (piece != nullptr)
-    put8<false>(piece, col, acc);
+    put8<false>(piece, col, acc, true);
   else
     finish8<WB>(p, cur, col, acc);
 }
@@ -409,6 +428,8 @@ __device__ __forceinline__ float4 add4(const float4 a, const float4 b) {
 __device__ __forceinline__ float* piece_of(const EmbeddingGradParams& p, int64_t chunk, int slot) {
   return p.partials + (chunk * 2 + slot) * p.H;
 }
+
+constexpr int kJoinFew = 64;  // most pieces of a run that the joins take 128 columns at a time
 
 // the last of the chunks [lo, hi] whose first position has `key`; chunk lo has, and those that have
 // come first. 32 probes a step.
@@ -424,25 +445,15 @@ __device__ __forceinline__ int64_t last_chunk_of(const EmbeddingGradParams& p, u
 }
 
 template <bool DB, bool WB>
-__global__ void __launch_bounds__(kSegWarps * 32) segment_kernel(const __grid_constant__ EmbeddingGradParams p,
+__global__ void __launch_bounds__(kSegWarps * 32, 6) segment_kernel(const __grid_constant__ EmbeddingGradParams p,
                                                                  int seg_ctas) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t width = uint32_t(p.row_start[p.n_shards]);
+  const uint32_t width = p.row_start[p.n_shards];
   grid_launch_dependents();
   grid_dependency_wait();
   if (int(blockIdx.x) >= seg_ctas) {  // zeros: 32 rows a CTA
-    const uint32_t word = blockIdx.x - seg_ctas;
-    const uint32_t present = p.present[word];
-    constexpr int per16 = WB ? 8 : 4;
-    for (int i = warp; i < 32; i += kSegWarps) {
-      const uint32_t r = word * 32 + i;
-      if (((present >> i) & 1u) != 0u || r >= width) continue;
-      int64_t off = 0;
-      char* base = static_cast<char*>(dw_row(p, r, &off));
-      if (!in_bounds(base != nullptr, p.err)) continue;
-      uint4* q = reinterpret_cast<uint4*>(base + off * (WB ? 2 : 4));
-      for (int c = lane; c < p.H / per16; c += 32) q[c] = make_uint4(0u, 0u, 0u, 0u);
-    }
+    const uint32_t word = p.early_words + blockIdx.x - seg_ctas;
+    zero_rows<kSegWarps>(p, word * 32, p.present[word]);
     return;
   }
   const uint32_t slabs = uint32_t(p.H + kSlab - 1) / kSlab;
@@ -465,83 +476,105 @@ __global__ void __launch_bounds__(kSegWarps * 32) segment_kernel(const __grid_co
   const int valid = __popc(__ballot_sync(0xffffffffu, own.x < width));
   const uint32_t left = __shfl_up_sync(0xffffffffu, own.x, 1);
   const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 ? eq_prev == 0u : own.x != left);
-  // a long run the chunk begins inside
-  if (eq_prev != 0u && begin == 0 && __popc(eq_prev) + n_first + (n_first == 32 ? next_last : 0) > kChunk)
-    sum_runs<DB, WB>(p, own, next, 0, n_first, col, piece_of(p, chunk, 0));
-  if (eq_prev != 0u && n_first == 32) return;
-  int limit = valid, stop = valid;  // the last short run begins before limit and ends at stop
-  if (valid == 32) {
-    stop = 32 + next_last;
-    if (n_last + next_last > kChunk) {  // a long run that begins here and goes on
-      limit = stop = 32 - n_last;
-      if (limit / kPart * kPart == begin) {
-        sum_runs<DB, WB>(p, own, next, limit, 32, col, piece_of(p, chunk, 1));
-        if (slab == 0) {
-          const int64_t end = last_chunk_of(p, last, chunk + 1, (T + kChunk - 1) / kChunk - 1);
-          if (lane == 0) p.joins[atomicAdd(p.n_joins, 1)] = make_int4(int(chunk), int(end - chunk) + 1, int(last), 0);
+  // this warp's stretches: the piece of a long run the chunk begins inside, the piece of one that
+  // begins here and goes on, and the short runs that begin in its part
+  int from[3] = {0, 0, 0}, to[3] = {0, 0, 0};
+  if (eq_prev != 0u && begin == 0 && __popc(eq_prev) + n_first + (n_first == 32 ? next_last : 0) > kChunk) to[0] = n_first;
+  if (eq_prev == 0u || n_first < 32) {
+    int limit = valid, stop = valid;  // the last short run begins before limit and ends at stop
+    if (valid == 32) {
+      stop = 32 + next_last;
+      if (n_last + next_last > kChunk) {
+        limit = stop = 32 - n_last;
+        if (limit / kPart * kPart == begin) {
+          from[1] = limit;
+          to[1] = 32;
+          if (slab == 0) {
+            const int64_t end = last_chunk_of(p, last, chunk + 1, (T + kChunk - 1) / kChunk - 1);
+            const int n = int(end - chunk) + 1, which = n > kJoinFew ? 1 : 0;
+            if (lane == 0)
+              p.joins[which][atomicAdd(p.n_joins + which, 1)] = make_int4(int(chunk), n, int(last), 0);
+          }
         }
+      }
+    }
+    const uint32_t here = starts & ~((1u << begin) - 1u);
+    if (here != 0u && __ffs(here) - 1 < min(begin + kPart, limit)) {
+      const uint32_t after = begin + kPart < 32 ? starts & ~((1u << (begin + kPart)) - 1u) : 0u;
+      from[2] = __ffs(here) - 1;
+      to[2] = after != 0u && __ffs(after) - 1 < limit ? __ffs(after) - 1 : stop;
+    }
+  }
+#pragma unroll 1
+  for (int i = 0; i < 3; ++i) {
+    const int a = i == 0 ? from[0] : i == 1 ? from[1] : from[2], b = i == 0 ? to[0] : i == 1 ? to[1] : to[2];
+    if (a < b) sum_runs<DB, WB>(p, own, next, a, b, col, i < 2 ? piece_of(p, chunk, i) : nullptr);
+  }
+}
+
+constexpr int kJoinWarps = 8;
+constexpr int kJoinCtas = 1216;
+constexpr int kManyCols = 16;    // columns of a CTA that joins many pieces
+
+// Adds the n pieces of a run in ascending order, COLS columns (four a lane) at a time: the CTA's
+// kJoinWarps * 128 / COLS groups of lanes take consecutive pieces, then the groups' sums are added in
+// their order. AHEAD: pieces in flight per lane. Runs of up to kJoinFew pieces are numerous and short,
+// and take 128 columns; the pieces of a longer run are spread over more CTAs and groups.
+template <bool WB, int COLS, int AHEAD>
+__device__ __forceinline__ void join_run(const EmbeddingGradParams& p, const int4 run, int slab, float4* part) {
+  constexpr int kLanes = COLS / 4, kGroups = kJoinWarps * 32 / kLanes;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes, col = slab * COLS + lane * 4;
+  const int64_t c0 = run.x;
+  const int n = run.y, per = (n + kGroups - 1) / kGroups;
+  const int a = min(n, group * per), b = min(n, a + per);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < p.H) {
+    for (int i0 = a; i0 < b; i0 += AHEAD) {
+      float4 x[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (i0 + u < b)
+          x[u] = __ldcg(reinterpret_cast<const float4*>(piece_of(p, c0 + i0 + u, i0 + u == 0 ? 1 : 0) + col));
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (i0 + u < b) s = i0 + u == a ? x[u] : add4(s, x[u]);
+    }
+  }
+  part[group * kLanes + lane] = s;
+  __syncthreads();
+  if (group == 0 && col < p.H) {
+    float4 sum = part[lane];
+    for (int g = 1; g < kGroups && g * per < n; ++g) sum = add4(sum, part[g * kLanes + lane]);
+    const float f[4] = {__fmul_rn(sum.x, p.scale), __fmul_rn(sum.y, p.scale), __fmul_rn(sum.z, p.scale),
+                        __fmul_rn(sum.w, p.scale)};
+    int64_t off = 0;
+    void* base = dw_row(p, uint32_t(run.z), &off);
+    if (base != nullptr && in_bounds(col + 4 <= p.H, p.err)) {
+      if constexpr (WB) {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + off + col) =
+            make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
+      } else {
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + off + col);
+        const float4 v = make_float4(f[0], f[1], f[2], f[3]);
+        *q = p.accumulate ? add4(*q, v) : v;
       }
     }
   }
-  // the short runs that begin in this warp's part
-  const uint32_t here = starts & ~((1u << begin) - 1u);
-  if (here == 0u || __ffs(here) - 1 >= min(begin + kPart, limit)) return;
-  const uint32_t after = begin + kPart < 32 ? starts & ~((1u << (begin + kPart)) - 1u) : 0u;
-  const int q1 = after != 0u && __ffs(after) - 1 < limit ? __ffs(after) - 1 : stop;
-  sum_runs<DB, WB>(p, own, next, __ffs(here) - 1, q1, col, nullptr);
+  __syncthreads();
 }
 
-constexpr int kJoinWarps = 16;
-constexpr int kJoinCols = 128;   // columns of a CTA: 4 a lane
-constexpr int kJoinAhead = 8;    // pieces in flight per lane
-constexpr int kJoinCtas = 608;
-
 template <bool WB>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ EmbeddingGradParams p) {
-  __shared__ float4 part[kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) join_kernel(const __grid_constant__ EmbeddingGradParams p) {
+  __shared__ float4 part[kJoinWarps * 32];
   grid_dependency_wait();
-  const int n_runs = *p.n_joins, slabs = (p.H + kJoinCols - 1) / kJoinCols;
-  for (int64_t item = blockIdx.x; item < int64_t(n_runs) * slabs; item += gridDim.x) {
-    const int4 run = p.joins[item / slabs];  // first chunk, pieces, row
-    const int64_t c0 = run.x, n = run.y, per = (n + kJoinWarps - 1) / kJoinWarps;
-    const uint32_t key = uint32_t(run.z);
-    const int col = int(item % slabs) * kJoinCols + lane * 4;
-    const int64_t a = min(n, warp * per), b = min(n, a + per);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (col < p.H) {
-      for (int64_t i0 = a; i0 < b; i0 += kJoinAhead) {
-        float4 x[kJoinAhead];
-#pragma unroll
-        for (int u = 0; u < kJoinAhead; ++u)
-          if (i0 + u < b)
-            x[u] = __ldcg(reinterpret_cast<const float4*>(piece_of(p, c0 + i0 + u, i0 + u == 0 ? 1 : 0) + col));
-#pragma unroll
-        for (int u = 0; u < kJoinAhead; ++u)
-          if (i0 + u < b) s = i0 + u == a ? x[u] : add4(s, x[u]);
-      }
-    }
-    part[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && col < p.H) {
-      float4 sum = part[0][lane];
-      for (int w = 1; w < kJoinWarps && w * per < n; ++w) sum = add4(sum, part[w][lane]);
-      const float f[4] = {__fmul_rn(sum.x, p.scale), __fmul_rn(sum.y, p.scale), __fmul_rn(sum.z, p.scale),
-                          __fmul_rn(sum.w, p.scale)};
-      int64_t off = 0;
-      void* base = dw_row(p, key, &off);
-      if (in_bounds(base != nullptr && col + 4 <= p.H, p.err)) {
-        if constexpr (WB) {
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + off + col) =
-              make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
-        } else {
-          float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + off + col);
-          const float4 v = make_float4(f[0], f[1], f[2], f[3]);
-          *q = p.accumulate ? add4(*q, v) : v;
-        }
-      }
-    }
-    __syncthreads();
+  const int few = p.n_joins[0], many = p.n_joins[1];
+  const int narrow = (p.H + kManyCols - 1) / kManyCols, wide = (p.H + 127) / 128;
+  const int64_t n_many = int64_t(many) * narrow, n_all = n_many + int64_t(few) * wide;
+  for (int64_t item = blockIdx.x; item < n_all; item += gridDim.x) {
+    if (item < n_many)
+      join_run<WB, kManyCols, 8>(p, p.joins[1][item / narrow], int(item % narrow), part);
+    else
+      join_run<WB, 128, 4>(p, p.joins[0][(item - n_many) / wide], int((item - n_many) % wide), part);
   }
 }
 
@@ -549,11 +582,60 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int64_t chunk_count(int64_t T) { return (T + kChunk - 1) / kChunk; }
 
+// Whether the current device can hold a cluster of 16 CTAs, which is above the portable size; found
+// once per device.
+bool cluster16_fits() {
+  static std::atomic<int> known[64];  // 0: not asked yet, 1: no, 2: yes
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return false;
+  }
+  int k = known[dev].load(std::memory_order_acquire);
+  if (k == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(kSortCtas, 1, 1);
+    cfg.blockDim = dim3(kSortThreads, 1, 1);
+    int active = 0;
+    k = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                cudaOccupancyMaxActiveClusters(&active, sort_kernel, &cfg) == cudaSuccess && active > 0
+            ? 2
+            : 1;
+    cudaGetLastError();
+    known[dev].store(k, std::memory_order_release);
+  }
+  return k == 2;
+}
+
+int sort_ctas(int64_t T) {
+  if (T >= kSortCtas * kSortMinPerCta16 && cluster16_fits()) return kSortCtas;
+  int ctas = 8;
+  while (ctas > 1 && T < ctas * kSortMinPerCta) ctas /= 2;
+  return ctas;
+}
+
+// Rows whose zeros the sort kernel writes, in words of 32: about what the rest of the GPU can write
+// while one cluster sorts.
+uint32_t early_words(const EmbeddingGradParams& p) {
+  if (p.accumulate) return 0u;
+  const int64_t row = int64_t(p.H) * (p.dw_bf16 ? 2 : 4);
+  const int64_t words = kEarlyBytes / (row * 32), all = (int64_t(p.row_start[p.n_shards]) + 31) / 32;
+  return uint32_t(words < all ? words : all);
+}
+
 cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
-  int ctas = kSortCtas;
-  while (ctas > 1 && p.T < ctas * kSortMinPerCta) ctas /= 2;
+  const int ctas = sort_ctas(p.T);
+  // zeros: whole clusters, one CTA per SM at most
+  const int64_t zero = p.early_words < 144u ? p.early_words : 144u;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ctas), 1, 1);
+  cfg.gridDim = dim3(unsigned(ctas + (zero + ctas - 1) / ctas * ctas), 1, 1);
   cfg.blockDim = dim3(kSortThreads, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -563,10 +645,7 @@ cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-#if LP_SORT_CLUSTER > 8
-  cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-#endif
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_kernel, p, ctas);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
 }
@@ -575,7 +654,7 @@ template <bool DB, bool WB>
 cudaError_t launch_sums(const EmbeddingGradParams& p, cudaStream_t s) {
   const int64_t slabs = (p.H + kSlab - 1) / kSlab;
   const int64_t seg = (chunk_count(p.T) * kParts * slabs + kSegWarps - 1) / kSegWarps;
-  const int64_t zero = p.accumulate ? 0 : (p.row_start[p.n_shards] + 31) / 32;
+  const int64_t zero = p.accumulate ? 0 : (int64_t(p.row_start[p.n_shards]) + 31) / 32 - p.early_words;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -604,8 +683,9 @@ cudaError_t launch_lookup(const EmbeddingParams& p, cudaStream_t s) {
   const int slabs = (p.H + kSlab - 1) / kSlab;
   const int per_row = slabs % 4 == 0 ? 4 : slabs % 2 == 0 ? 2 : 1, rows = kLookupWarps / per_row;
   const unsigned y = unsigned((slabs + per_row - 1) / per_row);
-  // four rows a warp once that leaves every SM its full 64 warps; below, rows come one a warp
-  if (int64_t(p.T) * slabs >= LP_LOOKUP_FEW)
+  // Four rows a warp, in flight together, once that leaves every SM its full 64 warps (8192 rows of H =
+  // 4096: 19.7 us, 24.2 with one); below, one row a warp (64 rows: 2.05 us, 2.46 with four).
+  if (int64_t(p.T) * slabs >= 4 * 64 * 152)
     embedding_kernel<WB, YB, 4><<<dim3(unsigned((p.T + rows * 4 - 1) / (rows * 4)), y), kLookupWarps * 32, 0, s>>>(p, per_row);
   else
     embedding_kernel<WB, YB, 1><<<dim3(unsigned((p.T + rows - 1) / rows), y), kLookupWarps * 32, 0, s>>>(p, per_row);
@@ -621,31 +701,36 @@ cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16,
 
 size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width) {
   const size_t chunks = size_t(chunk_count(T));
-  return 2 * up256(size_t(T) * sizeof(uint2)) + up256(sizeof(int4)) + up256(chunks * sizeof(int4)) +
+  return 256 + 2 * up256(size_t(T) * sizeof(uint2)) + up256(2 * sizeof(int32_t)) + 2 * up256(chunks * sizeof(int4)) +
          up256(size_t((width + 31) / 32) * sizeof(uint32_t)) + (T > kChunk ? chunks * 2 * size_t(H) * sizeof(float) : 0);
 }
 
 void embedding_backward_carve(EmbeddingGradParams* p, void* workspace, int64_t width) {
-  char* w = static_cast<char*>(workspace);
+  // the caller's buffer starts on a 16-byte boundary, the parts on 256-byte ones
+  char* w = reinterpret_cast<char*>(up256(reinterpret_cast<uintptr_t>(workspace)));
   for (int i = 0; i < 2; ++i) {
     p->sorted[i] = reinterpret_cast<uint2*>(w);
     w += up256(size_t(p->T) * sizeof(uint2));
   }
   p->n_joins = reinterpret_cast<int32_t*>(w);
-  w += up256(sizeof(int4));
-  p->joins = reinterpret_cast<int4*>(w);
-  w += up256(size_t(chunk_count(p->T)) * sizeof(int4));
+  w += up256(2 * sizeof(int32_t));
+  for (int i = 0; i < 2; ++i) {
+    p->joins[i] = reinterpret_cast<int4*>(w);
+    w += up256(size_t(chunk_count(p->T)) * sizeof(int4));
+  }
   p->present = reinterpret_cast<uint32_t*>(w);
   w += up256(size_t((width + 31) / 32) * sizeof(uint32_t));
   p->partials = reinterpret_cast<float*>(w);
 }
 
-cudaError_t launch_embedding_backward(const EmbeddingGradParams& p, bool dy_bf16, bool dw_bf16, cudaStream_t s) {
+cudaError_t launch_embedding_backward(const EmbeddingGradParams& params, bool dy_bf16, cudaStream_t s) {
+  EmbeddingGradParams p = params;
   if (p.row_start[p.n_shards] == 0) return cudaSuccess;  // no rows at all
-  cudaError_t e = launch_sort(p, s);
+  p.early_words = early_words(p);
+  const cudaError_t e = launch_sort(p, s);
   if (e != cudaSuccess) return e;
-  if (dy_bf16) return dw_bf16 ? launch_sums<true, true>(p, s) : launch_sums<true, false>(p, s);
-  return dw_bf16 ? launch_sums<false, true>(p, s) : launch_sums<false, false>(p, s);
+  if (dy_bf16) return p.dw_bf16 ? launch_sums<true, true>(p, s) : launch_sums<true, false>(p, s);
+  return p.dw_bf16 ? launch_sums<false, true>(p, s) : launch_sums<false, false>(p, s);
 }
 
 }  // namespace lp

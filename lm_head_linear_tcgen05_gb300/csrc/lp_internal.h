@@ -240,6 +240,7 @@ struct EmbeddingParams {
   int32_t T;
   int32_t H;
   float scale;
+  int32_t wide_w, wide_y;                // rows start on 32-byte boundaries
   unsigned int* err;
 };
 
@@ -249,27 +250,30 @@ struct EmbeddingGradParams {
   const void* dY;
   int64_t ld_dy;
   void* dW[LP_MAX_SHARDS];
-  int64_t row_start[LP_MAX_SHARDS + 1];  // first local row of each shard; [n_shards] = width
+  uint32_t row_start[LP_MAX_SHARDS + 1]; // first local row of each shard; [n_shards] = width
   int64_t lo;                            // id of local row 0
-  int64_t vocab_real;
+  int32_t vocab_real;
   int32_t n_shards;
   int32_t T;
   int32_t H;
   int32_t key_bits;                      // bits of the sort key (a local row, or width: no row)
+  int32_t dw_bf16;
   int32_t accumulate;
+  int32_t wide_dy, wide_dw;              // rows start on 32-byte boundaries
   float scale;
   unsigned int* err;
   uint2* sorted[2];                      // (local row, position), ping-pong; the last pass fills [0]
   float* partials;                       // [chunks][2][H]: pieces of runs longer than a chunk
-  int32_t* n_joins;                      // number of such runs
-  int4* joins;                           // their first chunk, number of pieces and row
+  int32_t* n_joins;                      // number of such runs of few and of many pieces
+  int4* joins[2];                        // their first chunk, number of pieces and row
   uint32_t* present;                     // bit per local row: some position names it (overwriting only)
+  uint32_t early_words;                  // words of 32 rows whose zeros the sort kernel writes
 };
 
 size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width);
 void embedding_backward_carve(EmbeddingGradParams* p, void* workspace, int64_t width);
 cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16, cudaStream_t s);
-cudaError_t launch_embedding_backward(const EmbeddingGradParams& p, bool dy_bf16, bool dw_bf16, cudaStream_t s);
+cudaError_t launch_embedding_backward(const EmbeddingGradParams& p, bool dy_bf16, cudaStream_t s);
 
 // ------------------------------------------------------------ losses
 struct PolicyParams {

@@ -53,13 +53,16 @@ lp_status lp_embedding(const int32_t* ids, int64_t T, int64_t H, const void* con
   std::memset(&p, 0, sizeof(p));
   if ((st = device_error_word(&p.err)) != LP_OK) return st;
   p.ids = ids;
+  p.wide_w = 1;  // H % 8 == 0: rows of 32 bytes or a multiple
   for (int k = 0; k < sh.n; ++k) {
     p.W[k] = W[k];
     p.shard_start[k] = int32_t(sh.start[k]);
     p.real[k] = int32_t(sh.real[k]);
+    if (sh.real[k] > 0 && !aligned(W[k], 32)) p.wide_w = 0;
   }
   p.Y = Y;
   p.ld_y = ld_y;
+  p.wide_y = aligned(Y, 32) && ld_y % 8 == 0;
   p.vocab_real = int32_t(sh.vocab_real);
   p.n_shards = sh.n;
   p.T = int32_t(T);
@@ -113,13 +116,17 @@ lp_status lp_embedding_backward(const int32_t* ids, int64_t T, int64_t H, const 
   p.ids = ids;
   p.dY = dY;
   p.ld_dy = ld_dy;
+  p.wide_dw = 1;  // H % 8 == 0: rows of 32 bytes or a multiple
   for (int k = 0; k < sh.n; ++k) {
     p.dW[k] = dW[k];
-    p.row_start[k] = sh.start[k] - sh.start[0];
+    p.row_start[k] = uint32_t(sh.start[k] - sh.start[0]);
+    if (sh.width[k] > 0 && !aligned(dW[k], 32)) p.wide_dw = 0;
   }
-  p.row_start[sh.n] = width;
+  p.row_start[sh.n] = uint32_t(width);
   p.lo = sh.start[0];
-  p.vocab_real = sh.vocab_real;
+  p.vocab_real = int32_t(sh.vocab_real);
+  p.dw_bf16 = dw_dtype == LP_DTYPE_BF16 ? 1 : 0;
+  p.wide_dy = aligned(dY, 32) && ld_dy % 8 == 0;
   p.n_shards = sh.n;
   p.T = int32_t(T);
   p.H = int32_t(H);
@@ -128,8 +135,7 @@ lp_status lp_embedding_backward(const int32_t* ids, int64_t T, int64_t H, const 
   p.accumulate = accumulate;
   p.scale = scale;
   embedding_backward_carve(&p, workspace, width);
-  if (launch_embedding_backward(p, dy_dtype == LP_DTYPE_BF16, dw_dtype == LP_DTYPE_BF16, s) != cudaSuccess)
-    return LP_ERR_CUDA;
+  if (launch_embedding_backward(p, dy_dtype == LP_DTYPE_BF16, s) != cudaSuccess) return LP_ERR_CUDA;
   return LP_OK;
 }
 

@@ -140,6 +140,20 @@ def test_gradient(lp, grad, dw, kind, T, H, part):
     assert lp.lp_get_device_error() == 0
 
 
+@pytest.mark.parametrize("T,H,grad,dw,kind", [(20011, 16, "bf16", "f32", "zipf"), (70001, 8, "f32", "bf16", "hot"),
+                                              (16384, 264, "bf16", "f32", "runs"), (5000, 40, "bf16", "bf16", "zipf")])
+def test_gradient_of_long_batches(lp, T, H, grad, dw, kind):
+    """Sorted by clusters of 8 and 16 CTAs, two and three digits; long runs joined from many pieces."""
+    import torch
+    for real, bounds in ((1000, [0, 1000]), (300000, [0, 100000, 100000, 300032])):
+        ids = _ids(kind, T, real, np.random.RandomState(T))
+        dY = _rand((T, H), _dtype(grad), 6)
+        out = lp.lp_embedding_backward(dev_i32(ids), dY, _part(lp, real, bounds), scale=2.0, dw_dtype=_dtype(dw))
+        want, mag, n = train.embedding_backward(ids, dY.double().cpu().numpy(), 0, bounds[-1], 2.0)
+        _check_gradient(torch.cat([g for g in out if g is not None]), dw == "bf16", want, mag, n)
+    assert lp.lp_get_device_error() == 0
+
+
 @pytest.mark.parametrize("kind", ["zipf", "hot", "runs"])
 def test_gradient_accumulates_one_add_per_element(lp, kind):
     import torch
