@@ -13,6 +13,14 @@ wrappers only route tensors between the two calls.
 
     logp, entropy = linear_logp(X, [W], None, part, y, tau)
     (logp * advantages).sum().backward()       # X.grad, W.grad
+
+The operator's neighbours in a training step have wrappers of the same kind: embedding,
+policy_loss and preference_loss.
+
+    X = block(embedding(ids, [W], part))
+    logp, entropy = linear_logp(X, [W], None, part, y, tau)
+    loss, metrics, counts = policy_loss(logp, old_logp, advantages, entropy=entropy, entropy_coef=1e-3)
+    loss.backward()
 """
 from __future__ import annotations
 
@@ -20,7 +28,8 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import lp_backward_ex, lp_backward_from_logits, lp_forward, lp_forward_from_logits
+from . import (lp_backward_ex, lp_backward_from_logits, lp_embedding, lp_embedding_backward, lp_forward,
+               lp_forward_from_logits, lp_policy_loss, lp_preference_loss)
 
 
 def _zeros_like_rows(ref: torch.Tensor) -> torch.Tensor:
@@ -107,3 +116,81 @@ def linear_logp_from_logits(logits: Sequence[torch.Tensor], part, y: torch.Tenso
         raise ValueError("logits must have one entry per shard")
     logp, entropy, _ = _LinearLogpFromLogits.apply(part, y, float(tau), *logits)
     return logp, entropy
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, part, scale, out_dtype, *W):
+        ctx.part, ctx.scale = part, scale
+        ctx.dtype = next(w.dtype for w in W if w is not None)
+        ctx.save_for_backward(ids)
+        return lp_embedding(ids, list(W), part, scale=scale, out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, g):
+        (ids,) = ctx.saved_tensors
+        # a gradient that was broadcast or transposed has rows the library does not take
+        if g.stride(1) != 1 or (g.stride(0) * g.element_size()) % 16 != 0 or g.data_ptr() % 16 != 0 \
+                or g.stride(0) < g.shape[1]:
+            g = g.clone(memory_format=torch.contiguous_format)
+        dW = lp_embedding_backward(ids, g, ctx.part, scale=ctx.scale, dw_dtype=ctx.dtype)
+        return (None, None, None, None, *[d if ctx.needs_input_grad[4 + k] else None for k, d in enumerate(dW)])
+
+
+def embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: float = 1.0, out_dtype=None):
+    """Embedding lookup with autograd: scale * W[ids] (see lp_embedding), differentiable with
+    respect to every W[k]; the gradients have the table's type. For a table that is tied to
+    the head and trained with fp32 gradients, call lp_embedding_backward with accumulate=True on
+    the dW of lp_backward_ex instead: that adds the two without rounding either."""
+    return _Embedding.apply(ids, part, float(scale), out_dtype, *W)
+
+
+class _PolicyLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, entropy, old_logp, advantages, options):
+        out = lp_policy_loss(logp, old_logp, advantages, entropy=entropy, grads=False, **options)
+        ctx.save_for_backward(logp, old_logp, advantages, *([] if entropy is None else [entropy]))
+        ctx.options = options
+        ctx.mark_non_differentiable(out["metrics"], out["counts"])
+        return out["metrics"][0].clone(), out["metrics"], out["counts"]
+
+    @staticmethod
+    def backward(ctx, g, _g_metrics, _g_counts):
+        logp, old_logp, advantages, *rest = ctx.saved_tensors
+        out = lp_policy_loss(logp, old_logp, advantages, entropy=rest[0] if rest else None, metrics=False,
+                             upstream=g.to(torch.float32), **ctx.options)
+        return (out["grad_logp"] if ctx.needs_input_grad[0] else None,
+                out["grad_entropy"] if ctx.needs_input_grad[1] else None, None, None, None)
+
+
+def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                entropy: Optional[torch.Tensor] = None, **options):
+    """lp_policy_loss with autograd: returns (loss, metrics, counts), the loss differentiable with
+    respect to logp and entropy. ``options`` are those of lp_policy_loss (ref_logp, mask, cu_seqlens,
+    clip_low, clip_high, dual_clip, kl_coef, kl_kind, entropy_coef, aggregation, denominator,
+    adv_per_seq). The backward is one library call that reads the inputs again and multiplies by
+    the upstream gradient where it is."""
+    return _PolicyLoss.apply(logp, entropy, old_logp, advantages, options)
+
+
+class _PreferenceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, cu_seqlens, options):
+        out = lp_preference_loss(logp, cu_seqlens, grads=False, **options)
+        ctx.save_for_backward(logp, cu_seqlens)
+        ctx.options = options
+        ctx.mark_non_differentiable(out["metrics"], out["counts"], out["margins"])
+        return out["metrics"][0].clone(), out["metrics"], out["counts"], out["margins"]
+
+    @staticmethod
+    def backward(ctx, g, _g_metrics, _g_counts, _g_margins):
+        logp, cu_seqlens = ctx.saved_tensors
+        out = lp_preference_loss(logp, cu_seqlens, metrics=False, upstream=g.to(torch.float32), **ctx.options)
+        return out["grad_logp"], None, None
+
+
+def preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, **options):
+    """lp_preference_loss with autograd: returns (loss, metrics, counts, margins), the loss
+    differentiable with respect to logp. ``options`` are those of lp_preference_loss (ref_logp,
+    mask, beta, kind, label_smoothing, length_normalised, margin, denominator)."""
+    return _PreferenceLoss.apply(logp, cu_seqlens, options)
