@@ -156,15 +156,18 @@ __global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __gr
 
 // ------------------------------------------------------------------ gradient: sort
 
-// the row of dW with local index r: the base pointer of the shard that holds it, the element offset
+// the row of dW with local index r < width: the base pointer of the shard that holds it (the last
+// that starts at or before it), the element offset
 __device__ __forceinline__ void* dw_row(const EmbeddingGradParams& p, uint32_t r, int64_t* off) {
-  void* base = nullptr;
-  for (int k = 0; k < p.n_shards; ++k)
-    if (r >= p.row_start[k] && r < p.row_start[k + 1]) {
+  void* base = p.dW[0];
+  uint32_t start = 0;
+  for (int k = 1; k < p.n_shards; ++k)
+    if (r >= p.row_start[k]) {
       base = p.dW[k];
-      *off = int64_t(r - p.row_start[k]) * p.H;
+      start = p.row_start[k];
     }
-  return base;
+  *off = int64_t(r - start) * p.H;
+  return r < p.row_start[p.n_shards] ? base : nullptr;
 }
 
 constexpr int kSortThreads = 512;
@@ -179,8 +182,18 @@ constexpr int kSortAhead = 4;  // loads in flight per lane
 // 151936 ids, whole call at H = 8: 38.1 us with 8, 35.6 with 16; T = 8192: 32.0 and 31.7).
 constexpr int64_t kSortMinPerCta = 512;
 constexpr int64_t kSortMinPerCta16 = 1024;
+// Most positions of a CTA that sorts in shared memory, 32768 in all with 16 CTAs. More would fit, but
+// an SM whose shared memory has to grow for the sort drains before and after it (T = 65537: 98 us a
+// call through global memory, 109 in shared memory).
+constexpr int64_t kSortLocal = 2048;
 // Zeros written while one cluster sorts (see launch_sort).
 constexpr int64_t kEarlyBytes = int64_t(48) << 20;
+
+// positions of a warp, whole steps of 32
+__host__ __device__ inline int64_t sort_stretch(int64_t T, int ctas) {
+  const int64_t warps = int64_t(ctas) * kSortWarps;
+  return ((T + warps - 1) / warps + 31) / 32 * 32;
+}
 
 __device__ __forceinline__ uint32_t ld_cluster(const void* local, uint32_t cta) {
   uint32_t v;
@@ -213,17 +226,27 @@ __device__ __forceinline__ void zero_rows(const EmbeddingGradParams& p, uint32_t
   }
 }
 
+__device__ __forceinline__ void st_cluster(const void* local, uint32_t cta, uint2 v) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr(local, cta)), "r"(v.x), "r"(v.y)
+               : "memory");
+}
+
 // The first cluster sorts. Each pass: every warp counts the digits of its stretch of positions, the
 // CTAs exchange their totals through distributed shared memory, and every warp walks its stretch
-// again, in order, writing each position where its digit's count says. The other clusters, when
-// overwriting, meanwhile write the zeros of the first rows.
+// again, in order, moving each position to where its digit's count says. LOCAL: the positions stay in
+// the cluster's shared memory (2 x 8 bytes each) until the last pass; otherwise they go through
+// global memory, which costs each pass two round trips to the L2 and a wait for its writes (T = 16384:
+// 15 us a sort, 11 in shared memory). The other clusters, when overwriting, meanwhile write the zeros
+// of the first rows.
+template <bool LOCAL>
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ EmbeddingGradParams p, int sort_ctas) {
-  if (int(blockIdx.x) >= sort_ctas) {  // the first rows' zeros, while one cluster sorts
+  if (int(blockIdx.x) >= sort_ctas) {
     grid_launch_dependents();
     for (uint32_t word = blockIdx.x - sort_ctas; word < p.early_words; word += gridDim.x - sort_ctas)
       zero_rows<kSortWarps>(p, word * 32, 0u);
     return;
   }
+  extern __shared__ uint2 local[];  // LOCAL: two buffers of the CTA's stretch
   __shared__ uint32_t hist[kSortWarps][kMaxBins];
   __shared__ uint32_t totals[kMaxBins];
   __shared__ uint32_t bin_base[kMaxBins];
@@ -234,9 +257,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   const int passes = (p.key_bits + kMaxDigit - 1) / kMaxDigit;
   const int bits = (p.key_bits + passes - 1) / passes;
   const uint32_t bins = 1u << bits;
-  const int64_t T = p.T, warps = int64_t(ctas) * kSortWarps;
-  const int64_t per_warp = ((T + warps - 1) / warps + 31) / 32 * 32;
-  const int64_t begin = min(T, (int64_t(cta) * kSortWarps + warp) * per_warp), end = min(T, begin + per_warp);
+  const int64_t T = p.T, per_warp = sort_stretch(T, sort_ctas), per_cta = per_warp * kSortWarps;
+  const int64_t cta_begin = int64_t(cta) * per_cta;
+  const int64_t begin = min(T, cta_begin + warp * per_warp), end = min(T, begin + per_warp);
   grid_launch_dependents();
   if (cta == 0 && tid < 2) p.n_joins[tid] = 0;
   if (!p.accumulate) {
@@ -244,8 +267,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     for (uint32_t i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) p.present[i] = 0u;
   }
   for (int pass = 0; pass < passes; ++pass) {
-    // passes alternate so that the last one fills sorted[0]
-    const uint2* src = p.sorted[(passes - pass) & 1];
+    // passes alternate between two buffers; the first reads the ids and, LOCAL, leaves their keys in
+    // buffer 1; the last fills sorted[0]
+    const uint2* src = LOCAL ? local + ((pass + 1) & 1) * per_cta : p.sorted[(passes - pass) & 1];
+    const int64_t src0 = LOCAL ? cta_begin : 0;  // the position at src[0]
+    const bool last = pass == passes - 1;
     uint2* dst = p.sorted[(passes - 1 - pass) & 1];
     const int shift = pass * bits;
     for (int w = 0; w < kSortWarps; ++w) hist[w][tid] = 0u;
@@ -256,7 +282,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
       for (int u = 0; u < kSortAhead; ++u) {
         const int64_t i = i0 + 32 * u + lane;
         key[u] = 0u;
-        if (i < end) key[u] = pass == 0 ? uint32_t(__ldg(p.ids + i)) : __ldcg(src + i).x;
+        if (i < end) key[u] = pass == 0 ? uint32_t(__ldg(p.ids + i)) : LOCAL ? src[i - src0].x : __ldcg(src + i).x;
       }
 #pragma unroll
       for (int u = 0; u < kSortAhead; ++u) {
@@ -269,6 +295,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
             const int id = int(k);
             k = position_key(p, id, width);
             if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+            if (LOCAL) local[per_cta + i - cta_begin] = make_uint2(k, uint32_t(i));
           }
           digit = (k >> shift) & (bins - 1);
         }
@@ -314,7 +341,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
         const int64_t i = i0 + 32 * u + lane;
         e[u] = make_uint2(0u, uint32_t(i));
         if (i < end) {
-          if (pass == 0)
+          if (LOCAL)
+            e[u] = src[i - src0];
+          else if (pass == 0)
             e[u].x = position_key(p, __ldg(p.ids + i), width);
           else
             e[u] = __ldcg(src + i);
@@ -336,7 +365,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
         if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
         __syncwarp();
         if (i < end) {
-          if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
+          if (in_bounds(int64_t(at) < T, p.err)) {
+            if (LOCAL && !last) {
+              const uint32_t to = at / uint32_t(per_cta);
+              st_cluster(local + (pass & 1) * per_cta + (at - to * uint32_t(per_cta)), to, e[u]);
+            } else {
+              dst[at] = e[u];
+            }
+          }
           if (before == 0) hist[warp][digit] += uint32_t(__popc(peers));
         }
         __syncwarp();
@@ -353,57 +389,129 @@ constexpr int kSegWarps = 4;
 constexpr int kParts = 4;               // warps that share a chunk's columns
 constexpr int kPart = kChunk / kParts;   // positions in which a warp's runs begin
 
-// dW[r][col..col+7] = or += scale * acc
-template <bool WB>
+__device__ __forceinline__ float4 add4(const float4 a, const float4 b) {
+  return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+
+// The eight columns a lane sums, as two groups of four: with bf16 rows both in one 16-byte piece, with
+// fp32 rows 128 columns apart, so that a warp's copies and stores are whole lines either way.
+template <bool DB>
+__device__ __forceinline__ int lane_column(int slab) {
+  return slab * kSlab + int(threadIdx.x & 31) * (DB ? 8 : 4);
+}
+template <bool DB>
+constexpr int kSecond = DB ? 4 : 128;  // the second group's distance
+
+// dW[r] = or += scale * acc in the lane's columns
+template <bool DB, bool WB>
 __device__ __forceinline__ void finish8(const EmbeddingGradParams& p, uint32_t r, int col, const float (&acc)[8]) {
   int64_t off = 0;
   void* base = dw_row(p, r, &off);
-  if (base == nullptr || !in_bounds(col + 8 <= p.H, p.err)) return;
-  const bool wide = p.wide_dw != 0;
+  if (base == nullptr || !in_bounds(col + 4 <= p.H, p.err)) return;
   float f[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(acc[i], p.scale);
-  if constexpr (!WB) {
-    if (p.accumulate) {
-      float old[8];
-      widen8<false>(load8<false>(base, off + col, wide), old);
+  if constexpr (DB) {
+    const bool wide = p.wide_dw != 0;
+    if constexpr (!WB) {
+      if (p.accumulate) {
+        float old[8];
+        widen8<false>(load8<false>(base, off + col, wide), old);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(old[i], f[i]);
+        for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(old[i], f[i]);
+      }
+    }
+    put8<WB>(base, off + col, f, wide);
+  } else {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int c = col + g * kSecond<DB>;
+      if (c >= p.H) break;
+      const float4 v = make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]);
+      if constexpr (WB) {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + off + c) =
+            make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
+      } else {
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + off + c);
+        *q = p.accumulate ? add4(*q, v) : v;
+      }
     }
   }
-  put8<WB>(base, off + col, f, wide);
 }
 
-// sum of the rows of positions [q0, q1) of the 64 sorted entries own | next, run by run;
-// a run is handed to dW, or to `piece` when that is given (then all positions are one run)
+// the piece's values in the lane's columns
+template <bool DB>
+__device__ __forceinline__ void finish_piece(const EmbeddingGradParams& p, float* piece, int col, const float (&acc)[8]) {
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int c = col + g * kSecond<DB>;
+    if (c < p.H)
+      *reinterpret_cast<float4*>(piece + c) = make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+  }
+}
+
+constexpr int kAhead = 4;  // rows of a batch; a warp has two batches in flight
+
+__device__ __forceinline__ void copy16(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Sum of the rows of positions [q0, q1) of the 64 sorted entries own | next, run by run; a run is
+// handed to dW, or to `piece` when that is given (then all positions are one run). Rows travel to
+// shared memory by asynchronous copies, each lane's columns to its own slots of `ring`, so that two
+// batches are in flight without holding registers and no lane waits for another.
 template <bool DB, bool WB>
 __device__ __forceinline__ void sum_runs(const EmbeddingGradParams& p, const uint2 own, const uint2 next, int q0, int q1,
-                                         int col, float* piece) {
-  constexpr int kAhead = 4;  // rows in flight
+                                         int col, float* piece, uint4* ring) {
+  constexpr int kVecs = DB ? 1 : 2;  // 16-byte pieces of a lane's 8 columns
+  const int lane = threadIdx.x & 31, n = q1 - q0;
   const bool live = col < p.H;
+  // lane l: the entries at q0 + l and q0 + 32 + l
+  uint2 win[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = q0 + 32 * i + lane;
+    const uint2 a = make_uint2(__shfl_sync(0xffffffffu, own.x, at & 31), __shfl_sync(0xffffffffu, own.y, at & 31));
+    const uint2 b = make_uint2(__shfl_sync(0xffffffffu, next.x, at & 31), __shfl_sync(0xffffffffu, next.y, at & 31));
+    win[i] = at < 32 ? a : b;
+  }
+  auto issue = [&](int k) {  // the batch of positions q0 + k ..
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t t = __shfl_sync(0xffffffffu, k < 32 ? win[0].y : win[1].y, (k + u) & 31);
+      if (k + u < n && live && in_bounds(t < p.T && p.H <= p.ld_dy, p.err)) {
+        uint4* slot = ring + ((k & kAhead) + u) * kVecs * 32;
+        const char* row = static_cast<const char*>(p.dY) + (t * p.ld_dy + col) * (DB ? 2 : 4);
+        copy16(slot, row);
+        if (!DB && col + kSecond<DB> < p.H) copy16(slot + 32, row + kSecond<DB> * 4);
+      }
+    }
+    copies_commit();
+  };
+  issue(0);
+  issue(kAhead);
   float acc[8];
   uint32_t cur = 0xffffffffu;
 #pragma unroll 1
-  for (int q = q0; q < q1; q += kAhead) {
-    Vec8<DB> v[kAhead];
+  for (int k = 0; k < n; k += kAhead) {
+    copies_wait<1>();
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int at = q + u;
-      const uint32_t t0 = __shfl_sync(0xffffffffu, own.y, at & 31), t1 = __shfl_sync(0xffffffffu, next.y, at & 31);
-      const int64_t t = at < 32 ? t0 : t1;
-      if (at < q1 && live && in_bounds(t < p.T && p.H <= p.ld_dy, p.err))
-        v[u] = load8<DB>(p.dY, t * p.ld_dy + col, p.wide_dy != 0);
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int at = q + u;
-      const uint32_t k0 = __shfl_sync(0xffffffffu, own.x, at & 31), k1 = __shfl_sync(0xffffffffu, next.x, at & 31);
-      const uint32_t key = at < 32 ? k0 : k1;
-      if (at >= q1) break;
+      const uint32_t key = __shfl_sync(0xffffffffu, k < 32 ? win[0].x : win[1].x, (k + u) & 31);
+      if (k + u >= n) break;
+      const uint4* slot = ring + ((k & kAhead) + u) * kVecs * 32;
+      Vec8<DB> v;
+      v.a = slot[0];
+      if constexpr (!DB) v.b = slot[32];
       float f[8];
-      widen8<DB>(v[u], f);
+      widen8<DB>(v, f);
       if (key != cur) {
-        if (cur != 0xffffffffu && live) finish8<WB>(p, cur, col, acc);
+        if (cur != 0xffffffffu && live) finish8<DB, WB>(p, cur, col, acc);
         cur = key;
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = f[i];
@@ -412,16 +520,14 @@ __device__ __forceinline__ void sum_runs(const EmbeddingGradParams& p, const uin
         for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], f[i]);
       }
     }
+    issue(k + 2 * kAhead);
   }
+  copies_wait<0>();
   if (cur == 0xffffffffu || !live) return;
   if (piece != nullptr)
-    put8<false>(piece, col, acc, true);
+    finish_piece<DB>(p, piece, col, acc);
   else
-    finish8<WB>(p, cur, col, acc);
-}
-
-__device__ __forceinline__ float4 add4(const float4 a, const float4 b) {
-  return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+    finish8<DB, WB>(p, cur, col, acc);
 }
 
 // piece `slot` (0: of the run the chunk begins in, 1: of the run it ends in) of a chunk
@@ -447,6 +553,7 @@ __device__ __forceinline__ int64_t last_chunk_of(const EmbeddingGradParams& p, u
 template <bool DB, bool WB>
 __global__ void __launch_bounds__(kSegWarps * 32, 6) segment_kernel(const __grid_constant__ EmbeddingGradParams p,
                                                                  int seg_ctas) {
+  __shared__ uint4 ring[kSegWarps][2 * kAhead * (DB ? 1 : 2)][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t width = p.row_start[p.n_shards];
   grid_launch_dependents();
@@ -459,7 +566,7 @@ __global__ void __launch_bounds__(kSegWarps * 32, 6) segment_kernel(const __grid
   const uint32_t slabs = uint32_t(p.H + kSlab - 1) / kSlab;
   const uint32_t unit = blockIdx.x * kSegWarps + warp, piece = unit / slabs;
   const int64_t chunk = piece / kParts, p0 = chunk * kChunk;
-  const int slab = int(unit - piece * slabs), col = slab * kSlab + lane * 8;
+  const int slab = int(unit - piece * slabs), col = lane_column<DB>(slab);
   const int begin = int(piece % kParts) * kPart;  // this warp's part of the chunk
   const int64_t T = p.T;
   if (p0 >= T) return;
@@ -508,7 +615,7 @@ __global__ void __launch_bounds__(kSegWarps * 32, 6) segment_kernel(const __grid
 #pragma unroll 1
   for (int i = 0; i < 3; ++i) {
     const int a = i == 0 ? from[0] : i == 1 ? from[1] : from[2], b = i == 0 ? to[0] : i == 1 ? to[1] : to[2];
-    if (a < b) sum_runs<DB, WB>(p, own, next, a, b, col, i < 2 ? piece_of(p, chunk, i) : nullptr);
+    if (a < b) sum_runs<DB, WB>(p, own, next, a, b, col, i < 2 ? piece_of(p, chunk, i) : nullptr, &ring[warp][0][lane]);
   }
 }
 
@@ -582,17 +689,26 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int64_t chunk_count(int64_t T) { return (T + kChunk - 1) / kChunk; }
 
-// Whether the current device can hold a cluster of 16 CTAs, which is above the portable size; found
-// once per device.
-bool cluster16_fits() {
-  static std::atomic<int> known[64];  // 0: not asked yet, 1: no, 2: yes
+// What the current device allows the sort, found once per device: shared memory for the LOCAL form,
+// and clusters of 16 CTAs, which is above the portable size.
+struct SortLimits {
+  bool local = false, wide_cluster = false;
+};
+
+SortLimits sort_limits() {
+  static std::atomic<int> known[64];  // 0: not asked yet, else 1 + bits
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
-    return false;
+    return SortLimits{};
   }
   int k = known[dev].load(std::memory_order_acquire);
   if (k == 0) {
+    const int bytes = int(2 * kSortLocal * sizeof(uint2));
+    const bool local =
+        cudaFuncSetAttribute(sort_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    bool wide = cudaFuncSetAttribute(sort_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                cudaFuncSetAttribute(sort_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -603,19 +719,21 @@ bool cluster16_fits() {
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(kSortCtas, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
+    cfg.dynamicSmemBytes = local ? size_t(bytes) : 0;
     int active = 0;
-    k = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                cudaOccupancyMaxActiveClusters(&active, sort_kernel, &cfg) == cudaSuccess && active > 0
-            ? 2
-            : 1;
+    wide = wide && cudaOccupancyMaxActiveClusters(&active, sort_kernel<true>, &cfg) == cudaSuccess && active > 0;
     cudaGetLastError();
+    k = 1 + (local ? 1 : 0) + (wide ? 2 : 0);
     known[dev].store(k, std::memory_order_release);
   }
-  return k == 2;
+  SortLimits r;
+  r.local = ((k - 1) & 1) != 0;
+  r.wide_cluster = ((k - 1) & 2) != 0;
+  return r;
 }
 
-int sort_ctas(int64_t T) {
-  if (T >= kSortCtas * kSortMinPerCta16 && cluster16_fits()) return kSortCtas;
+int sort_ctas(int64_t T, bool wide_cluster) {
+  if (T >= kSortCtas * kSortMinPerCta16 && wide_cluster) return kSortCtas;
   int ctas = 8;
   while (ctas > 1 && T < ctas * kSortMinPerCta) ctas /= 2;
   return ctas;
@@ -631,7 +749,10 @@ uint32_t early_words(const EmbeddingGradParams& p) {
 }
 
 cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
-  const int ctas = sort_ctas(p.T);
+  const SortLimits limits = sort_limits();
+  const int ctas = sort_ctas(p.T, limits.wide_cluster);
+  const int64_t per_cta = sort_stretch(p.T, ctas) * kSortWarps;
+  const bool local = limits.local && per_cta <= kSortLocal;
   // zeros: whole clusters, one CTA per SM at most
   const int64_t zero = p.early_words < 144u ? p.early_words : 144u;
   cudaLaunchConfig_t cfg = {};
@@ -645,7 +766,8 @@ cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_kernel, p, ctas);
+  cfg.dynamicSmemBytes = local ? size_t(2 * per_cta) * sizeof(uint2) : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, local ? sort_kernel<true> : sort_kernel<false>, p, ctas);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
 }

@@ -259,7 +259,7 @@ struct EmbeddingGradParams {
   int32_t key_bits;                      // bits of the sort key (a local row, or width: no row)
   int32_t dw_bf16;
   int32_t accumulate;
-  int32_t wide_dy, wide_dw;              // rows start on 32-byte boundaries
+  int32_t wide_dw;                       // rows of dW start on 32-byte boundaries
   float scale;
   unsigned int* err;
   uint2* sorted[2];                      // (local row, position), ping-pong; the last pass fills [0]

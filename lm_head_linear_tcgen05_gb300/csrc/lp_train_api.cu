@@ -126,7 +126,6 @@ lp_status lp_embedding_backward(const int32_t* ids, int64_t T, int64_t H, const 
   p.lo = sh.start[0];
   p.vocab_real = int32_t(sh.vocab_real);
   p.dw_bf16 = dw_dtype == LP_DTYPE_BF16 ? 1 : 0;
-  p.wide_dy = aligned(dY, 32) && ld_dy % 8 == 0;
   p.n_shards = sh.n;
   p.T = int32_t(T);
   p.H = int32_t(H);
