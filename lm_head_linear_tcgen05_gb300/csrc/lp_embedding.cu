@@ -182,10 +182,9 @@ constexpr int kSortAhead = 4;  // loads in flight per lane
 // 151936 ids, whole call at H = 8: 38.1 us with 8, 35.6 with 16; T = 8192: 32.0 and 31.7).
 constexpr int64_t kSortMinPerCta = 512;
 constexpr int64_t kSortMinPerCta16 = 1024;
-// Most positions of a CTA that sorts in shared memory, 32768 in all with 16 CTAs. More would fit, but
-// an SM whose shared memory has to grow for the sort drains before and after it (T = 65537: 98 us a
-// call through global memory, 109 in shared memory).
-constexpr int64_t kSortLocal = 2048;
+// Positions a lane keeps in registers: 4 (a warp's stretch of up to 128; 32768 positions in all with
+// 16 CTAs) or 12 (98304).
+constexpr int kKeepFew = 4, kKeepMany = 12;
 // Zeros written while one cluster sorts (see launch_sort).
 constexpr int64_t kEarlyBytes = int64_t(48) << 20;
 
@@ -231,14 +230,57 @@ __device__ __forceinline__ void st_cluster(const void* local, uint32_t cta, uint
                : "memory");
 }
 
-// The first cluster sorts. Each pass: every warp counts the digits of its stretch of positions, the
-// CTAs exchange their totals through distributed shared memory, and every warp walks its stretch
-// again, in order, moving each position to where its digit's count says. LOCAL: the positions stay in
-// the cluster's shared memory (2 x 8 bytes each) until the last pass; otherwise they go through
-// global memory, which costs each pass two round trips to the L2 and a wait for its writes (T = 16384:
-// 15 us a sort, 11 in shared memory). The other clusters, when overwriting, meanwhile write the zeros
-// of the first rows.
-template <bool LOCAL>
+// Exclusive places of a pass: from the CTA's per-warp digit counts in hist, the exclusive prefix over
+// the CTA's warps (into hist), then over the cluster's CTAs and over the bins (into bin_base). A thread
+// per bin. The cluster barrier inside separates what the CTAs did before the pass's writes from them.
+__device__ __forceinline__ void sort_places(uint32_t (&hist)[kSortWarps][kMaxBins], uint32_t* totals, uint32_t* bin_base,
+                                            uint32_t* warp_sum, uint32_t cta, uint32_t ctas) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t mine = 0;
+  for (int w = 0; w < kSortWarps; ++w) {
+    const uint32_t x = hist[w][tid];
+    hist[w][tid] = mine;
+    mine += x;
+  }
+  totals[tid] = mine;
+  cluster_sync();
+  uint32_t all = 0, before_me = 0, of_cta[kSortCtas];
+#pragma unroll
+  for (uint32_t c = 0; c < kSortCtas; ++c) of_cta[c] = c < ctas ? ld_cluster(totals + tid, c) : 0u;
+#pragma unroll
+  for (uint32_t c = 0; c < kSortCtas; ++c) {
+    if (c < cta) before_me += of_cta[c];
+    all += of_cta[c];
+  }
+  uint32_t incl = all;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  uint32_t base = incl - all + before_me;
+  for (int w = 0; w < warp; ++w) base += warp_sum[w];
+  bin_base[tid] = base;
+  __syncthreads();
+}
+
+// Marks the row of each lane's key; a lane whose first peer has its row leaves the mark to that one.
+__device__ __forceinline__ void mark_present(const EmbeddingGradParams& p, uint32_t key, uint32_t width, uint32_t peers,
+                                             bool first_peer, bool live) {
+  const uint32_t of_first = __shfl_sync(0xffffffffu, key, __ffs(peers) - 1);
+  if (live && key < width && (first_peer || key != of_first)) atomicOr(p.present + (key >> 5), 1u << (key & 31));
+}
+
+// The first cluster sorts; the others, when overwriting, meanwhile write the zeros of the first rows.
+// Each pass: every warp counts the digits of its stretch of positions, the CTAs exchange their totals
+// through distributed shared memory, and every warp moves its positions, in order, to where their
+// digits' counts say. KEEP > 0: a lane keeps its (up to KEEP) positions in registers from the count to
+// the move, and they travel between CTAs in shared memory until the last pass. KEEP = 0: the stretch
+// is walked twice and passes go through global memory, which costs each of them round trips to the
+// L2 and a wait for its writes.
+template <int KEEP>
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ EmbeddingGradParams p, int sort_ctas) {
   if (int(blockIdx.x) >= sort_ctas) {
     grid_launch_dependents();
@@ -246,7 +288,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
       zero_rows<kSortWarps>(p, word * 32, 0u);
     return;
   }
-  extern __shared__ uint2 local[];  // LOCAL: two buffers of the CTA's stretch
+  extern __shared__ uint2 local[];  // KEEP: the CTA's stretch
   __shared__ uint32_t hist[kSortWarps][kMaxBins];
   __shared__ uint32_t totals[kMaxBins];
   __shared__ uint32_t bin_base[kMaxBins];
@@ -267,115 +309,126 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     for (uint32_t i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) p.present[i] = 0u;
   }
   for (int pass = 0; pass < passes; ++pass) {
-    // passes alternate between two buffers; the first reads the ids and, LOCAL, leaves their keys in
-    // buffer 1; the last fills sorted[0]
-    const uint2* src = LOCAL ? local + ((pass + 1) & 1) * per_cta : p.sorted[(passes - pass) & 1];
-    const int64_t src0 = LOCAL ? cta_begin : 0;  // the position at src[0]
     const bool last = pass == passes - 1;
-    uint2* dst = p.sorted[(passes - 1 - pass) & 1];
     const int shift = pass * bits;
     for (int w = 0; w < kSortWarps; ++w) hist[w][tid] = 0u;
     __syncthreads();
-    for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
-      uint32_t key[kSortAhead];
+    if constexpr (KEEP > 0) {
+      uint2 e[KEEP];
+      uint32_t peers[KEEP];
 #pragma unroll
-      for (int u = 0; u < kSortAhead; ++u) {
-        const int64_t i = i0 + 32 * u + lane;
-        key[u] = 0u;
-        if (i < end) key[u] = pass == 0 ? uint32_t(__ldg(p.ids + i)) : LOCAL ? src[i - src0].x : __ldcg(src + i).x;
-      }
-#pragma unroll
-      for (int u = 0; u < kSortAhead; ++u) {
-        const int64_t i = i0 + 32 * u + lane;
-        if (i0 + 32 * u >= end) break;
-        uint32_t digit = bins;
-        if (i < end) {
-          uint32_t k = key[u];
-          if (pass == 0) {
-            const int id = int(k);
-            k = position_key(p, id, width);
-            if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
-            if (LOCAL) local[per_cta + i - cta_begin] = make_uint2(k, uint32_t(i));
-          }
-          digit = (k >> shift) & (bins - 1);
-        }
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
-        __syncwarp();
-      }
-    }
-    __syncthreads();
-    // a thread per bin: exclusive prefix over the CTA's warps, then over the CTAs, then over the bins
-    uint32_t mine = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t x = hist[w][tid];
-      hist[w][tid] = mine;
-      mine += x;
-    }
-    totals[tid] = mine;
-    cluster_sync();
-    uint32_t all = 0, before_me = 0, of_cta[kSortCtas];
-#pragma unroll
-    for (uint32_t c = 0; c < kSortCtas; ++c) of_cta[c] = c < ctas ? ld_cluster(totals + tid, c) : 0u;
-#pragma unroll
-    for (uint32_t c = 0; c < kSortCtas; ++c) {
-      if (c < cta) before_me += of_cta[c];
-      all += of_cta[c];
-    }
-    uint32_t incl = all;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += x;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    uint32_t base = incl - all + before_me;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
-    bin_base[tid] = base;
-    __syncthreads();
-    for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
-      uint2 e[kSortAhead];
-#pragma unroll
-      for (int u = 0; u < kSortAhead; ++u) {
-        const int64_t i = i0 + 32 * u + lane;
+      for (int u = 0; u < KEEP; ++u) {
+        const int64_t i = begin + 32 * u + lane;
         e[u] = make_uint2(0u, uint32_t(i));
         if (i < end) {
-          if (LOCAL)
-            e[u] = src[i - src0];
-          else if (pass == 0)
-            e[u].x = position_key(p, __ldg(p.ids + i), width);
+          if (pass == 0)
+            e[u].x = uint32_t(__ldg(p.ids + i));
           else
-            e[u] = __ldcg(src + i);
+            e[u] = local[i - cta_begin];
         }
       }
 #pragma unroll
-      for (int u = 0; u < kSortAhead; ++u) {
-        const int64_t i = i0 + 32 * u + lane;
-        if (i0 + 32 * u >= end) break;
-        const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
-        if (pass == 0 && !p.accumulate) {  // a lane whose first peer has its row leaves the mark to it
-          const uint32_t of_first = __shfl_sync(0xffffffffu, e[u].x, __ffs(peers) - 1);
-          if (i < end && e[u].x < width && (before == 0 || e[u].x != of_first))
-            atomicOr(p.present + (e[u].x >> 5), 1u << (e[u].x & 31));
+      for (int u = 0; u < KEEP; ++u) {
+        const int64_t i = begin + 32 * u + lane;
+        if (begin + 32 * u >= end) break;
+        if (pass == 0 && i < end) {
+          const int id = int(e[u].x);
+          e[u].x = position_key(p, id, width);
+          if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
         }
+        const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
+        peers[u] = __match_any_sync(0xffffffffu, digit);
+        if (i < end && lane == __ffs(peers[u]) - 1) hist[warp][digit] += uint32_t(__popc(peers[u]));
+        __syncwarp();
+      }
+      __syncthreads();
+      sort_places(hist, totals, bin_base, warp_sum, cta, ctas);
+#pragma unroll
+      for (int u = 0; u < KEEP; ++u) {
+        const int64_t i = begin + 32 * u + lane;
+        if (begin + 32 * u >= end) break;
+        const uint32_t digit = (e[u].x >> shift) & (bins - 1);
+        const uint32_t before = uint32_t(__popc(peers[u] & ((1u << lane) - 1)));
+        if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers[u], before == 0, i < end);
         uint32_t at = 0;
         if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
         __syncwarp();
         if (i < end) {
           if (in_bounds(int64_t(at) < T, p.err)) {
-            if (LOCAL && !last) {
-              const uint32_t to = at / uint32_t(per_cta);
-              st_cluster(local + (pass & 1) * per_cta + (at - to * uint32_t(per_cta)), to, e[u]);
+            if (last) {
+              p.sorted[0][at] = e[u];
             } else {
-              dst[at] = e[u];
+              const uint32_t to = at / uint32_t(per_cta);
+              st_cluster(local + (at - to * uint32_t(per_cta)), to, e[u]);
             }
           }
-          if (before == 0) hist[warp][digit] += uint32_t(__popc(peers));
+          if (before == 0) hist[warp][digit] += uint32_t(__popc(peers[u]));
         }
         __syncwarp();
+      }
+    } else {
+      // passes alternate between the two buffers so that the last one fills sorted[0]
+      const uint2* src = p.sorted[(passes - pass) & 1];
+      uint2* dst = p.sorted[(passes - 1 - pass) & 1];
+      for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
+        uint32_t key[kSortAhead];
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u) {
+          const int64_t i = i0 + 32 * u + lane;
+          key[u] = 0u;
+          if (i < end) key[u] = pass == 0 ? uint32_t(__ldg(p.ids + i)) : __ldcg(src + i).x;
+        }
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u) {
+          const int64_t i = i0 + 32 * u + lane;
+          if (i0 + 32 * u >= end) break;
+          uint32_t digit = bins;
+          if (i < end) {
+            uint32_t k = key[u];
+            if (pass == 0) {
+              const int id = int(k);
+              k = position_key(p, id, width);
+              if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+            }
+            digit = (k >> shift) & (bins - 1);
+          }
+          const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+          if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
+          __syncwarp();
+        }
+      }
+      __syncthreads();
+      sort_places(hist, totals, bin_base, warp_sum, cta, ctas);
+      for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
+        uint2 e[kSortAhead];
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u) {
+          const int64_t i = i0 + 32 * u + lane;
+          e[u] = make_uint2(0u, uint32_t(i));
+          if (i < end) {
+            if (pass == 0)
+              e[u].x = position_key(p, __ldg(p.ids + i), width);
+            else
+              e[u] = __ldcg(src + i);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u) {
+          const int64_t i = i0 + 32 * u + lane;
+          if (i0 + 32 * u >= end) break;
+          const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
+          const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+          const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
+          if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers, before == 0, i < end);
+          uint32_t at = 0;
+          if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
+          __syncwarp();
+          if (i < end) {
+            if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
+            if (before == 0) hist[warp][digit] += uint32_t(__popc(peers));
+          }
+          __syncwarp();
+        }
       }
     }
     cluster_sync();  // the pass's output and the totals' readers
@@ -689,26 +742,19 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int64_t chunk_count(int64_t T) { return (T + kChunk - 1) / kChunk; }
 
-// What the current device allows the sort, found once per device: shared memory for the LOCAL form,
-// and clusters of 16 CTAs, which is above the portable size.
-struct SortLimits {
-  bool local = false, wide_cluster = false;
-};
-
-SortLimits sort_limits() {
-  static std::atomic<int> known[64];  // 0: not asked yet, else 1 + bits
+// Whether the current device can hold clusters of kSortCtas CTAs, which is above the portable size;
+// found once per device, together with the shared memory that kKeepMany needs.
+bool wide_cluster_fits() {
+  static std::atomic<int> known[64];  // 0: not asked yet, 1: no, 2: yes
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
-    return SortLimits{};
+    return false;
   }
   int k = known[dev].load(std::memory_order_acquire);
   if (k == 0) {
-    const int bytes = int(2 * kSortLocal * sizeof(uint2));
-    const bool local =
-        cudaFuncSetAttribute(sort_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-    bool wide = cudaFuncSetAttribute(sort_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                cudaFuncSetAttribute(sort_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    constexpr int kBytes = kKeepMany * 32 * kSortWarps * int(sizeof(uint2));
+    constexpr auto kNonPortable = cudaFuncAttributeNonPortableClusterSizeAllowed;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -719,21 +765,24 @@ SortLimits sort_limits() {
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(kSortCtas, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
-    cfg.dynamicSmemBytes = local ? size_t(bytes) : 0;
+    cfg.dynamicSmemBytes = kBytes;
     int active = 0;
-    wide = wide && cudaOccupancyMaxActiveClusters(&active, sort_kernel<true>, &cfg) == cudaSuccess && active > 0;
+    const bool fits =
+        cudaFuncSetAttribute(sort_kernel<0>, kNonPortable, 1) == cudaSuccess &&
+        cudaFuncSetAttribute(sort_kernel<kKeepFew>, kNonPortable, 1) == cudaSuccess &&
+        cudaFuncSetAttribute(sort_kernel<kKeepMany>, kNonPortable, 1) == cudaSuccess &&
+        cudaFuncSetAttribute(sort_kernel<kKeepFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) == cudaSuccess &&
+        cudaFuncSetAttribute(sort_kernel<kKeepMany>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&active, sort_kernel<kKeepMany>, &cfg) == cudaSuccess && active > 0;
     cudaGetLastError();
-    k = 1 + (local ? 1 : 0) + (wide ? 2 : 0);
+    k = fits ? 2 : 1;
     known[dev].store(k, std::memory_order_release);
   }
-  SortLimits r;
-  r.local = ((k - 1) & 1) != 0;
-  r.wide_cluster = ((k - 1) & 2) != 0;
-  return r;
+  return k == 2;
 }
 
-int sort_ctas(int64_t T, bool wide_cluster) {
-  if (T >= kSortCtas * kSortMinPerCta16 && wide_cluster) return kSortCtas;
+int sort_ctas(int64_t T, bool wide) {
+  if (T >= kSortCtas * kSortMinPerCta16 && wide) return kSortCtas;
   int ctas = 8;
   while (ctas > 1 && T < ctas * kSortMinPerCta) ctas /= 2;
   return ctas;
@@ -749,10 +798,10 @@ uint32_t early_words(const EmbeddingGradParams& p) {
 }
 
 cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
-  const SortLimits limits = sort_limits();
-  const int ctas = sort_ctas(p.T, limits.wide_cluster);
-  const int64_t per_cta = sort_stretch(p.T, ctas) * kSortWarps;
-  const bool local = limits.local && per_cta <= kSortLocal;
+  const bool wide = wide_cluster_fits();
+  const int ctas = sort_ctas(p.T, wide);
+  const int64_t stretch = sort_stretch(p.T, ctas);
+  const int keep = !wide || stretch > 32 * kKeepMany ? 0 : stretch > 32 * kKeepFew ? kKeepMany : kKeepFew;
   // zeros: whole clusters, one CTA per SM at most
   const int64_t zero = p.early_words < 144u ? p.early_words : 144u;
   cudaLaunchConfig_t cfg = {};
@@ -766,8 +815,9 @@ cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.dynamicSmemBytes = local ? size_t(2 * per_cta) * sizeof(uint2) : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, local ? sort_kernel<true> : sort_kernel<false>, p, ctas);
+  cfg.dynamicSmemBytes = keep != 0 ? size_t(stretch) * kSortWarps * sizeof(uint2) : 0;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, keep == kKeepFew ? sort_kernel<kKeepFew> : keep == kKeepMany ? sort_kernel<kKeepMany> : sort_kernel<0>, p, ctas);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
 }
