@@ -14,8 +14,8 @@
 // what a launch and its dependencies cost, so one cluster runs all stages with its hardware barrier
 // between them.
 // Token terms and the sums of a thread, warp or CTA are fp32. Sums over tiles and pairs carry their
-// rounding along in a second fp32 (fp64 additions issue at a thirty-second of the fp32 rate here:
-// with them the pair stage took 19 us instead of 6 for 1024 pairs).
+// rounding along in a second fp32: an SM issues fp64 additions far too slowly (with fp64 sums the last
+// CTA of a policy loss of 4 M tokens alone took 20 us).
 // All sums have an order fixed by T and the offsets, never by timing. Everything the offsets index is
 // clamped to [0, T], so wrong offsets give LP_ERR_SEQ_OFFSETS and never a stray access.
 #include "lp_device.cuh"
@@ -26,23 +26,18 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCountBlock = 512;            // tokens of a count: 16 a lane
-constexpr int kStatCtas = 304;              // most CTAs of the per-sequence and per-pair stages
-constexpr int kTokenTile = 4 * kThreads;    // tokens of a CTA and step, four a thread
-#ifndef LP_TOKEN_MIN
-#define LP_TOKEN_MIN 3
-#endif
-#ifndef LP_TOKEN_CTAS
-#define LP_TOKEN_CTAS 456
-#endif
-constexpr int kTokenCtas = LP_TOKEN_CTAS;             // most CTAs of the token stages
-constexpr int kPrefTile = 256;              // tokens of a warp, eight a lane
-constexpr int kCluster = 8;                 // CTAs of the one-launch form
-#ifndef LP_LOSS_FUSED_T
-#define LP_LOSS_FUSED_T 16384
-#endif
-constexpr int64_t kFusedTokens = LP_LOSS_FUSED_T;  // batches up to this long run in one launch
-constexpr int64_t kFusedSeqs = 16384;              // of up to this many sequences
+constexpr int kCountBlock = 512;          // tokens of a count: 16 a lane
+constexpr int kStatCtas = 304;            // most CTAs of the per-sequence and per-pair stages
+constexpr int kTokenTile = 4 * kThreads;  // tokens of a CTA and step, four a thread
+constexpr int kTokenCtas = 456;           // most CTAs of the policy's tokens: three to an SM, 80 registers
+constexpr int kGradCtas = 1216;           // most CTAs of the preference gradient: eight to an SM
+constexpr int kPrefTile = 256;            // tokens of a warp, eight a lane
+// The one-launch form takes batches of up to this many tokens and sequences. On the GPU it and the
+// stages as launches take the same time there (16384 tokens: 12 us either way) and it loses above
+// (65536 tokens: 22 and 14 us); a launch less is some 3 us less on the host.
+constexpr int kCluster = 8;
+constexpr int64_t kFusedTokens = 16384;
+constexpr int64_t kFusedSeqs = 16384;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -495,7 +490,7 @@ __global__ void __launch_bounds__(kThreads) policy_stat_kernel(const __grid_cons
 }
 
 template <int KL, bool BY_SEQ>
-__global__ void __launch_bounds__(kThreads, LP_TOKEN_MIN)
+__global__ void __launch_bounds__(kThreads, 3)
     policy_token_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws, int stat_ctas) {
   __shared__ bool is_last;
   policy_tokens<KL, BY_SEQ>(p, ws, blockIdx.x, gridDim.x, stat_ctas, true);
@@ -613,76 +608,58 @@ __device__ __forceinline__ void pref_sum(const PreferenceParams& p, const PrefWs
     pref_sum_tile(p, ws, tile);
 }
 
-// Sums and kept tokens of the sequences that the lanes of a warp hold, one each, over tiles [first,
-// last] (none when last < first). Up to kPrefSerial tiles are added by the lane itself; a longer
-// sequence by the whole warp, 32 tiles at a time.
-constexpr int kPrefSerial = 8;
-
-__device__ __forceinline__ void sequence_sums(const PrefWs& ws, int s, int first, int last, Pair32* sum, int* n) {
-  const int lane = threadIdx.x & 31;
+// Sum and kept tokens of a sequence over tiles [first, last] (none when last < first), by the eight
+// lanes that hold it; each of them gets both.
+__device__ __forceinline__ void sequence_sum(const PrefWs& ws, int s, int first, int last, Pair32* sum, int* n) {
+  const int lane = threadIdx.x & 7;
   Pair32 v{0.f, 0.f};
   int k = 0;
   if (first == last) {  // beginning and ending on the tile's own edges counts as within it
-    const Piece c = read_piece(ws.whole + s);
+    const Piece c = lane == 0 ? read_piece(ws.whole + s) : Piece{0.f, 0};
     v.hi = c.sum;
     k = c.n;
-  } else if (first < last && last - first < kPrefSerial) {
-    Piece c[kPrefSerial];
-#pragma unroll
-    for (int i = 0; i < kPrefSerial; ++i)
-      c[i] = first + i <= last ? read_piece(ws.pieces + int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) : Piece{0.f, 0};
-#pragma unroll
-    for (int i = 0; i < kPrefSerial; ++i) {
-      v = add(v, c[i].sum);
-      k += c[i].n;
+  } else {
+#pragma unroll 4
+    for (int tile = first + lane; tile <= last; tile += 8) {
+      const Piece c = read_piece(ws.pieces + int64_t(tile) * 2 + (tile == first ? 1 : 0));
+      v = add(v, c.sum);
+      k += c.n;
     }
   }
-  for (uint32_t left = __ballot_sync(0xffffffffu, last - first >= kPrefSerial); left != 0u; left &= left - 1u) {
-    const int who = __ffs(left) - 1, f = __shfl_sync(0xffffffffu, first, who), l = __shfl_sync(0xffffffffu, last, who);
-    Pair32 w{0.f, 0.f};
-    int m = 0;
-    for (int tile = f + lane; tile <= l; tile += 32) {
-      const Piece c = read_piece(ws.pieces + int64_t(tile) * 2 + (tile == f ? 1 : 0));
-      w = add(w, c.sum);
-      m += c.n;
-    }
-    w = warp_add(w);
-    m = warp_sum_int(m);
-    if (lane == who) {
-      v = w;
-      k = m;
-    }
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) {
+    v = add(v, Pair32{__shfl_xor_sync(0xffffffffu, v.hi, off), __shfl_xor_sync(0xffffffffu, v.lo, off)});
+    k += __shfl_xor_sync(0xffffffffu, k, off);
   }
   *sum = v;
   *n = k;
 }
 
-// A lane per pair.
+// Eight lanes per sequence, two pairs a warp; the first lane of a pair's sixteen works out its loss.
 __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, bool wait) {
   __shared__ Pair32 scratch[kWarps][kPrefSums];
   const int lane = threadIdx.x & 31, n_seqs = 2 * p.n_pairs;
   Totals t{0, 0, 0};
   Pair32 m[kPrefSums] = {};
-  for (int64_t base = (int64_t(cta) * kWarps + (threadIdx.x >> 5)) * 32; base < p.n_pairs;
-       base += int64_t(ctas) * kWarps * 32) {
-    const int pair = int(base) + lane;
-    const bool live = pair < p.n_pairs;
-    int first[2] = {0, 0}, last[2] = {-1, -1};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int a = 0, b = 0;
-      if (live) sequence_range(p.in.cu_seqlens, n_seqs, p.T, 2 * pair + i, &a, &b, &t.bad);
+  for (int64_t base = (int64_t(cta) * kWarps + (threadIdx.x >> 5)) * 2; base < p.n_pairs;
+       base += int64_t(ctas) * kWarps * 2) {
+    const int s = int(2 * base) + (lane >> 3), pair = s >> 1;
+    int first = 0, last = -1;
+    if (pair < p.n_pairs) {
+      int a, b;
+      sequence_range(p.in.cu_seqlens, n_seqs, p.T, s, &a, &b, &t.bad);
       if (a < b) {
-        first[i] = a / kPrefTile;
-        last[i] = (b - 1) / kPrefTile;
+        first = a / kPrefTile;
+        last = (b - 1) / kPrefTile;
       }
     }
     if (wait) grid_dependency_wait();  // the offsets are the caller's, the tiles the kernel's before
-    Pair32 sc, sr;
-    int nc, nr;
-    sequence_sums(ws, 2 * pair, first[0], last[0], &sc, &nc);
-    sequence_sums(ws, 2 * pair + 1, first[1], last[1], &sr, &nr);
-    if (!live) continue;
+    Pair32 sc;
+    int nc;
+    sequence_sum(ws, s, first, last, &sc, &nc);
+    Pair32 sr{__shfl_down_sync(0xffffffffu, sc.hi, 8), __shfl_down_sync(0xffffffffu, sc.lo, 8)};
+    const int nr = __shfl_down_sync(0xffffffffu, nc, 8);
+    if ((lane & 15) != 0 || pair >= p.n_pairs) continue;
     const bool counted = nc > 0 && nr > 0;
     float h = 0.f, slope = 0.f;
     if (counted) {
@@ -779,7 +756,7 @@ __device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefW
   }
 }
 
-__global__ void __launch_bounds__(kThreads) pref_sum_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
+__global__ void __launch_bounds__(kThreads, 6) pref_sum_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
   grid_launch_dependents();
   pref_sum(p, ws, blockIdx.x, gridDim.x);
 }
@@ -896,12 +873,12 @@ cudaError_t launch_preference_loss(const PreferenceParams& params, cudaStream_t 
   p.vec = aligned_to(p.in.mask, 4) && aligned_to(p.out.grad_logp, 16);
   if (one_launch(p.T, 2 * int64_t(p.n_pairs)))
     return launch(pref_cluster_kernel, at_most(ceil_div(p.T, kTokenTile), kCluster), true, false, s, p, ws);
-  const int pair = at_most(ceil_div(p.n_pairs, kThreads), kStatCtas);
+  const int pair = at_most(ceil_div(p.n_pairs, 2 * kWarps), kStatCtas);
   cudaError_t e =
       launch(pref_sum_kernel, at_most(ceil_div(p.T, kPrefTile * kWarps), 1 << 30), false, false, s, p, ws);
   if (e == cudaSuccess) e = launch(pref_pair_kernel, pair, false, true, s, p, ws);
   if (e == cudaSuccess)
-    e = launch(pref_grad_kernel, at_most(ceil_div(p.T, kTokenTile), kTokenCtas), false, true, s, p, ws, pair);
+    e = launch(pref_grad_kernel, at_most(ceil_div(p.T, kTokenTile), kGradCtas), false, true, s, p, ws, pair);
   return e;
 }
 
