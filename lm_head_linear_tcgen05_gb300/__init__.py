@@ -959,7 +959,8 @@ def lp_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch
                    adv_per_seq: Optional[bool] = None) -> dict:
     """Clipped policy loss with a KL term (``ref_logp``, ``kl_coef``, ``kl_kind`` k1 / k2 / k3) and an
     entropy bonus, with its gradients. fp32 [T] per token; ``advantages`` [T], or one per sequence of
-    ``cu_seqlens`` (int32 [S + 1]; where S = T they are per token unless ``adv_per_seq``); ``mask`` bool or uint8 [T], zero = the token does not count.
+    ``cu_seqlens`` (int32 [S + 1]; where S = T they are per token unless ``adv_per_seq``); ``mask``
+    bool or uint8 [T], zero = the token does not count.
     ``aggregation``: token_mean, seq_mean_token_mean or seq_mean_token_sum; ``denominator`` replaces
     the number of tokens (sequences) of the mean; ``upstream`` (fp32, one element, on the GPU)
     multiplies the gradients. Returns loss (0-D), metrics [6] (POLICY_METRICS), counts int64 [2] (kept

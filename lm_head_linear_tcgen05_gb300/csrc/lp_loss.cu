@@ -13,6 +13,12 @@
 // (the policy's last stage is run by the CTA that finishes the tokens last). Short ones are bound by
 // what a launch and its dependencies cost, so one cluster runs all stages with its hardware barrier
 // between them.
+// Bounds: a long policy loss by memory and issue (4 M tokens with KL and entropy, 122 MB: 29.6 us, 4.1
+// TB/s, of which the stages before the tokens are 6 us and the tokens' stage issues some 60 instructions
+// a token); a long preference loss by the dependent steps of its three stages (2 M tokens, 27 MB: 17.7
+// us); short ones by those of their one launch (4096 tokens: 8 us policy, 9 us preference). So loads are
+// 16 bytes a lane and issued ahead of their use, what does not depend on an earlier kernel is loaded
+// before waiting for it, and a warp searches the offsets together, 32 probes a step.
 // Token terms and the sums of a thread, warp or CTA are fp32. Sums over tiles and pairs carry their
 // rounding along in a second fp32: an SM issues fp64 additions far too slowly (with fp64 sums the last
 // CTA of a policy loss of 4 M tokens alone took 20 us).
@@ -380,8 +386,11 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
   const int64_t step = int64_t(ctas) * kTokenTile, T = p.T;
   int64_t w0 = int64_t(cta) * kTokenTile + int64_t(threadIdx.x & ~31) * 4;  // the warp's 128 tokens
   auto lanes = [&](int64_t w) { return int(max(int64_t(0), min(int64_t(4), T - w - 4 * lane))); };
+  const int32_t* cu = p.in.cu_seqlens;
   Tokens cur;
   load_tokens<KL>(p, w0 + 4 * lane, lanes(w0), &cur);
+  SeqCursor at{0, 0, 0};
+  if (BY_SEQ && w0 < T) at.start(cu, p.n_seqs, w0, p.T);
   if (wait) grid_dependency_wait();  // only what the call's earlier kernels write has to wait
   const Totals tot = add_totals(ws.totals, stat_ctas);
   const bool seq_token_mean = p.aggregation == LP_AGG_SEQ_MEAN_TOKEN_MEAN, vec = p.vec != 0;
@@ -389,24 +398,19 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
   const float denom = p.denominator > 0.f ? p.denominator : own;
   const float w_all = denom > 0.f && !tot.bad ? __fdiv_rn(1.f, denom) : 0.f;
   const float up = p.in.upstream != nullptr ? __ldg(p.in.upstream) : 1.f;
-  const int32_t* cu = p.in.cu_seqlens;
   float sum[kPolicySums] = {0.f, 0.f, 0.f, 0.f, 0.f};
   for (; w0 < T; w0 += step) {
     const int64_t t0 = w0 + 4 * lane;
     const int n = lanes(w0);
     Tokens next;
     if (w0 + step < T) load_tokens<KL>(p, t0 + step, lanes(w0 + step), &next);
-    SeqCursor at{0, 0, 0};
     float w_seq = w_all, a_seq = 0.f;
     auto enter = [&](int64_t t) {
       at.find(cu, t);
       if (seq_token_mean) w_seq = tot.bad ? 0.f : __fdiv_rn(1.f, __fmul_rn(float(__ldcg(ws.seq_kept + at.seq)), denom));
       if (p.adv_per_seq) a_seq = __ldg(p.in.advantages + at.seq);
     };
-    if (BY_SEQ) {
-      at.start(cu, p.n_seqs, w0, p.T);
-      enter(min(t0, T - 1));
-    }
+    if (BY_SEQ) enter(min(t0, T - 1));
     float g[4], ge[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -446,6 +450,7 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
     if (p.out.grad_logp != nullptr) store4(p.out.grad_logp, t0, n, vec, g);
     if (p.out.grad_entropy != nullptr) store4(p.out.grad_entropy, t0, n, vec, ge);
     cur = next;
+    if (BY_SEQ && w0 + step < T) at.start(cu, p.n_seqs, w0 + step, p.T);
   }
 #pragma unroll
   for (int i = 0; i < kPolicySums; ++i) sum[i] = warp_sum(sum[i]);
@@ -711,10 +716,24 @@ __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefW
   }
 }
 
-__device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, int pair_ctas) {
+__device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, int pair_ctas,
+                                          bool wait) {
+  const int32_t* cu = p.in.cu_seqlens;
+  const bool vec = p.vec != 0, grad = p.out.grad_logp != nullptr;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t step = int64_t(ctas) * kTokenTile, T = p.T;
+  int64_t w0 = int64_t(cta) * kTokenTile + warp * 128;  // the warp's 128 tokens
+  auto lanes = [&](int64_t w) { return int(max(int64_t(0), min(int64_t(4), T - w - 4 * lane))); };
+  // the first tokens' masks and sequences, which need nothing of the earlier kernels
+  uint32_t mask = 0;
+  SeqCursor at{0, 0, 0};
+  if (grad && w0 < T) {
+    mask = load_mask4(p.in.mask, w0 + 4 * lane, lanes(w0), vec);
+    at.start(cu, 2 * p.n_pairs, w0, p.T);
+  }
+  if (wait) grid_dependency_wait();
   const Totals tot = add_totals(ws.totals, pair_ctas);
   const float denom = p.denominator > 0.f ? p.denominator : float(tot.seqs);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (cta == 0 && warp < kPrefSums) {  // a warp per metric
     Pair32 v{0.f, 0.f};
     for (int b = lane; b < pair_ctas; b += 32) {
@@ -726,26 +745,18 @@ __device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefW
       p.out.metrics[warp] = tot.bad ? NAN : denom > 0.f ? __fdiv_rn(v.value(), denom) : 0.f;
   }
   if (cta == 0 && threadIdx.x == 0 && p.out.counts != nullptr) p.out.counts[0] = tot.seqs;
-  if (p.out.grad_logp == nullptr) return;
+  if (!grad) return;
   const float scale = denom > 0.f ? __fdiv_rn(p.in.upstream != nullptr ? __ldg(p.in.upstream) : 1.f, denom) : 0.f;
-  const int32_t* cu = p.in.cu_seqlens;
-  const bool vec = p.vec != 0;
-  const int64_t tiles = ceil_div(p.T, kTokenTile);
-  for (int64_t tile = cta; tile < tiles; tile += ctas) {
-    const int64_t w0 = tile * kTokenTile + int64_t(threadIdx.x & ~31) * 4;  // the warp's 128 tokens
-    if (w0 >= p.T) continue;
-    const int64_t t0 = w0 + int64_t(threadIdx.x & 31) * 4;
-    const int n = int(max(int64_t(0), min(int64_t(4), p.T - t0)));
-    const uint32_t mask = load_mask4(p.in.mask, t0, n, vec);
-    SeqCursor at;
-    at.start(cu, 2 * p.n_pairs, w0, p.T);
+  while (w0 < T) {
+    const int64_t t0 = w0 + 4 * lane;
+    const int n = lanes(w0);
     float c = 0.f, g[4];
     auto enter = [&](int64_t t) {
       at.find(cu, t);
       const float slope = __ldcg(ws.slope + at.seq);
       c = slope == 0.f ? 0.f : __fmul_rn(slope, scale);
     };
-    enter(min(t0, int64_t(p.T) - 1));
+    enter(min(t0, T - 1));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool keep = mask_bit(mask, i) && !tot.bad;
@@ -753,6 +764,11 @@ __device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefW
       g[i] = keep ? c : 0.f;
     }
     store4(p.out.grad_logp, t0, n, vec, g);
+    w0 += step;
+    if (w0 < T) {
+      mask = load_mask4(p.in.mask, w0 + 4 * lane, lanes(w0), vec);
+      at.start(cu, 2 * p.n_pairs, w0, p.T);
+    }
   }
 }
 
@@ -768,8 +784,7 @@ __global__ void __launch_bounds__(kThreads) pref_pair_kernel(const __grid_consta
 
 __global__ void __launch_bounds__(kThreads) pref_grad_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws,
                                                              int pair_ctas) {
-  grid_dependency_wait();
-  pref_grad(p, ws, blockIdx.x, gridDim.x, pair_ctas);
+  pref_grad(p, ws, blockIdx.x, gridDim.x, pair_ctas, true);
 }
 
 __global__ void __launch_bounds__(kThreads) pref_cluster_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
@@ -778,7 +793,7 @@ __global__ void __launch_bounds__(kThreads) pref_cluster_kernel(const __grid_con
   cluster_sync();
   pref_pair(p, ws, cta, ctas, false);
   cluster_sync();
-  pref_grad(p, ws, cta, ctas, ctas);
+  pref_grad(p, ws, cta, ctas, ctas, false);
 }
 
 // ------------------------------------------------------------------ launches

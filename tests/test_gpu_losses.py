@@ -226,7 +226,8 @@ def test_preference_extremes_and_options(lp):
     x, ref = -torch.rand(4, device="cuda"), -torch.rand(4, device="cuda")
     base = lp.lp_preference_loss(x, cu, ref_logp=ref)
     up = lp.lp_preference_loss(x, cu, ref_logp=ref, denominator=1.0, upstream=torch.tensor(0.5, device="cuda"))
-    assert torch.allclose(up["grad_logp"], base["grad_logp"], rtol=8 * U) and abs(float(up["loss"]) - 2 * float(base["loss"])) < 1e-6
+    assert torch.allclose(up["grad_logp"], base["grad_logp"], rtol=8 * U)
+    assert abs(float(up["loss"]) - 2 * float(base["loss"])) < 1e-6
     empty = torch.zeros(0, device="cuda")
     out = lp.lp_preference_loss(empty, dev_i32([0, 0, 0]))
     assert torch.count_nonzero(out["metrics"]) == 0 and out["margins"].tolist() == [0.0]
