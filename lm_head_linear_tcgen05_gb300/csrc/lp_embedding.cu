@@ -195,8 +195,8 @@ constexpr int kSortAhead = 4;  // loads in flight per lane
 constexpr int64_t kSortMinPerCta = 512;
 constexpr int64_t kSortMinPerCta16 = 1024;
 // Positions a lane keeps in registers: 4 (a warp's stretch of up to 128; 32768 positions in all with
-// 16 CTAs) or 12 (98304). Kept, T = 16384 sorts in 12.4 us and T = 65537 in 22; through global memory
-// in 14.6 and 28.7.
+// 16 CTAs) or 12 (98304). Kept, T = 16384 sorts in 13 us and T = 65537 in 21; walked twice, in 14.6 and
+// 28.7.
 constexpr int kKeepFew = 4, kKeepMany = 12;
 // Zeros written while one cluster sorts (see launch_sort).
 constexpr int64_t kEarlyBytes = int64_t(48) << 20;
@@ -236,11 +236,6 @@ __device__ __forceinline__ void zero_rows(const EmbeddingGradParams& p, uint32_t
     uint4* q = reinterpret_cast<uint4*>(base + off * (p.dw_bf16 ? 2 : 4));
     for (int c = first; c < vecs; c += 32) q[c] = make_uint4(0u, 0u, 0u, 0u);
   }
-}
-
-__device__ __forceinline__ void st_cluster(const void* local, uint32_t cta, uint2 v) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr(local, cta)), "r"(v.x), "r"(v.y)
-               : "memory");
 }
 
 // Exclusive places of a pass: from the CTA's per-warp digit counts in hist, the exclusive prefix over
@@ -289,10 +284,10 @@ __device__ __forceinline__ void mark_present(const EmbeddingGradParams& p, uint3
 // The first cluster sorts; the others, when overwriting, meanwhile write the zeros of the first rows.
 // Each pass: every warp counts the digits of its stretch of positions, the CTAs exchange their totals
 // through distributed shared memory, and every warp moves its positions, in order, to where their
-// digits' counts say. KEEP > 0: a lane keeps its (up to KEEP) positions in registers from the count to
-// the move, and they travel between CTAs in shared memory until the last pass. KEEP = 0: the stretch
-// is walked twice and passes go through global memory, which costs each of them round trips to the
-// L2 and a wait for its writes.
+// digits' counts say. KEEP > 0: a lane keeps its (up to KEEP) positions, and which lanes share their
+// digits, in registers from the count to the move; KEEP = 0: the stretch is walked twice. Passes go
+// through global memory, which the L2 holds: moving them in distributed shared memory instead saved 1
+// us of a sort and nothing of a call.
 template <int KEEP>
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ EmbeddingGradParams p, int sort_ctas) {
   if (int(blockIdx.x) >= sort_ctas) {
@@ -301,7 +296,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
       zero_rows<kSortWarps>(p, word * 32, 0u);
     return;
   }
-  extern __shared__ uint2 local[];  // KEEP: the CTA's stretch
   __shared__ uint32_t hist[kSortWarps][kMaxBins];
   __shared__ uint32_t totals[kMaxBins];
   __shared__ uint32_t bin_base[kMaxBins];
@@ -312,9 +306,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   const int passes = (p.key_bits + kMaxDigit - 1) / kMaxDigit;
   const int bits = (p.key_bits + passes - 1) / passes;
   const uint32_t bins = 1u << bits;
-  const int64_t T = p.T, per_warp = sort_stretch(T, sort_ctas), per_cta = per_warp * kSortWarps;
-  const int64_t cta_begin = int64_t(cta) * per_cta;
-  const int64_t begin = min(T, cta_begin + warp * per_warp), end = min(T, begin + per_warp);
+  const int64_t T = p.T, per_warp = sort_stretch(T, sort_ctas);
+  const int64_t begin = min(T, (int64_t(cta) * kSortWarps + warp) * per_warp), end = min(T, begin + per_warp);
   grid_launch_dependents();
   if (cta == 0 && tid < 2) p.n_joins[tid] = 0;
   if (!p.accumulate) {
@@ -322,7 +315,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     for (uint32_t i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) p.present[i] = 0u;
   }
   for (int pass = 0; pass < passes; ++pass) {
-    const bool last = pass == passes - 1;
+    // passes alternate between the two buffers so that the last one fills sorted[0]
+    const uint2* src = p.sorted[(passes - pass) & 1];
+    uint2* dst = p.sorted[(passes - 1 - pass) & 1];
     const int shift = pass * bits;
     for (int w = 0; w < kSortWarps; ++w) hist[w][tid] = 0u;
     __syncthreads();
@@ -337,7 +332,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
           if (pass == 0)
             e[u].x = uint32_t(__ldg(p.ids + i));
           else
-            e[u] = local[i - cta_begin];
+            e[u] = __ldcg(src + i);
         }
       }
 #pragma unroll
@@ -367,22 +362,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
         if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
         __syncwarp();
         if (i < end) {
-          if (in_bounds(int64_t(at) < T, p.err)) {
-            if (last) {
-              p.sorted[0][at] = e[u];
-            } else {
-              const uint32_t to = at / uint32_t(per_cta);
-              st_cluster(local + (at - to * uint32_t(per_cta)), to, e[u]);
-            }
-          }
+          if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
           if (before == 0) hist[warp][digit] += uint32_t(__popc(peers[u]));
         }
         __syncwarp();
       }
     } else {
-      // passes alternate between the two buffers so that the last one fills sorted[0]
-      const uint2* src = p.sorted[(passes - pass) & 1];
-      uint2* dst = p.sorted[(passes - 1 - pass) & 1];
       for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
         uint32_t key[kSortAhead];
 #pragma unroll
@@ -756,7 +741,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int64_t chunk_count(int64_t T) { return (T + kChunk - 1) / kChunk; }
 
 // Whether the current device can hold clusters of kSortCtas CTAs, which is above the portable size;
-// found once per device, together with the shared memory that kKeepMany needs.
+// found once per device.
 bool wide_cluster_fits() {
   static std::atomic<int> known[64];  // 0: not asked yet, 1: no, 2: yes
   int dev = -1;
@@ -766,7 +751,6 @@ bool wide_cluster_fits() {
   }
   int k = known[dev].load(std::memory_order_acquire);
   if (k == 0) {
-    constexpr int kBytes = kKeepMany * 32 * kSortWarps * int(sizeof(uint2));
     constexpr auto kNonPortable = cudaFuncAttributeNonPortableClusterSizeAllowed;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -778,15 +762,11 @@ bool wide_cluster_fits() {
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(kSortCtas, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
-    cfg.dynamicSmemBytes = kBytes;
     int active = 0;
-    const bool fits =
-        cudaFuncSetAttribute(sort_kernel<0>, kNonPortable, 1) == cudaSuccess &&
-        cudaFuncSetAttribute(sort_kernel<kKeepFew>, kNonPortable, 1) == cudaSuccess &&
-        cudaFuncSetAttribute(sort_kernel<kKeepMany>, kNonPortable, 1) == cudaSuccess &&
-        cudaFuncSetAttribute(sort_kernel<kKeepFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) == cudaSuccess &&
-        cudaFuncSetAttribute(sort_kernel<kKeepMany>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&active, sort_kernel<kKeepMany>, &cfg) == cudaSuccess && active > 0;
+    const bool fits = cudaFuncSetAttribute(sort_kernel<0>, kNonPortable, 1) == cudaSuccess &&
+                      cudaFuncSetAttribute(sort_kernel<kKeepFew>, kNonPortable, 1) == cudaSuccess &&
+                      cudaFuncSetAttribute(sort_kernel<kKeepMany>, kNonPortable, 1) == cudaSuccess &&
+                      cudaOccupancyMaxActiveClusters(&active, sort_kernel<kKeepMany>, &cfg) == cudaSuccess && active > 0;
     cudaGetLastError();
     k = fits ? 2 : 1;
     known[dev].store(k, std::memory_order_release);
@@ -794,8 +774,8 @@ bool wide_cluster_fits() {
   return k == 2;
 }
 
-int sort_ctas(int64_t T, bool wide) {
-  if (T >= kSortCtas * kSortMinPerCta16 && wide) return kSortCtas;
+int sort_ctas(int64_t T) {
+  if (T >= kSortCtas * kSortMinPerCta16 && wide_cluster_fits()) return kSortCtas;
   int ctas = 8;
   while (ctas > 1 && T < ctas * kSortMinPerCta) ctas /= 2;
   return ctas;
@@ -812,10 +792,8 @@ uint32_t early_words(const EmbeddingGradParams& p) {
 }
 
 cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
-  const bool wide = wide_cluster_fits();
-  const int ctas = sort_ctas(p.T, wide);
+  const int ctas = sort_ctas(p.T);
   const int64_t stretch = sort_stretch(p.T, ctas);
-  const int keep = !wide || stretch > 32 * kKeepMany ? 0 : stretch > 32 * kKeepFew ? kKeepMany : kKeepFew;
   // zeros: whole clusters, one CTA per SM at most
   const int64_t zero = p.early_words < 144u ? p.early_words : 144u;
   cudaLaunchConfig_t cfg = {};
@@ -829,9 +807,10 @@ cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.dynamicSmemBytes = keep != 0 ? size_t(stretch) * kSortWarps * sizeof(uint2) : 0;
-  const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, keep == kKeepFew ? sort_kernel<kKeepFew> : keep == kKeepMany ? sort_kernel<kKeepMany> : sort_kernel<0>, p, ctas);
+  const auto kernel = stretch <= 32 * kKeepFew    ? sort_kernel<kKeepFew>
+                      : stretch <= 32 * kKeepMany ? sort_kernel<kKeepMany>
+                                                  : sort_kernel<0>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, ctas);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
 }

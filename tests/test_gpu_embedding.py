@@ -141,9 +141,11 @@ def test_gradient(lp, grad, dw, kind, T, H, part):
 
 
 @pytest.mark.parametrize("T,H,grad,dw,kind", [(20011, 16, "bf16", "f32", "zipf"), (70001, 8, "f32", "bf16", "hot"),
-                                              (16384, 264, "bf16", "f32", "runs"), (5000, 40, "bf16", "bf16", "zipf")])
+                                              (16384, 264, "bf16", "f32", "runs"), (5000, 40, "bf16", "bf16", "zipf"),
+                                              (100003, 8, "bf16", "f32", "zipf")])
 def test_gradient_of_long_batches(lp, T, H, grad, dw, kind):
-    """Sorted by clusters of 8 and 16 CTAs, two and three digits; long runs joined from many pieces."""
+    """Sorted by clusters of 8 and 16 CTAs, in two and three digits, with the positions kept in registers
+    and not; long runs joined from many pieces."""
     import torch
     for real, bounds in ((1000, [0, 1000]), (300000, [0, 100000, 100000, 300032])):
         ids = _ids(kind, T, real, np.random.RandomState(T))
