@@ -437,7 +437,8 @@ LP_API lp_status lp_embedding_backward(const int32_t* ids, int64_t T, int64_t H,
                                        size_t ws_bytes, lp_stream_t stream);
 
 /* Bytes of device scratch of lp_policy_loss (LP_OP_POLICY_LOSS) or lp_preference_loss
- * (LP_OP_PREFERENCE_LOSS; n_seqs = 2 * n_pairs). 0 for invalid arguments. */
+ * (LP_OP_PREFERENCE_LOSS; n_seqs = 2 * n_pairs, or 0 without cu_seqlens). 0 for short batches, which
+ * need none (workspace may then be NULL), and for invalid arguments. */
 LP_API size_t lp_loss_workspace_size(lp_op op, int64_t T, int64_t n_seqs);
 
 /* How token terms are weighted into the loss; n_i = kept tokens of sequence i, S = the

@@ -945,6 +945,15 @@ def _upstream(u: Optional[torch.Tensor], device: int) -> Optional[int]:
     return u.data_ptr()
 
 
+class LossOutputs(dict):
+    """What a loss returns, by name; ["loss"] is made when it is asked for, a 0-D view of metrics[0]."""
+
+    def __missing__(self, key):
+        if key == "loss" and self.get("metrics") is not None:
+            return self["metrics"][0]
+        raise KeyError(key)
+
+
 def lp_loss_workspace_size(op: int, T: int, n_seqs: int) -> int:
     return int(lib().lp_loss_workspace_size(int(op), int(T), int(n_seqs)))
 
@@ -956,7 +965,7 @@ def lp_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch
                    kl_kind: str = "k3", entropy_coef: float = 0.0, aggregation: str = "token_mean",
                    denominator: float = 0.0, upstream: Optional[torch.Tensor] = None, grads: bool = True,
                    metrics: bool = True, workspace: Optional[torch.Tensor] = None,
-                   adv_per_seq: Optional[bool] = None) -> dict:
+                   adv_per_seq: Optional[bool] = None) -> LossOutputs:
     """Clipped policy loss with a KL term (``ref_logp``, ``kl_coef``, ``kl_kind`` k1 / k2 / k3) and an
     entropy bonus, with its gradients. fp32 [T] per token; ``advantages`` [T], or one per sequence of
     ``cu_seqlens`` (int32 [S + 1]; where S = T they are per token unless ``adv_per_seq``); ``mask``
@@ -995,7 +1004,7 @@ def lp_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch
         ws, wsb = _workspace(L.lp_loss_workspace_size(LP_OP_POLICY_LOSS, T, S), dev, workspace)
         st = L.lp_policy_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb, _raw_stream(dev))
     _raise(st, "lp_policy_loss")
-    return {"loss": None if m is None else m[0], "metrics": m, "counts": c, "grad_logp": g, "grad_entropy": ge}
+    return LossOutputs(metrics=m, counts=c, grad_logp=g, grad_entropy=ge)
 
 
 def lp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
@@ -1031,4 +1040,4 @@ def lp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp: O
         st = L.lp_preference_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb,
                                   _raw_stream(dev))
     _raise(st, "lp_preference_loss")
-    return {"loss": None if m is None else m[0], "metrics": m, "counts": c, "margins": h, "grad_logp": g}
+    return LossOutputs(metrics=m, counts=c, margins=h, grad_logp=g)

@@ -40,12 +40,12 @@ constexpr int kGradCtas = 1216;           // most CTAs of the preference gradien
 constexpr int kPrefTile = 256;            // tokens of a warp, eight a lane
 // The one-launch form takes batches of up to this many tokens and sequences. On the GPU it and the
 // stages as launches take the same time there (16384 tokens: 12 us either way) and it loses above
-// (65536 tokens: 22 and 14 us); a launch less is some 3 us less on the host.
+// (65536 tokens: 22 and 14 us); a launch less is some 3 us less on the host. What its stages pass on
+// stays in the first CTA's shared memory (12 bytes a sequence and 48 a tile at most, 27 KB), so it needs no
+// workspace either.
 constexpr int kCluster = 8;
 constexpr int64_t kFusedTokens = 16384;
-constexpr int64_t kFusedSeqs = 16384;
-
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+constexpr int64_t kFusedSeqs = 2048;
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -56,12 +56,40 @@ struct __align__(16) Totals {
   int bad;  // offsets out of order
 };
 
-// Workspace written by an earlier stage is read past the L1, which another SM's writes do not
-// reach within a launch.
+// Reads of what an earlier stage wrote. ONE: in the one-launch form, where it lies in the first CTA's
+// shared memory; otherwise in the workspace, past the L1, which another SM's writes do not reach.
+template <bool ONE, typename V>
+__device__ __forceinline__ V from_stage(const V* p) {
+  if constexpr (ONE)
+    return *p;
+  else
+    return __ldcg(p);
+}
+
+template <bool ONE>
 __device__ __forceinline__ Totals read_totals(const Totals* t) {
-  const int4 v = __ldcg(reinterpret_cast<const int4*>(t));
+  const int4 v = from_stage<ONE>(reinterpret_cast<const int4*>(t));
   return Totals{(long long)(uint64_t(uint32_t(v.x)) | (uint64_t(uint32_t(v.y)) << 32)), v.z, v.w};
 }
+
+// The generic address, anywhere in the cluster, of the first CTA's dynamic shared memory.
+__device__ __forceinline__ void* first_cta_shared(void* mine) {
+  uint64_t p;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(p) : "l"(reinterpret_cast<uint64_t>(mine)), "r"(0));
+  return reinterpret_cast<void*>(p);
+}
+
+// Lays out the parts of a workspace one after another, `align` bytes apart.
+struct Carver {
+  char* at;
+  size_t align, used;
+  template <typename V>
+  __host__ __device__ V* take(int64_t n) {
+    V* p = reinterpret_cast<V*>(at + used);
+    used += (size_t(n) * sizeof(V) + align - 1) / align * align;
+    return p;
+  }
+};
 
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
@@ -132,10 +160,11 @@ __device__ __forceinline__ Totals cta_totals(Totals t) {
 }
 
 // Totals over the n CTAs of an earlier stage; every thread gets them.
+template <bool ONE>
 __device__ __forceinline__ Totals add_totals(const Totals* totals, int n) {
   Totals t{0, 0, 0};
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Totals o = read_totals(totals + i);
+    const Totals o = read_totals<ONE>(totals + i);
     t.kept += o.kept;
     t.seqs += o.seqs;
     t.bad |= o.bad;
@@ -259,26 +288,21 @@ constexpr int kPolicySums = 5;
 struct PolicyWs {
   int32_t* block_kept;  // [ceil(T / kCountBlock)]
   int32_t* seq_kept;    // [n_seqs]
-  Totals* totals;       // [kStatCtas]
-  float* sums;          // [kTokenCtas][kPolicySums]
+  Totals* totals;       // [CTAs of the stat stage]
+  float* sums;          // [CTAs of the token stage][kPolicySums]
   uint32_t* done;       // CTAs that have finished their tokens
 };
 
-PolicyWs policy_carve(void* workspace, int64_t T, int64_t n_seqs, size_t* bytes) {
-  char* w = static_cast<char*>(workspace);
-  size_t off = 0;
-  auto take = [&](size_t n) {
-    char* at = w + off;
-    off += up256(n);
-    return at;
-  };
+__host__ __device__ inline PolicyWs policy_carve(void* base, size_t align, int64_t T, int64_t n_seqs, int stat_ctas,
+                                                 int token_ctas, size_t* bytes) {
+  Carver c{static_cast<char*>(base), align, 0};
   PolicyWs r;
-  r.block_kept = reinterpret_cast<int32_t*>(take(size_t(ceil_div(T, kCountBlock)) * 4));
-  r.seq_kept = reinterpret_cast<int32_t*>(take(size_t(n_seqs) * 4));
-  r.totals = reinterpret_cast<Totals*>(take(kStatCtas * sizeof(Totals)));
-  r.sums = reinterpret_cast<float*>(take(size_t(kTokenCtas) * kPolicySums * 4));
-  r.done = reinterpret_cast<uint32_t*>(take(4));
-  *bytes = off;
+  r.totals = c.take<Totals>(stat_ctas);
+  r.sums = c.take<float>(int64_t(token_ctas) * kPolicySums);
+  r.done = c.take<uint32_t>(1);
+  r.block_kept = c.take<int32_t>(ceil_div(T, kCountBlock));
+  r.seq_kept = c.take<int32_t>(n_seqs);
+  *bytes = c.used;
   return r;
 }
 
@@ -291,6 +315,7 @@ __device__ __forceinline__ void policy_count(const PolicyParams& p, const Policy
   }
 }
 
+template <bool ONE>
 __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyWs& ws, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
   const int gw = cta * kWarps + int(threadIdx.x >> 5), n_warps = ctas * kWarps;
@@ -302,7 +327,7 @@ __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyW
     } else {
       const int64_t blocks = ceil_div(p.T, kCountBlock);
       int c = 0;
-      for (int64_t i = int64_t(gw) * 32 + lane; i < blocks; i += int64_t(n_warps) * 32) c += __ldcg(ws.block_kept + i);
+      for (int64_t i = int64_t(gw) * 32 + lane; i < blocks; i += int64_t(n_warps) * 32) c += from_stage<ONE>(ws.block_kept + i);
       t.kept = warp_sum_int(c);
     }
   } else {
@@ -314,7 +339,7 @@ __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyW
         const int b0 = int(ceil_div(a, kCountBlock)), b1 = b / kCountBlock;  // whole blocks [b0, b1)
         if (b0 < b1) {
           int c = 0;
-          for (int i = b0 + lane; i < b1; i += 32) c += __ldcg(ws.block_kept + i);
+          for (int i = b0 + lane; i < b1; i += 32) c += from_stage<ONE>(ws.block_kept + i);
           n = warp_sum_int(c) + count_kept(mask, a, b0 * kCountBlock) + count_kept(mask, b1 * kCountBlock, b);
         } else {
           n = count_kept(mask, a, b);
@@ -378,9 +403,9 @@ __device__ __forceinline__ void load_tokens(const PolicyParams& p, int64_t t0, i
 // KL: the estimator, or kNoKl without a reference. BY_SEQ: weights or advantages go by sequence.
 // A lane loads its next four tokens before it works on the present ones. A token that is not kept
 // is worked on as zeros of weight zero, so that no lane leaves the others' path.
-template <int KL, bool BY_SEQ>
+template <int KL, bool BY_SEQ, bool ONE>
 __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const PolicyWs& ws, int cta, int ctas,
-                                              int stat_ctas, bool wait) {
+                                              int stat_ctas) {
   __shared__ float scratch[kWarps][kPolicySums];
   const int lane = threadIdx.x & 31;
   const int64_t step = int64_t(ctas) * kTokenTile, T = p.T;
@@ -391,8 +416,8 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
   load_tokens<KL>(p, w0 + 4 * lane, lanes(w0), &cur);
   SeqCursor at{0, 0, 0};
   if (BY_SEQ && w0 < T) at.start(cu, p.n_seqs, w0, p.T);
-  if (wait) grid_dependency_wait();  // only what the call's earlier kernels write has to wait
-  const Totals tot = add_totals(ws.totals, stat_ctas);
+  if (!ONE) grid_dependency_wait();  // only what the call's earlier kernels write has to wait
+  const Totals tot = add_totals<ONE>(ws.totals, stat_ctas);
   const bool seq_token_mean = p.aggregation == LP_AGG_SEQ_MEAN_TOKEN_MEAN, vec = p.vec != 0;
   const float own = p.aggregation == LP_AGG_TOKEN_MEAN ? float(tot.kept) : float(tot.seqs);
   const float denom = p.denominator > 0.f ? p.denominator : own;
@@ -407,7 +432,8 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
     float w_seq = w_all, a_seq = 0.f;
     auto enter = [&](int64_t t) {
       at.find(cu, t);
-      if (seq_token_mean) w_seq = tot.bad ? 0.f : __fdiv_rn(1.f, __fmul_rn(float(__ldcg(ws.seq_kept + at.seq)), denom));
+      if (seq_token_mean)
+        w_seq = tot.bad ? 0.f : __fdiv_rn(1.f, __fmul_rn(float(from_stage<ONE>(ws.seq_kept + at.seq)), denom));
       if (p.adv_per_seq) a_seq = __ldg(p.in.advantages + at.seq);
     };
     if (BY_SEQ) enter(min(t0, T - 1));
@@ -458,13 +484,14 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
   if (threadIdx.x < kPolicySums) ws.sums[cta * kPolicySums + threadIdx.x] = s;
 }
 
+template <bool ONE>
 __device__ __forceinline__ void policy_final(const PolicyParams& p, const PolicyWs& ws, int stat_ctas, int token_ctas) {
   __shared__ Pair32 m[kPolicySums];
-  const Totals tot = add_totals(ws.totals, stat_ctas);
+  const Totals tot = add_totals<ONE>(ws.totals, stat_ctas);
   const int lane = threadIdx.x & 31, i = threadIdx.x >> 5;
   if (i < kPolicySums) {  // a warp per sum
     Pair32 v{0.f, 0.f};
-    for (int b = lane; b < token_ctas; b += 32) v = add(v, __ldcg(ws.sums + b * kPolicySums + i));
+    for (int b = lane; b < token_ctas; b += 32) v = add(v, from_stage<ONE>(ws.sums + b * kPolicySums + i));
     v = warp_add(v);
     if (lane == 0) m[i] = v;
   }
@@ -491,14 +518,14 @@ __global__ void __launch_bounds__(kThreads) policy_count_kernel(const __grid_con
 __global__ void __launch_bounds__(kThreads) policy_stat_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws) {
   grid_launch_dependents();
   grid_dependency_wait();
-  policy_stat(p, ws, blockIdx.x, gridDim.x);
+  policy_stat<false>(p, ws, blockIdx.x, gridDim.x);
 }
 
 template <int KL, bool BY_SEQ>
 __global__ void __launch_bounds__(kThreads, 3)
     policy_token_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws, int stat_ctas) {
   __shared__ bool is_last;
-  policy_tokens<KL, BY_SEQ>(p, ws, blockIdx.x, gridDim.x, stat_ctas, true);
+  policy_tokens<KL, BY_SEQ, false>(p, ws, blockIdx.x, gridDim.x, stat_ctas);
   // the CTA that finishes last adds the partial sums, in the order of the CTAs
   __threadfence();
   __syncthreads();
@@ -506,21 +533,25 @@ __global__ void __launch_bounds__(kThreads, 3)
   __syncthreads();
   if (!is_last) return;
   __threadfence();
-  policy_final(p, ws, stat_ctas, gridDim.x);
+  policy_final<false>(p, ws, stat_ctas, gridDim.x);
 }
 
 template <int KL, bool BY_SEQ>
-__global__ void __launch_bounds__(kThreads) policy_cluster_kernel(const __grid_constant__ PolicyParams p, const PolicyWs ws) {
+__global__ void __launch_bounds__(kThreads) policy_cluster_kernel(const __grid_constant__ PolicyParams p) {
+  extern __shared__ int4 stage[];
   const int cta = blockIdx.x, ctas = gridDim.x;
+  size_t bytes;
+  const PolicyWs ws = policy_carve(first_cta_shared(stage), 16, p.T, p.n_seqs, ctas, ctas, &bytes);
+  cluster_sync();  // the first CTA has started
   if (p.in.mask != nullptr) {
     policy_count(p, ws, cta, ctas);
     cluster_sync();
   }
-  policy_stat(p, ws, cta, ctas);
+  policy_stat<true>(p, ws, cta, ctas);
   cluster_sync();
-  policy_tokens<KL, BY_SEQ>(p, ws, cta, ctas, ctas, false);
-  cluster_sync();
-  if (cta == 0) policy_final(p, ws, ctas, ctas);
+  policy_tokens<KL, BY_SEQ, true>(p, ws, cta, ctas, ctas);
+  cluster_sync();  // and the others have read what they need of its shared memory
+  if (cta == 0) policy_final<true>(p, ws, ctas, ctas);
 }
 
 // ------------------------------------------------------------------ preference
@@ -531,8 +562,9 @@ struct __align__(8) Piece {
   int n;
 };
 
+template <bool ONE>
 __device__ __forceinline__ Piece read_piece(const Piece* c) {
-  const int2 v = __ldcg(reinterpret_cast<const int2*>(c));
+  const int2 v = from_stage<ONE>(reinterpret_cast<const int2*>(c));
   return Piece{__int_as_float(v.x), v.y};
 }
 
@@ -542,25 +574,20 @@ struct PrefWs {
   Piece* pieces;   // [tiles][2]: of the sequence a tile begins in, of the one it ends in
   Piece* whole;    // [2 n_pairs]: of the sequences that lie within one tile
   float* slope;    // [2 n_pairs]: d (sum of pair losses) / d logp of a kept token
-  Totals* totals;  // [kStatCtas], seqs = counted pairs
-  Pair32* sums;    // [kStatCtas][kPrefSums]
+  Totals* totals;  // [CTAs of the pair stage], seqs = counted pairs
+  Pair32* sums;    // [CTAs of the pair stage][kPrefSums]
 };
 
-PrefWs pref_carve(void* workspace, int64_t T, int64_t n_seqs, size_t* bytes) {
-  char* w = static_cast<char*>(workspace);
-  size_t off = 0;
-  auto take = [&](size_t n) {
-    char* at = w + off;
-    off += up256(n);
-    return at;
-  };
+__host__ __device__ inline PrefWs pref_carve(void* base, size_t align, int64_t T, int64_t n_seqs, int pair_ctas,
+                                             size_t* bytes) {
+  Carver c{static_cast<char*>(base), align, 0};
   PrefWs r;
-  r.pieces = reinterpret_cast<Piece*>(take(size_t(ceil_div(T, kPrefTile)) * 2 * sizeof(Piece)));
-  r.whole = reinterpret_cast<Piece*>(take(size_t(n_seqs) * sizeof(Piece)));
-  r.slope = reinterpret_cast<float*>(take(size_t(n_seqs) * 4));
-  r.totals = reinterpret_cast<Totals*>(take(kStatCtas * sizeof(Totals)));
-  r.sums = reinterpret_cast<Pair32*>(take(size_t(kStatCtas) * kPrefSums * 8));
-  *bytes = off;
+  r.totals = c.take<Totals>(pair_ctas);
+  r.sums = c.take<Pair32>(int64_t(pair_ctas) * kPrefSums);
+  r.pieces = c.take<Piece>(ceil_div(T, kPrefTile) * 2);
+  r.whole = c.take<Piece>(n_seqs);
+  r.slope = c.take<float>(n_seqs);
+  *bytes = c.used;
   return r;
 }
 
@@ -615,18 +642,19 @@ __device__ __forceinline__ void pref_sum(const PreferenceParams& p, const PrefWs
 
 // Sum and kept tokens of a sequence over tiles [first, last] (none when last < first), by the eight
 // lanes that hold it; each of them gets both.
+template <bool ONE>
 __device__ __forceinline__ void sequence_sum(const PrefWs& ws, int s, int first, int last, Pair32* sum, int* n) {
   const int lane = threadIdx.x & 7;
   Pair32 v{0.f, 0.f};
   int k = 0;
   if (first == last) {  // beginning and ending on the tile's own edges counts as within it
-    const Piece c = lane == 0 ? read_piece(ws.whole + s) : Piece{0.f, 0};
+    const Piece c = lane == 0 ? read_piece<ONE>(ws.whole + s) : Piece{0.f, 0};
     v.hi = c.sum;
     k = c.n;
   } else {
 #pragma unroll 4
     for (int tile = first + lane; tile <= last; tile += 8) {
-      const Piece c = read_piece(ws.pieces + int64_t(tile) * 2 + (tile == first ? 1 : 0));
+      const Piece c = read_piece<ONE>(ws.pieces + int64_t(tile) * 2 + (tile == first ? 1 : 0));
       v = add(v, c.sum);
       k += c.n;
     }
@@ -641,7 +669,8 @@ __device__ __forceinline__ void sequence_sum(const PrefWs& ws, int s, int first,
 }
 
 // Eight lanes per sequence, two pairs a warp; the first lane of a pair's sixteen works out its loss.
-__device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, bool wait) {
+template <bool ONE>
+__device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas) {
   __shared__ Pair32 scratch[kWarps][kPrefSums];
   const int lane = threadIdx.x & 31, n_seqs = 2 * p.n_pairs;
   Totals t{0, 0, 0};
@@ -658,10 +687,10 @@ __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefW
         last = (b - 1) / kPrefTile;
       }
     }
-    if (wait) grid_dependency_wait();  // the offsets are the caller's, the tiles the kernel's before
+    if (!ONE) grid_dependency_wait();  // the offsets are the caller's, the tiles the kernel's before
     Pair32 sc;
     int nc;
-    sequence_sum(ws, s, first, last, &sc, &nc);
+    sequence_sum<ONE>(ws, s, first, last, &sc, &nc);
     Pair32 sr{__shfl_down_sync(0xffffffffu, sc.hi, 8), __shfl_down_sync(0xffffffffu, sc.lo, 8)};
     const int nr = __shfl_down_sync(0xffffffffu, nc, 8);
     if ((lane & 15) != 0 || pair >= p.n_pairs) continue;
@@ -702,7 +731,7 @@ __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefW
     ws.slope[2 * pair + 1] = p.length_normalised && counted ? -slope / float(nr) : -slope;
     if (p.out.margins != nullptr) p.out.margins[pair] = h;
   }
-  if (wait) grid_dependency_wait();
+  if (!ONE) grid_dependency_wait();
   t.seqs = warp_sum_int(t.seqs);
   t.bad = __reduce_or_sync(0xffffffffu, t.bad);
 #pragma unroll
@@ -716,8 +745,8 @@ __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefW
   }
 }
 
-__device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, int pair_ctas,
-                                          bool wait) {
+template <bool ONE>
+__device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas, int pair_ctas) {
   const int32_t* cu = p.in.cu_seqlens;
   const bool vec = p.vec != 0, grad = p.out.grad_logp != nullptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -731,13 +760,13 @@ __device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefW
     mask = load_mask4(p.in.mask, w0 + 4 * lane, lanes(w0), vec);
     at.start(cu, 2 * p.n_pairs, w0, p.T);
   }
-  if (wait) grid_dependency_wait();
-  const Totals tot = add_totals(ws.totals, pair_ctas);
+  if (!ONE) grid_dependency_wait();
+  const Totals tot = add_totals<ONE>(ws.totals, pair_ctas);
   const float denom = p.denominator > 0.f ? p.denominator : float(tot.seqs);
   if (cta == 0 && warp < kPrefSums) {  // a warp per metric
     Pair32 v{0.f, 0.f};
     for (int b = lane; b < pair_ctas; b += 32) {
-      const float2 o = __ldcg(reinterpret_cast<const float2*>(ws.sums + b * kPrefSums + warp));
+      const float2 o = from_stage<ONE>(reinterpret_cast<const float2*>(ws.sums + b * kPrefSums + warp));
       v = add(v, Pair32{o.x, o.y});
     }
     v = warp_add(v);
@@ -753,7 +782,7 @@ __device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefW
     float c = 0.f, g[4];
     auto enter = [&](int64_t t) {
       at.find(cu, t);
-      const float slope = __ldcg(ws.slope + at.seq);
+      const float slope = from_stage<ONE>(ws.slope + at.seq);
       c = slope == 0.f ? 0.f : __fmul_rn(slope, scale);
     };
     enter(min(t0, T - 1));
@@ -779,21 +808,26 @@ __global__ void __launch_bounds__(kThreads, 6) pref_sum_kernel(const __grid_cons
 
 __global__ void __launch_bounds__(kThreads) pref_pair_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
   grid_launch_dependents();
-  pref_pair(p, ws, blockIdx.x, gridDim.x, true);
+  pref_pair<false>(p, ws, blockIdx.x, gridDim.x);
 }
 
 __global__ void __launch_bounds__(kThreads) pref_grad_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws,
                                                              int pair_ctas) {
-  pref_grad(p, ws, blockIdx.x, gridDim.x, pair_ctas, true);
+  pref_grad<false>(p, ws, blockIdx.x, gridDim.x, pair_ctas);
 }
 
-__global__ void __launch_bounds__(kThreads) pref_cluster_kernel(const __grid_constant__ PreferenceParams p, const PrefWs ws) {
+__global__ void __launch_bounds__(kThreads) pref_cluster_kernel(const __grid_constant__ PreferenceParams p) {
+  extern __shared__ int4 stage[];
   const int cta = blockIdx.x, ctas = gridDim.x;
+  size_t bytes;
+  const PrefWs ws = pref_carve(first_cta_shared(stage), 16, p.T, 2 * int64_t(p.n_pairs), ctas, &bytes);
+  cluster_sync();  // the first CTA has started
   pref_sum(p, ws, cta, ctas);
   cluster_sync();
-  pref_pair(p, ws, cta, ctas, false);
+  pref_pair<true>(p, ws, cta, ctas);
   cluster_sync();
-  pref_grad(p, ws, cta, ctas, ctas, false);
+  pref_grad<true>(p, ws, cta, ctas, ctas);
+  cluster_sync();  // the others have read what they need of its shared memory
 }
 
 // ------------------------------------------------------------------ launches
@@ -802,12 +836,30 @@ int at_most(int64_t n, int most) { return int(n < 1 ? 1 : n < most ? n : most); 
 
 bool one_launch(int64_t T, int64_t n_seqs) { return T <= kFusedTokens && n_seqs <= kFusedSeqs; }
 
-// `grid` CTAs of kThreads; as one cluster, or as the programmatic dependent of the kernel before it
+// CTAs of the one-launch form, and the shared memory its stages pass their results in
+int cluster_ctas(int64_t T) { return at_most(ceil_div(T, kTokenTile), kCluster); }
+
+size_t policy_stage_bytes(int64_t T, int64_t n_seqs) {
+  size_t bytes = 0;
+  policy_carve(nullptr, 16, T, n_seqs, cluster_ctas(T), cluster_ctas(T), &bytes);
+  return bytes;
+}
+
+size_t pref_stage_bytes(int64_t T, int64_t n_seqs) {
+  size_t bytes = 0;
+  pref_carve(nullptr, 16, T, n_seqs, cluster_ctas(T), &bytes);
+  return bytes;
+}
+
+// `grid` CTAs of kThreads; as one cluster with `shared` bytes a CTA, or as the programmatic dependent of
+// the kernel before it
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int grid, bool cluster, bool dependent, cudaStream_t s, const A&... args) {
+cudaError_t launch(void (*kernel)(P...), int grid, bool cluster, bool dependent, size_t shared, cudaStream_t s,
+                   const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = shared;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   if (cluster) {
@@ -832,68 +884,70 @@ bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 size_t policy_ws_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
-  policy_carve(nullptr, T, n_seqs, &bytes);
+  if (!one_launch(T, n_seqs)) policy_carve(nullptr, 256, T, n_seqs, kStatCtas, kTokenCtas, &bytes);
   return bytes;
 }
 
 size_t preference_ws_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
-  pref_carve(nullptr, T, n_seqs, &bytes);
+  if (!one_launch(T, n_seqs)) pref_carve(nullptr, 256, T, n_seqs, kStatCtas, &bytes);
   return bytes;
 }
 
 namespace {
 
 template <int KL, bool BY_SEQ>
-cudaError_t launch_policy(const PolicyParams& p, const PolicyWs& ws, cudaStream_t s) {
+cudaError_t launch_policy(const PolicyParams& p, cudaStream_t s) {
   if (one_launch(p.T, p.n_seqs))
-    return launch(policy_cluster_kernel<KL, BY_SEQ>, at_most(ceil_div(p.T, kTokenTile), kCluster), true, false, s, p, ws);
+    return launch(policy_cluster_kernel<KL, BY_SEQ>, cluster_ctas(p.T), true, false, policy_stage_bytes(p.T, p.n_seqs), s,
+                  p);
+  size_t bytes = 0;
+  const PolicyWs ws = policy_carve(p.workspace, 256, p.T, p.n_seqs, kStatCtas, kTokenCtas, &bytes);
   const int64_t blocks = ceil_div(p.T, kCountBlock);
   cudaError_t e = cudaSuccess;
   if (p.in.mask != nullptr)
-    e = launch(policy_count_kernel, at_most(ceil_div(blocks, kWarps), 1 << 30), false, false, s, p, ws);
+    e = launch(policy_count_kernel, at_most(ceil_div(blocks, kWarps), 1 << 30), false, false, 0, s, p, ws);
   const int stat = at_most(ceil_div(p.n_seqs > 0 ? int64_t(p.n_seqs) : ceil_div(blocks, 32), kWarps), kStatCtas);
-  if (e == cudaSuccess) e = launch(policy_stat_kernel, stat, false, p.in.mask != nullptr, s, p, ws);
+  if (e == cudaSuccess) e = launch(policy_stat_kernel, stat, false, p.in.mask != nullptr, 0, s, p, ws);
   if (e == cudaSuccess)
-    e = launch(policy_token_kernel<KL, BY_SEQ>, at_most(ceil_div(p.T, kTokenTile), kTokenCtas), false, true, s, p, ws,
+    e = launch(policy_token_kernel<KL, BY_SEQ>, at_most(ceil_div(p.T, kTokenTile), kTokenCtas), false, true, 0, s, p, ws,
                stat);
   return e;
 }
 
 template <int KL>
-cudaError_t launch_policy(const PolicyParams& p, const PolicyWs& ws, cudaStream_t s) {
+cudaError_t launch_policy(const PolicyParams& p, cudaStream_t s) {
   const bool by_seq = p.aggregation == LP_AGG_SEQ_MEAN_TOKEN_MEAN || p.adv_per_seq;
-  return by_seq ? launch_policy<KL, true>(p, ws, s) : launch_policy<KL, false>(p, ws, s);
+  return by_seq ? launch_policy<KL, true>(p, s) : launch_policy<KL, false>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_policy_loss(const PolicyParams& params, cudaStream_t s) {
   PolicyParams p = params;
-  size_t bytes = 0;
-  const PolicyWs ws = policy_carve(p.workspace, p.T, p.n_seqs, &bytes);
   p.vec = aligned_to(p.in.logp, 16) && aligned_to(p.in.old_logp, 16) && aligned_to(p.in.ref_logp, 16) &&
           aligned_to(p.in.entropy, 16) && (p.adv_per_seq || aligned_to(p.in.advantages, 16)) &&
           aligned_to(p.in.mask, 4) && aligned_to(p.out.grad_logp, 16) && aligned_to(p.out.grad_entropy, 16);
-  if (p.in.ref_logp == nullptr) return launch_policy<kNoKl>(p, ws, s);
-  if (p.kl_kind == LP_KL_K1) return launch_policy<LP_KL_K1>(p, ws, s);
-  if (p.kl_kind == LP_KL_K2) return launch_policy<LP_KL_K2>(p, ws, s);
-  return launch_policy<LP_KL_K3>(p, ws, s);
+  if (p.in.ref_logp == nullptr) return launch_policy<kNoKl>(p, s);
+  if (p.kl_kind == LP_KL_K1) return launch_policy<LP_KL_K1>(p, s);
+  if (p.kl_kind == LP_KL_K2) return launch_policy<LP_KL_K2>(p, s);
+  return launch_policy<LP_KL_K3>(p, s);
 }
 
 cudaError_t launch_preference_loss(const PreferenceParams& params, cudaStream_t s) {
   PreferenceParams p = params;
-  size_t bytes = 0;
-  const PrefWs ws = pref_carve(p.workspace, p.T, 2 * int64_t(p.n_pairs), &bytes);
+  const int64_t n_seqs = 2 * int64_t(p.n_pairs);
   p.vec = aligned_to(p.in.mask, 4) && aligned_to(p.out.grad_logp, 16);
-  if (one_launch(p.T, 2 * int64_t(p.n_pairs)))
-    return launch(pref_cluster_kernel, at_most(ceil_div(p.T, kTokenTile), kCluster), true, false, s, p, ws);
+  if (one_launch(p.T, n_seqs))
+    return launch(pref_cluster_kernel, cluster_ctas(p.T), true, false, pref_stage_bytes(p.T, n_seqs), s, p);
+  size_t bytes = 0;
+  const PrefWs ws = pref_carve(p.workspace, 256, p.T, n_seqs, kStatCtas, &bytes);
   const int pair = at_most(ceil_div(p.n_pairs, 2 * kWarps), kStatCtas);
   cudaError_t e =
-      launch(pref_sum_kernel, at_most(ceil_div(p.T, kPrefTile * kWarps), 1 << 30), false, false, s, p, ws);
-  if (e == cudaSuccess) e = launch(pref_pair_kernel, pair, false, true, s, p, ws);
+      launch(pref_sum_kernel, at_most(ceil_div(p.T, kPrefTile * kWarps), 1 << 30), false, false, 0, s, p, ws);
+  if (e == cudaSuccess) e = launch(pref_pair_kernel, pair, false, true, 0, s, p, ws);
   if (e == cudaSuccess)
-    e = launch(pref_grad_kernel, at_most(ceil_div(p.T, kTokenTile), kGradCtas), false, true, s, p, ws, pair);
+    e = launch(pref_grad_kernel, at_most(ceil_div(p.T, kTokenTile), kGradCtas), false, true, 0, s, p, ws, pair);
   return e;
 }
 

@@ -183,7 +183,8 @@ lp_status lp_policy_loss(int64_t T, const lp_policy_inputs* in, const lp_policy_
     return LP_OK;
   }
   const int64_t n_seqs = in->cu_seqlens != nullptr ? in->n_seqs : 0;
-  if (workspace == nullptr || ws_bytes < policy_ws_bytes(T, n_seqs)) return LP_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = policy_ws_bytes(T, n_seqs);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LP_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 16)) return LP_ERR_ALIGNMENT;
   if ((st = device_error_word(&p.err)) != LP_OK) return st;
   p.in = *in;
@@ -237,7 +238,8 @@ lp_status lp_preference_loss(int64_t T, const lp_preference_inputs* in, const lp
       return LP_ERR_CUDA;
     return LP_OK;
   }
-  if (workspace == nullptr || ws_bytes < preference_ws_bytes(T, 2 * in->n_pairs)) return LP_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = preference_ws_bytes(T, 2 * in->n_pairs);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LP_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 16)) return LP_ERR_ALIGNMENT;
   if ((st = device_error_word(&p.err)) != LP_OK) return st;
   p.in = *in;

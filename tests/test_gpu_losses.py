@@ -30,7 +30,7 @@ def lp():
 
 LENGTHS = {
     "one": [1], "few": [3, 0, 1, 7], "ragged": [300, 0, 1, 513, 2, 255, 256, 257, 90], "long": [9000, 5, 4096, 0, 4097, 1],
-    "empty_ends": [0, 0, 40, 0, 0], "many": [1, 2, 0, 3] * 500, "tiles": [256, 256, 1024, 4096, 0, 512],
+    "empty_ends": [0, 0, 40, 0, 0], "many": [1, 2, 0, 3] * 500, "tiles": [256, 256, 1024, 4096, 0, 512], "crowded": [3, 0, 1, 2] * 700, "over": [16385, 0, 3, 40],
 }
 
 

@@ -273,3 +273,33 @@ def test_the_binding_refuses_tensors_that_do_not_fit(lp):
         with pytest.raises((TypeError, ValueError, RuntimeError)):
             f()
     assert lp.lp_get_device_error() == 0
+
+
+def test_back_to_back_calls_repeat_their_bits(lp):
+    """Calls of two inputs in turn, nothing waiting in between: every result is that of the first call."""
+    import torch
+    part = lp.VocabPartition(5000, 5120, ((0, 2000), (2000, 5120)))
+    sets = []
+    for seed, T in ((1, 18000), (2, 701)):
+        rs = np.random.RandomState(seed)
+        ids = rs.randint(-1, 5000, T)
+        ids[rs.rand(T) < 0.4] = 7
+        cu = np.sort(np.concatenate([[0, T], rs.randint(0, T + 1, 31)]))
+        sets.append((dev_i32(ids), _normal((T, 136), torch.bfloat16, seed), dev_f32(-rs.rand(T)), dev_f32(-rs.rand(T)),
+                     dev_i32(cu), torch.from_numpy(rs.rand(T) < 0.7).cuda()))
+
+    def calls(s):
+        ids, dY, x, old, cu, mask = s
+        g = lp.lp_embedding_backward(ids, dY, part, scale=0.5)
+        lp.lp_embedding_backward(ids, dY, part, accumulate=True, dW=g)
+        p = lp.lp_policy_loss(x, old, old, ref_logp=old, entropy=old, mask=mask, cu_seqlens=cu, kl_coef=0.1,
+                              entropy_coef=0.1, aggregation="seq_mean_token_mean")
+        q = lp.lp_preference_loss(x, cu, ref_logp=old, mask=mask)
+        return [*g, *(p[k] for k in ("metrics", "counts", "grad_logp", "grad_entropy")),
+                *(q[k] for k in ("metrics", "margins", "grad_logp"))]
+
+    want = [calls(s) for s in sets]
+    for _ in range(12):
+        got = [calls(sets[i % 2]) for i in range(10)]
+        assert all(torch.equal(a, b) for i, g in enumerate(got) for a, b in zip(g, want[i % 2]))
+    assert lp.lp_get_device_error() == 0

@@ -79,7 +79,10 @@ def test_workspace_sizes(lp):
     assert size(0) == 0 and size(10, 60) == 0 and 0 < size(10) <= size(1000) <= size(100000)
     for op in (lp.LP_OP_POLICY_LOSS, lp.LP_OP_PREFERENCE_LOSS):
         assert lp.lib().lp_workspace_size(op, 10, 64, ctypes.byref(cp)) == 0
-        assert 0 < lp.lp_loss_workspace_size(op, 10, 2) <= lp.lp_loss_workspace_size(op, 10 ** 6, 1000)
+        assert 0 < lp.lp_loss_workspace_size(op, 10 ** 5, 2) <= lp.lp_loss_workspace_size(op, 10 ** 6, 1000)
+        # short batches run in one launch, which needs none
+        assert lp.lp_loss_workspace_size(op, 16384, 2048) == 0
+        assert lp.lp_loss_workspace_size(op, 16385, 2) > 0 and lp.lp_loss_workspace_size(op, 16384, 2050) > 0
         assert lp.lp_loss_workspace_size(op, 0, 2) == 0 and lp.lp_loss_workspace_size(op, -1, 2) == 0
         assert lp.lp_loss_workspace_size(op, 10, -1) == 0
     assert lp.lp_loss_workspace_size(lp.LP_OP_FORWARD, 10, 2) == 0
@@ -87,9 +90,9 @@ def test_workspace_sizes(lp):
 
 @no_gpu
 def test_policy_loss_refuses(lp):
-    need = lp.lp_loss_workspace_size(lp.LP_OP_POLICY_LOSS, 100, 4)
+    need = lp.lp_loss_workspace_size(lp.LP_OP_POLICY_LOSS, 20000, 4)
 
-    def call(T=100, ws=A, wsb=need, metrics=A, counts=A, g=A, ge=None, **kw):
+    def call(T=20000, ws=A, wsb=need, metrics=A, counts=A, g=A, ge=None, **kw):
         i = dict(logp=A, old_logp=A, ref_logp=None, entropy=None, advantages=A, mask=None, cu_seqlens=A, upstream=None,
                  n_seqs=4)
         o = dict(clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, entropy_coef=0.0, denominator=0.0,
@@ -112,14 +115,15 @@ def test_policy_loss_refuses(lp):
                 dict(counts=A + 4), dict(upstream=A + 3), dict(ws=A + 8)):
         assert call(**bad) == ALIGN, bad
     assert call(wsb=need - 1) == WORKSPACE and call(ws=None) == WORKSPACE
+    assert call(T=100, ws=None, wsb=0) == DEVICE
     assert call(T=0, logp=None, ws=None, wsb=0) == DEVICE and call(T=0, clip_low=-1.0) == INVALID
 
 
 @no_gpu
 def test_preference_loss_refuses(lp):
-    need = lp.lp_loss_workspace_size(lp.LP_OP_PREFERENCE_LOSS, 100, 4)
+    need = lp.lp_loss_workspace_size(lp.LP_OP_PREFERENCE_LOSS, 20000, 4)
 
-    def call(T=100, ws=A, wsb=need, metrics=A, counts=A, h=A, g=A, **kw):
+    def call(T=20000, ws=A, wsb=need, metrics=A, counts=A, h=A, g=A, **kw):
         i = dict(logp=A, ref_logp=None, mask=None, cu_seqlens=A, upstream=None, n_pairs=2)
         o = dict(beta=0.1, label_smoothing=0.0, margin=0.0, denominator=0.0, kind=0, length_normalised=0)
         for k, v in kw.items():
@@ -135,7 +139,7 @@ def test_preference_loss_refuses(lp):
         assert call(**bad) == INVALID, bad
     for bad in (dict(logp=A + 2), dict(g=A + 1), dict(h=A + 2), dict(counts=A + 4), dict(ws=A + 4)):
         assert call(**bad) == ALIGN, bad
-    assert call(wsb=need - 1) == WORKSPACE
+    assert call(wsb=need - 1) == WORKSPACE and call(T=100, ws=None, wsb=0) == DEVICE
     assert call(T=0, logp=None, ws=None, wsb=0) == DEVICE
 
 
