@@ -815,38 +815,56 @@ def _partition_ref(part):
         return ctypes.byref(_c_partition(part)[0])
 
 
-def _rows(t: torch.Tensor, name: str, dtype, T: int, H: int) -> int:
+_POINTERS = [ctypes.c_void_p * max(n, 1) for n in range(LP_MAX_SHARDS + 1)]
+
+
+def _on_device(t: torch.Tensor, name: str, device: int):
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, T: int, H: int, device: int) -> int:
     """Checks a [T, H] matrix whose rows are contiguous; returns its row stride in elements."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
         raise TypeError(f"{name} must be a 2-D CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _shape(t, name, (T, H))
-    if t.stride(1) != 1 and t.numel():
+    _on_device(t, name, device)
+    if t.shape[0] != T or t.shape[1] != H:
+        raise ValueError(f"{name} must have shape {(T, H)}, got {tuple(t.shape)}")
+    if T == 0:
+        return H
+    if t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     # the stride of a lone row has no meaning; what torch reports for it may not be a multiple of 16 bytes
     return t.stride(0) if T > 1 else (H + 7) // 8 * 8
 
 
-def _table(W, part, name: str, dtypes) -> Tuple[list, int, torch.dtype]:
-    """The shards of a [V, H] table: (list, H, dtype)."""
-    n = len(part.ranges)
-    if len(W) != n:
-        raise ValueError(f"{name} must have one entry per shard ({n})")
-    given = [w for w in W if w is not None]
-    if not given:
-        raise ValueError(f"{name} holds no shard")
-    H, dtype = given[0].shape[-1], given[0].dtype
-    if dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
-    for k, (w, (s, e)) in enumerate(zip(W, part.ranges)):
+def _table(W, part, name: str, dtypes, device: int, padding: bool):
+    """Checks the [V_k, H] shards of a table: (pointers, H, dtype). A shard may be None when it holds no
+    ids (with ``padding``) or no real ids (without)."""
+    ranges = part.ranges
+    n = len(ranges)
+    if len(W) != n or n > LP_MAX_SHARDS:
+        raise ValueError(f"{name} must have one entry per shard ({n}, at most {LP_MAX_SHARDS})")
+    pointers, H, dtype = _POINTERS[n](), None, None
+    for k, w in enumerate(W):
+        start, end = ranges[k]
         if w is None:
-            if e > s and s < part.vocab_real:
+            if end > start and (padding or start < part.vocab_real):
                 raise ValueError(f"{name}[{k}] is None")
             continue
-        _check(w, f"{name}[{k}]", dtype, 2)
-        _shape(w, f"{name}[{k}]", (e - s, H))
-    return list(W), H, dtype
+        if H is None and isinstance(w, torch.Tensor) and w.dim() == 2:
+            H, dtype = w.shape[1], w.dtype
+            if dtype not in dtypes:
+                raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
+        if not (isinstance(w, torch.Tensor) and w.dtype is dtype and w.get_device() == device and w.dim() == 2
+                and w.is_contiguous() and w.shape[0] == end - start and w.shape[1] == H):
+            _check(w, f"{name}[{k}]", dtype if dtype is not None else torch.float32, 2)
+            _on_device(w, f"{name}[{k}]", device)
+            _shape(w, f"{name}[{k}]", (end - start, H))
+        pointers[k] = w.data_ptr()
+    return pointers, H, dtype
 
 
 def lp_embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: float = 1.0, out_dtype=None,
@@ -855,23 +873,20 @@ def lp_embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: floa
     table's type). ids int32 [T] global ids, -1 = unused (a zero row); W[k] bf16 or fp32
     [V_k, H]. ``out`` may be a [T, H] view with a row stride that is a multiple of 16 bytes."""
     _check(ids, "ids", torch.int32, 1)
-    W, H, dtype = _table(W, part, "W", _LP_DTYPES)
-    out_dtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    T, d, dev = ids.shape[0], ids.get_device(), ids.device
+    pointers, H, dtype = _table(W, part, "W", _LP_DTYPES, d, False)
+    if H is None:
+        raise ValueError("W holds no shard")
+    if out_dtype is None:
+        out_dtype = dtype if out is None else out.dtype
     if out_dtype not in _LP_DTYPES:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-    T = ids.shape[0]
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype, device=ids.device)
-        ld = H
+        out, ld = torch.empty((T, H), dtype=out_dtype, device=dev), H
     else:
-        ld = _rows(out, "out", out_dtype, T, H)
-    for w in W:
-        if w is not None:
-            _same_device(ids, w)
-    _same_device(ids, out)
-    dev = ids.device
+        ld = _rows(out, "out", out_dtype, T, H, d)
     with _on(dev):
-        st = lib().lp_embedding(ids.data_ptr(), T, H, _ptr_array(W), _LP_DTYPES[dtype], _partition_ref(part), scale,
+        st = lib().lp_embedding(ids.data_ptr(), T, H, pointers, _LP_DTYPES[dtype], _partition_ref(part), scale,
                                 out.data_ptr(), ld, _LP_DTYPES[out_dtype], _raw_stream(dev))
     _raise(st, "lp_embedding")
     return out
@@ -884,36 +899,27 @@ def lp_embedding_backward(ids: torch.Tensor, dY: torch.Tensor, part, scale: floa
     [T, H] (a row stride that is a multiple of 16 bytes is fine). ``accumulate`` adds into the
     caller's fp32 ``dW`` (for example the dW of lp_backward_ex, for a table tied to the head)."""
     _check(ids, "ids", torch.int32, 1)
-    T = ids.shape[0]
+    T, d, dev = ids.shape[0], ids.get_device(), ids.device
     if not isinstance(dY, torch.Tensor) or dY.dim() != 2 or dY.dtype not in _LP_DTYPES:
         raise TypeError("dY must be a 2-D fp32 or bf16 tensor")
     H = dY.shape[1]
-    ld = _rows(dY, "dY", dY.dtype, T, H)
-    _same_device(ids, dY)
+    ld = _rows(dY, "dY", dY.dtype, T, H, d)
     if dw_dtype not in _LP_DTYPES:
         raise TypeError("dw_dtype must be torch.float32 or torch.bfloat16")
-    if accumulate and dw_dtype != torch.float32:
-        raise ValueError("accumulation needs fp32 dW")
-    if accumulate and dW is None:
-        raise ValueError("accumulate=True adds into the caller's dW: pass it")
-    n = len(part.ranges)
-    widths = [e - s for s, e in part.ranges]
+    if accumulate and (dW is None or dw_dtype != torch.float32):
+        raise ValueError("accumulate=True adds into the caller's fp32 dW: pass it")
     if dW is None:
-        dW = [torch.empty((w, H), dtype=dw_dtype, device=ids.device) if w else None for w in widths]
-    else:
-        dW = _shard_list(dW, n, "dW", dw_dtype, 2, True)
-        for k, (t, w) in enumerate(zip(dW, widths)):
-            if w and (t is None or tuple(t.shape) != (w, H)):
-                raise ValueError(f"dW[{k}] must be {dw_dtype} [{w}, {H}]")
-            if t is not None:
-                _same_device(ids, t)
+        dW = [torch.empty((e - s, H), dtype=dw_dtype, device=dev) if e > s else None for s, e in part.ranges]
+    pointers, width, _ = _table(dW, part, "dW", (dw_dtype,), d, True)
+    if width is not None and width != H:
+        raise ValueError(f"dW must have rows of {H}, got {width}")
     cp = _partition_ref(part)
     opts = _EmbeddingOptions(_LP_DTYPES[dw_dtype], 1 if accumulate else 0)
-    L, dev = lib(), ids.device
+    L = lib()
     with _on(dev):
         ws, wsb = _workspace(L.lp_workspace_size(LP_OP_EMBEDDING_BACKWARD, T, H, cp), dev, workspace)
         st = L.lp_embedding_backward(ids.data_ptr(), T, H, dY.data_ptr(), ld, _LP_DTYPES[dY.dtype], cp, scale,
-                                     _ptr_array(dW), ctypes.byref(opts), _ptr(ws), wsb, _raw_stream(dev))
+                                     pointers, ctypes.byref(opts), _ptr(ws), wsb, _raw_stream(dev))
     _raise(st, "lp_embedding_backward")
     return dW
 
@@ -925,8 +931,7 @@ def _vector(t, name: str, dtype, n: Optional[int], device: int) -> int:
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.dim() == 1
             and t.is_contiguous() and (n is None or t.shape[0] == n)):
         _check(t, name, dtype, 1)
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+        _on_device(t, name, device)
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
     return t.data_ptr()
 
