@@ -15,7 +15,7 @@
 // between them.
 // Bounds: a long policy loss by memory and issue (4 M tokens with KL and entropy, 122 MB: 29.6 us, 4.1
 // TB/s, of which the stages before the tokens are 6 us and the tokens' stage issues some 60 instructions
-// a token); a long preference loss by the dependent steps of its three stages (2 M tokens, 27 MB: 17.7
+// a token); a long preference loss by the dependent steps of its three stages (2 M tokens, 27 MB: 18.8
 // us); short ones by those of their one launch (4096 tokens: 8 us policy, 9 us preference). So loads are
 // 16 bytes a lane and issued ahead of their use, what does not depend on an earlier kernel is loaded
 // before waiting for it, and a warp searches the offsets together, 32 probes a step.
@@ -315,6 +315,19 @@ __device__ __forceinline__ void policy_count(const PolicyParams& p, const Policy
   }
 }
 
+// Kept tokens of [a, b) by one warp, from the counts of the whole blocks in it and the ragged ends.
+template <bool ONE>
+__device__ __forceinline__ int count_kept_blocks(const uint8_t* mask, const int32_t* block_kept, int a, int b) {
+  const int b0 = int(ceil_div(a, kCountBlock)), b1 = b / kCountBlock;  // whole blocks [b0, b1)
+  if (b0 >= b1) return count_kept(mask, a, b);
+  int c = 0;
+#pragma unroll 8
+  for (int i = b0 + int(threadIdx.x & 31); i < b1; i += 32) c += from_stage<ONE>(block_kept + i);
+  return warp_sum_int(c) + count_kept(mask, a, b0 * kCountBlock) + count_kept(mask, b1 * kCountBlock, b);
+}
+
+constexpr int kLaneTokens = 64;  // most tokens of a sequence that a lane counts (65536 of 16: 26 us, 33 without)
+
 template <bool ONE>
 __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyWs& ws, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
@@ -331,24 +344,33 @@ __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyW
       t.kept = warp_sum_int(c);
     }
   } else {
-    for (int s = gw; s < p.n_seqs; s += n_warps) {
-      int a, b;
-      sequence_range(p.in.cu_seqlens, p.n_seqs, p.T, s, &a, &b, &t.bad);
-      int n = b - a;
-      if (mask != nullptr) {
-        const int b0 = int(ceil_div(a, kCountBlock)), b1 = b / kCountBlock;  // whole blocks [b0, b1)
-        if (b0 < b1) {
-          int c = 0;
-          for (int i = b0 + lane; i < b1; i += 32) c += from_stage<ONE>(ws.block_kept + i);
-          n = warp_sum_int(c) + count_kept(mask, a, b0 * kCountBlock) + count_kept(mask, b1 * kCountBlock, b);
-        } else {
-          n = count_kept(mask, a, b);
-        }
+    // a warp takes up to 32 sequences at a time, as many as give every warp some: a lane counts a short one
+    // itself, and the warp the others, one by one
+    const int per = int(min(int64_t(32), ceil_div(p.n_seqs, n_warps)));
+    for (int64_t base = int64_t(gw) * per; base < p.n_seqs; base += int64_t(n_warps) * per) {
+      const int s = int(base) + lane;
+      const bool mine = lane < per && s < p.n_seqs;
+      int a = 0, b = 0, n = 0;
+      if (mine) sequence_range(p.in.cu_seqlens, p.n_seqs, p.T, s, &a, &b, &t.bad);
+      const bool alone = mask == nullptr || b - a <= kLaneTokens;
+      if (mask == nullptr) {
+        n = b - a;
+      } else if (alone) {
+        for (int i = a; i < b; ++i) n += __ldg(mask + i) != 0;
       }
-      if (lane == 0) ws.seq_kept[s] = n;
+      for (uint32_t left = __ballot_sync(0xffffffffu, !alone); left != 0u; left &= left - 1u) {
+        const int who = __ffs(left) - 1;
+        const int c = count_kept_blocks<ONE>(mask, ws.block_kept, __shfl_sync(0xffffffffu, a, who),
+                                             __shfl_sync(0xffffffffu, b, who));
+        if (lane == who) n = c;
+      }
+      if (mine) ws.seq_kept[s] = n;
       t.kept += n;
       t.seqs += n > 0;
     }
+    t.kept = warp_sum(t.kept);
+    t.seqs = warp_sum_int(t.seqs);
+    t.bad = __reduce_or_sync(0xffffffffu, t.bad);
   }
   t = cta_totals(t);
   if (threadIdx.x == 0) {
@@ -591,6 +613,10 @@ __host__ __device__ inline PrefWs pref_carve(void* base, size_t align, int64_t T
   return r;
 }
 
+// Sequences of a tile from which each gets a lane (7522 tokens in 1368: 22 us, 34 walked by the warp;
+// 262144 in 16384: 22.6 and 23.4; with 12 in a tile the walk is faster).
+constexpr int kPrefMany = 24;
+
 __device__ __forceinline__ void pref_sum_tile(const PreferenceParams& p, const PrefWs& ws, int64_t tile) {
   const int lane = threadIdx.x & 31;
   const int64_t t0 = tile * kPrefTile;
@@ -604,9 +630,40 @@ __device__ __forceinline__ void pref_sum_tile(const PreferenceParams& p, const P
     x[i] = t < b ? __ldg(p.in.logp + t) : 0.f;
     ref[i] = t < b && p.in.ref_logp != nullptr ? __ldg(p.in.ref_logp + t) : 0.f;
   }
-  // the sequences of the tile; empty ones are passed over by a search, and offsets out of order end
-  // the walk
   int s = sequence_of(p.in.cu_seqlens, n, a);
+  if (s + kPrefMany <= n && __ldg(p.in.cu_seqlens + s + kPrefMany - 1) < b) {
+    // many short sequences: a lane each, added with their rounding (up to twice the tile's tokens of
+    // them; beyond, most are empty and the walk below passes over those)
+    const int count = sequence_of(p.in.cu_seqlens, n, b - 1) - s + 1;
+    if (count <= 2 * kPrefTile) {
+      for (int q = s + lane; q < s + count; q += 32) {
+        const int s0 = __ldg(p.in.cu_seqlens + q), s1 = __ldg(p.in.cu_seqlens + q + 1);
+        Pair32 v{0.f, 0.f};
+        int k = 0;
+        for (int t = max(s0, a); t < min(s1, b); t += 4) {  // four tokens' loads at a time
+          const int n4 = min(4, min(s1, b) - t);
+          float l[4], r[4] = {0.f, 0.f, 0.f, 0.f};
+          load4(p.in.logp, t, n4, false, l);
+          if (p.in.ref_logp != nullptr) load4(p.in.ref_logp, t, n4, false, r);
+          const uint32_t keep4 = load_mask4(p.in.mask, t, n4, false);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (!mask_bit(keep4, i)) continue;
+            v = add(v, __fsub_rn(l[i], r[i]));
+            ++k;
+          }
+        }
+        const Piece c{v.value(), k};
+        if (s0 >= a && s1 <= b)
+          ws.whole[q] = c;
+        else
+          ws.pieces[tile * 2 + (s0 < a ? 0 : 1)] = c;
+      }
+      return;
+    }
+  }
+  // few sequences, one after another by the whole warp; empty ones are passed over by a search, and
+  // offsets out of order end the walk
   for (int at = a; at < b;) {
     const int s0 = __ldg(p.in.cu_seqlens + s), s1 = __ldg(p.in.cu_seqlens + s + 1);
     const int s2 = s + 2 <= n ? __ldg(p.in.cu_seqlens + s + 2) : s1;
@@ -640,44 +697,65 @@ __device__ __forceinline__ void pref_sum(const PreferenceParams& p, const PrefWs
     pref_sum_tile(p, ws, tile);
 }
 
-// Sum and kept tokens of a sequence over tiles [first, last] (none when last < first), by the eight
-// lanes that hold it; each of them gets both.
+// Sum and kept tokens over the tiles first, first + step, ... to last of a sequence that spans several.
 template <bool ONE>
-__device__ __forceinline__ void sequence_sum(const PrefWs& ws, int s, int first, int last, Pair32* sum, int* n) {
-  const int lane = threadIdx.x & 7;
-  Pair32 v{0.f, 0.f};
-  int k = 0;
-  if (first == last) {  // beginning and ending on the tile's own edges counts as within it
-    const Piece c = lane == 0 ? read_piece<ONE>(ws.whole + s) : Piece{0.f, 0};
-    v.hi = c.sum;
-    k = c.n;
-  } else {
+__device__ __forceinline__ void add_tiles(const PrefWs& ws, int first, int from, int last, int step, Pair32* v, int* k) {
 #pragma unroll 4
-    for (int tile = first + lane; tile <= last; tile += 8) {
-      const Piece c = read_piece<ONE>(ws.pieces + int64_t(tile) * 2 + (tile == first ? 1 : 0));
-      v = add(v, c.sum);
-      k += c.n;
+  for (int tile = from; tile <= last; tile += step) {
+    const Piece c = read_piece<ONE>(ws.pieces + int64_t(tile) * 2 + (tile == first ? 1 : 0));
+    *v = add(*v, c.sum);
+    *k += c.n;
+  }
+}
+
+// Sequences of more than kPairTiles tiles are added by the whole CTA, one by one. Each thread comes with
+// the tiles of its own sequence (eight lanes to a sequence) and gets its sum in the first of the eight.
+constexpr int kPairTiles = 256;
+
+template <bool ONE>
+__device__ __noinline__ void add_long_sequences(const PrefWs& ws, int first, int last, Pair32* sum, int* n) {
+  __shared__ int2 tiles[kThreads / 8];
+  __shared__ Pair32 part[kWarps];
+  __shared__ int part_n[kWarps];
+  const int mine = threadIdx.x >> 3, warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 7) == 0) tiles[mine] = last - first >= kPairTiles ? make_int2(first, last) : make_int2(0, -1);
+  __syncthreads();
+  for (int q = 0; q < kThreads / 8; ++q) {
+    const int2 r = tiles[q];
+    if (r.y < r.x) continue;
+    Pair32 v{0.f, 0.f};
+    int k = 0;
+    add_tiles<ONE>(ws, r.x, r.x + int(threadIdx.x), r.y, kThreads, &v, &k);
+    v = warp_add(v);
+    k = warp_sum_int(k);
+    if ((threadIdx.x & 31) == 0) {
+      part[warp] = v;
+      part_n[warp] = k;
     }
+    __syncthreads();
+    if (int(threadIdx.x) == 8 * q) {
+      v = part[0];
+      k = part_n[0];
+      for (int w = 1; w < kWarps; ++w) {
+        v = add(v, part[w]);
+        k += part_n[w];
+      }
+      *sum = v;
+      *n = k;
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int off = 4; off >= 1; off >>= 1) {
-    v = add(v, Pair32{__shfl_xor_sync(0xffffffffu, v.hi, off), __shfl_xor_sync(0xffffffffu, v.lo, off)});
-    k += __shfl_xor_sync(0xffffffffu, k, off);
-  }
-  *sum = v;
-  *n = k;
 }
 
 // Eight lanes per sequence, two pairs a warp; the first lane of a pair's sixteen works out its loss.
 template <bool ONE>
 __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefWs& ws, int cta, int ctas) {
   __shared__ Pair32 scratch[kWarps][kPrefSums];
-  const int lane = threadIdx.x & 31, n_seqs = 2 * p.n_pairs;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_seqs = 2 * p.n_pairs;
   Totals t{0, 0, 0};
   Pair32 m[kPrefSums] = {};
-  for (int64_t base = (int64_t(cta) * kWarps + (threadIdx.x >> 5)) * 2; base < p.n_pairs;
-       base += int64_t(ctas) * kWarps * 2) {
-    const int s = int(2 * base) + (lane >> 3), pair = s >> 1;
+  for (int64_t base = int64_t(cta) * kWarps * 2; base < p.n_pairs; base += int64_t(ctas) * kWarps * 2) {
+    const int s = int(2 * base) + warp * 4 + (lane >> 3), pair = s >> 1;
     int first = 0, last = -1;
     if (pair < p.n_pairs) {
       int a, b;
@@ -687,10 +765,24 @@ __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefW
         last = (b - 1) / kPrefTile;
       }
     }
+    const bool is_long = last - first >= kPairTiles;
+    const bool any_long = __syncthreads_or(is_long) != 0;
     if (!ONE) grid_dependency_wait();  // the offsets are the caller's, the tiles the kernel's before
-    Pair32 sc;
-    int nc;
-    sequence_sum<ONE>(ws, s, first, last, &sc, &nc);
+    Pair32 sc{0.f, 0.f};
+    int nc = 0;
+    if (any_long) add_long_sequences<ONE>(ws, first, last, &sc, &nc);
+    if (first == last) {  // beginning and ending on the tile's own edges counts as within it
+      const Piece c = (lane & 7) == 0 ? read_piece<ONE>(ws.whole + s) : Piece{0.f, 0};
+      sc.hi = c.sum;
+      nc = c.n;
+    } else if (!is_long) {
+      add_tiles<ONE>(ws, first, first + (lane & 7), last, 8, &sc, &nc);
+    }
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) {
+      sc = add(sc, Pair32{__shfl_xor_sync(0xffffffffu, sc.hi, off), __shfl_xor_sync(0xffffffffu, sc.lo, off)});
+      nc += __shfl_xor_sync(0xffffffffu, nc, off);
+    }
     Pair32 sr{__shfl_down_sync(0xffffffffu, sc.hi, 8), __shfl_down_sync(0xffffffffu, sc.lo, 8)};
     const int nr = __shfl_down_sync(0xffffffffu, nc, 8);
     if ((lane & 15) != 0 || pair >= p.n_pairs) continue;

@@ -212,6 +212,24 @@ def test_preference(lp, lengths, kind, smoothing, normalised, with_ref):
     assert lp.lp_get_device_error() == 0
 
 
+@pytest.mark.parametrize("lengths", [[70001, 66000], [5, 90000, 300, 0, 140000, 257], [2] * 9000 + [70000, 4]])
+def test_long_and_crowded_sequences(lp, lengths):
+    """Sequences of more tiles than eight lanes add, beside short ones, and tiles of many sequences."""
+    cu, logp, old, ref, _, mask, rs = _tokens(lengths, 31)
+    want = train.preference_loss(logp, cu, ref=ref, mask=mask, beta=0.01)
+    out = lp.lp_preference_loss(dev_f32(logp), dev_i32(cu), ref_logp=dev_f32(ref), mask=dev_u8(mask), beta=0.01)
+    herr = 16 * U * (want["mag"][0::2] + want["mag"][1::2]) + 2 * U * np.abs(want["margins"])
+    assert np.all(np.abs(out["margins"].double().cpu().numpy() - want["margins"]) <= herr + 1e-38)
+    assert int(out["counts"][0]) == want["count"]
+    adv = rs.randn(len(lengths)).astype(np.float32)
+    want = train.policy_loss(logp, old, adv, mask=mask, cu=cu, aggregation="seq_mean_token_mean", per_seq=True)
+    out = lp.lp_policy_loss(dev_f32(logp), dev_f32(old), dev_f32(adv), mask=dev_u8(mask), cu_seqlens=dev_i32(cu),
+                            aggregation="seq_mean_token_mean")
+    assert tuple(out["counts"].tolist()) == want["counts"]
+    assert np.all(np.abs(out["metrics"].double().cpu().numpy() - want["metrics"]) <= 128 * U * want["mag"] + 1e-30)
+    assert lp.lp_get_device_error() == 0
+
+
 def test_preference_extremes_and_options(lp):
     import torch
     cu = dev_i32([0, 1, 2, 3, 4])
