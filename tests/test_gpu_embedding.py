@@ -209,6 +209,35 @@ def test_gradient_rank_local_strided_and_refused_ids(lp):
     assert lp.lp_get_device_error() == 0
 
 
+def test_offsets_past_32_bits(lp):
+    """Tables and batches of more than 2^31 elements: the rows at their far ends."""
+    import torch
+    V, H = 530001, 4096
+    part = _part(lp, V, [0, V])
+    W = torch.zeros((V, H), dtype=torch.bfloat16, device="cuda")
+    W[V - 1], W[V - 2], W[0] = 3.0, 2.0, 1.0
+    y = lp.lp_embedding(dev_i32([V - 1, 0, V - 2, 5]), [W], part)
+    assert y.float().mean(dim=1).tolist() == [3.0, 1.0, 2.0, 0.0]
+    # a batch as large: the table of a few rows, the named positions at both ends
+    small = _part(lp, 40, [0, 40])
+    ids = np.full(V, -1)
+    ids[[0, V - 1]], ids[V - 2], ids[V - 40:V - 2] = 39, 7, 38
+    dY = W                                          # row V-1 threes, row V-2 twos, row 0 ones
+    g = lp.lp_embedding_backward(dev_i32(ids), dY, small)[0]
+    want = torch.zeros(40, device="cuda")
+    want[39], want[7] = 4.0, 2.0
+    assert torch.equal(g, want[:, None].expand(40, H))
+    y = lp.lp_embedding(dev_i32(ids), [W[:40].contiguous()], small)
+    assert int(torch.count_nonzero(y)) == 0 and y.shape == (V, H)
+    # a gradient as large
+    ones = torch.ones((5, H), dtype=torch.bfloat16, device="cuda")
+    g = lp.lp_embedding_backward(dev_i32([V - 1, 0, V - 1, -1, V - 2]), ones, part, dw_dtype=torch.bfloat16)[0]
+    sums = g.sum(dim=1, dtype=torch.float32)
+    assert sums[[V - 1, V - 2, 0]].tolist() == [2.0 * H, 1.0 * H, 1.0 * H]
+    assert float(sums.sum()) == 4.0 * H
+    assert lp.lp_get_device_error() == 0
+
+
 def test_gradient_is_the_transpose_of_the_lookup(lp):
     """<lookup(V), dY> = <V, gradient(dY)> for any V: on integers, where fp32 is exact."""
     import torch
