@@ -219,7 +219,8 @@ __device__ __forceinline__ uint32_t position_key(const EmbeddingGradParams& p, i
   return id >= 0 && id < p.vocab_real && r >= 0 && r < int64_t(width) ? uint32_t(r) : width;
 }
 
-// Writes zeros to the rows of [r0, r0 + 32) whose bit in `skip` is clear, by all warps of a CTA.
+// Writes zeros to the rows of [r0, r0 + 32) whose bit in `skip` is clear, by all warps of a CTA; they leave
+// the L2 first, since nothing here reads them again.
 template <int WARPS>
 __device__ __forceinline__ void zero_rows(const EmbeddingGradParams& p, uint32_t r0, uint32_t skip) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -234,7 +235,7 @@ __device__ __forceinline__ void zero_rows(const EmbeddingGradParams& p, uint32_t
     char* base = static_cast<char*>(dw_row(p, r, &off));
     if (base == nullptr) continue;
     uint4* q = reinterpret_cast<uint4*>(base + off * (p.dw_bf16 ? 2 : 4));
-    for (int c = first; c < vecs; c += 32) q[c] = make_uint4(0u, 0u, 0u, 0u);
+    for (int c = first; c < vecs; c += 32) __stcs(q + c, make_uint4(0u, 0u, 0u, 0u));
   }
 }
 

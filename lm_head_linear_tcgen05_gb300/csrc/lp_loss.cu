@@ -484,7 +484,7 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
     if (w.at + w.step < w.end) load_tokens<KL>(p, t0 + w.step, lanes(w.at + w.step), &next);
     auto enter = [&](int64_t t) {
       at.find(cu, t);
-      if (at.seq == entered) return;
+      if (at.seq == entered || !in_bounds(at.seq >= 0 && at.seq < p.n_seqs, p.err)) return;
       entered = at.seq;
       if (seq_token_mean)
         w_seq = tot.bad ? 0.f : __fdiv_rn(1.f, __fmul_rn(float(from_stage<ONE>(ws.seq_kept + at.seq)), denom));
@@ -527,8 +527,9 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams& p, const Polic
       g[i] = keep ? __fmul_rn(up, __fmul_rn(wt, slope)) : 0.f;
       ge[i] = keep ? -__fmul_rn(up, __fmul_rn(wt, p.entropy_coef)) : 0.f;
     }
-    if (p.out.grad_logp != nullptr) store4(p.out.grad_logp, t0, n, vec, g);
-    if (p.out.grad_entropy != nullptr) store4(p.out.grad_entropy, t0, n, vec, ge);
+    const bool inside = in_bounds(n == 0 || t0 + n <= T, p.err);
+    if (inside && p.out.grad_logp != nullptr) store4(p.out.grad_logp, t0, n, vec, g);
+    if (inside && p.out.grad_entropy != nullptr) store4(p.out.grad_entropy, t0, n, vec, ge);
     cur = next;
     if (BY_SEQ && w.at + w.step < w.end) at.move(cu, p.n_seqs, w.at + w.step, T);
   }
@@ -686,6 +687,7 @@ __device__ __forceinline__ void pref_sum_tile(const PreferenceParams& p, const P
           }
         }
         const Piece c{v.value(), k};
+        if (!in_bounds(q >= 0 && q < n, p.err)) continue;
         if (s0 >= a && s1 <= b)
           ws.whole[q] = c;
         else
@@ -712,7 +714,7 @@ __device__ __forceinline__ void pref_sum_tile(const PreferenceParams& p, const P
     }
     c.sum = warp_sum(c.sum);
     c.n = warp_sum_int(c.n);
-    if (lane == 0) {
+    if (lane == 0 && in_bounds(s >= 0 && s < n, p.err)) {
       if (s0 >= a && s1 <= b)
         ws.whole[s] = c;
       else
@@ -908,7 +910,7 @@ __device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefW
     float g[4];
     auto enter = [&](int64_t t) {
       at.find(cu, t);
-      if (at.seq == entered) return;
+      if (at.seq == entered || !in_bounds(at.seq >= 0 && at.seq < 2 * p.n_pairs, p.err)) return;
       entered = at.seq;
       const float slope = from_stage<ONE>(ws.slope + at.seq);
       c = slope == 0.f ? 0.f : __fmul_rn(slope, scale);
@@ -920,7 +922,7 @@ __device__ __forceinline__ void pref_grad(const PreferenceParams& p, const PrefW
       if (keep && t0 + i >= at.next) enter(t0 + i);
       g[i] = keep ? c : 0.f;
     }
-    store4(p.out.grad_logp, t0, n, vec, g);
+    if (in_bounds(n == 0 || t0 + n <= T, p.err)) store4(p.out.grad_logp, t0, n, vec, g);
     w.at += w.step;
     if (w.at < w.end) {
       mask = load_mask4(p.in.mask, w.at + 4 * lane, lanes(w.at), vec);

@@ -64,7 +64,7 @@ def test_autograd_gradients_are_the_library_calls(lp):
     (3.0 * loss).backward()
     direct = lp.lp_policy_loss(logp, old, adv, entropy=ent, upstream=torch.tensor(3.0, device="cuda"), **opts)
     assert torch.equal(a.grad, direct["grad_logp"]) and torch.equal(b.grad, direct["grad_entropy"])
-    assert torch.equal(metrics, direct["metrics"]) and float(loss) == float(direct["loss"])
+    assert torch.equal(metrics, direct["metrics"]) and float(loss.detach()) == float(direct["loss"])
     assert torch.equal(counts, direct["counts"])
     a = logp.clone().requires_grad_()
     loss, _, _, margins = preference_loss(a, cu, ref_logp=ref, mask=mask, beta=0.5)
