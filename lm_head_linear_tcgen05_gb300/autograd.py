@@ -27,6 +27,7 @@ from __future__ import annotations
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (lp_backward_ex, lp_backward_from_logits, lp_embedding, lp_embedding_backward, lp_forward,
                lp_forward_from_logits, lp_policy_loss, lp_preference_loss)
@@ -127,6 +128,7 @@ class _Embedding(torch.autograd.Function):
         return lp_embedding(ids, list(W), part, scale=scale, out_dtype=out_dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         (ids,) = ctx.saved_tensors
         # a gradient that was broadcast or transposed has rows the library does not take
@@ -145,20 +147,34 @@ def embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: float =
     return _Embedding.apply(ids, part, float(scale), out_dtype, *W)
 
 
+def _save(ctx, inputs, options):
+    """Keeps the inputs and the tensors among the options with autograd, which notices when one was changed in
+    place before the backward reads it again."""
+    ctx.names = [k for k, v in options.items() if isinstance(v, torch.Tensor) and k != "workspace"]
+    ctx.options = {k: v for k, v in options.items() if k not in ctx.names}
+    ctx.save_for_backward(*inputs, *[options[k] for k in ctx.names])
+
+
+def _saved(ctx, n):
+    """The n inputs, and the options, that _save kept."""
+    saved = ctx.saved_tensors
+    return saved[:n], {**ctx.options, **dict(zip(ctx.names, saved[n:]))}
+
+
 class _PolicyLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logp, entropy, old_logp, advantages, options):
         out = lp_policy_loss(logp, old_logp, advantages, entropy=entropy, grads=False, **options)
-        ctx.save_for_backward(logp, old_logp, advantages, *([] if entropy is None else [entropy]))
-        ctx.options = options
+        _save(ctx, (logp, entropy, old_logp, advantages), options)
         ctx.mark_non_differentiable(out["metrics"], out["counts"])
         return out["metrics"][0].clone(), out["metrics"], out["counts"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _g_metrics, _g_counts):
-        logp, old_logp, advantages, *rest = ctx.saved_tensors
-        out = lp_policy_loss(logp, old_logp, advantages, entropy=rest[0] if rest else None, metrics=False,
-                             upstream=g.to(torch.float32), **ctx.options)
+        (logp, entropy, old_logp, advantages), options = _saved(ctx, 4)
+        out = lp_policy_loss(logp, old_logp, advantages, entropy=entropy, metrics=False,
+                             upstream=g.to(torch.float32), **options)
         return (out["grad_logp"] if ctx.needs_input_grad[0] else None,
                 out["grad_entropy"] if ctx.needs_input_grad[1] else None, None, None, None)
 
@@ -177,15 +193,15 @@ class _PreferenceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logp, cu_seqlens, options):
         out = lp_preference_loss(logp, cu_seqlens, grads=False, **options)
-        ctx.save_for_backward(logp, cu_seqlens)
-        ctx.options = options
+        _save(ctx, (logp, cu_seqlens), options)
         ctx.mark_non_differentiable(out["metrics"], out["counts"], out["margins"])
         return out["metrics"][0].clone(), out["metrics"], out["counts"], out["margins"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _g_metrics, _g_counts, _g_margins):
-        logp, cu_seqlens = ctx.saved_tensors
-        out = lp_preference_loss(logp, cu_seqlens, metrics=False, upstream=g.to(torch.float32), **ctx.options)
+        (logp, cu_seqlens), options = _saved(ctx, 2)
+        out = lp_preference_loss(logp, cu_seqlens, metrics=False, upstream=g.to(torch.float32), **options)
         return out["grad_logp"], None, None
 
 

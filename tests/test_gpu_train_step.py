@@ -75,6 +75,47 @@ def test_autograd_gradients_are_the_library_calls(lp):
     assert lp.lp_get_device_error() == 0
 
 
+def test_autograd_notices_inputs_changed_in_place(lp):
+    # the backward reads the inputs again: one that was changed since must not be used in silence
+    import torch
+    from lm_head_linear_tcgen05_gb300.autograd import embedding, policy_loss, preference_loss
+    rs = np.random.RandomState(5)
+    cu, old = dev_i32([0, 30, 64]), dev_f32(-rs.rand(64))
+    for name in ("mask", "ref_logp", "old_logp", "advantages", "entropy", "cu_seqlens"):
+        logp = dev_f32(-rs.rand(64)).requires_grad_()
+        args = {"old_logp": old.clone(), "advantages": dev_f32(rs.randn(64)), "entropy": dev_f32(rs.rand(64)),
+                "ref_logp": old.clone(), "mask": torch.ones(64, dtype=torch.bool, device="cuda"),
+                "cu_seqlens": cu.clone()}
+        loss, *_ = policy_loss(logp, kl_coef=0.1, aggregation="seq_mean_token_mean", **args)
+        args[name].zero_()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    for name in ("mask", "ref_logp", "cu_seqlens"):
+        logp = dev_f32(-rs.rand(64)).requires_grad_()
+        args = {"ref_logp": old.clone(), "mask": torch.ones(64, dtype=torch.bool, device="cuda"),
+                "cu_seqlens": cu.clone()}
+        loss, *_ = preference_loss(logp, **args)
+        args[name].zero_()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    ids, W = dev_i32(rs.randint(0, 50, 9)), _normal((50, 16), torch.float32, 1).requires_grad_()
+    y = embedding(ids, [W], lp.VocabPartition(50, 50, ((0, 50),)))
+    ids.zero_()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_autograd_refuses_second_derivatives(lp):
+    import torch
+    from lm_head_linear_tcgen05_gb300.autograd import preference_loss
+    rs = np.random.RandomState(6)
+    logp = dev_f32(-rs.rand(64)).requires_grad_()
+    loss, *_ = preference_loss(logp, dev_i32([0, 30, 64]))
+    (g,) = torch.autograd.grad(loss * logp.sum(), logp, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
 def test_tied_table_step_matches_fp64(lp):
     """lookup -> linear-logp -> policy loss -> backward -> the lookup's gradient added to the head's:
     the table's whole gradient against fp64 autograd of the same function (X rounded to bf16 alike)."""
