@@ -823,6 +823,16 @@ def _on_device(t: torch.Tensor, name: str, device: int):
         raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
 
 
+def _scratch(nbytes: int, dev: torch.device, workspace: Optional[torch.Tensor]):
+    """(address, bytes) of the caller's workspace, or of a new one that the third entry keeps alive."""
+    if workspace is not None:
+        if not (isinstance(workspace, torch.Tensor) and workspace.is_contiguous()):
+            raise TypeError("workspace must be a contiguous CUDA tensor")
+        _on_device(workspace, "workspace", dev.index)
+    ws, n = _workspace(nbytes, dev, workspace)
+    return _ptr(ws), n, ws
+
+
 def _rows(t: torch.Tensor, name: str, dtype, T: int, H: int, device: int) -> int:
     """Checks a [T, H] matrix whose rows are contiguous; returns its row stride in elements."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
@@ -917,9 +927,9 @@ def lp_embedding_backward(ids: torch.Tensor, dY: torch.Tensor, part, scale: floa
     opts = _EmbeddingOptions(_LP_DTYPES[dw_dtype], 1 if accumulate else 0)
     L = lib()
     with _on(dev):
-        ws, wsb = _workspace(L.lp_workspace_size(LP_OP_EMBEDDING_BACKWARD, T, H, cp), dev, workspace)
+        at, wsb, _kept = _scratch(L.lp_workspace_size(LP_OP_EMBEDDING_BACKWARD, T, H, cp), dev, workspace)
         st = L.lp_embedding_backward(ids.data_ptr(), T, H, dY.data_ptr(), ld, _LP_DTYPES[dY.dtype], cp, scale,
-                                     pointers, ctypes.byref(opts), _ptr(ws), wsb, _raw_stream(dev))
+                                     pointers, ctypes.byref(opts), at, wsb, _raw_stream(dev))
     _raise(st, "lp_embedding_backward")
     return dW
 
@@ -1006,8 +1016,8 @@ def lp_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch
     ge = torch.empty_like(logp) if grads and entropy is not None else None
     cr = _PolicyOutputs(_ptr(m), _ptr(c), _ptr(g), _ptr(ge))
     with _on(dev):
-        ws, wsb = _workspace(L.lp_loss_workspace_size(LP_OP_POLICY_LOSS, T, S), dev, workspace)
-        st = L.lp_policy_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb, _raw_stream(dev))
+        at, wsb, _kept = _scratch(L.lp_loss_workspace_size(LP_OP_POLICY_LOSS, T, S), dev, workspace)
+        st = L.lp_policy_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), at, wsb, _raw_stream(dev))
     _raise(st, "lp_policy_loss")
     return LossOutputs(metrics=m, counts=c, grad_logp=g, grad_entropy=ge)
 
@@ -1041,8 +1051,8 @@ def lp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp: O
     g = torch.empty_like(logp) if grads else None
     cr = _PreferenceOutputs(_ptr(m), _ptr(c), _ptr(h), _ptr(g))
     with _on(dev):
-        ws, wsb = _workspace(L.lp_loss_workspace_size(LP_OP_PREFERENCE_LOSS, T, 2 * P), dev, workspace)
-        st = L.lp_preference_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _ptr(ws), wsb,
+        at, wsb, _kept = _scratch(L.lp_loss_workspace_size(LP_OP_PREFERENCE_LOSS, T, 2 * P), dev, workspace)
+        st = L.lp_preference_loss(T, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), at, wsb,
                                   _raw_stream(dev))
     _raise(st, "lp_preference_loss")
     return LossOutputs(metrics=m, counts=c, margins=h, grad_logp=g)

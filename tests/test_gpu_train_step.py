@@ -316,6 +316,28 @@ def test_the_binding_refuses_tensors_that_do_not_fit(lp):
     assert lp.lp_get_device_error() == 0
 
 
+def test_the_binding_refuses_workspaces_that_do_not_fit(lp):
+    # every call refuses before anything is launched
+    import torch
+    T = 20000
+    part = lp.VocabPartition(100, 100, ((0, 100),))
+    ids, dY, x = dev_i32(np.zeros(T)), torch.zeros((T, 16), device="cuda"), torch.zeros(T, device="cuda")
+    cu = dev_i32([0, 3, T])
+    n = 1 << 22
+    assert lp.lp_loss_workspace_size(lp.LP_OP_POLICY_LOSS, T, 2) > 0
+    assert lp.lp_loss_workspace_size(lp.LP_OP_PREFERENCE_LOSS, T, 2) > 0
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty(16, dtype=torch.uint8, device="cuda"), n):
+        for call in (lambda: lp.lp_embedding_backward(ids, dY, part, workspace=ws),
+                     lambda: lp.lp_policy_loss(x, x, x, cu_seqlens=cu, workspace=ws),
+                     lambda: lp.lp_preference_loss(x, cu, workspace=ws)):
+            with pytest.raises((TypeError, ValueError, RuntimeError)):
+                call()
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert lp.lp_policy_loss(x, x, x, cu_seqlens=cu, workspace=ws)["counts"].tolist() == [T, 2]
+    assert lp.lp_get_device_error() == 0
+
+
 def test_back_to_back_calls_repeat_their_bits(lp):
     """Calls of two inputs in turn, nothing waiting in between: every result is that of the first call."""
     import torch
