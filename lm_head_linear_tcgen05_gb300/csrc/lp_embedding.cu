@@ -1,8 +1,8 @@
 // lp_embedding.cu - embedding lookup with scaling, and its gradient by sorted tokens.
 //
 // Forward: Y[t] = scale W[id_t]. A copy, bound by memory: 8192 rows of H = 4096 in bf16 from four
-// shards take 19.7 us, 6.8 TB/s of rows read and written (1.0 of the measured copy rate); 64 rows,
-// bound by a launch and two dependent loads, 2.1 us.
+// shards take 18.9 us, 7.1 TB/s of rows read and written (1.05 of the measured copy rate); 64 rows,
+// bound by a launch and two dependent loads, 2.3 us.
 //
 // Gradient: dW[v] = scale sum_{t: id_t = v} dY[t], bound by memory too: every row of dY read once,
 // every row of dW written (or, accumulating, the named ones read and written). Adding rows into dW with
@@ -26,8 +26,8 @@
 //                   consecutive pieces, and their sums are added in the order of the groups. Bound by
 //                   its dependent loads: 7 us where 16384 positions leave some 50 long runs.
 // Each launch is the programmatic dependent of the one before. Whole calls: T = 4096, H = 4096 over V =
-// 151936, fp32 (2.5 GB, nearly all of it zeros to write) 348 us, 7.2 TB/s; T = 65537, H = 1024, 70 % of
-// one id, bf16 dW over V = 32749 90 us, 3.7 TB/s; T = 64 11 us.
+// 151936, fp32 (2.5 GB, nearly all of it zeros to write) 347 us, 7.2 TB/s; T = 65537, H = 1024, 70 % of
+// one id, bf16 dW over V = 32749 91 us, 3.7 TB/s; T = 64 11 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -784,7 +784,8 @@ int sort_ctas(int64_t T) {
 
 // Rows whose zeros the sort kernel writes, in words of 32: 48 MB, about what the rest of the GPU can
 // write while one cluster sorts (T = 4096, H = 4096, V = 151936: 350 us, 357 without; 96 MB: 360, since
-// these rows are zeroed whether a position names them or not).
+// these rows are zeroed whether a position names them or not). Asking the L2 for 32 to 128 MB of dY at that
+// time gains nothing (2 calls of T = 16384: 120.5 us, 121.2 to 123.9 with).
 uint32_t early_words(const EmbeddingGradParams& p) {
   if (p.accumulate) return 0u;
   const int64_t row = int64_t(p.H) * (p.dw_bf16 ? 2 : 4);

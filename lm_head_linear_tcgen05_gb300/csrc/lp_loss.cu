@@ -15,7 +15,7 @@
 // between them.
 // Bounds: a long policy loss by memory and issue (4 M tokens with KL and entropy, 122 MB: 29.6 us, 4.1
 // TB/s, of which the stages before the tokens are 6 us and the tokens' stage issues some 60 instructions
-// a token); a long preference loss by the dependent steps of its three stages (2 M tokens, 27 MB: 18.8
+// a token); a long preference loss by the dependent steps of its three stages (2 M tokens, 27 MB: 18.4
 // us); short ones by those of their one launch (4096 tokens: 8 us policy, 9 us preference). So loads are
 // 16 bytes a lane and issued ahead of their use, what does not depend on an earlier kernel is loaded
 // before waiting for it, and a warp searches the offsets together, 32 probes a step.
