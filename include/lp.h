@@ -420,8 +420,8 @@ typedef struct {
 /* Gradient of lp_embedding with respect to the table:
  *   dW[v] = scale * sum of dY[t] over the positions t with ids[t] = v.
  * The sum is in fp32 and its order is fixed: the positions are sorted by id, equal ids by
- * position; sums of up to 32 positions are taken in ascending order, longer ones in
- * pieces that are joined in ascending order. The result is bitwise the same from run to
+ * position; sums of up to 32 positions (64 when T <= 64) are taken in ascending order, longer
+ * ones in pieces that are joined in ascending order. The result is bitwise the same from run to
  * run (it depends on where an id's positions fall in the sorted batch, so a row's bits may
  * differ between batches that share it, unlike the forward's).
  *   dY       [T, H] of type dy_dtype, row stride ld_dy elements (ld_dy >= H; rows must

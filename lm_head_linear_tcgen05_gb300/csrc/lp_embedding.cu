@@ -9,13 +9,14 @@
 // atomics would make the bits depend on the order the hardware ran them in, so the positions are sorted
 // by id first (stably: equal ids stay in ascending position) and every row of dW is then written by one
 // owner that adds its positions in that order:
-//   sort_kernel     LSD radix sort of (local row, position), up to 9 bits a pass, in one cluster: a
-//                   launch, with hardware barriers and distributed shared memory between the passes,
-//                   instead of three launches a pass. An unused or foreign position gets the key
+//   sort_kernel     sorts (local row, position) in one cluster: short batches by counting, for each
+//                   position, those before it; longer ones by an LSD radix sort of up to 9 bits a
+//                   pass, in one launch, with hardware barriers and distributed shared memory between
+//                   the passes, instead of three launches a pass. An unused or foreign position gets the key
 //                   `width` and sorts last. It also marks the rows that some position names. Bound by
-//                   its chain of dependent steps, not by data: 12 us for 16384 positions, 8 for 64.
+//                   its chain of dependent steps, not by data: 12 us for 16384 positions, 2 for 64.
 //   segment_kernel  four warps per (chunk of 32 sorted positions, 256 columns). A run of equal
-//                   rows of at most 32 positions is summed by the warp in whose quarter of a
+//                   rows of at most 32 positions (64 in a batch of no more) is summed by the warp in whose quarter of a
 //                   chunk it begins, which follows it as far as it goes; a longer run is summed
 //                   in pieces, one per chunk it touches, that go to the workspace. Which of the two
 //                   holds is decided from the 96 keys around the chunk, so every warp reaches it alone,
@@ -26,8 +27,8 @@
 //                   consecutive pieces, and their sums are added in the order of the groups. Bound by
 //                   its dependent loads: 7 us where 16384 positions leave some 50 long runs.
 // Each launch is the programmatic dependent of the one before. Whole calls: T = 4096, H = 4096 over V =
-// 151936, fp32 (2.5 GB, nearly all of it zeros to write) 347 us, 7.2 TB/s; T = 65537, H = 1024, 70 % of
-// one id, bf16 dW over V = 32749 91 us, 3.7 TB/s; T = 64 11 us.
+// 151936, fp32 (2.5 GB, nearly all of it zeros to write) 346 us, 7.2 TB/s; T = 65537, H = 1024, 70 % of
+// one id, bf16 dW over V = 32749 92 us, 3.7 TB/s; T = 64 5.3 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -198,8 +199,12 @@ constexpr int64_t kSortMinPerCta16 = 1024;
 // 16 CTAs) or 12 (98304). Kept, T = 16384 sorts in 13 us and T = 65537 in 21; walked twice, in 14.6 and
 // 28.7.
 constexpr int kKeepFew = 4, kKeepMany = 12;
-// Zeros written while one cluster sorts (see launch_sort).
-constexpr int64_t kEarlyBytes = int64_t(48) << 20;
+// Zeros written while one cluster sorts (see early_words), by CTAs of at least kZeroBytes. More CTAs hold up
+// the sort, fewer do not keep up (T = 4096, V = 151936, H = 4096: 346.8 us with 96, 347.0 with 112, 349.8 with
+// 144, 348.8 with 80; two calls of T = 16384: 118.2, 120.9, 120.1, 118.3).
+constexpr int64_t kEarlyBytes = int64_t(56) << 20;
+constexpr int64_t kZeroCtas = 96;
+constexpr int64_t kZeroBytes = 8 * 1024;
 
 // positions of a warp, whole steps of 32
 __host__ __device__ inline int64_t sort_stretch(int64_t T, int ctas) {
@@ -219,23 +224,15 @@ __device__ __forceinline__ uint32_t position_key(const EmbeddingGradParams& p, i
   return id >= 0 && id < p.vocab_real && r >= 0 && r < int64_t(width) ? uint32_t(r) : width;
 }
 
-// Writes zeros to the rows of [r0, r0 + 32) whose bit in `skip` is clear, by all warps of a CTA; they leave
-// the L2 first, since nothing here reads them again.
-template <int WARPS>
-__device__ __forceinline__ void zero_rows(const EmbeddingGradParams& p, uint32_t r0, uint32_t skip) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int vecs = p.H * (p.dw_bf16 ? 2 : 4) / 16;           // 16-byte pieces of a row
-  const int per = vecs < 32 ? 32 / vecs : 1;                 // rows of a warp at a time
-  const int row = vecs < 32 ? lane / vecs : 0, first = vecs < 32 ? lane % vecs : lane;
-  if (row >= per) return;
-  for (int i = warp * per + row; i < 32; i += WARPS * per) {
-    const uint32_t r = r0 + i;
-    if (((skip >> i) & 1u) != 0u || r >= p.row_start[p.n_shards]) continue;
-    int64_t off = 0;
-    char* base = static_cast<char*>(dw_row(p, r, &off));
-    if (base == nullptr) continue;
-    uint4* q = reinterpret_cast<uint4*>(base + off * (p.dw_bf16 ? 2 : 4));
-    for (int c = first; c < vecs; c += 32) __stcs(q + c, make_uint4(0u, 0u, 0u, 0u));
+// Writes zeros to the first early_words * 32 rows, shared among `ctas` CTAs of kSortThreads; they leave the L2
+// first, since nothing here reads them again.
+__device__ __forceinline__ void zero_early(const EmbeddingGradParams& p, uint32_t cta, uint32_t ctas) {
+  const int64_t vecs = int64_t(p.H) * (p.dw_bf16 ? 2 : 4) / 16;  // 16-byte pieces of a row
+  for (int k = 0; k < p.n_shards; ++k) {
+    const int64_t a = p.row_start[k], b = min(int64_t(p.row_start[k + 1]), int64_t(p.early_words) * 32);
+    uint4* q = static_cast<uint4*>(p.dW[k]);
+    for (int64_t i = int64_t(cta) * kSortThreads + threadIdx.x; i < (b - a) * vecs; i += int64_t(ctas) * kSortThreads)
+      __stcs(q + i, make_uint4(0u, 0u, 0u, 0u));
   }
 }
 
@@ -282,156 +279,222 @@ __device__ __forceinline__ void mark_present(const EmbeddingGradParams& p, uint3
   if (live && key < width && (first_peer || key != of_first)) atomicOr(p.present + (key >> 5), 1u << (key & 31));
 }
 
+// Most positions that are sorted by comparing each with all, a CTA for 128 of them, up to 16 CTAs; above, by
+// digits (whole calls of H = 256 over V = 1000 by rank and by digits: T = 64 6.1 and 10.6 us, 256 8.6 and 12.3,
+// 1024 12.7 and 15.6, 1500 13.9 and 16.8, 2048 16.1 and 16.4, 2560 23.7 and 17.5).
+constexpr int kRankMost = 1536;
+constexpr int kRankPositions = 128;     // of a CTA at a time
+constexpr int kRankGroups = kSortThreads / kRankPositions;  // of threads, which share the comparisons
+
+// The sort of a short batch without passes: a position goes where the number of those before it in (row,
+// position) order says, which each CTA counts for its positions from all the batch's keys. The marks are
+// cleared before, and the cluster barrier says by all.
+__device__ __forceinline__ void sort_by_rank(const EmbeddingGradParams& p, uint32_t cta, uint32_t ctas, uint32_t width) {
+  __shared__ __align__(16) uint32_t keys[(kRankMost + 127) / 128 * 128];
+  __shared__ uint32_t counts[kRankGroups][kRankPositions];
+  const int T = p.T, quads = (T + 3) / 4;
+  for (int t = threadIdx.x; t < quads * 4; t += kSortThreads) {
+    uint32_t key = 0xffffffffu;  // of no position: after all
+    if (t < T) {
+      const int id = __ldg(p.ids + t);
+      key = position_key(p, id, width);
+      if (cta == 0 && (id < -1 || id >= p.vocab_real)) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+    }
+    keys[t] = key;
+  }
+  cluster_sync();
+  const int mine = threadIdx.x % kRankPositions, group = threadIdx.x / kRankPositions;
+  const int lane = threadIdx.x & 31;
+  const uint4* keys4 = reinterpret_cast<const uint4*>(keys);
+  for (int base = int(cta) * kRankPositions; base < T; base += int(ctas) * kRankPositions) {
+    const int i = base + mine, q0 = (i - lane) / 4, q1 = min(quads, q0 + 8);  // the quads of the warp's positions
+    const uint32_t key = i < T ? keys[i] : 0u;
+    uint32_t n = 0;
+    // equal keys of earlier positions count, those of later ones do not
+#pragma unroll 4
+    for (int q = group; q < min(q0, quads); q += kRankGroups) {
+      const uint4 k = keys4[q];
+      n += uint32_t(k.x <= key) + uint32_t(k.y <= key) + uint32_t(k.z <= key) + uint32_t(k.w <= key);
+    }
+    for (int q = q0 + group; q < q1; q += kRankGroups) {
+      const uint4 k = keys4[q];
+      const int j = 4 * q;
+      n += uint32_t(k.x < key + (j < i)) + uint32_t(k.y < key + (j + 1 < i)) + uint32_t(k.z < key + (j + 2 < i)) +
+           uint32_t(k.w < key + (j + 3 < i));
+    }
+#pragma unroll 4
+    for (int q = q0 + 8 + group; q < quads; q += kRankGroups) {
+      const uint4 k = keys4[q];
+      n += uint32_t(k.x < key) + uint32_t(k.y < key) + uint32_t(k.z < key) + uint32_t(k.w < key);
+    }
+    counts[group][mine] = n;
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 1; g < kRankGroups; ++g) n += counts[g][mine];
+      if (i < T && in_bounds(n < uint32_t(T), p.err)) p.sorted[0][n] = make_uint2(key, uint32_t(i));
+      if (!p.accumulate) {
+        const uint32_t peers = __match_any_sync(0xffffffffu, i < T ? key : width);
+        if (i < T && key < width && lane == __ffs(peers) - 1) atomicOr(p.present + (key >> 5), 1u << (key & 31));
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // The first cluster sorts; the others, when overwriting, meanwhile write the zeros of the first rows.
 // Each pass: every warp counts the digits of its stretch of positions, the CTAs exchange their totals
 // through distributed shared memory, and every warp moves its positions, in order, to where their
 // digits' counts say. KEEP > 0: a lane keeps its (up to KEEP) positions, and which lanes share their
 // digits, in registers from the count to the move; KEEP = 0: the stretch is walked twice. Passes go
 // through global memory, which the L2 holds: moving them in distributed shared memory instead saved 1
-// us of a sort and nothing of a call.
+// us of a sort and nothing of a call. KEEP < 0: no passes, sort_by_rank.
 template <int KEEP>
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ EmbeddingGradParams p, int sort_ctas) {
   if (int(blockIdx.x) >= sort_ctas) {
     grid_launch_dependents();
-    for (uint32_t word = blockIdx.x - sort_ctas; word < p.early_words; word += gridDim.x - sort_ctas)
-      zero_rows<kSortWarps>(p, word * 32, 0u);
+    zero_early(p, blockIdx.x - sort_ctas, gridDim.x - sort_ctas);
     return;
   }
-  __shared__ uint32_t hist[kSortWarps][kMaxBins];
-  __shared__ uint32_t totals[kMaxBins];
-  __shared__ uint32_t bin_base[kMaxBins];
-  __shared__ uint32_t warp_sum[kSortWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const uint32_t cta = blockIdx.x, ctas = sort_ctas;  // the first cluster: the block index is the rank
   const uint32_t width = p.row_start[p.n_shards];
-  const int passes = (p.key_bits + kMaxDigit - 1) / kMaxDigit;
-  const int bits = (p.key_bits + passes - 1) / passes;
-  const uint32_t bins = 1u << bits;
-  const int64_t T = p.T, per_warp = sort_stretch(T, sort_ctas);
-  const int64_t begin = min(T, (int64_t(cta) * kSortWarps + warp) * per_warp), end = min(T, begin + per_warp);
   grid_launch_dependents();
   if (cta == 0 && tid < 2) p.n_joins[tid] = 0;
   if (!p.accumulate) {
     const uint32_t words = (width + 31) / 32;
     for (uint32_t i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) p.present[i] = 0u;
   }
-  for (int pass = 0; pass < passes; ++pass) {
-    // passes alternate between the two buffers so that the last one fills sorted[0]
-    const uint2* src = p.sorted[(passes - pass) & 1];
-    uint2* dst = p.sorted[(passes - 1 - pass) & 1];
-    const int shift = pass * bits;
-    for (int w = 0; w < kSortWarps; ++w) hist[w][tid] = 0u;
-    __syncthreads();
-    if constexpr (KEEP > 0) {
-      uint2 e[KEEP];
-      uint32_t peers[KEEP];
-#pragma unroll
-      for (int u = 0; u < KEEP; ++u) {
-        const int64_t i = begin + 32 * u + lane;
-        e[u] = make_uint2(0u, uint32_t(i));
-        if (i < end) {
-          if (pass == 0)
-            e[u].x = uint32_t(__ldg(p.ids + i));
-          else
-            e[u] = __ldcg(src + i);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < KEEP; ++u) {
-        const int64_t i = begin + 32 * u + lane;
-        if (begin + 32 * u >= end) break;
-        if (pass == 0 && i < end) {
-          const int id = int(e[u].x);
-          e[u].x = position_key(p, id, width);
-          if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
-        }
-        const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
-        peers[u] = __match_any_sync(0xffffffffu, digit);
-        if (i < end && lane == __ffs(peers[u]) - 1) hist[warp][digit] += uint32_t(__popc(peers[u]));
-        __syncwarp();
-      }
+  if constexpr (KEEP < 0) {
+    sort_by_rank(p, cta, ctas, width);
+  } else {
+    __shared__ uint32_t hist[kSortWarps][kMaxBins];
+    __shared__ uint32_t totals[kMaxBins];
+    __shared__ uint32_t bin_base[kMaxBins];
+    __shared__ uint32_t warp_sum[kSortWarps];
+    const int lane = tid & 31, warp = tid >> 5;
+    const int passes = (p.key_bits + kMaxDigit - 1) / kMaxDigit;
+    const int bits = (p.key_bits + passes - 1) / passes;
+    const uint32_t bins = 1u << bits;
+    const int64_t T = p.T, per_warp = sort_stretch(T, sort_ctas);
+    const int64_t begin = min(T, (int64_t(cta) * kSortWarps + warp) * per_warp), end = min(T, begin + per_warp);
+    for (int pass = 0; pass < passes; ++pass) {
+      // passes alternate between the two buffers so that the last one fills sorted[0]
+      const uint2* src = p.sorted[(passes - pass) & 1];
+      uint2* dst = p.sorted[(passes - 1 - pass) & 1];
+      const int shift = pass * bits;
+      for (int w = 0; w < kSortWarps; ++w) hist[w][tid] = 0u;
       __syncthreads();
-      sort_places(hist, totals, bin_base, warp_sum, cta, ctas);
-#pragma unroll
-      for (int u = 0; u < KEEP; ++u) {
-        const int64_t i = begin + 32 * u + lane;
-        if (begin + 32 * u >= end) break;
-        const uint32_t digit = (e[u].x >> shift) & (bins - 1);
-        const uint32_t before = uint32_t(__popc(peers[u] & ((1u << lane) - 1)));
-        if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers[u], before == 0, i < end);
-        uint32_t at = 0;
-        if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
-        __syncwarp();
-        if (i < end) {
-          if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
-          if (before == 0) hist[warp][digit] += uint32_t(__popc(peers[u]));
-        }
-        __syncwarp();
-      }
-    } else {
-      for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
-        uint32_t key[kSortAhead];
-#pragma unroll
-        for (int u = 0; u < kSortAhead; ++u) {
-          const int64_t i = i0 + 32 * u + lane;
-          key[u] = 0u;
-          if (i < end) key[u] = pass == 0 ? uint32_t(__ldg(p.ids + i)) : __ldcg(src + i).x;
-        }
-#pragma unroll
-        for (int u = 0; u < kSortAhead; ++u) {
-          const int64_t i = i0 + 32 * u + lane;
-          if (i0 + 32 * u >= end) break;
-          uint32_t digit = bins;
-          if (i < end) {
-            uint32_t k = key[u];
-            if (pass == 0) {
-              const int id = int(k);
-              k = position_key(p, id, width);
-              if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
-            }
-            digit = (k >> shift) & (bins - 1);
-          }
-          const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-          if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
-          __syncwarp();
-        }
-      }
-      __syncthreads();
-      sort_places(hist, totals, bin_base, warp_sum, cta, ctas);
-      for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
-        uint2 e[kSortAhead];
-#pragma unroll
-        for (int u = 0; u < kSortAhead; ++u) {
-          const int64_t i = i0 + 32 * u + lane;
+      if constexpr (KEEP > 0) {
+        uint2 e[KEEP];
+        uint32_t peers[KEEP];
+  #pragma unroll
+        for (int u = 0; u < KEEP; ++u) {
+          const int64_t i = begin + 32 * u + lane;
           e[u] = make_uint2(0u, uint32_t(i));
           if (i < end) {
             if (pass == 0)
-              e[u].x = position_key(p, __ldg(p.ids + i), width);
+              e[u].x = uint32_t(__ldg(p.ids + i));
             else
               e[u] = __ldcg(src + i);
           }
         }
-#pragma unroll
-        for (int u = 0; u < kSortAhead; ++u) {
-          const int64_t i = i0 + 32 * u + lane;
-          if (i0 + 32 * u >= end) break;
+  #pragma unroll
+        for (int u = 0; u < KEEP; ++u) {
+          const int64_t i = begin + 32 * u + lane;
+          if (begin + 32 * u >= end) break;
+          if (pass == 0 && i < end) {
+            const int id = int(e[u].x);
+            e[u].x = position_key(p, id, width);
+            if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+          }
           const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
-          const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-          const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
-          if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers, before == 0, i < end);
+          peers[u] = __match_any_sync(0xffffffffu, digit);
+          if (i < end && lane == __ffs(peers[u]) - 1) hist[warp][digit] += uint32_t(__popc(peers[u]));
+          __syncwarp();
+        }
+        __syncthreads();
+        sort_places(hist, totals, bin_base, warp_sum, cta, ctas);
+  #pragma unroll
+        for (int u = 0; u < KEEP; ++u) {
+          const int64_t i = begin + 32 * u + lane;
+          if (begin + 32 * u >= end) break;
+          const uint32_t digit = (e[u].x >> shift) & (bins - 1);
+          const uint32_t before = uint32_t(__popc(peers[u] & ((1u << lane) - 1)));
+          if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers[u], before == 0, i < end);
           uint32_t at = 0;
           if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
           __syncwarp();
           if (i < end) {
             if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
-            if (before == 0) hist[warp][digit] += uint32_t(__popc(peers));
+            if (before == 0) hist[warp][digit] += uint32_t(__popc(peers[u]));
           }
           __syncwarp();
         }
+      } else {
+        for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
+          uint32_t key[kSortAhead];
+  #pragma unroll
+          for (int u = 0; u < kSortAhead; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            key[u] = 0u;
+            if (i < end) key[u] = pass == 0 ? uint32_t(__ldg(p.ids + i)) : __ldcg(src + i).x;
+          }
+  #pragma unroll
+          for (int u = 0; u < kSortAhead; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            if (i0 + 32 * u >= end) break;
+            uint32_t digit = bins;
+            if (i < end) {
+              uint32_t k = key[u];
+              if (pass == 0) {
+                const int id = int(k);
+                k = position_key(p, id, width);
+                if (id < -1 || id >= p.vocab_real) record_error(p.err, LP_ERR_TOKEN_OUT_OF_RANGE);
+              }
+              digit = (k >> shift) & (bins - 1);
+            }
+            const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+            if (i < end && lane == __ffs(peers) - 1) hist[warp][digit] += uint32_t(__popc(peers));
+            __syncwarp();
+          }
+        }
+        __syncthreads();
+        sort_places(hist, totals, bin_base, warp_sum, cta, ctas);
+        for (int64_t i0 = begin; i0 < end; i0 += 32 * kSortAhead) {
+          uint2 e[kSortAhead];
+  #pragma unroll
+          for (int u = 0; u < kSortAhead; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            e[u] = make_uint2(0u, uint32_t(i));
+            if (i < end) {
+              if (pass == 0)
+                e[u].x = position_key(p, __ldg(p.ids + i), width);
+              else
+                e[u] = __ldcg(src + i);
+            }
+          }
+  #pragma unroll
+          for (int u = 0; u < kSortAhead; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            if (i0 + 32 * u >= end) break;
+            const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
+            const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+            const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
+            if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers, before == 0, i < end);
+            uint32_t at = 0;
+            if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
+            __syncwarp();
+            if (i < end) {
+              if (in_bounds(int64_t(at) < T, p.err)) dst[at] = e[u];
+              if (before == 0) hist[warp][digit] += uint32_t(__popc(peers));
+            }
+            __syncwarp();
+          }
+        }
       }
-    }
-    cluster_sync();  // the pass's output and the totals' readers
-  }
+      cluster_sync();  // the pass's output and the totals' readers
+    }  }
 }
 
 // ------------------------------------------------------------------ gradient: sums
@@ -501,6 +564,11 @@ __device__ __forceinline__ void finish_piece(const EmbeddingGradParams& p, float
       *reinterpret_cast<float4*>(piece + c) = make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
   }
 }
+
+// Positions of a batch up to which no run is cut in pieces, since a warp sees that far from its chunk's start,
+// and no joins are launched (T = 64: 5.7 us, 6.6 with them, and 2.5 us less on the host; all of one id
+// 10.2 us, 9.4 with them).
+constexpr int kWhole = 64;
 
 constexpr int kAhead = 4;  // rows of a batch; a warp has two batches in flight
 
@@ -602,6 +670,24 @@ __device__ __forceinline__ int64_t last_chunk_of(const EmbeddingGradParams& p, u
   return lo;
 }
 
+// Writes zeros to the rows of [r0, r0 + 32) whose bit in `skip` is clear, by all warps of a CTA.
+__device__ __forceinline__ void zero_rows(const EmbeddingGradParams& p, uint32_t r0, uint32_t skip) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vecs = p.H * (p.dw_bf16 ? 2 : 4) / 16;           // 16-byte pieces of a row
+  const int per = vecs < 32 ? 32 / vecs : 1;                 // rows of a warp at a time
+  const int row = vecs < 32 ? lane / vecs : 0, first = vecs < 32 ? lane % vecs : lane;
+  if (row >= per) return;
+  for (int i = warp * per + row; i < 32; i += kSegWarps * per) {
+    const uint32_t r = r0 + i;
+    if (((skip >> i) & 1u) != 0u || r >= p.row_start[p.n_shards]) continue;
+    int64_t off = 0;
+    char* base = static_cast<char*>(dw_row(p, r, &off));
+    if (base == nullptr) continue;
+    uint4* q = reinterpret_cast<uint4*>(base + off * (p.dw_bf16 ? 2 : 4));
+    for (int c = first; c < vecs; c += 32) __stcs(q + c, make_uint4(0u, 0u, 0u, 0u));
+  }
+}
+
 template <bool DB, bool WB>
 __global__ void __launch_bounds__(kSegWarps * 32, 6) segment_kernel(const __grid_constant__ EmbeddingGradParams p,
                                                                  int seg_ctas) {
@@ -612,7 +698,7 @@ __global__ void __launch_bounds__(kSegWarps * 32, 6) segment_kernel(const __grid
   grid_dependency_wait();
   if (int(blockIdx.x) >= seg_ctas) {  // zeros: 32 rows a CTA
     const uint32_t word = p.early_words + blockIdx.x - seg_ctas;
-    zero_rows<kSegWarps>(p, word * 32, p.present[word]);
+    zero_rows(p, word * 32, p.present[word]);
     return;
   }
   const uint32_t slabs = uint32_t(p.H + kSlab - 1) / kSlab;
@@ -635,15 +721,16 @@ __global__ void __launch_bounds__(kSegWarps * 32, 6) segment_kernel(const __grid
   const int valid = __popc(__ballot_sync(0xffffffffu, own.x < width));
   const uint32_t left = __shfl_up_sync(0xffffffffu, own.x, 1);
   const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 ? eq_prev == 0u : own.x != left);
+  const int most = T <= kWhole ? kWhole : kChunk;  // positions of a run that is not cut
   // this warp's stretches: the piece of a long run the chunk begins inside, the piece of one that
   // begins here and goes on, and the short runs that begin in its part
   int from[3] = {0, 0, 0}, to[3] = {0, 0, 0};
-  if (eq_prev != 0u && begin == 0 && __popc(eq_prev) + n_first + (n_first == 32 ? next_last : 0) > kChunk) to[0] = n_first;
+  if (eq_prev != 0u && begin == 0 && __popc(eq_prev) + n_first + (n_first == 32 ? next_last : 0) > most) to[0] = n_first;
   if (eq_prev == 0u || n_first < 32) {
     int limit = valid, stop = valid;  // the last short run begins before limit and ends at stop
     if (valid == 32) {
       stop = 32 + next_last;
-      if (n_last + next_last > kChunk) {
+      if (n_last + next_last > most) {
         limit = stop = 32 - n_last;
         if (limit / kPart * kPart == begin) {
           from[1] = limit;
@@ -764,7 +851,8 @@ bool wide_cluster_fits() {
     cfg.gridDim = dim3(kSortCtas, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
     int active = 0;
-    const bool fits = cudaFuncSetAttribute(sort_kernel<0>, kNonPortable, 1) == cudaSuccess &&
+    const bool fits = cudaFuncSetAttribute(sort_kernel<-1>, kNonPortable, 1) == cudaSuccess &&
+                      cudaFuncSetAttribute(sort_kernel<0>, kNonPortable, 1) == cudaSuccess &&
                       cudaFuncSetAttribute(sort_kernel<kKeepFew>, kNonPortable, 1) == cudaSuccess &&
                       cudaFuncSetAttribute(sort_kernel<kKeepMany>, kNonPortable, 1) == cudaSuccess &&
                       cudaOccupancyMaxActiveClusters(&active, sort_kernel<kKeepMany>, &cfg) == cudaSuccess && active > 0;
@@ -776,15 +864,21 @@ bool wide_cluster_fits() {
 }
 
 int sort_ctas(int64_t T) {
+  if (T <= kRankMost) {
+    int ctas = 1;
+    while (ctas * kRankPositions < T && (ctas < 8 || (ctas < kSortCtas && wide_cluster_fits()))) ctas *= 2;
+    return ctas;
+  }
   if (T >= kSortCtas * kSortMinPerCta16 && wide_cluster_fits()) return kSortCtas;
   int ctas = 8;
   while (ctas > 1 && T < ctas * kSortMinPerCta) ctas /= 2;
   return ctas;
 }
 
-// Rows whose zeros the sort kernel writes, in words of 32: 48 MB, about what the rest of the GPU can
-// write while one cluster sorts (T = 4096, H = 4096, V = 151936: 350 us, 357 without; 96 MB: 360, since
-// these rows are zeroed whether a position names them or not). Asking the L2 for 32 to 128 MB of dY at that
+// Rows whose zeros the sort kernel writes, in words of 32: 56 MB, about what other SMs can write while
+// one cluster sorts (T = 4096, H = 4096, V = 151936: 346 us, 349 with 24 MB, 347 with 80; two calls of T = 16384:
+// 117.5, 119.7 and 116.9; T = 65537: 92.0, 92.1 and 92.4). More is not taken, since these rows are zeroed
+// whether a position names them or not. Asking the L2 for 32 to 128 MB of dY at that
 // time gains nothing (2 calls of T = 16384: 120.5 us, 121.2 to 123.9 with).
 uint32_t early_words(const EmbeddingGradParams& p) {
   if (p.accumulate) return 0u;
@@ -796,8 +890,9 @@ uint32_t early_words(const EmbeddingGradParams& p) {
 cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
   const int ctas = sort_ctas(p.T);
   const int64_t stretch = sort_stretch(p.T, ctas);
-  // zeros: whole clusters, one CTA per SM at most
-  const int64_t zero = p.early_words < 144u ? p.early_words : 144u;
+  // zeros: whole clusters
+  const int64_t bytes = int64_t(p.early_words) * 32 * p.H * (p.dw_bf16 ? 2 : 4);
+  const int64_t zero = bytes < kZeroCtas * kZeroBytes ? (bytes + kZeroBytes - 1) / kZeroBytes : kZeroCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas + (zero + ctas - 1) / ctas * ctas), 1, 1);
   cfg.blockDim = dim3(kSortThreads, 1, 1);
@@ -809,7 +904,8 @@ cudaError_t launch_sort(const EmbeddingGradParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = stretch <= 32 * kKeepFew    ? sort_kernel<kKeepFew>
+  const auto kernel = p.T <= kRankMost            ? sort_kernel<-1>
+                      : stretch <= 32 * kKeepFew  ? sort_kernel<kKeepFew>
                       : stretch <= 32 * kKeepMany ? sort_kernel<kKeepMany>
                                                   : sort_kernel<0>;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, ctas);
@@ -832,7 +928,7 @@ cudaError_t launch_sums(const EmbeddingGradParams& p, cudaStream_t s) {
   cfg.gridDim = dim3(unsigned(seg + zero), 1, 1);
   cfg.blockDim = dim3(kSegWarps * 32, 1, 1);
   cudaError_t e = cudaLaunchKernelEx(&cfg, segment_kernel<DB, WB>, p, int(seg));
-  if (e == cudaSuccess && p.T > kChunk) {
+  if (e == cudaSuccess && p.T > kWhole) {
     cfg.gridDim = dim3(kJoinCtas, 1, 1);
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     e = cudaLaunchKernelEx(&cfg, join_kernel<WB>, p);
@@ -869,7 +965,7 @@ cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16,
 size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width) {
   const size_t chunks = size_t(chunk_count(T));
   return 256 + 2 * up256(size_t(T) * sizeof(uint2)) + up256(2 * sizeof(int32_t)) + 2 * up256(chunks * sizeof(int4)) +
-         up256(size_t((width + 31) / 32) * sizeof(uint32_t)) + (T > kChunk ? chunks * 2 * size_t(H) * sizeof(float) : 0);
+         up256(size_t((width + 31) / 32) * sizeof(uint32_t)) + (T > kWhole ? chunks * 2 * size_t(H) * sizeof(float) : 0);
 }
 
 void embedding_backward_carve(EmbeddingGradParams* p, void* workspace, int64_t width) {

@@ -140,6 +140,32 @@ def test_gradient(lp, grad, dw, kind, T, H, part):
     assert lp.lp_get_device_error() == 0
 
 
+@pytest.mark.parametrize("kind", ["zipf", "hot", "one", "runs", "unused"])
+@pytest.mark.parametrize("T", [32, 63, 64, 65, 96, 127, 128, 129, 257, 513, 1024, 1025, 1535, 1536, 1537, 2049])
+@pytest.mark.parametrize("acc", [False, True])
+def test_gradient_where_the_method_changes(lp, kind, T, acc):
+    """Around the batches from which runs are cut, and from which positions are sorted by digits."""
+    import torch
+    real, bounds, H = 997, [0, 200, 200, 600, 1024], 264
+    rs = np.random.RandomState(T)
+    ids = _ids(kind, T, real, rs)
+    dY = _rand((T, H), torch.float32, T + 1)
+    part, i = _part(lp, real, bounds), dev_i32(ids)
+    want, mag, n = train.embedding_backward(ids, dY.double().cpu().numpy(), 0, bounds[-1], 0.75)
+    fresh = lp.lp_embedding_backward(i, dY, part, scale=0.75,
+                                     dW=[torch.full((b - a, H), 7.0, device="cuda") for a, b in zip(bounds[:-1], bounds[1:])])
+    _check_gradient(torch.cat(fresh), False, want, mag, n)
+    if acc:
+        base = [_rand((b - a, H), torch.float32, a) for a, b in zip(bounds[:-1], bounds[1:])]
+        dW = [b.clone() for b in base]
+        lp.lp_embedding_backward(i, dY, part, scale=0.75, accumulate=True, dW=dW)
+        assert all(torch.equal(d, b + f) for d, b, f in zip(dW, base, fresh))
+    else:
+        again = lp.lp_embedding_backward(i, dY, part, scale=0.75)
+        assert all(torch.equal(x, y) for x, y in zip(again, fresh) if x is not None)
+    assert lp.lp_get_device_error() == 0
+
+
 @pytest.mark.parametrize("T,H,grad,dw,kind", [(20011, 16, "bf16", "f32", "zipf"), (70001, 8, "f32", "bf16", "hot"),
                                               (16384, 264, "bf16", "f32", "runs"), (5000, 40, "bf16", "bf16", "zipf"),
                                               (100003, 8, "bf16", "f32", "zipf")])
