@@ -302,7 +302,10 @@ __device__ __forceinline__ void sort_by_rank(const EmbeddingGradParams& p, uint3
     }
     keys[t] = key;
   }
-  cluster_sync();
+  if (ctas > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   const int mine = threadIdx.x % kRankPositions, group = threadIdx.x / kRankPositions;
   const int lane = threadIdx.x & 31;
   const uint4* keys4 = reinterpret_cast<const uint4*>(keys);
