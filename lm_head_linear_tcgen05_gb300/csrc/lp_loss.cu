@@ -2,7 +2,7 @@
 //
 // Both are sums over tokens whose weights need a sum over all of them first (the kept tokens, the
 // counted sequences or pairs), so each runs in stages over the tokens:
-//   policy       count   kept tokens of every block of 512
+//   policy       count   kept tokens of every block of 512 (long batches)
 //                stat    kept tokens of every sequence (whole blocks plus the two ragged ends), totals
 //                tokens  every token's term, gradients, partial sums
 //                final   the metrics
@@ -16,7 +16,7 @@
 // Bounds: a long policy loss by memory and issue (4 M tokens with KL and entropy, 122 MB: 29.6 us, 4.1
 // TB/s, of which the stages before the tokens are 6 us and the tokens' stage issues some 60 instructions
 // a token); a long preference loss by the dependent steps of its three stages (2 M tokens, 27 MB: 18.4
-// us); short ones by those of their one launch (4096 tokens: 8 us policy, 9 us preference). So loads are
+// us); short ones by those of their one launch (4096 tokens: 6.6 us policy, 9 us preference). So loads are
 // 16 bytes a lane and issued ahead of their use, what does not depend on an earlier kernel is loaded
 // before waiting for it, and a warp searches the offsets together, 32 probes a step.
 // Token terms and the sums of a thread, warp or CTA are fp32. Sums over tiles and pairs carry their
@@ -345,18 +345,19 @@ __device__ __forceinline__ void policy_count(const PolicyParams& p, const Policy
 }
 
 // Kept tokens of [a, b) by one warp, from the counts of the whole blocks in it and the ragged ends.
-template <bool ONE>
 __device__ __forceinline__ int count_kept_blocks(const uint8_t* mask, const int32_t* block_kept, int a, int b) {
   const int b0 = int(ceil_div(a, kCountBlock)), b1 = b / kCountBlock;  // whole blocks [b0, b1)
   if (b0 >= b1) return count_kept(mask, a, b);
   int c = 0;
 #pragma unroll 8
-  for (int i = b0 + int(threadIdx.x & 31); i < b1; i += 32) c += from_stage<ONE>(block_kept + i);
+  for (int i = b0 + int(threadIdx.x & 31); i < b1; i += 32) c += __ldcg(block_kept + i);
   return warp_sum_int(c) + count_kept(mask, a, b0 * kCountBlock) + count_kept(mask, b1 * kCountBlock, b);
 }
 
 constexpr int kLaneTokens = 64;  // most tokens of a sequence that a lane counts (65536 of 16: 26 us, 33 without)
 
+// ONE: of short batches, whose masks a warp counts itself; the blocks' counts and the barrier behind them cost
+// more (4096 tokens in 8 sequences: 6.6 us, 7.8 with them; 16384 in 64: 9.0 and 9.8; in one: 10.2 and 9.4).
 template <bool ONE>
 __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyWs& ws, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
@@ -366,10 +367,13 @@ __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyW
   if (p.n_seqs == 0) {
     if (mask == nullptr) {
       t.kept = gw == 0 ? p.T : 0;
+    } else if constexpr (ONE) {
+      const int per = int(ceil_div(p.T, n_warps));
+      t.kept = count_kept(mask, min(p.T, gw * per), min(p.T, (gw + 1) * per));
     } else {
-      const int64_t blocks = ceil_div(p.T, kCountBlock);
+      const int64_t n = ceil_div(p.T, kCountBlock);
       int c = 0;
-      for (int64_t i = int64_t(gw) * 32 + lane; i < blocks; i += int64_t(n_warps) * 32) c += from_stage<ONE>(ws.block_kept + i);
+      for (int64_t i = int64_t(gw) * 32 + lane; i < n; i += int64_t(n_warps) * 32) c += __ldcg(ws.block_kept + i);
       t.kept = warp_sum_int(c);
     }
   } else {
@@ -389,8 +393,8 @@ __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyW
       }
       for (uint32_t left = __ballot_sync(0xffffffffu, !alone); left != 0u; left &= left - 1u) {
         const int who = __ffs(left) - 1;
-        const int c = count_kept_blocks<ONE>(mask, ws.block_kept, __shfl_sync(0xffffffffu, a, who),
-                                             __shfl_sync(0xffffffffu, b, who));
+        const int from = __shfl_sync(0xffffffffu, a, who), to = __shfl_sync(0xffffffffu, b, who);
+        const int c = ONE ? count_kept(mask, from, to) : count_kept_blocks(mask, ws.block_kept, from, to);
         if (lane == who) n = c;
       }
       if (mine) ws.seq_kept[s] = n;
@@ -598,10 +602,6 @@ __global__ void __launch_bounds__(kThreads) policy_cluster_kernel(const __grid_c
   size_t bytes;
   const PolicyWs ws = policy_carve(first_cta_shared(stage), 16, p.T, p.n_seqs, ctas, ctas, &bytes);
   cluster_sync();  // the first CTA has started
-  if (p.in.mask != nullptr) {
-    policy_count(p, ws, cta, ctas);
-    cluster_sync();
-  }
   policy_stat<true>(p, ws, cta, ctas);
   cluster_sync();
   policy_tokens<KL, BY_SEQ, true>(p, ws, cta, ctas, ctas);
