@@ -39,13 +39,16 @@ constexpr int kTokenCtas = 456;           // most CTAs of the policy's tokens: t
 constexpr int kGradCtas = 912;            // most CTAs of the preference gradient: six to an SM
 constexpr int kPrefTile = 256;            // tokens of a warp, eight a lane
 // The one-launch form takes batches of up to this many tokens and sequences. On the GPU it and the
-// stages as launches take the same time there (16384 tokens: 12 us either way) and it loses above
-// (65536 tokens: 22 and 14 us); a launch less is some 3 us less on the host. What its stages pass on
-// stays in the first CTA's shared memory (12 bytes a sequence and 48 a tile at most, 27 KB), so it needs no
-// workspace either.
+// stages as launches take the same time there (16384 to 20000 tokens: 9 to 11 us either way) and it loses
+// above (49152 tokens: 14 to 18 and 10 us); a launch less is some 3 us less on the host. What its stages pass
+// on stays in the first CTA's shared memory (14 KB at most), so it needs no workspace either.
 constexpr int kCluster = 8;
 constexpr int64_t kFusedTokens = 16384;
 constexpr int64_t kFusedSeqs = 2048;
+// and a preference loss of up to this many answers, whose pairs eight CTAs work off more slowly (2048 to 16384
+// tokens in one and in three launches, 512 answers: 12.3 to 14.7 and 10.2 to 11.3 us, 1024: 14.3 to 16.5 and
+// 10.2 to 13.1, 2048: 18 to 22 and 10.7 to 16; one saves 9 us on the host).
+constexpr int64_t kFusedAnswers = 1024;
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -646,9 +649,9 @@ __host__ __device__ inline PrefWs pref_carve(void* base, size_t align, int64_t T
   return r;
 }
 
-// Sequences of a tile from which each gets a lane (7522 tokens in 1368: 22 us, 34 walked by the warp;
-// 262144 in 16384: 22.6 and 23.4; with 12 in a tile the walk is faster).
-constexpr int kPrefMany = 24;
+// Sequences of a tile from which each gets a lane (1 M tokens in sequences of 24, 16 and 12: 26.4, 29.1 and 31.6
+// us, 28.4, 33.2 and 42.1 walked by the warp; of 32: 29.9 and 23.8).
+constexpr int kPrefMany = 10;
 
 __device__ __forceinline__ void pref_sum_tile(const PreferenceParams& p, const PrefWs& ws, int64_t tile) {
   const int lane = threadIdx.x & 31;
@@ -964,10 +967,16 @@ __global__ void __launch_bounds__(kThreads) pref_cluster_kernel(const __grid_con
 
 int at_most(int64_t n, int most) { return int(n < 1 ? 1 : n < most ? n : most); }
 
-bool one_launch(int64_t T, int64_t n_seqs) { return T <= kFusedTokens && n_seqs <= kFusedSeqs; }
+bool policy_one_launch(int64_t T, int64_t n_seqs) { return T <= kFusedTokens && n_seqs <= kFusedSeqs; }
+bool pref_one_launch(int64_t T, int64_t n_seqs) { return T <= kFusedTokens && n_seqs <= kFusedAnswers; }
 
 // CTAs of the one-launch form, and the shared memory its stages pass their results in
 int cluster_ctas(int64_t T) { return at_most(ceil_div(T, kTokenTile), kCluster); }
+// and for the pairs, 16 of a CTA at a time (2048 tokens in 2048 answers: 21.7 us, 45.5 by tokens alone)
+int pref_cluster_ctas(int64_t T, int64_t n_seqs) {
+  const int64_t by_tokens = ceil_div(T, kTokenTile), by_pairs = ceil_div(n_seqs, 4 * kWarps);
+  return at_most(by_tokens > by_pairs ? by_tokens : by_pairs, kCluster);
+}
 
 size_t policy_stage_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
@@ -977,7 +986,7 @@ size_t policy_stage_bytes(int64_t T, int64_t n_seqs) {
 
 size_t pref_stage_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
-  pref_carve(nullptr, 16, T, n_seqs, cluster_ctas(T), &bytes);
+  pref_carve(nullptr, 16, T, n_seqs, pref_cluster_ctas(T, n_seqs), &bytes);
   return bytes;
 }
 
@@ -1014,13 +1023,13 @@ bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 size_t policy_ws_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
-  if (!one_launch(T, n_seqs)) policy_carve(nullptr, 256, T, n_seqs, kStatCtas, kTokenCtas, &bytes);
+  if (!policy_one_launch(T, n_seqs)) policy_carve(nullptr, 256, T, n_seqs, kStatCtas, kTokenCtas, &bytes);
   return bytes;
 }
 
 size_t preference_ws_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
-  if (!one_launch(T, n_seqs)) pref_carve(nullptr, 256, T, n_seqs, kStatCtas, &bytes);
+  if (!pref_one_launch(T, n_seqs)) pref_carve(nullptr, 256, T, n_seqs, kStatCtas, &bytes);
   return bytes;
 }
 
@@ -1028,7 +1037,7 @@ namespace {
 
 template <int KL, bool BY_SEQ>
 cudaError_t launch_policy(const PolicyParams& p, cudaStream_t s) {
-  if (one_launch(p.T, p.n_seqs))
+  if (policy_one_launch(p.T, p.n_seqs))
     return launch(policy_cluster_kernel<KL, BY_SEQ>, cluster_ctas(p.T), true, false, policy_stage_bytes(p.T, p.n_seqs), s,
                   p);
   size_t bytes = 0;
@@ -1068,8 +1077,8 @@ cudaError_t launch_preference_loss(const PreferenceParams& params, cudaStream_t 
   PreferenceParams p = params;
   const int64_t n_seqs = 2 * int64_t(p.n_pairs);
   p.vec = aligned_to(p.in.mask, 4) && aligned_to(p.out.grad_logp, 16);
-  if (one_launch(p.T, n_seqs))
-    return launch(pref_cluster_kernel, cluster_ctas(p.T), true, false, pref_stage_bytes(p.T, n_seqs), s, p);
+  if (pref_one_launch(p.T, n_seqs))
+    return launch(pref_cluster_kernel, pref_cluster_ctas(p.T, n_seqs), true, false, pref_stage_bytes(p.T, n_seqs), s, p);
   size_t bytes = 0;
   const PrefWs ws = pref_carve(p.workspace, 256, p.T, n_seqs, kStatCtas, &bytes);
   const int pair = at_most(ceil_div(p.n_pairs, 2 * kWarps), kStatCtas);

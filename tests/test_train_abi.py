@@ -81,7 +81,7 @@ def test_workspace_sizes(lp):
         assert lp.lib().lp_workspace_size(op, 10, 64, ctypes.byref(cp)) == 0
         assert 0 < lp.lp_loss_workspace_size(op, 10 ** 5, 2) <= lp.lp_loss_workspace_size(op, 10 ** 6, 1000)
         # short batches run in one launch, which needs none
-        assert lp.lp_loss_workspace_size(op, 16384, 2048) == 0
+        assert lp.lp_loss_workspace_size(op, 16384, 1024) == 0
         assert lp.lp_loss_workspace_size(op, 16385, 2) > 0 and lp.lp_loss_workspace_size(op, 16384, 2050) > 0
         assert lp.lp_loss_workspace_size(op, 0, 2) == 0 and lp.lp_loss_workspace_size(op, -1, 2) == 0
         assert lp.lp_loss_workspace_size(op, 10, -1) == 0
