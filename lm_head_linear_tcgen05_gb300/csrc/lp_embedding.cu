@@ -127,14 +127,14 @@ __device__ __forceinline__ void put8(void* base, int64_t off, const float (&f)[8
 constexpr int kLookupWarps = 4;
 
 // A CTA takes `rows` consecutive rows (ROWS of a warp at a time, their loads in flight together)
-// by kLookupWarps * 32 lanes of 8 columns.
+// by kLookupWarps * 32 lanes of 8 columns; rows of up to 128 columns share a warp, `lanes` of it each.
 template <bool WB, bool YB, int ROWS>
 __global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __grid_constant__ EmbeddingParams p,
-                                                                      int warps_per_row) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = int(blockIdx.y * warps_per_row + (warp & (warps_per_row - 1))) * kSlab + lane * 8;
-  const int rows = kLookupWarps / warps_per_row;  // rows of the CTA at a time
-  const int t0 = int(blockIdx.x) * rows * ROWS + warp / warps_per_row;
+                                                                      int warps_per_row, int lanes, int rows) {
+  // powers of two; part: which `lanes` of the CTA
+  const int lane = threadIdx.x & (lanes - 1), part = int(threadIdx.x) >> (__ffs(lanes) - 1);
+  const int col = int(blockIdx.y * warps_per_row + (part & (warps_per_row - 1))) * kSlab + lane * 8;
+  const int t0 = int(blockIdx.x) * rows * ROWS + (part >> (__ffs(warps_per_row) - 1));  // rows: of the CTA at a time
   int id[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) id[r] = t0 + r * rows < p.T ? __ldg(p.ids + t0 + r * rows) : -1;
@@ -272,13 +272,6 @@ __device__ __forceinline__ void sort_places(uint32_t (&hist)[kSortWarps][kMaxBin
   __syncthreads();
 }
 
-// Marks the row of each lane's key; a lane whose first peer has its row leaves the mark to that one.
-__device__ __forceinline__ void mark_present(const EmbeddingGradParams& p, uint32_t key, uint32_t width, uint32_t peers,
-                                             bool first_peer, bool live) {
-  const uint32_t of_first = __shfl_sync(0xffffffffu, key, __ffs(peers) - 1);
-  if (live && key < width && (first_peer || key != of_first)) atomicOr(p.present + (key >> 5), 1u << (key & 31));
-}
-
 // Most positions that are sorted by comparing each with all, a CTA for 128 of them, up to 16 CTAs; above, by
 // digits (whole calls of H = 256 over V = 1000 by rank and by digits: T = 64 6.1 and 10.6 us, 256 8.6 and 12.3,
 // 1024 12.7 and 15.6, 1500 13.9 and 16.8, 2048 16.1 and 16.4, 2560 23.7 and 17.5).
@@ -342,6 +335,18 @@ __device__ __forceinline__ void sort_by_rank(const EmbeddingGradParams& p, uint3
       }
     }
     __syncthreads();
+  }
+}
+
+// Marks the rows named by the sorted positions [begin, end) of a warp: one mark a row, by its first position.
+// (Marking while counting, by every position but those next to an equal one, cost 20 us of a call of T =
+// 100000 over V = 1000.)
+__device__ __forceinline__ void mark_rows(const EmbeddingGradParams& p, int64_t begin, int64_t end, uint32_t width) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int64_t i = begin + lane; i < end; i += 32) {
+    const uint32_t key = __ldcg(&p.sorted[0][i].x), prev = i > 0 ? __ldcg(&p.sorted[0][i - 1].x) : width;
+    if (key < width && key != prev) atomicOr(p.present + (key >> 5), 1u << (key & 31));
   }
 }
 
@@ -424,7 +429,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
           if (begin + 32 * u >= end) break;
           const uint32_t digit = (e[u].x >> shift) & (bins - 1);
           const uint32_t before = uint32_t(__popc(peers[u] & ((1u << lane) - 1)));
-          if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers[u], before == 0, i < end);
           uint32_t at = 0;
           if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
           __syncwarp();
@@ -484,7 +488,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
             const uint32_t digit = i < end ? (e[u].x >> shift) & (bins - 1) : bins;
             const uint32_t peers = __match_any_sync(0xffffffffu, digit);
             const uint32_t before = uint32_t(__popc(peers & ((1u << lane) - 1)));
-            if (pass == 0 && !p.accumulate) mark_present(p, e[u].x, width, peers, before == 0, i < end);
             uint32_t at = 0;
             if (i < end) at = bin_base[digit] + hist[warp][digit] + before;
             __syncwarp();
@@ -947,14 +950,17 @@ namespace {
 template <bool WB, bool YB>
 cudaError_t launch_lookup(const EmbeddingParams& p, cudaStream_t s) {
   const int slabs = (p.H + kSlab - 1) / kSlab;
-  const int per_row = slabs % 4 == 0 ? 4 : slabs % 2 == 0 ? 2 : 1, rows = kLookupWarps / per_row;
+  const int per_row = slabs % 4 == 0 ? 4 : slabs % 2 == 0 ? 2 : 1;
+  int lanes = 32;
+  while (lanes > 1 && lanes * 4 >= p.H) lanes /= 2;
+  const int rows = kLookupWarps * 32 / lanes / per_row;
   const unsigned y = unsigned((slabs + per_row - 1) / per_row);
   // Four rows a warp, in flight together, once that leaves every SM its full 64 warps (8192 rows of H =
   // 4096: 19.7 us, 24.2 with one); below, one row a warp (64 rows: 2.05 us, 2.46 with four).
-  if (int64_t(p.T) * slabs >= 4 * 64 * 152)
-    embedding_kernel<WB, YB, 4><<<dim3(unsigned((p.T + rows * 4 - 1) / (rows * 4)), y), kLookupWarps * 32, 0, s>>>(p, per_row);
+  if (int64_t(p.T) * slabs * lanes >= 4 * 64 * 152 * 32)
+    embedding_kernel<WB, YB, 4><<<dim3(unsigned((p.T + rows * 4 - 1) / (rows * 4)), y), kLookupWarps * 32, 0, s>>>(p, per_row, lanes, rows);
   else
-    embedding_kernel<WB, YB, 1><<<dim3(unsigned((p.T + rows - 1) / rows), y), kLookupWarps * 32, 0, s>>>(p, per_row);
+    embedding_kernel<WB, YB, 1><<<dim3(unsigned((p.T + rows - 1) / rows), y), kLookupWarps * 32, 0, s>>>(p, per_row, lanes, rows);
   return cudaGetLastError();
 }
 

@@ -67,6 +67,21 @@ def test_lookup(lp, table, out, T, H, part):
     assert lp.lp_get_device_error() == 0
 
 
+@pytest.mark.parametrize("H", [8, 16, 24, 32, 40, 64, 120, 128, 136])
+@pytest.mark.parametrize("T", [1, 3, 127, 1000, 100003, 1250007])
+def test_lookup_of_few_columns(lp, H, T):
+    import torch
+    V = 5000
+    W = _rand((V, H), torch.bfloat16, H)
+    ids = np.random.RandomState(T).randint(-1, V, T)
+    i = dev_i32(ids)
+    buf = torch.full((T + 2, H), 3.0, device="cuda")
+    y = lp.lp_embedding(i, [W], _part(lp, V, [0, V]), scale=1.5, out=buf[1:T + 1])
+    want = torch.where((i >= 0)[:, None], W[i.long().clamp(min=0)].float() * 1.5, 0.0)
+    assert torch.equal(y, want) and bool((buf[0] == 3).all()) and bool((buf[T + 1] == 3).all())
+    assert lp.lp_get_device_error() == 0
+
+
 def test_lookup_rank_local_strided_and_refused_ids(lp):
     import torch
     real, H = 1000, 136
