@@ -197,6 +197,26 @@ def test_gradient_of_long_batches(lp, T, H, grad, dw, kind):
     assert lp.lp_get_device_error() == 0
 
 
+@pytest.mark.parametrize("kind", ["spread", "dense"])
+@pytest.mark.parametrize("T", [1, 60, 600, 1537, 2000, 20000, 40000, 98304, 100000])
+def test_gradient_of_large_tables(lp, kind, T):
+    """A table of 300 MB, most of whose rows get zeros according to the marks of the named ones, over every method
+    of sorting. Whole numbers, so that every order of summation gives the same."""
+    import torch
+    V, H = 1200000, 64
+    rs = np.random.RandomState(T)
+    ids = rs.randint(-1, V, T) if kind == "spread" else V - 1 - rs.randint(0, 3 * T, T)
+    ids[rs.rand(T) < 0.05] = V - 3
+    dY = torch.from_numpy(rs.randint(-8, 9, (T, H)).astype(np.float32)).cuda()
+    dW = [torch.full((500000, H), 7.0, device="cuda"), torch.full((V - 500000, H), 7.0, device="cuda")]
+    i = dev_i32(ids)
+    lp.lp_embedding_backward(i, dY, _part(lp, V, [0, 500000, V]), scale=2.0, dW=dW)
+    used = (i >= 0)[:, None]
+    want = torch.zeros((V, H), device="cuda").index_add_(0, i.long().clamp(min=0), torch.where(used, dY * 2, 0.0))
+    assert torch.equal(torch.cat(dW), want)
+    assert lp.lp_get_device_error() == 0
+
+
 @pytest.mark.parametrize("kind", ["zipf", "hot", "runs"])
 def test_gradient_accumulates_one_add_per_element(lp, kind):
     import torch
