@@ -1,8 +1,8 @@
 // lp_embedding.cu - embedding lookup with scaling, and its gradient by sorted tokens.
 //
 // Forward: Y[t] = scale W[id_t]. A copy, bound by memory: 8192 rows of H = 4096 in bf16 from four
-// shards take 18.9 us, 7.1 TB/s of rows read and written (1.05 of the measured copy rate); 64 rows,
-// bound by a launch and two dependent loads, 2.3 us.
+// shards take 18.0 us, 7.4 TB/s of rows read and written (1.1 of the measured copy rate, the L2 holding some);
+// 64 rows, bound by a launch and two dependent loads, 2.1 us.
 //
 // Gradient: dW[v] = scale sum_{t: id_t = v} dY[t], bound by memory too: every row of dY read once,
 // every row of dW written (or, accumulating, the named ones read and written). Adding rows into dW with
@@ -27,8 +27,8 @@
 //                   consecutive pieces, and their sums are added in the order of the groups. Bound by
 //                   its dependent loads: 7 us where 16384 positions leave some 50 long runs.
 // Each launch is the programmatic dependent of the one before. Whole calls: T = 4096, H = 4096 over V =
-// 151936, fp32 (2.5 GB, nearly all of it zeros to write) 346 us, 7.2 TB/s; T = 65537, H = 1024, 70 % of
-// one id, bf16 dW over V = 32749 92 us, 3.7 TB/s; T = 64 5.3 us.
+// 151936, fp32 (2.5 GB, nearly all of it zeros to write) 347 us, 7.2 TB/s; T = 65537, H = 1024, 70 % of
+// one id, bf16 dW over V = 32749 93 us, 3.6 TB/s; T = 64 5.7 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -127,7 +127,8 @@ __device__ __forceinline__ void put8(void* base, int64_t off, const float (&f)[8
 constexpr int kLookupWarps = 4;
 
 // A CTA takes `rows` consecutive rows (ROWS of a warp at a time, their loads in flight together)
-// by kLookupWarps * 32 lanes of 8 columns; rows of up to 128 columns share a warp, `lanes` of it each.
+// by kLookupWarps * 32 lanes of 8 columns; rows of up to 128 columns share a warp, `lanes` of it each (1 M rows of H
+// = 64 27 us, 101 with a warp each).
 template <bool WB, bool YB, int ROWS>
 __global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __grid_constant__ EmbeddingParams p,
                                                                       int warps_per_row, int lanes, int rows) {
