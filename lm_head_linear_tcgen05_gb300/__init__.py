@@ -791,7 +791,7 @@ def lp_sum_partials(parts: Sequence[torch.Tensor], out_dtype=torch.float32,
 # ------------------------------------------------------------------ embedding
 # These calls can be as short as a launch, so what surrounds the launch is kept short too: the
 # device is switched only when it is not the current one, the stream is read as a raw handle, and
-# a partition's C form is made once per partition value.
+# a VocabPartition's C form is made once per value.
 
 _SAME_DEVICE = contextlib.nullcontext()
 
@@ -808,11 +808,14 @@ _cached_partition = functools.lru_cache(maxsize=64)(_c_partition)
 
 
 def _partition_ref(part):
-    """A pointer to the C form of ``part`` for a call (which only reads it)."""
-    try:
-        return ctypes.byref(_cached_partition(part)[0])
-    except TypeError:                       # not hashable: ranges given as a list
-        return ctypes.byref(_c_partition(part)[0])
+    """A pointer to the C form of ``part`` for a call (which only reads it). Only a VocabPartition, frozen and
+    hashed by its fields, is looked up: another object with these fields may change and still hash alike."""
+    if type(part) is VocabPartition:
+        try:
+            return ctypes.byref(_cached_partition(part)[0])
+        except TypeError:                   # not hashable: ranges given as a list
+            pass
+    return ctypes.byref(_c_partition(part)[0])
 
 
 _POINTERS = [ctypes.c_void_p * max(n, 1) for n in range(LP_MAX_SHARDS + 1)]

@@ -1,0 +1,52 @@
+"""What the binding of the embedding and the losses does before a call (CPU only)."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lp():
+    import lm_head_linear_tcgen05_gb300 as mod
+    return mod
+
+
+def _ranges(ref):
+    part = ref._obj
+    return [(part.shards[k].vocab_start, part.shards[k].vocab_end) for k in range(part.n_shards)]
+
+
+def test_a_partition_that_changes_is_read_again(lp):
+    """Any object with the three fields is a partition; one of an ordinary class hashes by identity, so what
+    was read from it before says nothing of what it holds now."""
+    class Partition:
+        vocab_real, vocab_padded, ranges = 1000, 1024, ((0, 1024),)
+
+    part = Partition()
+    assert _ranges(lp._partition_ref(part)) == [(0, 1024)]
+    part.ranges = ((0, 100), (100, 512), (512, 1024))
+    assert _ranges(lp._partition_ref(part)) == [(0, 100), (100, 512), (512, 1024)]
+    part.vocab_real, part.local = 600, True
+    assert (lp._partition_ref(part)._obj.vocab_real, lp._partition_ref(part)._obj.local) == (600, 1)
+
+    class Derived(lp.VocabPartition):
+        __hash__ = object.__hash__
+
+        def __eq__(self, other):
+            return self is other
+
+    part = Derived(1000, 1024, ((0, 1024),))
+    assert _ranges(lp._partition_ref(part)) == [(0, 1024)]
+    object.__setattr__(part, "ranges", ((0, 24), (24, 1024)))
+    assert _ranges(lp._partition_ref(part)) == [(0, 24), (24, 1024)]
+
+
+def test_partitions_are_told_apart_by_value(lp):
+    whole, halves = lp.VocabPartition(1000, 1024, ((0, 1024),)), lp.VocabPartition(1000, 1024, ((0, 512), (512, 1024)))
+    local = lp.VocabPartition(1000, 1024, ((0, 1024),), local=True)
+    listed = lp.VocabPartition(1000, 1024, [(0, 8), (8, 1024)])        # not hashable
+    for _ in range(2):
+        assert _ranges(lp._partition_ref(whole)) == [(0, 1024)] and lp._partition_ref(whole)._obj.local == 0
+        assert _ranges(lp._partition_ref(halves)) == [(0, 512), (512, 1024)]
+        assert lp._partition_ref(local)._obj.local == 1
+        assert _ranges(lp._partition_ref(listed)) == [(0, 8), (8, 1024)]
+        listed.ranges[:] = [(0, 16), (16, 1024)]
+        assert _ranges(lp._partition_ref(listed)) == [(0, 16), (16, 1024)]
+        listed.ranges[:] = [(0, 8), (8, 1024)]
