@@ -147,6 +147,13 @@ def embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: float =
     return _Embedding.apply(ids, part, float(scale), out_dtype, *W)
 
 
+def _check_options(function, options):
+    """Refuses the options of the library call that the wrapper gives itself."""
+    for name in ("upstream", "grads", "metrics"):
+        if name in options:
+            raise TypeError(f"{name} is not an option of {function} under autograd, which sets it")
+
+
 def _save(ctx, inputs, options):
     """Keeps the inputs and the tensors among the options with autograd, which notices when one was changed in
     place before the backward reads it again."""
@@ -184,8 +191,9 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     """lp_policy_loss with autograd: returns (loss, metrics, counts), the loss differentiable with
     respect to logp and entropy. ``options`` are those of lp_policy_loss (ref_logp, mask, cu_seqlens,
     clip_low, clip_high, dual_clip, kl_coef, kl_kind, entropy_coef, aggregation, denominator,
-    adv_per_seq). The backward is one library call that reads the inputs again and multiplies by
+    adv_per_seq, workspace). The backward is one library call that reads the inputs again and multiplies by
     the upstream gradient where it is."""
+    _check_options("policy_loss", options)
     return _PolicyLoss.apply(logp, entropy, old_logp, advantages, options)
 
 
@@ -208,5 +216,6 @@ class _PreferenceLoss(torch.autograd.Function):
 def preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, **options):
     """lp_preference_loss with autograd: returns (loss, metrics, counts, margins), the loss
     differentiable with respect to logp. ``options`` are those of lp_preference_loss (ref_logp,
-    mask, beta, kind, label_smoothing, length_normalised, margin, denominator)."""
+    mask, beta, kind, label_smoothing, length_normalised, margin, denominator, workspace)."""
+    _check_options("preference_loss", options)
     return _PreferenceLoss.apply(logp, cu_seqlens, options)

@@ -50,3 +50,16 @@ def test_partitions_are_told_apart_by_value(lp):
         listed.ranges[:] = [(0, 16), (16, 1024)]
         assert _ranges(lp._partition_ref(listed)) == [(0, 16), (16, 1024)]
         listed.ranges[:] = [(0, 8), (8, 1024)]
+
+
+@pytest.mark.parametrize("name,value", [("upstream", None), ("upstream", 2.0), ("grads", True), ("grads", False),
+                                        ("metrics", True), ("metrics", False)])
+def test_the_autograd_losses_refuse_what_autograd_gives(lp, name, value):
+    """At the call, by name: not in the backward, after a forward that took the option."""
+    import torch
+    from lm_head_linear_tcgen05_gb300.autograd import policy_loss, preference_loss
+    x, cu = torch.zeros(4, requires_grad=True), torch.tensor([0, 2, 4], dtype=torch.int32)
+    with pytest.raises(TypeError, match=f"{name} is not an option"):
+        policy_loss(x, x.detach(), x.detach(), **{name: value})
+    with pytest.raises(TypeError, match=f"{name} is not an option"):
+        preference_loss(x, cu, **{name: value})
