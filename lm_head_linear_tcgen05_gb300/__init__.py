@@ -964,12 +964,38 @@ def _upstream(u: Optional[torch.Tensor], device: int) -> Optional[int]:
 
 
 class LossOutputs(dict):
-    """What a loss returns, by name; ["loss"] is made when it is asked for, a 0-D view of metrics[0]."""
+    """What a loss returns, by name. "loss", a 0-D view of metrics[0], is made when it, or the dict as a whole,
+    is first asked for; without metrics there is none."""
+
+    _whole = False
+
+    def _complete(self):
+        if not self._whole:
+            self._whole = True
+            metrics = dict.get(self, "metrics")
+            if metrics is not None and not dict.__contains__(self, "loss"):
+                dict.__setitem__(self, "loss", metrics[0])
 
     def __missing__(self, key):
-        if key == "loss" and self.get("metrics") is not None:
-            return self["metrics"][0]
-        raise KeyError(key)
+        self._complete()
+        if not dict.__contains__(self, key):
+            raise KeyError(key)
+        return dict.__getitem__(self, key)
+
+
+def _reads_the_whole(name):
+    of_dict = getattr(dict, name)
+
+    @functools.wraps(of_dict)
+    def method(self, *args):
+        self._complete()
+        return of_dict(self, *args)
+    return method
+
+
+for _name in ("__contains__", "__delitem__", "__eq__", "__ior__", "__iter__", "__len__", "__ne__", "__or__", "__repr__",
+              "__reversed__", "__ror__", "copy", "get", "items", "keys", "pop", "popitem", "setdefault", "values"):
+    setattr(LossOutputs, _name, _reads_the_whole(_name))
 
 
 def lp_loss_workspace_size(op: int, T: int, n_seqs: int) -> int:
@@ -1029,7 +1055,7 @@ def lp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp: O
                        mask: Optional[torch.Tensor] = None, beta: float = 0.1, kind: str = "sigmoid",
                        label_smoothing: float = 0.0, length_normalised: bool = False, margin: float = 0.0,
                        denominator: float = 0.0, upstream: Optional[torch.Tensor] = None, grads: bool = True,
-                       metrics: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+                       metrics: bool = True, workspace: Optional[torch.Tensor] = None) -> LossOutputs:
     """Preference loss over pairs of answers with its gradient: sequences 2p and 2p + 1 of
     ``cu_seqlens`` (int32 [2 P + 1]) are the chosen and the rejected answer of pair p. logp and
     ref_logp fp32 [T] (None: a reference-free loss), mask bool or uint8 [T]. ``kind``: sigmoid, hinge or

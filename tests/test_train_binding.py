@@ -63,3 +63,44 @@ def test_the_autograd_losses_refuse_what_autograd_gives(lp, name, value):
         policy_loss(x, x.detach(), x.detach(), **{name: value})
     with pytest.raises(TypeError, match=f"{name} is not an option"):
         preference_loss(x, cu, **{name: value})
+
+
+def _outputs(lp, metrics=True):
+    import torch
+    return lp.LossOutputs(metrics=torch.arange(5, 11, dtype=torch.float32) if metrics else None, counts=None,
+                          grad_logp=torch.zeros(3))
+
+
+def test_the_loss_is_there_however_it_is_asked_for(lp):
+    """Each question put to outputs of its own, so that none finds what an earlier one left."""
+    import copy
+    import pickle
+    names = {"loss", "metrics", "counts", "grad_logp"}
+    assert float(_outputs(lp)["loss"]) == 5.0 and float(_outputs(lp).get("loss")) == 5.0
+    assert "loss" in _outputs(lp) and len(_outputs(lp)) == 4
+    assert set(_outputs(lp)) == set(_outputs(lp).keys()) == set(reversed(_outputs(lp))) == names
+    assert float(dict(_outputs(lp).items())["loss"]) == 5.0 and len(_outputs(lp).values()) == 4
+    (lambda loss, metrics, counts, grad_logp: None)(**_outputs(lp))
+    filled = {}
+    filled.update(_outputs(lp))
+    whole = (dict(_outputs(lp)), {**_outputs(lp)}, filled, _outputs(lp).copy(), copy.copy(_outputs(lp)),
+             pickle.loads(pickle.dumps(_outputs(lp))), _outputs(lp) | {}, {} | _outputs(lp))
+    assert all(set(w) == names and float(w["loss"]) == 5.0 for w in whole)
+    assert float(_outputs(lp).pop("loss")) == 5.0 and float(_outputs(lp).setdefault("loss", 1.0)) == 5.0
+    assert "loss" in repr(_outputs(lp))
+    out = _outputs(lp)
+    assert out["loss"] is out["loss"] and out["loss"].data_ptr() == out["metrics"].data_ptr()
+    for take in (lambda o: o.pop("loss"), lambda o: o.__delitem__("loss")):
+        out = _outputs(lp)
+        take(out)
+        assert "loss" not in out and out.get("loss") is None and len(out) == 3
+    out = _outputs(lp)
+    out["loss"] = 2.0
+    assert out["loss"] == out.get("loss") == dict(out)["loss"] == 2.0
+    # without metrics there is no loss
+    none = _outputs(lp, metrics=False)
+    assert "loss" not in none and none.get("loss") is None and set(none) == names - {"loss"}
+    with pytest.raises(KeyError):
+        none["loss"]
+    with pytest.raises(KeyError):
+        _outputs(lp)["grad"]
