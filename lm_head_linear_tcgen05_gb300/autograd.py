@@ -122,10 +122,11 @@ def linear_logp_from_logits(logits: Sequence[torch.Tensor], part, y: torch.Tenso
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, part, scale, out_dtype, *W):
+        y = lp_embedding(ids, list(W), part, scale=scale, out_dtype=out_dtype)
         ctx.part, ctx.scale = part, scale
         ctx.dtype = next(w.dtype for w in W if w is not None)
         ctx.save_for_backward(ids)
-        return lp_embedding(ids, list(W), part, scale=scale, out_dtype=out_dtype)
+        return y
 
     @staticmethod
     @once_differentiable

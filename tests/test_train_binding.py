@@ -104,3 +104,15 @@ def test_the_loss_is_there_however_it_is_asked_for(lp):
         none["loss"]
     with pytest.raises(KeyError):
         _outputs(lp)["grad"]
+
+
+def test_an_embedding_without_shards_is_refused_alike(lp):
+    """Under autograd with the library call's error."""
+    import torch
+    from lm_head_linear_tcgen05_gb300.autograd import embedding
+    ids, part = torch.zeros(3, dtype=torch.int32), lp.VocabPartition(8, 8, ((0, 8),))
+    for W in ([None], [torch.zeros(8, 8).tolist()], []):
+        with pytest.raises((TypeError, ValueError)):
+            lp.lp_embedding(ids, W, part)
+        with pytest.raises((TypeError, ValueError)):
+            embedding(ids, W, part)
