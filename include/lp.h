@@ -629,9 +629,10 @@ LP_API lp_status lp_set_wait_limit(uint64_t limit_ns);
  * which compiles the checks away. */
 LP_API int lp_debug_bounds_build(void);
 
-/* Self-test of the bounds checks: one thread checks an index equal to its extent. A
- * bounds-checked build records LP_ERR_BOUNDS (read it with lp_get_device_error()); the
- * regular build records nothing. No memory is accessed either way. */
+/* Self-test of the bounds checks: one thread checks an index equal to its extent, and asks
+ * for the gradient row after a table's last. A bounds-checked build in which both are noticed
+ * records LP_ERR_BOUNDS (read it with lp_get_device_error()); the regular build records
+ * nothing. No buffer is accessed either way. */
 LP_API lp_status lp_selftest_bounds(lp_stream_t stream);
 
 /* Identity of this build: a hash of the sources and code flags it was compiled from (a

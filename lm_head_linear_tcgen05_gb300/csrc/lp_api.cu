@@ -36,12 +36,6 @@ __global__ void wait_timeout_selftest_kernel(uint64_t limit_ns, unsigned int* er
   __syncthreads();
 }
 
-// One thread checks an index equal to its extent: a bounds-checked build records
-// LP_ERR_BOUNDS, the regular build nothing. No memory is read or written.
-__global__ void bounds_selftest_kernel(int64_t extent, unsigned int* err) {
-  if (threadIdx.x == 0) (void)in_bounds(extent < extent, err);
-}
-
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -879,8 +873,7 @@ lp_status lp_selftest_bounds(lp_stream_t stream) {
   DeviceState* dev = nullptr;
   lp_status st = device_state(&dev);
   if (st != LP_OK) return st;
-  bounds_selftest_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(int64_t(1), dev->err);
-  return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+  return launch_bounds_selftest(dev->err, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 
 lp_status lp_set_wait_limit(uint64_t limit_ns) {

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __gr
   int id[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) id[r] = t0 + r * rows < p.T ? __ldg(p.ids + t0 + r * rows) : -1;
-  if (col >= p.H || !in_bounds(p.H <= p.ld_y, p.err)) return;
+  if (col >= p.H || !in_bounds(col + 8 <= p.H && p.H <= p.ld_y, p.err)) return;
   Vec8<WB> v[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kLookupWarps * 32) embedding_kernel(const __gr
 // ------------------------------------------------------------------ gradient: sort
 
 // the row of dW with local index r < width: the base pointer of the shard that holds it (the last
-// that starts at or before it), the element offset
+// that starts at or before it), the element offset. No caller has another r unless the sort went wrong: such a
+// row is not written, in any build, and the bounds-checked one says so.
 __device__ __forceinline__ void* dw_row(const EmbeddingGradParams& p, uint32_t r, int64_t* off) {
   void* base = p.dW[0];
   uint32_t start = 0;
@@ -180,7 +181,8 @@ __device__ __forceinline__ void* dw_row(const EmbeddingGradParams& p, uint32_t r
       start = p.row_start[k];
     }
   *off = int64_t(r - start) * p.H;
-  return r < p.row_start[p.n_shards] ? base : nullptr;
+  const bool has_row = r < p.row_start[p.n_shards];
+  return in_bounds(has_row, p.err) && has_row ? base : nullptr;
 }
 
 constexpr int kSortThreads = 512;
@@ -972,6 +974,33 @@ cudaError_t launch_lookup(const EmbeddingParams& p, cudaStream_t s) {
 cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16, cudaStream_t s) {
   if (w_bf16) return y_bf16 ? launch_lookup<true, true>(p, s) : launch_lookup<true, false>(p, s);
   return y_bf16 ? launch_lookup<false, true>(p, s) : launch_lookup<false, false>(p, s);
+}
+
+namespace {
+
+// One thread checks an index equal to its extent, and asks for the row after a table's last; each has to record
+// LP_ERR_BOUNDS in a word of its own for the kernel to record it. Touches no memory but its own.
+__global__ void bounds_selftest_kernel(EmbeddingGradParams p, int64_t extent, unsigned int* err) {
+  __shared__ unsigned int seen[2];
+  if (threadIdx.x != 0) return;
+  seen[0] = seen[1] = 0u;
+  (void)in_bounds(extent < extent, seen);
+  p.err = seen + 1;
+  int64_t off;
+  const bool written = dw_row(p, p.row_start[p.n_shards], &off) != nullptr;
+  if (seen[0] == LP_ERR_BOUNDS && seen[1] == LP_ERR_BOUNDS && !written) record_error(err, LP_ERR_BOUNDS);
+}
+
+}  // namespace
+
+cudaError_t launch_bounds_selftest(unsigned int* err, cudaStream_t s) {
+  EmbeddingGradParams p = {};
+  p.n_shards = 2;
+  p.row_start[1] = 3;
+  p.row_start[2] = 8;
+  p.H = 8;
+  bounds_selftest_kernel<<<1, 32, 0, s>>>(p, int64_t(1), err);
+  return cudaGetLastError();
 }
 
 size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width) {

@@ -274,6 +274,7 @@ size_t embedding_backward_ws_bytes(int64_t T, int64_t H, int64_t width);
 void embedding_backward_carve(EmbeddingGradParams* p, void* workspace, int64_t width);
 cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16, cudaStream_t s);
 cudaError_t launch_embedding_backward(const EmbeddingGradParams& p, bool dy_bf16, cudaStream_t s);
+cudaError_t launch_bounds_selftest(unsigned int* err, cudaStream_t s);
 
 // ------------------------------------------------------------ losses
 struct PolicyParams {
