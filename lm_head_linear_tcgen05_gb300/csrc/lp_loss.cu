@@ -318,21 +318,24 @@ struct SeqCursor {
 constexpr int kPolicySums = 5;
 
 struct PolicyWs {
-  int32_t* block_kept;  // [ceil(T / kCountBlock)]
   int32_t* seq_kept;    // [n_seqs]
   Totals* totals;       // [CTAs of the stat stage]
   float* sums;          // [CTAs of the token stage][kPolicySums]
-  uint32_t* done;       // CTAs that have finished their tokens
+  int32_t* block_kept;  // [ceil(T / kCountBlock)], and
+  uint32_t* done;       // CTAs that have finished their tokens: of the launches, not of the one-launch form
 };
 
-__host__ __device__ inline PolicyWs policy_carve(void* base, size_t align, int64_t T, int64_t n_seqs, int stat_ctas,
-                                                 int token_ctas, size_t* bytes) {
-  Carver c{static_cast<char*>(base), align, 0};
-  PolicyWs r;
+template <bool ONE>
+__host__ __device__ inline PolicyWs policy_carve(void* base, int64_t T, int64_t n_seqs, int stat_ctas, int token_ctas,
+                                                 size_t* bytes) {
+  Carver c{static_cast<char*>(base), ONE ? size_t(16) : size_t(256), 0};
+  PolicyWs r{};
   r.totals = c.take<Totals>(stat_ctas);
   r.sums = c.take<float>(int64_t(token_ctas) * kPolicySums);
-  r.done = c.take<uint32_t>(1);
-  r.block_kept = c.take<int32_t>(ceil_div(T, kCountBlock));
+  if constexpr (!ONE) {
+    r.done = c.take<uint32_t>(1);
+    r.block_kept = c.take<int32_t>(ceil_div(T, kCountBlock));
+  }
   r.seq_kept = c.take<int32_t>(n_seqs);
   *bytes = c.used;
   return r;
@@ -412,7 +415,8 @@ __device__ __forceinline__ void policy_stat(const PolicyParams& p, const PolicyW
   if (threadIdx.x == 0) {
     if (t.bad) record_error(p.err, LP_ERR_SEQ_OFFSETS);
     ws.totals[cta] = t;
-    if (cta == 0) *ws.done = 0u;
+    if constexpr (!ONE)
+      if (cta == 0) *ws.done = 0u;
   }
 }
 
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kThreads) policy_cluster_kernel(const __grid_c
   extern __shared__ int4 stage[];
   const int cta = blockIdx.x, ctas = gridDim.x;
   size_t bytes;
-  const PolicyWs ws = policy_carve(first_cta_shared(stage), 16, p.T, p.n_seqs, ctas, ctas, &bytes);
+  const PolicyWs ws = policy_carve<true>(first_cta_shared(stage), p.T, p.n_seqs, ctas, ctas, &bytes);
   cluster_sync();  // the first CTA has started
   policy_stat<true>(p, ws, cta, ctas);
   cluster_sync();
@@ -748,8 +752,8 @@ __device__ __forceinline__ void add_tiles(const PrefWs& ws, int first, int from,
 // Sequences of more than kPairTiles tiles are added by the whole CTA, one by one. Each thread comes with
 // the tiles of its own sequence (eight lanes to a sequence) and gets its sum in the first of the eight.
 constexpr int kPairTiles = 256;
+static_assert(kFusedTokens <= int64_t(kPairTiles) * kPrefTile, "the one-launch form has no such sequences");
 
-template <bool ONE>
 __device__ __noinline__ void add_long_sequences(const PrefWs& ws, int first, int last, Pair32* sum, int* n) {
   __shared__ int2 tiles[kThreads / 8];
   __shared__ Pair32 part[kWarps];
@@ -762,7 +766,7 @@ __device__ __noinline__ void add_long_sequences(const PrefWs& ws, int first, int
     if (r.y < r.x) continue;
     Pair32 v{0.f, 0.f};
     int k = 0;
-    add_tiles<ONE>(ws, r.x, r.x + int(threadIdx.x), r.y, kThreads, &v, &k);
+    add_tiles<false>(ws, r.x, r.x + int(threadIdx.x), r.y, kThreads, &v, &k);
     v = warp_add(v);
     k = warp_sum_int(k);
     if ((threadIdx.x & 31) == 0) {
@@ -802,12 +806,15 @@ __device__ __forceinline__ void pref_pair(const PreferenceParams& p, const PrefW
         last = (b - 1) / kPrefTile;
       }
     }
-    const bool is_long = last - first >= kPairTiles;
-    const bool any_long = __syncthreads_or(is_long) != 0;
-    if (!ONE) grid_dependency_wait();  // the offsets are the caller's, the tiles the kernel's before
     Pair32 sc{0.f, 0.f};
     int nc = 0;
-    if (any_long) add_long_sequences<ONE>(ws, first, last, &sc, &nc);
+    bool is_long = false;
+    if constexpr (!ONE) {
+      is_long = last - first >= kPairTiles;
+      const bool any_long = __syncthreads_or(is_long) != 0;
+      grid_dependency_wait();  // the offsets are the caller's, the tiles the kernel's before
+      if (any_long) add_long_sequences(ws, first, last, &sc, &nc);
+    }
     if (first == last) {  // beginning and ending on the tile's own edges counts as within it
       const Piece c = (lane & 7) == 0 ? read_piece<ONE>(ws.whole + s) : Piece{0.f, 0};
       sc.hi = c.sum;
@@ -980,7 +987,7 @@ int pref_cluster_ctas(int64_t T, int64_t n_seqs) {
 
 size_t policy_stage_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
-  policy_carve(nullptr, 16, T, n_seqs, cluster_ctas(T), cluster_ctas(T), &bytes);
+  policy_carve<true>(nullptr, T, n_seqs, cluster_ctas(T), cluster_ctas(T), &bytes);
   return bytes;
 }
 
@@ -1023,7 +1030,7 @@ bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 size_t policy_ws_bytes(int64_t T, int64_t n_seqs) {
   size_t bytes = 0;
-  if (!policy_one_launch(T, n_seqs)) policy_carve(nullptr, 256, T, n_seqs, kStatCtas, kTokenCtas, &bytes);
+  if (!policy_one_launch(T, n_seqs)) policy_carve<false>(nullptr, T, n_seqs, kStatCtas, kTokenCtas, &bytes);
   return bytes;
 }
 
@@ -1041,7 +1048,7 @@ cudaError_t launch_policy(const PolicyParams& p, cudaStream_t s) {
     return launch(policy_cluster_kernel<KL, BY_SEQ>, cluster_ctas(p.T), true, false, policy_stage_bytes(p.T, p.n_seqs), s,
                   p);
   size_t bytes = 0;
-  const PolicyWs ws = policy_carve(p.workspace, 256, p.T, p.n_seqs, kStatCtas, kTokenCtas, &bytes);
+  const PolicyWs ws = policy_carve<false>(p.workspace, p.T, p.n_seqs, kStatCtas, kTokenCtas, &bytes);
   const int64_t blocks = ceil_div(p.T, kCountBlock);
   cudaError_t e = cudaSuccess;
   if (p.in.mask != nullptr)
