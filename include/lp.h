@@ -390,7 +390,7 @@ LP_API lp_status lp_sum_partials(const float* const* parts, int32_t n_parts, int
  * --------------------------------------------------------------------------------- */
 
 /* Embedding lookup with scaling: Y[t] = scale * W[ids[t]], the product in fp32, then rounded to
- * Y's type (an exact copy when scale = 1 and the types agree).
+ * Y's type (exact when scale = 1 and the types agree; a NaN stays one, its payload may change).
  *   ids      int32 [T] global ids: [0, vocab_real), or -1 for an unused position
  *   W        host array [n_shards] of device pointers, shard k [V_k, H] row-major of type
  *            w_dtype (NULL allowed for a shard without real ids), H % 8 == 0

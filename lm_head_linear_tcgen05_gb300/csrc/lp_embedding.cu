@@ -1,8 +1,8 @@
 // lp_embedding.cu - embedding lookup with scaling, and its gradient by sorted tokens.
 //
 // Forward: Y[t] = scale W[id_t]. A copy, bound by memory: 8192 rows of H = 4096 in bf16 from four
-// shards take 18.0 us, 7.4 TB/s of rows read and written (1.1 of the measured copy rate, the L2 holding some);
-// 64 rows, bound by a launch and two dependent loads, 2.1 us.
+// shards take 17.7 us repeated, 7.6 TB/s of rows read and written, of which the L2 holds the output (19 us with it
+// cold); 64 rows, bound by a launch and two dependent loads, 2.1 us.
 //
 // Gradient: dW[v] = scale sum_{t: id_t = v} dY[t], bound by memory too: every row of dY read once,
 // every row of dW written (or, accumulating, the named ones read and written). Adding rows into dW with
@@ -14,7 +14,7 @@
 //                   pass, in one launch, with hardware barriers and distributed shared memory between
 //                   the passes, instead of three launches a pass. An unused or foreign position gets the key
 //                   `width` and sorts last. It also marks the rows that some position names. Bound by
-//                   its chain of dependent steps, not by data: 12 us for 16384 positions, 2 for 64.
+//                   its chain of dependent steps, not by data: 13 us for 16384 positions, 22 for 65537.
 //   segment_kernel  four warps per (chunk of 32 sorted positions, 256 columns). A run of equal
 //                   rows of at most 32 positions (64 in a batch of no more) is summed by the warp in whose quarter of a
 //                   chunk it begins, which follows it as far as it goes; a longer run is summed
@@ -28,7 +28,7 @@
 //                   its dependent loads: 7 us where 16384 positions leave some 50 long runs.
 // Each launch is the programmatic dependent of the one before. Whole calls: T = 4096, H = 4096 over V =
 // 151936, fp32 (2.5 GB, nearly all of it zeros to write) 347 us, 7.2 TB/s; T = 65537, H = 1024, 70 % of
-// one id, bf16 dW over V = 32749 93 us, 3.6 TB/s; T = 64 5.7 us.
+// one id, bf16 dW over V = 32749 92 us, 3.6 TB/s; T = 64 5.7 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -193,9 +193,9 @@ static_assert(kMaxBins == kSortThreads, "a thread per bin");
 constexpr int kSortCtas = 16;  // most CTAs of the sorting cluster
 constexpr int kSortAhead = 4;  // loads in flight per lane
 // Positions of a CTA below which half the CTAs sort: up to 8 (the portable cluster size) their
-// barriers and exchanges cost more than they save below 512, 16 pay from 1024 on (T = 16384 over
-// 151936 ids, whole call at H = 8: 38.1 us with 8, 35.6 with 16; T = 65537: 77.9 and 64.3; T = 8192:
-// 32.0 and 31.7, within the noise).
+// barriers and exchanges cost more than they save below 512, 16 pay from 1024 on (whole calls of H = 8 over
+// 151936 ids with 8 CTAs and with 16: T = 4096 18.1 and 19.9 us, 8192 20.5 and 19.7, 12288 22.6 and 22.1, 16384
+// 24.2 and 22.5, 65537 65.6 and 42.2, 400000 281 and 182).
 constexpr int64_t kSortMinPerCta = 512;
 constexpr int64_t kSortMinPerCta16 = 1024;
 // Positions a lane keeps in registers: 4 (a warp's stretch of up to 128; 32768 positions in all with
@@ -203,8 +203,8 @@ constexpr int64_t kSortMinPerCta16 = 1024;
 // 28.7.
 constexpr int kKeepFew = 4, kKeepMany = 12;
 // Zeros written while one cluster sorts (see early_words), by CTAs of at least kZeroBytes. More CTAs hold up
-// the sort, fewer do not keep up (T = 4096, V = 151936, H = 4096: 346.8 us with 96, 347.0 with 112, 349.8 with
-// 144, 348.8 with 80; two calls of T = 16384: 118.2, 120.9, 120.1, 118.3).
+// the sort, fewer do not keep up (T = 4096, V = 151936, H = 4096: 356 us with 48, 347 with 96, 351 with 144; T =
+// 16384, V = 32768, H = 2048: 73.7, 66.4 and 69.2; T = 65537, where the sort is longer: the same with each).
 constexpr int64_t kEarlyBytes = int64_t(56) << 20;
 constexpr int64_t kZeroCtas = 96;
 constexpr int64_t kZeroBytes = 8 * 1024;
@@ -276,8 +276,8 @@ __device__ __forceinline__ void sort_places(uint32_t (&hist)[kSortWarps][kMaxBin
 }
 
 // Most positions that are sorted by comparing each with all, a CTA for 128 of them, up to 16 CTAs; above, by
-// digits (whole calls of H = 256 over V = 1000 by rank and by digits: T = 64 6.1 and 10.6 us, 256 8.6 and 12.3,
-// 1024 12.7 and 15.6, 1500 13.9 and 16.8, 2048 16.1 and 16.4, 2560 23.7 and 17.5).
+// digits (whole calls of H = 256 over V = 1000 by rank and by digits: T = 64 5.7 and 9.4 us, 256 9.4 and 12.9,
+// 1024 12.7 and 15.2, 1500 15.2 and 17.8, 2048 16.5 and 16.5, 2560 23.8 and 18.1).
 constexpr int kRankMost = 1536;
 constexpr int kRankPositions = 128;     // of a CTA at a time
 constexpr int kRankGroups = kSortThreads / kRankPositions;  // of threads, which share the comparisons
@@ -886,10 +886,11 @@ int sort_ctas(int64_t T) {
   return ctas;
 }
 
-// Rows whose zeros the sort kernel writes, in words of 32: 56 MB, about what other SMs can write while
-// one cluster sorts (T = 4096, H = 4096, V = 151936: 346 us, 349 with 24 MB, 347 with 80; two calls of T = 16384:
-// 117.5, 119.7 and 116.9; T = 65537: 92.0, 92.1 and 92.4). More is not taken, since these rows are zeroed
-// whether a position names them or not. Asking the L2 for 32 to 128 MB of dY at that
+// Rows whose zeros the sort kernel writes, in words of 32: 56 MB whatever the batch, although the sort's
+// length, and what other SMs can write meanwhile, grows with it (without, with 24, 56 and 80 MB: T = 4096, H = 4096,
+// V = 151936 353.8, 350.9, 347.5 and 348.4 us; T = 16384, H = 2048, V = 32768 72.0, 69.8, 66.4 and 65.9; T = 65537,
+// H = 1024, V = 32749, bf16 88.1, 86.8, 86.9 and 86.9; it loses where the sort is short: T = 1024, H = 2048 46.8,
+// 48.0, 48.1 and 46.8). More is not taken, since these rows are zeroed whether a position names them or not. Asking the L2 for 32 to 128 MB of dY at that
 // time gains nothing (2 calls of T = 16384: 120.5 us, 121.2 to 123.9 with).
 uint32_t early_words(const EmbeddingGradParams& p) {
   if (p.accumulate) return 0u;

@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCountBlock = 512;          // tokens of a count: 16 a lane
+// CTA counts are multiples of a GB300's 152 SMs
 constexpr int kStatCtas = 304;            // most CTAs of the per-sequence and per-pair stages
 constexpr int kTokenTile = 4 * kThreads;  // tokens of a CTA and step, four a thread
 constexpr int kTokenCtas = 456;           // most CTAs of the policy's tokens: three to an SM, 80 registers
