@@ -79,7 +79,8 @@ typedef enum {
   LP_ERR_BOUNDS = 10,              /* device, bounds-checked builds only: an index failed its check and
                                       the access was skipped (see lp_debug_bounds_build) */
   LP_ERR_TOKEN_OUT_OF_RANGE = 11,  /* device: an embedding id not in {-1} U [0, vocab_real) */
-  LP_ERR_SEQ_OFFSETS = 12          /* device: cu_seqlens does not ascend from 0 to T */
+  LP_ERR_SEQ_OFFSETS = 12,         /* device: cu_seqlens does not ascend from 0 to T */
+  LP_ERR_EXPERT_OUT_OF_RANGE = 13  /* device: an expert id not in {-1} U [0, E) */
 } lp_status;
 
 typedef enum {
@@ -597,6 +598,243 @@ typedef struct {
 LP_API lp_status lp_preference_loss(int64_t T, const lp_preference_inputs* in, const lp_preference_options* opts,
                                     const lp_preference_outputs* out, void* workspace, size_t ws_bytes,
                                     lp_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * What a training step runs between the embedding and the head, and on a router. The pages
+ * have no counterpart to these entry points either: they are what the blocks between
+ * lp_embedding and lp_forward do to the hidden states besides their products, and the loss
+ * that keeps a policy's routed experts evenly used.
+ * --------------------------------------------------------------------------------- */
+
+/* Dropout's random bits. They come from Philox4x32-10 (a counter-based generator; Salmon, Moraes,
+ * Dror, Shaw, 2011) and are never stored: the backward makes them again. With G = H / 8 groups
+ * of eight neighbours in a row, group g of row t has the counter (row_start + t) G + g in its
+ * low 64 bits and `offset` in its high 64 bits; `seed` is the key. Element j of the group has
+ * the j-th 16 bits of the four words (low half first) and is dropped when they are below
+ * round(65536 p): p is held to 1 / 65536, and what is kept is divided by exactly one minus the
+ * p that is held. So an element's fate depends on seed, offset and its row's number alone: rows
+ * that are passed in parts (micro-batches, ranks) with the right row_start are dropped as in one
+ * call. Different tensors, layers and steps need different (seed, offset). */
+
+/* Dropout of a [T, H] matrix: out = x / (1 - p) where an element is kept, else 0 (whatever x
+ * holds there, NaN and infinities among them). The gradient is the same call on the gradient.
+ *   x, out   of type dtype, row strides ld_x, ld_out elements; rows start on 16-byte
+ *            boundaries, H % 8 == 0. out may be x (with the same stride); no other overlap
+ *   p        in [0, 1]; 1 drops everything
+ *   row_start >= 0, with (row_start + T) (H / 8) < 2^63
+ *   rng      NULL, or device uint64 [2] (8-byte aligned): added to seed and offset (modulo
+ *            2^64) when the kernel runs, so that a captured graph draws other bits when it is
+ *            replayed after the caller has changed them
+ * Needs no workspace. */
+LP_API lp_status lp_dropout(const void* x, int64_t T, int64_t H, int64_t ld_x, lp_dtype dtype, float p, uint64_t seed,
+                            uint64_t offset, int64_t row_start, const uint64_t* rng, void* out, int64_t ld_out,
+                            lp_stream_t stream);
+
+/* What a gate multiplies the block's output by. */
+typedef enum {
+  LP_GATE_NONE = 0,
+  LP_GATE_CHANNEL = 1, /* [H] of type w_dtype: one factor a column */
+  LP_GATE_TOKEN = 2,   /* fp32 [T]: one factor a row */
+  LP_GATE_FULL = 3     /* [T, H] of type y_dtype, row stride ld_gate */
+} lp_gate;
+
+#define LP_MAX_NORM_WIDTH 16384
+
+/* Inputs of lp_residual_norm, device pointers.
+ *   h            residual stream [T, H] of type h_dtype, row stride ld_h
+ *   y            the block's output [T, H] of type y_dtype, row stride ld_y; NULL: the norm
+ *                of h alone
+ *   weight       [H] of type w_dtype, of the norm after the sum; NULL: no weights (factor 1)
+ *   post_weight  [H] of type w_dtype, of the norm on y (options.post_norm); NULL: no weights
+ *   gate         by options.gate_kind
+ *   rng          as in lp_dropout
+ * Rows, and vectors [H], start on 16-byte boundaries; H % 8 == 0, H <= LP_MAX_NORM_WIDTH. */
+typedef struct {
+  const void* h;
+  const void* y;
+  const void* weight;
+  const void* post_weight;
+  const void* gate;
+  const uint64_t* rng;
+  int64_t ld_h;
+  int64_t ld_y;
+  int64_t ld_gate;
+} lp_norm_inputs;
+
+/* Options of lp_residual_norm and its gradient.
+ *   eps             > 0, added to the mean square of a row
+ *   residual_scale  R, finite
+ *   weight_offset   o, finite: a weight w multiplies by o + w (1 for weights held as
+ *                   differences from one)
+ *   dropout         p in [0, 1], of the gated block output (seed, offset and row_start as in
+ *                   lp_dropout)
+ *   post_norm       1: y is normalised first
+ * Without y, post_norm and dropout are 0, gate_kind LP_GATE_NONE and residual_scale 1. */
+typedef struct {
+  float eps;
+  float residual_scale;
+  float weight_offset;
+  float dropout;
+  uint64_t seed;
+  uint64_t offset;
+  int64_t row_start;
+  int32_t h_dtype;
+  int32_t y_dtype;
+  int32_t w_dtype;
+  int32_t gate_kind;
+  int32_t post_norm;
+} lp_norm_options;
+
+/* Outputs of lp_residual_norm, device pointers.
+ *   h_out  the stream after the block [T, H] of type h_dtype; required with y, NULL without.
+ *          May be h (with the same stride)
+ *   norm   its norm [T, H] of type y_dtype; NULL: not wanted. May be y (with the same stride)
+ * No other overlaps. */
+typedef struct {
+  void* h_out;
+  void* norm;
+  int64_t ld_h_out;
+  int64_t ld_norm;
+} lp_norm_outputs;
+
+/* The end of one block and the start of the next in one pass: an optional norm on the block's
+ * output, its gate, dropout, the residual sum and the next norm. Per row
+ *   b     = y                       or, with post_norm,  y / sqrt(mean y^2 + eps) (o + post_weight)
+ *   h_out = R h + dropout(gate b)
+ *   norm  = h_out / sqrt(mean h_out^2 + eps) (o + weight)
+ * in fp32, each output rounded once: the norm is of the unrounded sum. A row's results depend on
+ * that row alone, and on its number where there is dropout. Needs no workspace. */
+LP_API lp_status lp_residual_norm(int64_t T, int64_t H, const lp_norm_inputs* in, const lp_norm_options* opts,
+                                  const lp_norm_outputs* out, lp_stream_t stream);
+
+/* Gradients of lp_residual_norm, device pointers.
+ * Read:
+ *   d_norm         [T, H] of type y_dtype, of norm; NULL: none
+ *   d_h_out        [T, H] of type h_dtype, of h_out (without y: what else reaches h); NULL: none.
+ *                  One of the two is needed
+ * Written:
+ *   d_h            [T, H] of type h_dtype, required. May be d_h_out (with the same stride)
+ *   d_y            [T, H] of type y_dtype, required with y, NULL without. May be d_norm (with
+ *                  the same stride)
+ *   d_gate         by gate_kind: [H] of type dw_dtype, fp32 [T], or [T, H] of type y_dtype with
+ *                  row stride ld_d_gate; NULL: not wanted
+ *   d_weight       [H] of type dw_dtype; NULL: not wanted; needs weight and d_norm
+ *   d_post_weight  [H] of type dw_dtype; NULL: not wanted; needs post_weight
+ *   dw_dtype       of d_weight, d_post_weight and a channel gate's gradient: LP_DTYPE_F32, or
+ *                  LP_DTYPE_BF16 (the fp32 sum rounded once)
+ *   accumulate     1: those three are added to (one fp32 add per element; needs fp32) */
+typedef struct {
+  const void* d_norm;
+  const void* d_h_out;
+  void* d_h;
+  void* d_y;
+  void* d_gate;
+  void* d_weight;
+  void* d_post_weight;
+  int64_t ld_d_norm;
+  int64_t ld_d_h_out;
+  int64_t ld_d_h;
+  int64_t ld_d_y;
+  int64_t ld_d_gate;
+  int32_t dw_dtype;
+  int32_t accumulate;
+} lp_norm_grads;
+
+/* Gradient of lp_residual_norm, from what it was given and returned: in->h is here the stream
+ * after the block (h_out; without y, h itself), in->y, the weights and the gate are as in the
+ * forward, and so are the options. With u = h_out, r = 1 / sqrt(mean u^2 + eps) and
+ * a = d_norm (o + weight),
+ *   D      = d_h_out + r a - u r^3 mean(a u),   d_h = R D,   c = dropout(D)
+ *   d_gate = c b  (summed over tokens or columns for the broadcast gates),   e = c gate
+ *   d_y    = e,  or with post_norm  q a' - y q^3 mean(a' y),  a' = e (o + post_weight),
+ *            q = 1 / sqrt(mean y^2 + eps)
+ *   d_weight = sum_t d_norm u r,   d_post_weight = sum_t e y q
+ * Rows depend on their own inputs alone; the sums over tokens have an order fixed by T and H, so
+ * results are bitwise the same from run to run. T = 0 writes zeros to the three sums (nothing
+ * when accumulating). Workspace: lp_norm_workspace_size(T, H). */
+LP_API lp_status lp_residual_norm_backward(int64_t T, int64_t H, const lp_norm_inputs* in, const lp_norm_options* opts,
+                                           const lp_norm_grads* grads, void* workspace, size_t ws_bytes,
+                                           lp_stream_t stream);
+
+/* Bytes of device scratch of lp_residual_norm_backward; 0 for invalid arguments. */
+LP_API size_t lp_norm_workspace_size(int64_t T, int64_t H);
+
+#define LP_MAX_EXPERTS 1024
+#define LP_MAX_EXPERT_SLOTS 64
+
+/* What a router's logits l are turned into, p summing to one over a token's experts. */
+typedef enum {
+  LP_SCORE_SOFTMAX = 0, /* p = softmax(l) */
+  LP_SCORE_SIGMOID = 1  /* p = s / sum s, s = 1 / (1 + e^-l) */
+} lp_score;
+
+/* Inputs of lp_balance_loss, device pointers.
+ *   logits      [T, E] of type options.logits_dtype, row stride ld_logits >= E (any alignment
+ *               of the type; rows on 16-byte boundaries are faster), 1 <= E <= LP_MAX_EXPERTS
+ *   ids         int32 [T, K], the experts that each token went to: [0, E), or -1 for a slot
+ *               that was not used; 1 <= K <= LP_MAX_EXPERT_SLOTS, T K < 2^31
+ *   mask        uint8 [T], nonzero = the token counts; NULL keeps every token. What logits and
+ *               ids hold where the mask is zero has no effect
+ *   cu_seqlens  int32 [n_seqs + 1], ascending from 0 to T: the balance is taken within each
+ *               sequence; NULL: over the batch
+ *   upstream    device fp32 [1], the gradient of what follows with respect to the loss; NULL: 1 */
+typedef struct {
+  const void* logits;
+  const int32_t* ids;
+  const uint8_t* mask;
+  const int32_t* cu_seqlens;
+  const float* upstream;
+  int64_t ld_logits;
+  int64_t n_seqs;
+} lp_balance_inputs;
+
+/* Options of lp_balance_loss: the factors of the two terms (finite; z_coef needs softmax). */
+typedef struct {
+  float coef;
+  float z_coef;
+  int32_t score;
+  int32_t logits_dtype;
+  int32_t grad_dtype;
+} lp_balance_options;
+
+#define LP_BALANCE_METRICS 4
+
+/* Outputs of lp_balance_loss, device arrays; any may be NULL (at least one must not be).
+ *   metrics        fp32 [4]: the loss, the balance, the z term, and the largest expert's count
+ *                  over the mean one (E max_e c_e / (K N))
+ *   expert_counts  int64 [E]: slots of kept tokens that name each expert
+ *   counts         int64 [2]: kept tokens, and sequences with at least one (0 without cu_seqlens)
+ *   grad_logits    [T, E] of type options.grad_dtype, row stride ld_grad >= E: upstream * d loss / d logits.
+ *                  May be logits (same type and stride) */
+typedef struct {
+  float* metrics;
+  int64_t* expert_counts;
+  int64_t* counts;
+  void* grad_logits;
+  int64_t ld_grad;
+} lp_balance_outputs;
+
+/* Balance loss of a router with its gradient and the experts' counts, in one call. With N the kept
+ * tokens, c_e the kept tokens' slots that name e and f_e = c_e E / (K N) (1 when evenly used):
+ *   balance = 1/N sum_t d_t,   d_t = sum_e f_e p_te
+ *   z       = 1/N sum_t (log sum_e e^l_te)^2         (softmax; 0 for sigmoid)
+ *   loss    = coef balance + z_coef z
+ *   grad_te = upstream (coef w_t p_te (f_e - d_t) v_te + z_coef 2 lse_t p_te / N),
+ *             w_t = 1/N,  v = 1 for softmax, 1 - s_te for sigmoid
+ * (counts are not differentiated). With cu_seqlens, f_e and d_t are of the token's own sequence
+ * with its N_s kept tokens, and w_t = 1 / (S N_s) over the S sequences that keep one. Tokens that
+ * are not kept get zero gradients; a batch that keeps none has loss 0. A token whose logits are all
+ * -inf has p = 0 (and no z term). An id outside {-1} U [0, E) of a kept token records
+ * LP_ERR_EXPERT_OUT_OF_RANGE and counts for no expert. Offsets that do not ascend from 0 to T
+ * record LP_ERR_SEQ_OFFSETS; metrics are then NaN and gradients zero. Sums have a fixed order:
+ * results are bitwise the same from run to run. T = 0 gives loss 0.
+ * Workspace: lp_balance_workspace_size(T, E, K, n_seqs), n_seqs = 0 without cu_seqlens. */
+LP_API lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balance_inputs* in,
+                                 const lp_balance_options* opts, const lp_balance_outputs* out, void* workspace,
+                                 size_t ws_bytes, lp_stream_t stream);
+
+/* Bytes of device scratch of lp_balance_loss; 0 for invalid arguments. */
+LP_API size_t lp_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t n_seqs);
 
 /* Synchronises `stream`, returns the first device-side error recorded on the
  * current device since the last call (LP_OK if none) and clears it. */

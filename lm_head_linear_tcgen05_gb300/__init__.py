@@ -49,6 +49,7 @@ STATUS_NAMES = {
     10: "LP_ERR_BOUNDS",
     11: "LP_ERR_TOKEN_OUT_OF_RANGE",
     12: "LP_ERR_SEQ_OFFSETS",
+    13: "LP_ERR_EXPERT_OUT_OF_RANGE",
 }
 
 LP_OP_FORWARD = 0
@@ -66,6 +67,12 @@ LP_AGGREGATIONS = {"token_mean": 0, "seq_mean_token_mean": 1, "seq_mean_token_su
 LP_KL_KINDS = {"k1": 0, "k2": 1, "k3": 2}
 LP_PREFERENCES = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 POLICY_METRICS = ("loss", "policy", "kl", "entropy", "clip_fraction", "ratio")
+LP_SCORES = {"softmax": 0, "sigmoid": 1}
+LP_GATE_NONE, LP_GATE_CHANNEL, LP_GATE_TOKEN, LP_GATE_FULL = range(4)
+LP_MAX_NORM_WIDTH = 16384
+LP_MAX_EXPERTS = 1024
+LP_MAX_EXPERT_SLOTS = 64
+BALANCE_METRICS = ("loss", "balance", "z", "peak_load")
 PREFERENCE_METRICS = ("loss", "accuracy", "margin", "chosen_reward", "rejected_reward")
 
 LP_DTYPE_F32 = 0
@@ -79,7 +86,8 @@ EXPORTED = ("lp_workspace_size", "lp_forward", "lp_forward_noalloc", "lp_forward
             "lp_selftest_bounds", "lp_debug_bounds_build", "lp_device_supported", "lp_status_string",
             "lp_build_id", "lp_merge_shard_stats", "lp_sum_partials", "lp_set_wait_limit",
             "lp_embedding", "lp_embedding_backward", "lp_loss_workspace_size", "lp_policy_loss",
-            "lp_preference_loss")
+            "lp_preference_loss", "lp_dropout", "lp_residual_norm", "lp_residual_norm_backward",
+            "lp_norm_workspace_size", "lp_balance_loss", "lp_balance_workspace_size")
 
 
 class LPError(RuntimeError):
@@ -156,6 +164,44 @@ class _PreferenceOutputs(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in ("metrics", "counts", "margins", "grad_logp")]
 
 
+class _NormInputs(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("h", "y", "weight", "post_weight", "gate", "rng")]
+                + [(k, ctypes.c_int64) for k in ("ld_h", "ld_y", "ld_gate")])
+
+
+class _NormOptions(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_float) for k in ("eps", "residual_scale", "weight_offset", "dropout")]
+                + [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("row_start", ctypes.c_int64)]
+                + [(k, ctypes.c_int32) for k in ("h_dtype", "y_dtype", "w_dtype", "gate_kind", "post_norm")])
+
+
+class _NormOutputs(ctypes.Structure):
+    _fields_ = [("h_out", ctypes.c_void_p), ("norm", ctypes.c_void_p), ("ld_h_out", ctypes.c_int64),
+                ("ld_norm", ctypes.c_int64)]
+
+
+class _NormGrads(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("d_norm", "d_h_out", "d_h", "d_y", "d_gate", "d_weight",
+                                                "d_post_weight")]
+                + [(k, ctypes.c_int64) for k in ("ld_d_norm", "ld_d_h_out", "ld_d_h", "ld_d_y", "ld_d_gate")]
+                + [("dw_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)])
+
+
+class _BalanceInputs(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("logits", "ids", "mask", "cu_seqlens", "upstream")]
+                + [("ld_logits", ctypes.c_int64), ("n_seqs", ctypes.c_int64)])
+
+
+class _BalanceOptions(ctypes.Structure):
+    _fields_ = ([("coef", ctypes.c_float), ("z_coef", ctypes.c_float)]
+                + [(k, ctypes.c_int32) for k in ("score", "logits_dtype", "grad_dtype")])
+
+
+class _BalanceOutputs(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("metrics", "expert_counts", "counts", "grad_logits")]
+                + [("ld_grad", ctypes.c_int64)])
+
+
 _lib = None
 
 
@@ -208,6 +254,15 @@ def lib() -> ctypes.CDLL:
     L.lp_policy_loss.argtypes = [i64, P(_PolicyInputs), P(_PolicyOptions), P(_PolicyOutputs), vp, sz, vp]
     L.lp_preference_loss.argtypes = [i64, P(_PreferenceInputs), P(_PreferenceOptions), P(_PreferenceOutputs), vp, sz,
                                      vp]
+    u64 = ctypes.c_uint64
+    L.lp_dropout.argtypes = [vp, i64, i64, i64, ctypes.c_int, f32, u64, u64, i64, vp, vp, i64, vp]
+    L.lp_residual_norm.argtypes = [i64, i64, P(_NormInputs), P(_NormOptions), P(_NormOutputs), vp]
+    L.lp_residual_norm_backward.argtypes = [i64, i64, P(_NormInputs), P(_NormOptions), P(_NormGrads), vp, sz, vp]
+    L.lp_norm_workspace_size.argtypes = [i64, i64]
+    L.lp_norm_workspace_size.restype = sz
+    L.lp_balance_loss.argtypes = [i64, i64, i64, P(_BalanceInputs), P(_BalanceOptions), P(_BalanceOutputs), vp, sz, vp]
+    L.lp_balance_workspace_size.argtypes = [i64, i64, i64, i64]
+    L.lp_balance_workspace_size.restype = sz
     L.lp_get_device_error.argtypes = [vp]
     L.lp_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     L.lp_set_wait_limit.argtypes = [ctypes.c_uint64]
@@ -221,7 +276,8 @@ def lib() -> ctypes.CDLL:
                  "lp_backward", "lp_backward_ex", "lp_backward_from_logits", "lp_forward_host", "lp_get_device_error",
                  "lp_selftest_wait_timeout", "lp_selftest_bounds", "lp_debug_bounds_build", "lp_device_supported",
                  "lp_merge_shard_stats", "lp_sum_partials", "lp_set_wait_limit", "lp_embedding",
-                 "lp_embedding_backward", "lp_policy_loss", "lp_preference_loss"):
+                 "lp_embedding_backward", "lp_policy_loss", "lp_preference_loss", "lp_dropout", "lp_residual_norm",
+                 "lp_residual_norm_backward", "lp_balance_loss"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -1085,3 +1141,281 @@ def lp_preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, ref_logp: O
                                   _raw_stream(dev))
     _raise(st, "lp_preference_loss")
     return LossOutputs(metrics=m, counts=c, margins=h, grad_logp=g)
+
+
+# ------------------------------------------------------------------ between the embedding and the head
+
+def _matrix(t: torch.Tensor, name: str, device: Optional[int] = None):
+    """Checks a [T, H] fp32 or bf16 matrix whose rows are contiguous: (T, H, its dtype's code, row stride)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
+        raise TypeError(f"{name} must be a 2-D CUDA tensor")
+    if t.dtype not in _LP_DTYPES:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    T, H = t.shape
+    return T, H, _LP_DTYPES[t.dtype], _rows(t, name, t.dtype, T, H, t.get_device() if device is None else device)
+
+
+_U64 = (1 << 64) - 1
+
+
+def _rng(rng: Optional[torch.Tensor], device: int) -> Optional[int]:
+    if rng is None:
+        return None
+    return _vector(rng, "rng", torch.int64, 2, device)
+
+
+def lp_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, row_start: int = 0,
+               rng: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Dropout of a bf16 or fp32 [T, H] matrix: x / (1 - p) where an element is kept, else 0; ``p`` in [0, 1]
+    is held to 1 / 65536. Which elements are kept follows from ``seed``, ``offset`` (64-bit) and the number
+    ``row_start`` + t of their row: the gradient is the same call on the gradient, and rows passed in parts
+    are dropped as in one call. ``rng`` (int64 [2] on the GPU) is added to seed and offset when the kernel
+    runs. ``out`` may be x; row strides may be any multiple of 16 bytes."""
+    T, H, dtype, ld = _matrix(x, "x")
+    d, dev = x.get_device(), x.device
+    if out is None:
+        out, ld_out = torch.empty((T, H), dtype=x.dtype, device=dev), H
+    else:
+        ld_out = _rows(out, "out", x.dtype, T, H, d)
+    with _on(dev):
+        st = lib().lp_dropout(x.data_ptr(), T, H, ld, dtype, p, seed & _U64, offset & _U64, row_start, _rng(rng, d),
+                              out.data_ptr(), ld_out, _raw_stream(dev))
+    _raise(st, "lp_dropout")
+    return out
+
+
+def _norm_call(h, y, weight, post_norm, post_weight, gate, residual_scale, eps, weight_offset, dropout, seed, offset,
+               row_start, rng, y_dtype):
+    """Checks what the residual norm and its gradient share: (T, H, device index, inputs, options, weights' dtype)."""
+    T, H, h_dtype, ld_h = _matrix(h, "h")
+    d = h.get_device()
+    ld_y = 0
+    if y is not None:
+        if not isinstance(y, torch.Tensor) or y.dtype not in _LP_DTYPES:
+            raise TypeError("y must be an fp32 or bf16 CUDA tensor")
+        ld_y = _rows(y, "y", y.dtype, T, H, d)
+        y_dtype = y.dtype
+    if y_dtype not in _LP_DTYPES:
+        raise TypeError("the norm's type must be torch.float32 or torch.bfloat16")
+    kind, ld_gate, w_dtype = LP_GATE_NONE, 0, None
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        if gate.dim() == 1:
+            kind, w_dtype = LP_GATE_CHANNEL, gate.dtype
+            _vector(gate, "gate", gate.dtype, H, d)
+        elif gate.dim() == 2 and gate.shape[1] == 1 and gate.shape[0] == T:
+            kind = LP_GATE_TOKEN
+            if gate.dtype is not torch.float32 or not gate.is_contiguous():
+                raise TypeError("a gate of [T, 1] must be contiguous fp32")
+            _on_device(gate, "gate", d)
+        else:
+            kind = LP_GATE_FULL
+            ld_gate = _rows(gate, "gate", y_dtype, T, H, d)
+    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+        if t is not None:
+            w_dtype = getattr(t, "dtype", None) if w_dtype is None else w_dtype
+            _vector(t, name, w_dtype, H, d)
+    if w_dtype is None:
+        w_dtype = torch.float32
+    if w_dtype not in _LP_DTYPES:
+        raise TypeError("weights must be torch.float32 or torch.bfloat16")
+    ci = _NormInputs(h.data_ptr(), _ptr(y), _ptr(weight), _ptr(post_weight), _ptr(gate), _rng(rng, d), ld_h, ld_y, ld_gate)
+    co = _NormOptions(eps, residual_scale, weight_offset, dropout, seed & _U64, offset & _U64, row_start, h_dtype,
+                      _LP_DTYPES[y_dtype], _LP_DTYPES[w_dtype], kind, 1 if post_norm else 0)
+    return T, H, d, ci, co, y_dtype
+
+
+def lp_residual_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                     post_norm: bool = False, post_weight: Optional[torch.Tensor] = None,
+                     gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                     weight_offset: float = 0.0, dropout: float = 0.0, seed: int = 0, offset: int = 0,
+                     row_start: int = 0, rng: Optional[torch.Tensor] = None, norm: bool = True, norm_dtype=None,
+                     out: Optional[dict] = None):
+    """The end of one block and the start of the next in one pass over the rows: (h_out, norm) with
+
+        b     = y,  or with ``post_norm``  y / sqrt(mean y^2 + eps) * (weight_offset + post_weight)
+        h_out = residual_scale * h + dropout(gate * b)
+        norm  = h_out / sqrt(mean h_out^2 + eps) * (weight_offset + weight)
+
+    h: the residual stream, bf16 or fp32 [T, H]; y: the block's output [T, H] (None: (h, the norm of h)); weights
+    [H], all of one type, None for none; ``gate``: [H], fp32 [T, 1] or [T, H] of y's type. norm has y's type (without
+    y: ``norm_dtype``, default h's); ``norm=False`` leaves it out. Dropout as in lp_dropout. ``out`` may hold
+    "h_out" (h itself is allowed) and "norm"."""
+    if norm_dtype is None and y is None:
+        norm_dtype = getattr(h, "dtype", None)
+    T, H, d, ci, co, y_dtype = _norm_call(h, y, weight, post_norm, post_weight, gate, residual_scale, eps, weight_offset,
+                                          dropout, seed, offset, row_start, rng, norm_dtype)
+    if norm_dtype is not None and norm_dtype is not y_dtype:
+        raise TypeError(f"the norm has y's type, {y_dtype}")
+    dev, h_out, n, ld_h_out, ld_n = h.device, None, None, H, H
+    given = {} if out is None else out
+    if y is not None:
+        h_out = given.get("h_out")
+        if h_out is None:
+            h_out = torch.empty((T, H), dtype=h.dtype, device=dev)
+        else:
+            ld_h_out = _rows(h_out, "out['h_out']", h.dtype, T, H, d)
+    elif given.get("h_out") is not None:
+        raise ValueError("out['h_out'] needs y")
+    if norm:
+        n = given.get("norm")
+        if n is None:
+            n = torch.empty((T, H), dtype=y_dtype, device=dev)
+        else:
+            ld_n = _rows(n, "out['norm']", y_dtype, T, H, d)
+    elif given.get("norm") is not None:
+        raise ValueError("out['norm'] needs norm=True")
+    cr = _NormOutputs(_ptr(h_out), _ptr(n), ld_h_out, ld_n)
+    with _on(dev):
+        st = lib().lp_residual_norm(T, H, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _raw_stream(dev))
+    _raise(st, "lp_residual_norm")
+    return (h if y is None else h_out), n
+
+
+def lp_norm_workspace_size(T: int, H: int) -> int:
+    return int(lib().lp_norm_workspace_size(int(T), int(H)))
+
+
+def lp_residual_norm_backward(h_out: torch.Tensor, y: Optional[torch.Tensor], d_norm: Optional[torch.Tensor],
+                              d_h_out: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                              post_norm: bool = False, post_weight: Optional[torch.Tensor] = None,
+                              gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                              weight_offset: float = 0.0, dropout: float = 0.0, seed: int = 0, offset: int = 0,
+                              row_start: int = 0, rng: Optional[torch.Tensor] = None, dw_dtype=torch.float32,
+                              accumulate: bool = False, out: Optional[dict] = None, gate_grad: bool = True,
+                              weight_grad: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of lp_residual_norm from the stream after the block (without y: h), the block's output and the
+    gradients of its two outputs (either may be None), with the forward's weights, gate and options. Returns d_h
+    (of h_out's type), d_y, d_weight and d_post_weight ([H], ``dw_dtype``) and d_gate (of the gate's shape: [H] of
+    ``dw_dtype``, fp32 [T, 1], or [T, H] of y's type), None for what was not given. ``accumulate`` adds into
+    the fp32 [H] sums held by ``out``, which may also hold any of the other results (d_h may be d_h_out, d_y may be
+    d_norm). ``weight_grad=False`` and ``gate_grad=False`` leave those gradients out."""
+    y_dtype = d_norm.dtype if isinstance(d_norm, torch.Tensor) else getattr(h_out, "dtype", None)
+    T, H, d, ci, co, y_dtype = _norm_call(h_out, y, weight, post_norm, post_weight, gate, residual_scale, eps,
+                                          weight_offset, dropout, seed, offset, row_start, rng, y_dtype)
+    if dw_dtype not in _LP_DTYPES:
+        raise TypeError("dw_dtype must be torch.float32 or torch.bfloat16")
+    ld_dn = 0 if d_norm is None else _rows(d_norm, "d_norm", y_dtype, T, H, d)
+    ld_dh = 0 if d_h_out is None else _rows(d_h_out, "d_h_out", h_out.dtype, T, H, d)
+    dev, given = h_out.device, {} if out is None else out
+    r = dict.fromkeys(("d_h", "d_y", "d_weight", "d_post_weight", "d_gate"))
+
+    def rows(name, dtype):
+        t = given.get(name)
+        if t is None:
+            r[name] = torch.empty((T, H), dtype=dtype, device=dev)
+            return H
+        r[name] = t
+        return _rows(t, f"out[{name!r}]", dtype, T, H, d)
+
+    def vector(name):
+        t = given.get(name)
+        if t is None:
+            if accumulate:
+                raise ValueError(f"accumulate=True adds into the caller's {name}: pass it in out")
+            t = torch.empty(H, dtype=dw_dtype, device=dev)
+        _vector(t, f"out[{name!r}]", dw_dtype, H, d)
+        r[name] = t
+
+    ld_out = rows("d_h", h_out.dtype)
+    ld_y = rows("d_y", y_dtype) if y is not None else 0
+    ld_gate = 0
+    if weight is not None and d_norm is not None and weight_grad:
+        vector("d_weight")
+    if post_weight is not None and weight_grad:
+        vector("d_post_weight")
+    if gate is not None and gate_grad:
+        if co.gate_kind == LP_GATE_CHANNEL:
+            vector("d_gate")
+        elif co.gate_kind == LP_GATE_FULL:
+            ld_gate = rows("d_gate", y_dtype)
+        else:
+            t = given.get("d_gate")
+            if t is None:
+                t = torch.empty((T, 1), dtype=torch.float32, device=dev)
+            _check(t, "out['d_gate']", torch.float32, 2)
+            _shape(t, "out['d_gate']", (T, 1))
+            _on_device(t, "out['d_gate']", d)
+            r["d_gate"] = t
+    for name in given:
+        if given[name] is not None and r.get(name) is None:
+            raise ValueError(f"out[{name!r}] is not a gradient of this call")
+    cg = _NormGrads(_ptr(d_norm), _ptr(d_h_out), _ptr(r["d_h"]), _ptr(r["d_y"]), _ptr(r["d_gate"]), _ptr(r["d_weight"]),
+                    _ptr(r["d_post_weight"]), ld_dn, ld_dh, ld_out, ld_y, ld_gate, _LP_DTYPES[dw_dtype],
+                    1 if accumulate else 0)
+    L = lib()
+    sums = r["d_weight"] is not None or r["d_post_weight"] is not None or co.gate_kind == LP_GATE_CHANNEL
+    with _on(dev):
+        at, wsb, _kept = _scratch(L.lp_norm_workspace_size(T, H) if sums else 0, dev, workspace)
+        st = L.lp_residual_norm_backward(T, H, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cg), at, wsb,
+                                         _raw_stream(dev))
+    _raise(st, "lp_residual_norm_backward")
+    return r
+
+
+def lp_balance_workspace_size(T: int, E: int, K: int, n_seqs: int) -> int:
+    return int(lib().lp_balance_workspace_size(int(T), int(E), int(K), int(n_seqs)))
+
+
+def lp_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float = 1.0, z_coef: float = 0.0,
+                    score: str = "softmax", mask: Optional[torch.Tensor] = None,
+                    cu_seqlens: Optional[torch.Tensor] = None, upstream: Optional[torch.Tensor] = None,
+                    grads: bool = True, metrics: bool = True, grad_dtype=None, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> LossOutputs:
+    """Balance loss of a router with its gradient: ``coef`` * E / (K N) sum_e c_e mean_t p_te (+ ``z_coef`` times the
+    mean squared log-sum-exp), c_e the slots of kept tokens that name expert e. logits bf16 or fp32 [T, E], ids int32
+    [T, K] (-1 = unused slot), ``score`` softmax or sigmoid (normalised), mask bool or uint8 [T]; with ``cu_seqlens``
+    (int32 [S + 1]) the balance is taken within each sequence and averaged. ``upstream`` (fp32, one element, on the
+    GPU) multiplies the gradient. Returns loss (0-D), metrics [4] (BALANCE_METRICS), expert_counts int64 [E], counts
+    int64 [2] (kept tokens, sequences that keep one) and grad_logits (``grad_dtype``, default the logits' type;
+    written to ``out`` when given, which may be logits)."""
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2):
+        raise TypeError("logits must be a 2-D CUDA tensor")
+    if logits.dtype not in _LP_DTYPES:
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    T, E = logits.shape
+    d, dev = logits.get_device(), logits.device
+    if T > 0 and E > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have unit column stride")
+    _check(ids, "ids", torch.int32, 2)
+    _on_device(ids, "ids", d)
+    if ids.shape[0] != T:
+        raise ValueError(f"ids must have {T} rows, got {ids.shape[0]}")
+    K = ids.shape[1]
+    if score not in LP_SCORES:
+        raise ValueError(f"score is one of {tuple(LP_SCORES)}")
+    S, cu = 0, None
+    if cu_seqlens is not None:
+        cu = _vector(cu_seqlens, "cu_seqlens", torch.int32, None, d)
+        S = cu_seqlens.shape[0] - 1
+        if S < 0:
+            raise ValueError("cu_seqlens must have n_seqs + 1 entries")
+    if out is not None and not grads:
+        raise ValueError("out needs grads=True")
+    grad_dtype = (logits.dtype if out is None else out.dtype) if grad_dtype is None else grad_dtype
+    if grad_dtype not in _LP_DTYPES:
+        raise TypeError("grad_dtype must be torch.float32 or torch.bfloat16")
+    g, ld_g = out, E
+    if grads and g is None:
+        g = torch.empty((T, E), dtype=grad_dtype, device=dev)
+    elif g is not None:
+        if not (isinstance(g, torch.Tensor) and g.dtype is grad_dtype and g.dim() == 2 and tuple(g.shape) == (T, E)):
+            raise TypeError(f"out must be {grad_dtype} of shape {(T, E)}")
+        _on_device(g, "out", d)
+        if T > 0 and E > 1 and g.stride(1) != 1:
+            raise ValueError("out must have unit column stride")
+        ld_g = max(g.stride(0), E) if T <= 1 else g.stride(0)
+    ld = max(logits.stride(0), E) if T <= 1 else logits.stride(0)
+    m = torch.empty(len(BALANCE_METRICS), dtype=torch.float32, device=dev) if metrics else None
+    experts = torch.empty(E, dtype=torch.int64, device=dev) if metrics else None
+    c = torch.empty(2, dtype=torch.int64, device=dev) if metrics else None
+    ci = _BalanceInputs(logits.data_ptr(), ids.data_ptr(), _mask_bytes(mask, T, d), cu, _upstream(upstream, d), ld, S)
+    co = _BalanceOptions(coef, z_coef, LP_SCORES[score], _LP_DTYPES[logits.dtype], _LP_DTYPES[grad_dtype])
+    cr = _BalanceOutputs(_ptr(m), _ptr(experts), _ptr(c), _ptr(g), ld_g)
+    L = lib()
+    with _on(dev):
+        at, wsb, _kept = _scratch(L.lp_balance_workspace_size(T, E, K, S), dev, workspace)
+        st = L.lp_balance_loss(T, E, K, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), at, wsb, _raw_stream(dev))
+    _raise(st, "lp_balance_loss")
+    return LossOutputs(metrics=m, expert_counts=experts, counts=c, grad_logits=g)

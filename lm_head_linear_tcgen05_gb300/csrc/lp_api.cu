@@ -249,6 +249,7 @@ const char* lp_status_string(lp_status s) {
     case LP_ERR_BOUNDS: return "LP_ERR_BOUNDS: a device bounds check failed (bounds-checked build)";
     case LP_ERR_TOKEN_OUT_OF_RANGE: return "LP_ERR_TOKEN_OUT_OF_RANGE: an embedding id is neither -1 nor in [0, vocab_real)";
     case LP_ERR_SEQ_OFFSETS: return "LP_ERR_SEQ_OFFSETS: cu_seqlens does not ascend from 0 to T";
+    case LP_ERR_EXPERT_OUT_OF_RANGE: return "LP_ERR_EXPERT_OUT_OF_RANGE: an expert id is neither -1 nor in [0, E)";
   }
   return "unknown lp_status";
 }

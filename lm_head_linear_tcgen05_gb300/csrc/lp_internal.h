@@ -305,6 +305,63 @@ size_t preference_ws_bytes(int64_t T, int64_t n_seqs);
 cudaError_t launch_policy_loss(const PolicyParams& p, cudaStream_t s);
 cudaError_t launch_preference_loss(const PreferenceParams& p, cudaStream_t s);
 
+// ------------------------------------------------------------ between embedding and losses
+struct DropoutParams {
+  uint64_t seed, offset;
+  const uint64_t* rng;                   // NULL, or {added to seed, added to offset} on the device
+  int64_t row_start;
+  uint32_t threshold;                    // of 65536; 0: nothing is dropped
+  float factor;                          // 1 / (1 - p), 0 when everything is dropped
+};
+
+struct DropoutCall {
+  DropoutParams drop;
+  const void* x;
+  void* out;
+  int64_t ld_x, ld_out;
+  int32_t T, groups;                     // groups of eight elements a row
+  unsigned int* err;
+};
+
+struct NormParams {
+  DropoutParams drop;
+  const void *h, *y, *w, *wp, *gate;     // backward: h is the stream after the block
+  void *h_out, *norm;
+  int64_t ld_h, ld_y, ld_gate, ld_h_out, ld_norm;
+  float eps, scale, offset, inv_width;
+  int32_t gate_kind, post, w_bf16;
+  int32_t T, groups;
+  unsigned int* err;
+};
+
+struct NormGradParams {
+  NormParams f;                          // h_out and norm unused
+  const void *d_norm, *d_h_out;
+  void *d_h, *d_y, *d_gate, *d_w, *d_wp; // d_gate: by kind
+  int64_t ld_d_norm, ld_d_h_out, ld_d_h, ld_d_y, ld_d_gate;
+  int32_t accumulate, dw_bf16;
+  float* partials;                       // [parts][sums][H]
+};
+
+size_t norm_backward_ws_bytes(int64_t T, int64_t H);
+cudaError_t launch_residual_norm(const NormParams& p, bool h_f32, bool y_f32, cudaStream_t s);
+cudaError_t launch_residual_norm_backward(const NormGradParams& p, bool h_f32, bool y_f32, cudaStream_t s);
+cudaError_t launch_dropout(const DropoutCall& p, bool f32, cudaStream_t s);
+
+struct BalanceParams {
+  lp_balance_inputs in;
+  lp_balance_outputs out;
+  float coef, z_coef;
+  int32_t T, E, K, n_seqs;               // n_seqs 0: over the whole batch
+  int32_t score;
+  int32_t vec;                           // rows of logits and gradient allow 16-byte accesses
+  void* workspace;
+  unsigned int* err;
+};
+
+size_t balance_ws_bytes(int64_t T, int64_t E, int64_t K, int64_t n_seqs);
+cudaError_t launch_balance_loss(const BalanceParams& p, bool logits_f32, bool grad_f32, cudaStream_t s);
+
 // Argument checks and per-device state shared by the translation units of the C ABI.
 lp_status check_partition(const lp_vocab_partition* part, Shards* sh);
 bool valid_rows(int64_t T);
