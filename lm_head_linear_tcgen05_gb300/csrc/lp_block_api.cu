@@ -36,6 +36,11 @@ bool make_drop(DropoutParams* d, int64_t T, int64_t H, float p, uint64_t seed, u
   d->rng = rng;
   d->row_start = row_start;
   d->threshold = uint32_t(std::lrint(double(p) * 65536.0));
+  d->limit = uint32_t(d->threshold * uint64_t(65536) - 1);
+  for (uint32_t r = 0; r < 10; ++r) {
+    d->keys[2 * r] = uint32_t(seed) + r * kPhiloxStep0;
+    d->keys[2 * r + 1] = uint32_t(seed >> 32) + r * kPhiloxStep1;
+  }
   d->factor = d->threshold < 65536 ? float(65536.0 / double(65536 - d->threshold)) : 0.f;
   return true;
 }
@@ -69,9 +74,9 @@ lp_status check_norm(int64_t T, int64_t H, const lp_norm_inputs* in, const lp_no
   p->w = in->weight;
   p->wp = in->post_weight;
   p->gate = in->gate;
-  p->ld_h = in->ld_h;
-  p->ld_y = in->ld_y;
-  p->ld_gate = in->ld_gate;
+  p->ld_h = in->ld_h * size_of(o->h_dtype);
+  p->ld_y = in->ld_y * size_of(o->y_dtype);
+  p->ld_gate = in->ld_gate * size_of(o->y_dtype);
   p->eps = o->eps;
   p->scale = o->residual_scale;
   p->offset = o->weight_offset;
@@ -104,8 +109,8 @@ lp_status lp_dropout(const void* x, int64_t T, int64_t H, int64_t ld_x, lp_dtype
   if ((st = device_error_word(&c.err)) != LP_OK) return st;
   c.x = x;
   c.out = out;
-  c.ld_x = ld_x;
-  c.ld_out = ld_out;
+  c.ld_x = ld_x * size_of(dtype);
+  c.ld_out = ld_out * size_of(dtype);
   c.T = int32_t(T);
   c.groups = int32_t(H / 8);
   return launch_dropout(c, dtype == LP_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LP_OK
@@ -128,8 +133,8 @@ lp_status lp_residual_norm(int64_t T, int64_t H, const lp_norm_inputs* in, const
   if ((st = device_error_word(&p.err)) != LP_OK) return st;
   p.h_out = out->h_out;
   p.norm = out->norm;
-  p.ld_h_out = out->ld_h_out;
-  p.ld_norm = out->ld_norm;
+  p.ld_h_out = out->ld_h_out * size_of(opts->h_dtype);
+  p.ld_norm = out->ld_norm * size_of(opts->y_dtype);
   return launch_residual_norm(p, opts->h_dtype == LP_DTYPE_F32, opts->y_dtype == LP_DTYPE_F32,
                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? LP_OK
@@ -190,11 +195,11 @@ lp_status lp_residual_norm_backward(int64_t T, int64_t H, const lp_norm_inputs* 
   p.d_gate = g->d_gate;
   p.d_w = g->d_weight;
   p.d_wp = g->d_post_weight;
-  p.ld_d_norm = g->ld_d_norm;
-  p.ld_d_h_out = g->ld_d_h_out;
-  p.ld_d_h = g->ld_d_h;
-  p.ld_d_y = g->ld_d_y;
-  p.ld_d_gate = g->ld_d_gate;
+  p.ld_d_norm = g->ld_d_norm * size_of(opts->y_dtype);
+  p.ld_d_h_out = g->ld_d_h_out * size_of(opts->h_dtype);
+  p.ld_d_h = g->ld_d_h * size_of(opts->h_dtype);
+  p.ld_d_y = g->ld_d_y * size_of(opts->y_dtype);
+  p.ld_d_gate = g->ld_d_gate * size_of(opts->y_dtype);
   p.accumulate = g->accumulate;
   p.dw_bf16 = g->dw_dtype == LP_DTYPE_BF16;
   return launch_residual_norm_backward(p, opts->h_dtype == LP_DTYPE_F32, opts->y_dtype == LP_DTYPE_F32, s) ==
@@ -259,9 +264,8 @@ lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balance_inpu
   p.K = int32_t(K);
   p.n_seqs = int32_t(n_seqs);
   p.workspace = workspace;
-  return launch_balance_loss(p, opts->logits_dtype == LP_DTYPE_F32, opts->grad_dtype == LP_DTYPE_F32, s) == cudaSuccess
-             ? LP_OK
-             : LP_ERR_CUDA;
+  p.grad_f32 = opts->grad_dtype == LP_DTYPE_F32;
+  return launch_balance_loss(p, opts->logits_dtype == LP_DTYPE_F32, s) == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 
 }  // extern "C"

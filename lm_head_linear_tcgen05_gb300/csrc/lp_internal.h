@@ -311,14 +311,19 @@ struct DropoutParams {
   const uint64_t* rng;                   // NULL, or {added to seed, added to offset} on the device
   int64_t row_start;
   uint32_t threshold;                    // of 65536; 0: nothing is dropped
+  uint32_t limit;                        // threshold 2^16 - 1 (threshold > 0)
   float factor;                          // 1 / (1 - p), 0 when everything is dropped
+  uint32_t keys[20];                     // of the generator's ten rounds, from seed
 };
+
+// key increments of Philox4x32 (Salmon and others, 2011)
+constexpr uint32_t kPhiloxStep0 = 0x9E3779B9u, kPhiloxStep1 = 0xBB67AE85u;
 
 struct DropoutCall {
   DropoutParams drop;
   const void* x;
   void* out;
-  int64_t ld_x, ld_out;
+  int64_t ld_x, ld_out;                  // in bytes, as all row strides of these calls
   int32_t T, groups;                     // groups of eight elements a row
   unsigned int* err;
 };
@@ -353,14 +358,13 @@ struct BalanceParams {
   lp_balance_outputs out;
   float coef, z_coef;
   int32_t T, E, K, n_seqs;               // n_seqs 0: over the whole batch
-  int32_t score;
-  int32_t vec;                           // rows of logits and gradient allow 16-byte accesses
+  int32_t score, grad_f32;
   void* workspace;
   unsigned int* err;
 };
 
 size_t balance_ws_bytes(int64_t T, int64_t E, int64_t K, int64_t n_seqs);
-cudaError_t launch_balance_loss(const BalanceParams& p, bool logits_f32, bool grad_f32, cudaStream_t s);
+cudaError_t launch_balance_loss(const BalanceParams& p, bool logits_f32, cudaStream_t s);
 
 // Argument checks and per-device state shared by the translation units of the C ABI.
 lp_status check_partition(const lp_vocab_partition* part, Shards* sh);

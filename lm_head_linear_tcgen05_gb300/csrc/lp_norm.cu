@@ -6,8 +6,10 @@
 // sums, so each input is read once and each output written once. Rows of up to 512 columns belong to part of a
 // warp or a whole one, wider ones to a CTA; which depends on H alone, and so does the order of a row's
 // sums: its bits do not depend on the batch.
-// Bounds: memory. Each thread copies its part of the next rows into shared memory (cp.async) while it works on
-// the present one, so that the reads need neither registers nor a row's sums to be finished.
+// Bounds: memory, if little enough is issued for each element. So CTAs stay for many rows, with their columns'
+// weights in registers (the post norm's and a channel gate's as one product), arithmetic is in pairs, and each
+// thread copies its part of the next rows into shared memory (cp.async) while it works on the present one: the
+// reads need neither registers nor a row's sums to be finished.
 #include "lp_rows.cuh"
 
 namespace lp {
@@ -16,75 +18,68 @@ namespace {
 
 constexpr int kSmallThreads = 256;  // CTAs whose rows are parts of warps
 constexpr int kMaxThreads = 512;    // a CTA per row
-constexpr int kMaxDepth = 3;        // rows in flight, the present one among them
+constexpr int kSms = 152;
+constexpr int64_t kShared = 220 * 1024;  // of an SM, for the rows in flight
 
-// N sums over the CTA, in the order of the warps; every thread gets them. Calls alternate between two
-// halves of `scratch`, so that one barrier a call is enough.
-template <int N>
-__device__ __forceinline__ void sum_cta(float (&v)[N], float (*scratch)[kMaxThreads / 32], int& half) {
-  sum_lanes<32>(v);
-  float (*at)[kMaxThreads / 32] = scratch + half * N;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) at[i][threadIdx.x >> 5] = v[i];
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = at[i][0];
-    for (int w = 1; w < warps; ++w) s = __fadd_rn(s, at[i][w]);
-    v[i] = s;
-  }
-  half ^= 1;
-}
+// What joins the stream: nothing, y times factors of its row and columns, or that with a factor of every element
+// (full gate, dropout).
+enum Branch { kNoBranch, kScaled, kElementwise };
 
 // LANES lanes to a row (0: the CTA), each with CPL groups of eight columns.
-template <bool HF, bool YF, int LANES, int CPL>
-__global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES > 0 ? 4 : CPL > 2 ? 1 : 2)
+template <bool HF, bool YF, int LANES, int CPL, int BRANCH>
+__global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES > 0 ? 2 : 1)
     norm_kernel(const __grid_constant__ NormParams p, int depth) {
+  constexpr int kY = kUnits<HF> * CPL, kGate = kY + kUnits<YF> * CPL;  // units of a stage before y's, the gate's
+  constexpr int kStage = BRANCH == kNoBranch ? kY : BRANCH == kScaled ? kGate : kGate + kUnits<YF> * CPL;
   extern __shared__ uint4 ring[];
-  __shared__ float scratch[2][kMaxThreads / 32];
+  __shared__ CtaSums<1> sums;
   int half = 0;
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const int width = LANES > 0 ? LANES : threads, lane = LANES > 0 ? tid % width : tid;
-  const int per_cta = LANES > 0 ? kSmallThreads / width : 1;
-  const bool has_y = p.y != nullptr, full = p.gate_kind == LP_GATE_FULL, drop = p.drop.threshold > 0;
-  const int at_y = kUnits<HF>, at_gate = at_y + kUnits<YF>;
-  const int units = has_y ? (full ? at_gate + kUnits<YF> : at_gate) : at_y;
-  auto slot = [&](int stage, int unit, int c) -> uint4* { return ring + ((stage * units + unit) * CPL + c) * threads + tid; };
+  if constexpr (LANES == 0) sums.clear();
+  const int tid = threadIdx.x;
+  const int width = LANES > 0 ? LANES : blockDim.x, lane = LANES > 0 ? tid % LANES : tid;
+  const int per_cta = LANES > 0 ? kSmallThreads / (LANES > 0 ? LANES : 1) : 1;
+  const bool full = BRANCH == kElementwise && p.gate_kind == LP_GATE_FULL;
+  const uint32_t part = smem_u32(ring) + uint32_t(tid) * part_units(depth, kStage) * 16;
+  const Rows h{(char*)p.h, p.ld_h}, y{(char*)p.y, p.ld_y}, z{(char*)p.gate, p.ld_gate};
+  const Rows h_out{(char*)p.h_out, p.ld_h_out}, norm{(char*)p.norm, p.ld_norm};
   auto fetch = [&](int64_t row, int stage) {
+    const uint32_t to = part + stage * (kStage * 16);
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
       const int g = lane + c * width;
       if (row >= p.T || g >= p.groups) continue;
-      const uint4* h = group_at<HF>(p.h, row, p.ld_h, g);
 #pragma unroll
-      for (int i = 0; i < kUnits<HF>; ++i) copy_async16(slot(stage, i, c), h + i);
-      if (!has_y) continue;
-      const uint4* y = group_at<YF>(p.y, row, p.ld_y, g);
+      for (int i = 0; i < kUnits<HF>; ++i) copy_async16(to + (c * kUnits<HF> + i) * 16, h.at<HF>(row, g) + i);
+      if constexpr (BRANCH != kNoBranch) {
 #pragma unroll
-      for (int i = 0; i < kUnits<YF>; ++i) copy_async16(slot(stage, at_y + i, c), y + i);
-      if (!full) continue;
-      const uint4* z = group_at<YF>(p.gate, row, p.ld_gate, g);
+        for (int i = 0; i < kUnits<YF>; ++i) copy_async16(to + (kY + c * kUnits<YF> + i) * 16, y.at<YF>(row, g) + i);
+      }
+      if (full) {
 #pragma unroll
-      for (int i = 0; i < kUnits<YF>; ++i) copy_async16(slot(stage, at_gate + i, c), z + i);
+        for (int i = 0; i < kUnits<YF>; ++i) copy_async16(to + (kGate + c * kUnits<YF> + i) * 16, z.at<YF>(row, g) + i);
+      }
     }
   };
-  auto read_y = [&](int stage, int unit, int c, float (&f)[8]) {
+  auto read_h = [&](uint32_t at, int c) {
+    Group<HF> v;
+#pragma unroll
+    for (int i = 0; i < kUnits<HF>; ++i) v.v[i] = read_shared16(at + (c * kUnits<HF> + i) * 16);
+    return v.unpack();
+  };
+  auto read_y = [&](uint32_t at, int first, int c) {
     Group<YF> v;
 #pragma unroll
-    for (int i = 0; i < kUnits<YF>; ++i) v.v[i] = *slot(stage, unit + i, c);
-    v.unpack(f);
+    for (int i = 0; i < kUnits<YF>; ++i) v.v[i] = read_shared16(at + (first + c * kUnits<YF> + i) * 16);
+    return v.unpack();
   };
-  auto row_sum = [&](float x) {
-    float v[1] = {x};
+  auto row_sum = [&](uint64_t pair) {
+    float v[1] = {both_of(pair)};
     if constexpr (LANES > 0)
       sum_lanes<LANES>(v);
     else
-      sum_cta(v, scratch, half);
+      sums.add(v, half);
     return v[0];
   };
-  const Philox rng(p.drop);
   const int64_t step = int64_t(gridDim.x) * per_cta;
   int64_t row = int64_t(blockIdx.x) * per_cta + (LANES > 0 ? tid / width : 0);
   // rows that share a warp are worked on together, so a warp goes on while its first one exists
@@ -93,118 +88,106 @@ __global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES
     fetch(row + d * step, d);
     copy_async_commit();
   }
-  for (int stage = 0; first < p.T; first += step, row += step) {
-    const int ahead = stage == 0 ? depth - 1 : stage - 1;
-    fetch(row + (depth - 1) * step, ahead);
-    copy_async_commit();
-    if (depth == 3)
-      copy_async_wait<2>();
-    else if (depth == 2)
-      copy_async_wait<1>();
-    else
-      copy_async_wait<0>();
-    const bool here = row < p.T;
-    float u[CPL][8], square = 0.f;
-    float ry = 1.f;
-    if (p.post) {
-      float s = 0.f;
+  // the columns' factors of the norm, and of y
+  Eight w[CPL], before[BRANCH == kNoBranch ? 1 : CPL];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        if (!here || lane + c * width >= p.groups) continue;
-        float y[8];
-        read_y(stage, at_y, c, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = __fmaf_rn(y[i], y[i], s);
-      }
-      ry = __frsqrt_rn(__fmaf_rn(row_sum(s), p.inv_width, p.eps));
+  for (int c = 0; c < CPL; ++c) {
+    const int g = lane + c * width;
+    w[c] = all_of(0.f);
+    if constexpr (BRANCH != kNoBranch) before[c] = all_of(0.f);
+    if (g >= p.groups) continue;
+    w[c] = weight_factor(p.w, p.w_bf16, p.offset, g);
+    if constexpr (BRANCH != kNoBranch) {
+      before[c] = weight_factor(p.wp, p.w_bf16, p.offset, g);
+      if (p.gate_kind == LP_GATE_CHANNEL) before[c] = before[c] * load_vector(p.gate, p.w_bf16, g);
     }
-    const float token = p.gate_kind == LP_GATE_TOKEN && here ? __ldg(static_cast<const float*>(p.gate) + row) : 1.f;
+  }
+  const Philox<false> rng(p.drop);
+  for (int stage = 0; first < p.T; first += step, row += step) {
+    fetch(row + (depth - 1) * step, stage == 0 ? depth - 1 : stage - 1);
+    copy_async_commit();
+    copy_async_oldest(depth);
+    const uint32_t at = part + stage * (kStage * 16);
+    const bool here = row < p.T;
+    float mult = 1.f;  // the row's factor of y
+    if constexpr (BRANCH != kNoBranch) {
+      if (p.post) {
+        uint64_t s = 0;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+          if (!here || lane + c * width >= p.groups) continue;
+          const Eight b = read_y(at, kY, c);
+          dot8(s, b, b);
+        }
+        mult = rsqrtf(__fmaf_rn(row_sum(s), p.inv_width, p.eps));
+      }
+      if (p.gate_kind == LP_GATE_TOKEN && here) mult *= __ldg(static_cast<const float*>(p.gate) + row);
+    }
+    Eight u[CPL];
+    uint64_t square = 0;
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
       const int g = lane + c * width;
       if (!here || g >= p.groups) continue;
-      Group<HF> h;
-#pragma unroll
-      for (int i = 0; i < kUnits<HF>; ++i) h.v[i] = *slot(stage, i, c);
-      h.unpack(u[c]);
-      if (has_y) {
-        float b[8], f[8];
-        read_y(stage, at_y, c, b);
-        if (p.post) {
-          if (p.wp != nullptr) load_vector(p.wp, p.w_bf16, g, f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] *= p.wp != nullptr ? ry * (p.offset + f[i]) : ry;
+      u[c] = read_h(at, c);
+      if constexpr (BRANCH != kNoBranch) {
+        Eight b = read_y(at, kY, c) * (before[c] * mult);
+        if constexpr (BRANCH == kElementwise) {
+          if (full) b = b * read_y(at, kGate, c);
+          if (p.drop.threshold > 0)
+            b = drop8(b, rng.words(uint64_t(p.drop.row_start + row) * uint32_t(p.groups) + g), p.drop.limit, p.drop.factor);
         }
-        if (p.gate_kind == LP_GATE_TOKEN) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] *= token;
-        } else if (p.gate_kind != LP_GATE_NONE) {
-          if (full)
-            read_y(stage, at_gate, c, f);
-          else
-            load_vector(p.gate, p.w_bf16, g, f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] *= f[i];
-        }
-        if (drop) {
-          const uint32_t kept = kept_bits(rng, uint64_t(p.drop.row_start + row) * uint32_t(p.groups) + g, p.drop.threshold);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] = (kept >> i) & 1u ? b[i] * p.drop.factor : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[c][i] = __fmaf_rn(p.scale, u[c][i], b[i]);
-        store_group<HF>(group_at<HF>(p.h_out, row, p.ld_h_out, g), u[c]);
+        u[c] = fma8(u[c], p.scale, b);
+        store_group<HF>(h_out.at<HF>(row, g), u[c]);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) square = __fmaf_rn(u[c][i], u[c][i], square);
+      dot8(square, u[c], u[c]);
     }
     if (p.norm != nullptr) {
-      const float r = __frsqrt_rn(__fmaf_rn(row_sum(square), p.inv_width, p.eps));
+      const float r = rsqrtf(__fmaf_rn(row_sum(square), p.inv_width, p.eps));
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
         const int g = lane + c * width;
-        if (!here || g >= p.groups) continue;
-        float f[8];
-        if (p.w != nullptr) load_vector(p.w, p.w_bf16, g, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[c][i] = p.w != nullptr ? u[c][i] * r * (p.offset + f[i]) : u[c][i] * r;
-        store_group<YF>(group_at<YF>(p.norm, row, p.ld_norm, g), u[c]);
+        if (here && g < p.groups) store_group<YF>(norm.at<YF>(row, g), u[c] * (w[c] * r));
       }
     }
     if (++stage == depth) stage = 0;
   }
 }
 
-constexpr int kSms = 152;
-constexpr int64_t kShared = 220 * 1024;  // of an SM, for the rows in flight
-
-template <bool HF, bool YF, int LANES, int CPL>
+template <bool HF, bool YF, int LANES, int CPL, int BRANCH>
 cudaError_t launch_rows(const NormParams& p, cudaStream_t s) {
   const int threads = LANES > 0 ? kSmallThreads : (p.groups + 32 * CPL - 1) / (32 * CPL) * 32;
   const int per_cta = LANES > 0 ? kSmallThreads / (LANES > 0 ? LANES : 1) : 1;
-  const int units = kUnits<HF> + (p.y != nullptr ? kUnits<YF> * (p.gate_kind == LP_GATE_FULL ? 2 : 1) : 0);
-  const int64_t stage = int64_t(units) * CPL * threads * 16;
-  const int resident = (CPL > 2 ? 512 : 1024) / threads;  // CTAs an SM holds by registers
-  int depth = int(kShared / (resident * stage));
-  depth = depth < 1 ? 1 : depth > kMaxDepth ? kMaxDepth : depth;
+  const int units = CPL * (kUnits<HF> + (BRANCH == kNoBranch ? 0 : BRANCH == kScaled ? 1 : 2) * kUnits<YF>);
+  constexpr int kHeld = CPL > 2 || BRANCH == kElementwise ? 512 : 768;  // threads that an SM's registers hold
+  const int resident = kHeld / threads;
+  int depth = kMaxDepth;
+  while (depth > 1 && int64_t(resident) * part_units(depth, units) * 16 * threads > kShared) --depth;
   const int64_t ctas = (int64_t(p.T) + per_cta - 1) / per_cta;
-  const size_t shared = size_t(depth * stage);
+  const size_t shared = size_t(part_units(depth, units)) * 16 * threads;
   cudaError_t e = cudaSuccess;
-  if (shared > 40 * 1024) e = allow_shared<norm_kernel<HF, YF, LANES, CPL>>();
+  if (shared > 40 * 1024) e = allow_shared<norm_kernel<HF, YF, LANES, CPL, BRANCH>>();
   if (e != cudaSuccess) return e;
-  norm_kernel<HF, YF, LANES, CPL><<<int(ctas < int64_t(kSms) * resident ? ctas : int64_t(kSms) * resident), threads,
-                                   shared, s>>>(p, depth);
+  norm_kernel<HF, YF, LANES, CPL, BRANCH><<<int(ctas < int64_t(kSms) * resident ? ctas : int64_t(kSms) * resident),
+                                           threads, shared, s>>>(p, depth);
   return cudaGetLastError();
+}
+
+template <bool HF, bool YF, int BRANCH>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
+  if (p.groups <= 8) return launch_rows<HF, YF, 8, 1, BRANCH>(p, s);
+  if (p.groups <= 16) return launch_rows<HF, YF, 16, 1, BRANCH>(p, s);
+  if (p.groups <= 32) return launch_rows<HF, YF, 32, 1, BRANCH>(p, s);
+  if (p.groups <= 64) return launch_rows<HF, YF, 32, 2, BRANCH>(p, s);
+  if (p.groups <= 1024) return launch_rows<HF, YF, 0, 2, BRANCH>(p, s);
+  return launch_rows<HF, YF, 0, 4, BRANCH>(p, s);
 }
 
 template <bool HF, bool YF>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
-  if (p.groups <= 8) return launch_rows<HF, YF, 8, 1>(p, s);
-  if (p.groups <= 16) return launch_rows<HF, YF, 16, 1>(p, s);
-  if (p.groups <= 32) return launch_rows<HF, YF, 32, 1>(p, s);
-  if (p.groups <= 64) return launch_rows<HF, YF, 32, 2>(p, s);
-  if (p.groups <= 1024) return launch_rows<HF, YF, 0, 2>(p, s);
-  return launch_rows<HF, YF, 0, 4>(p, s);
+  if (p.y == nullptr) return launch_norm<HF, YF, kNoBranch>(p, s);
+  if (p.gate_kind == LP_GATE_FULL || p.drop.threshold > 0) return launch_norm<HF, YF, kElementwise>(p, s);
+  return launch_norm<HF, YF, kScaled>(p, s);
 }
 
 // ------------------------------------------------------------------ dropout
@@ -212,35 +195,47 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
 constexpr int kDropThreads = 256;
 constexpr int kDropGroups = 4;  // groups of a thread
 
-template <bool F32>
+// LINEAR: the rows follow one another without gaps, so a group's place in memory is its counter's.
+template <bool F32, bool LINEAR, bool HOST_KEYS>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropoutCall p) {
-  const Philox rng(p.drop);
+  const Philox<HOST_KEYS> rng(p.drop);
   const int64_t n = int64_t(p.T) * p.groups;
   const int64_t base = int64_t(blockIdx.x) * (kDropThreads * kDropGroups) + threadIdx.x;
+  const Rows x{(char*)p.x, p.ld_x}, out{(char*)p.out, p.ld_out};
   Group<F32> v[kDropGroups];
-  uint4* to[kDropGroups];
+  auto place = [&](const Rows& m, int64_t i) {
+    if constexpr (LINEAR) return reinterpret_cast<uint4*>(m.base) + i * kUnits<F32>;
+    const int64_t row = n <= int64_t(UINT32_MAX) ? int64_t(uint32_t(i) / uint32_t(p.groups)) : i / p.groups;
+    return m.at<F32>(row, int(i - row * p.groups));
+  };
 #pragma unroll
   for (int k = 0; k < kDropGroups; ++k) {
     const int64_t i = base + k * kDropThreads;
     if (i >= n) continue;
-    const int64_t row = i / p.groups;
-    const int g = int(i - row * p.groups);
-    const uint4* x = group_at<F32>(p.x, row, p.ld_x, g);
-    to[k] = group_at<F32>(p.out, row, p.ld_out, g);
+    const uint4* from = place(x, i);
 #pragma unroll
-    for (int j = 0; j < kUnits<F32>; ++j) v[k].v[j] = x[j];
+    for (int j = 0; j < kUnits<F32>; ++j) v[k].v[j] = from[j];
   }
+  const uint64_t counter = uint64_t(p.drop.row_start) * uint32_t(p.groups) + base;
 #pragma unroll
   for (int k = 0; k < kDropGroups; ++k) {
     const int64_t i = base + k * kDropThreads;
     if (i >= n) continue;
-    const uint32_t kept = kept_bits(rng, uint64_t(p.drop.row_start) * uint32_t(p.groups) + i, p.drop.threshold);
-    float f[8];
-    v[k].unpack(f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = (kept >> j) & 1u ? f[j] * p.drop.factor : 0.f;
-    store_group<F32>(to[k], f);
+    Eight e = v[k].unpack();
+    if (p.drop.threshold > 0) e = drop8(e, rng.words(counter + k * kDropThreads), p.drop.limit, p.drop.factor);
+    store_group<F32>(place(out, i), e);
   }
+}
+
+template <bool F32, bool LINEAR>
+cudaError_t launch_drop(const DropoutCall& p, cudaStream_t s) {
+  const int64_t n = int64_t(p.T) * p.groups, per = kDropThreads * kDropGroups;
+  const unsigned ctas = unsigned((n + per - 1) / per);
+  if (p.drop.rng == nullptr)
+    dropout_kernel<F32, LINEAR, true><<<ctas, kDropThreads, 0, s>>>(p);
+  else
+    dropout_kernel<F32, LINEAR, false><<<ctas, kDropThreads, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -251,13 +246,10 @@ cudaError_t launch_residual_norm(const NormParams& p, bool h_f32, bool y_f32, cu
 }
 
 cudaError_t launch_dropout(const DropoutCall& p, bool f32, cudaStream_t s) {
-  const int64_t n = int64_t(p.T) * p.groups, per = kDropThreads * kDropGroups;
-  const unsigned ctas = unsigned((n + per - 1) / per);
-  if (f32)
-    dropout_kernel<true><<<ctas, kDropThreads, 0, s>>>(p);
-  else
-    dropout_kernel<false><<<ctas, kDropThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const int64_t row = int64_t(p.groups) * (f32 ? 32 : 16);
+  const bool linear = (p.ld_x == row && p.ld_out == row) || p.T == 1;
+  if (f32) return linear ? launch_drop<true, true>(p, s) : launch_drop<true, false>(p, s);
+  return linear ? launch_drop<false, true>(p, s) : launch_drop<false, false>(p, s);
 }
 
 }  // namespace lp

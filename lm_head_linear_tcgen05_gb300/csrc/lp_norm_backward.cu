@@ -2,10 +2,13 @@
 //
 // Per row, u the stream after the block, r = rsqrt(mean u^2 + eps), a = dn (o + w), D = dh + r a - u r^3 mean(a u):
 // the gradient of u, from which d_h = R D and, through dropout, gate and the norm on y, d_y. The sums over
-// tokens (d_weight, d_post_weight, a channel gate's gradient) stay in the registers of the thread that has the
-// columns; each CTA writes its own and a second kernel adds the CTAs' in order.
-// Bounds: memory. A thread's part of the next rows is copied to shared memory while it works on the present one,
-// and read from there as often as the sums need it.
+// tokens stay in the registers of the thread that has the columns; each CTA writes its own and a second kernel
+// adds the CTAs' in order. Two suffice: d_weight, and S = sum of dropout(D) y / rms(y) (times the gate of the
+// token or element), for of its columns d_post_weight is S times the channel gate and a channel gate's gradient
+// S times the post norm's weight.
+// Bounds: memory, if little enough is issued for each element: as in the forward, columns' weights stay in
+// registers and a thread's part of the next rows is copied to shared memory while it works on the present one,
+// and read from there as often as the row's sums need it.
 #include "lp_rows.cuh"
 
 namespace lp {
@@ -14,32 +17,13 @@ namespace {
 
 constexpr int kSmallThreads = 256;
 constexpr int kMaxThreads = 512;
-constexpr int kMaxDepth = 3;
-constexpr int kSums = 3;  // over tokens: d_weight, d_post_weight, a channel gate's gradient
+constexpr int kSums = 2;  // over tokens
 constexpr int kSms = 152;
 constexpr int64_t kShared = 220 * 1024;
-constexpr int kPairGroups = 1024;  // rows of more groups belong to a cluster of two CTAs
+constexpr int kPairGroups = 1024;  // rows of more groups belong to a cluster of two CTAs, half of the columns each
 
-template <int N>
-__device__ __forceinline__ void sum_cta(float (&v)[N], float (*scratch)[kMaxThreads / 32], int& half) {
-  sum_lanes<32>(v);
-  float (*at)[kMaxThreads / 32] = scratch + half * 3;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) at[i][threadIdx.x >> 5] = v[i];
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = at[i][0];
-    for (int w = 1; w < warps; ++w) s = __fadd_rn(s, at[i][w]);
-    v[i] = s;
-  }
-  half ^= 1;
-}
-
-// The same sums over the two CTAs of a cluster, each of which has written its own to both. `half` has already been
-// turned by sum_cta.
+// The sums over the two CTAs of a cluster, each of which writes its own to both. Calls alternate between the
+// halves of `both`.
 template <int N>
 __device__ __forceinline__ void sum_pair(float (&v)[N], float (*both)[2][3], int half) {
   const uint32_t rank = cluster_ctarank();
@@ -57,79 +41,77 @@ __device__ __forceinline__ void sum_pair(float (&v)[N], float (*both)[2][3], int
   for (int i = 0; i < N; ++i) v[i] = __fadd_rn(both[half][0][i], both[half][1][i]);
 }
 
-template <bool HF, bool YF, int LANES, int CPL, bool PAIR>
+// As in the forward: nothing joins the stream, y times factors of its row and columns, or of every element too.
+enum Branch { kNoBranch, kScaled, kElementwise };
+
+template <bool HF, bool YF, int LANES, int CPL, bool PAIR, int BRANCH>
 __global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES > 0 ? 2 : 1)
     norm_grad_kernel(const __grid_constant__ NormGradParams p, int depth) {
+  constexpr bool kHasY = BRANCH != kNoBranch;
+  constexpr int kUH = kUnits<HF> * CPL, kUY = kUnits<YF> * CPL;
+  constexpr int kN = kUH, kD = kN + kUY, kY = kD + kUH, kGate = kY + kUY;  // units of a stage before dn's, dh's, y's, the gate's
+  constexpr int kStage = BRANCH == kNoBranch ? kY : BRANCH == kScaled ? kGate : kGate + kUY;
   extern __shared__ uint4 ring[];
-  __shared__ float scratch[6][kMaxThreads / 32];
+  __shared__ CtaSums<3> sums;
   __shared__ float both[2][2][3];
   int half = 0;
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const int width = LANES > 0 ? LANES : threads, lane = LANES > 0 ? tid % width : tid;
-  const int per_cta = LANES > 0 ? kSmallThreads / width : 1;
+  if constexpr (LANES == 0) sums.clear();
+  const int tid = threadIdx.x;
+  const int width = LANES > 0 ? LANES : blockDim.x, lane = LANES > 0 ? tid % (LANES > 0 ? LANES : 1) : tid;
+  const int per_cta = LANES > 0 ? kSmallThreads / (LANES > 0 ? LANES : 1) : 1;
   const int unit = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x), grid_units = PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
-  const int g0 = PAIR ? int(blockIdx.x & 1) * (threads * CPL) : 0;  // the CTA's first group
-  const bool has_y = p.f.y != nullptr, has_n = p.d_norm != nullptr, has_h = p.d_h_out != nullptr;
-  const bool full = p.f.gate_kind == LP_GATE_FULL, channel = p.f.gate_kind == LP_GATE_CHANNEL,
-             token_gate = p.f.gate_kind == LP_GATE_TOKEN, drop = p.f.drop.threshold > 0;
-  const int at_y = kUnits<HF>, at_n = at_y + (has_y ? kUnits<YF> : 0), at_h = at_n + (has_n ? kUnits<YF> : 0),
-            at_gate = at_h + (has_h ? kUnits<HF> : 0), units = at_gate + (full ? kUnits<YF> : 0);
-  auto slot = [&](int stage, int u, int c) -> uint4* { return ring + ((stage * units + u) * CPL + c) * threads + tid; };
-  auto copy_h = [&](const void* base, int64_t row, int64_t ld, int g, int stage, int u, int c) {
-    const uint4* x = group_at<HF>(base, row, ld, g);
+  const int g0 = (PAIR ? int(blockIdx.x & 1) * (int(blockDim.x) * CPL) : 0) + lane;  // the thread's first group
+  const int T = p.f.T, groups = p.f.groups;
+  const bool has_n = p.d_norm != nullptr, has_d = p.d_h_out != nullptr, post = kHasY && p.f.post;
+  const bool full = BRANCH == kElementwise && p.f.gate_kind == LP_GATE_FULL, drop = BRANCH == kElementwise && p.f.drop.threshold > 0;
+  const bool channel = kHasY && p.f.gate_kind == LP_GATE_CHANNEL, token_gate = kHasY && p.f.gate_kind == LP_GATE_TOKEN;
+  const uint32_t part = smem_u32(ring) + uint32_t(tid) * part_units(depth, kStage) * 16;
+  const Rows h{(char*)p.f.h, p.f.ld_h}, y{(char*)p.f.y, p.f.ld_y}, z{(char*)p.f.gate, p.f.ld_gate};
+  const Rows dn{(char*)p.d_norm, p.ld_d_norm}, dh{(char*)p.d_h_out, p.ld_d_h_out};
+  auto copy_h = [&](const Rows& from, int64_t row, int g, uint32_t to) {
 #pragma unroll
-    for (int i = 0; i < kUnits<HF>; ++i) copy_async16(slot(stage, u + i, c), x + i);
+    for (int i = 0; i < kUnits<HF>; ++i) copy_async16(to + i * 16, from.at<HF>(row, g) + i);
   };
-  auto copy_y = [&](const void* base, int64_t row, int64_t ld, int g, int stage, int u, int c) {
-    const uint4* x = group_at<YF>(base, row, ld, g);
+  auto copy_y = [&](const Rows& from, int64_t row, int g, uint32_t to) {
 #pragma unroll
-    for (int i = 0; i < kUnits<YF>; ++i) copy_async16(slot(stage, u + i, c), x + i);
+    for (int i = 0; i < kUnits<YF>; ++i) copy_async16(to + i * 16, from.at<YF>(row, g) + i);
   };
   auto fetch = [&](int64_t row, int stage) {
+    const uint32_t to = part + stage * (kStage * 16);
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
-      const int g = g0 + lane + c * width;
-      if (row >= p.f.T || g >= p.f.groups) continue;
-      copy_h(p.f.h, row, p.f.ld_h, g, stage, 0, c);
-      if (has_y) copy_y(p.f.y, row, p.f.ld_y, g, stage, at_y, c);
-      if (has_n) copy_y(p.d_norm, row, p.ld_d_norm, g, stage, at_n, c);
-      if (has_h) copy_h(p.d_h_out, row, p.ld_d_h_out, g, stage, at_h, c);
-      if (full) copy_y(p.f.gate, row, p.f.ld_gate, g, stage, at_gate, c);
+      const int g = g0 + c * width;
+      if (row >= T || g >= groups) continue;
+      const uint32_t th = to + c * (kUnits<HF> * 16), ty = to + c * (kUnits<YF> * 16);
+      copy_h(h, row, g, th);
+      if (has_n) copy_y(dn, row, g, ty + kN * 16);
+      if (has_d) copy_h(dh, row, g, th + kD * 16);
+      if constexpr (kHasY) copy_y(y, row, g, ty + kY * 16);
+      if (full) copy_y(z, row, g, ty + kGate * 16);
     }
   };
-  auto read_h = [&](int stage, int u, int c, float (&f)[8]) {
+  auto read_h = [&](uint32_t at, int first, int c) {
     Group<HF> v;
 #pragma unroll
-    for (int i = 0; i < kUnits<HF>; ++i) v.v[i] = *slot(stage, u + i, c);
-    v.unpack(f);
+    for (int i = 0; i < kUnits<HF>; ++i) v.v[i] = read_shared16(at + (first + c * kUnits<HF> + i) * 16);
+    return v.unpack();
   };
-  auto read_y = [&](int stage, int u, int c, float (&f)[8]) {
+  auto read_y = [&](uint32_t at, int first, int c) {
     Group<YF> v;
 #pragma unroll
-    for (int i = 0; i < kUnits<YF>; ++i) v.v[i] = *slot(stage, u + i, c);
-    v.unpack(f);
-  };
-  // a weight's factor for the eight columns of group g
-  auto factor = [&](const void* w, int g, float (&f)[8]) {
-    if (w != nullptr) load_vector(w, p.f.w_bf16, g, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = w != nullptr ? p.f.offset + f[i] : 1.f;
+    for (int i = 0; i < kUnits<YF>; ++i) v.v[i] = read_shared16(at + (first + c * kUnits<YF> + i) * 16);
+    return v.unpack();
   };
   auto row_sums = [&](auto& v) {
     if constexpr (LANES > 0) {
       sum_lanes<LANES>(v);
     } else {
-      sum_cta(v, scratch, half);
-      if constexpr (PAIR) sum_pair(v, both, half);
+      [[maybe_unused]] const int turn = half;
+      sums.add(v, half);
+      if constexpr (PAIR) sum_pair(v, both, turn);
     }
   };
   if constexpr (PAIR) cluster_sync();  // the other CTA has started
-  const Philox rng(p.f.drop);
-  float dw[CPL][8], dwp[CPL][8], dg[CPL][8];
-#pragma unroll
-  for (int c = 0; c < CPL; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[c][i] = dwp[c][i] = dg[c][i] = 0.f;
   const int64_t step = int64_t(grid_units) * per_cta;
   int64_t row = int64_t(unit) * per_cta + (LANES > 0 ? tid / width : 0);
   int64_t first = LANES > 0 ? row - (tid & 31) / width : row;
@@ -137,167 +119,143 @@ __global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES
     fetch(row + d * step, d);
     copy_async_commit();
   }
-  for (int stage = 0; first < p.f.T; first += step, row += step) {
-    const int ahead = stage == 0 ? depth - 1 : stage - 1;
-    fetch(row + (depth - 1) * step, ahead);
+  const Philox<false> rng(p.f.drop);
+  Eight w[CPL], before[kHasY ? CPL : 1], dw[CPL], S[kHasY ? CPL : 1];  // before: the columns' factors of y
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    const int g = g0 + c * width;
+    w[c] = dw[c] = all_of(0.f);
+    if constexpr (kHasY) before[c] = S[c] = all_of(0.f);
+    if (g >= groups) continue;
+    w[c] = weight_factor(p.f.w, p.f.w_bf16, p.f.offset, g);
+    if constexpr (kHasY) {
+      before[c] = weight_factor(p.f.wp, p.f.w_bf16, p.f.offset, g);
+      if (channel) before[c] = before[c] * load_vector(p.f.gate, p.f.w_bf16, g);
+    }
+  }
+  for (int stage = 0; first < T; first += step, row += step) {
+    fetch(row + (depth - 1) * step, stage == 0 ? depth - 1 : stage - 1);
     copy_async_commit();
-    if (depth == 3)
-      copy_async_wait<2>();
-    else if (depth == 2)
-      copy_async_wait<1>();
-    else
-      copy_async_wait<0>();
-    const bool here = row < p.f.T;
-    float s[3] = {0.f, 0.f, 0.f};  // of u^2, a u, y^2
+    copy_async_oldest(depth);
+    const uint32_t at = part + stage * (kStage * 16);
+    const bool here = row < T;
+    float r = 0.f, k = 0.f, ry = 1.f;
+    if (has_n || post) {
+      uint64_t uu = 0, au = 0, yy = 0;
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      const int g = g0 + lane + c * width;
-      if (!here || g >= p.f.groups) continue;
-      if (has_n) {
-        float u[8], n[8], f[8];
-        read_h(stage, 0, c, u);
-        read_y(stage, at_n, c, n);
-        factor(p.f.w, g, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = __fmaf_rn(u[i], u[i], s[0]);
-          s[1] = __fmaf_rn(n[i] * f[i], u[i], s[1]);
+      for (int c = 0; c < CPL; ++c) {
+        if (!here || g0 + c * width >= groups) continue;
+        if (has_n) {
+          const Eight u = read_h(at, 0, c);
+          dot8(uu, u, u);
+          dot8(au, read_y(at, kN, c) * w[c], u);
+        }
+        if (post) {
+          const Eight b = read_y(at, kY, c);
+          dot8(yy, b, b);
         }
       }
-      if (p.f.post) {
-        float y[8];
-        read_y(stage, at_y, c, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] = __fmaf_rn(y[i], y[i], s[2]);
-      }
+      float s[3] = {both_of(uu), both_of(au), both_of(yy)};
+      row_sums(s);
+      r = rsqrtf(__fmaf_rn(s[0], p.f.inv_width, p.f.eps));
+      k = -(r * r * r * (s[1] * p.f.inv_width));
+      if (post) ry = rsqrtf(__fmaf_rn(s[2], p.f.inv_width, p.f.eps));
     }
-    if (has_n || p.f.post) row_sums(s);
-    const float r = __frsqrt_rn(__fmaf_rn(s[0], p.f.inv_width, p.f.eps)), k = r * r * r * (s[1] * p.f.inv_width);
-    const float ry = p.f.post ? __frsqrt_rn(__fmaf_rn(s[2], p.f.inv_width, p.f.eps)) : 1.f;
     const float token = token_gate && here ? __ldg(static_cast<const float*>(p.f.gate) + row) : 1.f;
-    float t[2] = {0.f, 0.f};  // of the token gate's gradient, a' y
-    float a2[CPL][8];
+    uint64_t cy = 0;  // sum over the row of dropout(D) (full gate) (columns' factors) y
+    Eight e[kHasY ? CPL : 1];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
-      const int g = g0 + lane + c * width;
-      if (!here || g >= p.f.groups) continue;
-      float D[8], f[8];
-      if (has_h) {
-        read_h(stage, at_h, c, D);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) D[i] = 0.f;
-      }
+      const int g = g0 + c * width;
+      if (!here || g >= groups) continue;
+      Eight D = has_d ? read_h(at, kD, c) : all_of(0.f);
       if (has_n) {
-        float u[8], n[8];
-        read_h(stage, 0, c, u);
-        read_y(stage, at_n, c, n);
-        factor(p.f.w, g, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          D[i] += r * (n[i] * f[i]) - u[i] * k;
-          dw[c][i] = __fmaf_rn(n[i], u[i] * r, dw[c][i]);
+        const Eight u = read_h(at, 0, c), n = read_y(at, kN, c);
+        D = fma8(u, k, fma8(n * w[c], r, D));
+        dw[c] = fma8(n, u * r, dw[c]);
+      }
+      store_group<HF>(Rows{(char*)p.d_h, p.ld_d_h}.template at<HF>(row, g), D * p.f.scale);
+      if constexpr (kHasY) {
+        const Eight b = read_y(at, kY, c);
+        if constexpr (BRANCH == kElementwise) {
+          uint4 bits;
+          if (drop) {
+            bits = rng.words(uint64_t(p.f.drop.row_start + row) * uint32_t(groups) + g);
+            D = drop8(D, bits, p.f.drop.limit, p.f.drop.factor);
+          }
+          if (full) {
+            if (p.d_gate != nullptr) {
+              Eight q = D * b * (before[c] * ry);
+              if (drop) q = drop8(q, bits, p.f.drop.limit, 1.f);  // where y is not finite
+              store_group<YF>(Rows{(char*)p.d_gate, p.ld_d_gate}.template at<YF>(row, g), q);
+            }
+            D = D * read_y(at, kGate, c);
+            if (drop) D = drop8(D, bits, p.f.drop.limit, 1.f);  // where the gate is not finite
+          }
+          Eight x = b * (ry * token);
+          if (drop) x = drop8(x, bits, p.f.drop.limit, 1.f);
+          S[c] = fma8(D, x, S[c]);
+          e[c] = D * before[c];
+          dot8(cy, e[c], drop ? drop8(b, bits, p.f.drop.limit, 1.f) : b);
+        } else {
+          S[c] = fma8(D, b * (ry * token), S[c]);
+          e[c] = D * before[c];
+          dot8(cy, e[c], b);
         }
-      }
-      {
-        float d[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = p.f.scale * D[i];
-        store_group<HF>(group_at<HF>(p.d_h, row, p.ld_d_h, g), d);
-      }
-      if (!has_y) continue;
-      float y[8], z[8];
-      read_y(stage, at_y, c, y);
-      uint32_t kept = 0xffu;
-      if (drop) {
-        kept = kept_bits(rng, uint64_t(p.f.drop.row_start + row) * uint32_t(p.f.groups) + g, p.f.drop.threshold);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) D[i] *= p.f.drop.factor;
-      }
-      if (p.f.post) factor(p.f.wp, g, f);
-      if (channel)
-        load_vector(p.f.gate, p.f.w_bf16, g, z);
-      else if (full)
-        read_y(stage, at_gate, c, z);
-      float q[8];  // the gate's gradient, element by element
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float b = p.f.post ? y[i] * (ry * f[i]) : y[i];
-        q[i] = (kept >> i) & 1u ? D[i] * b : 0.f;
-        D[i] = (kept >> i) & 1u ? D[i] * (channel || full ? z[i] : token) : 0.f;
-      }
-      if (channel) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dg[c][i] += q[i];
-      } else if (token_gate) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[0] += q[i];
-      } else if (full && p.d_gate != nullptr) {
-        store_group<YF>(group_at<YF>(p.d_gate, row, p.ld_d_gate, g), q);
-      }
-      if (p.f.post) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dwp[c][i] = __fmaf_rn(D[i], y[i] * ry, dwp[c][i]);
-          a2[c][i] = D[i] * f[i];
-          t[1] = __fmaf_rn(a2[c][i], y[i], t[1]);
-        }
-      } else {
-        store_group<YF>(group_at<YF>(p.d_y, row, p.ld_d_y, g), D);
+        if (!post) store_group<YF>(Rows{(char*)p.d_y, p.ld_d_y}.template at<YF>(row, g), e[c] * token);
       }
     }
-    if (p.f.post || token_gate) {
-      row_sums(t);
-      if (token_gate && here && p.d_gate != nullptr && lane == 0 && g0 == 0) static_cast<float*>(p.d_gate)[row] = t[0];
-      if (p.f.post) {
-        const float ky = ry * ry * ry * (t[1] * p.f.inv_width);
+    if constexpr (kHasY) {
+      if (post || token_gate) {
+        float t[1] = {both_of(cy)};
+        row_sums(t);
+        if (token_gate && here && p.d_gate != nullptr && g0 == 0) static_cast<float*>(p.d_gate)[row] = ry * t[0];
+        if (post) {
+          const float ky = -(ry * ry * ry * (token * t[0] * p.f.inv_width));
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-          const int g = g0 + lane + c * width;
-          if (!here || g >= p.f.groups) continue;
-          float y[8];
-          read_y(stage, at_y, c, y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = ry * a2[c][i] - y[i] * ky;
-          store_group<YF>(group_at<YF>(p.d_y, row, p.ld_d_y, g), y);
+          for (int c = 0; c < CPL; ++c) {
+            const int g = g0 + c * width;
+            if (here && g < groups)
+              store_group<YF>(Rows{(char*)p.d_y, p.ld_d_y}.template at<YF>(row, g),
+                              fma8(read_y(at, kY, c), ky, e[c] * (ry * token)));
+          }
         }
       }
     }
     if (++stage == depth) stage = 0;
   }
   grid_launch_dependents();
-  if (p.partials == nullptr) return;
-  const int64_t H = int64_t(p.f.groups) * 8;
-  float* part = p.partials + int64_t(unit) * kSums * H;
-  auto write = [&](int k, float (&v)[CPL][8]) {
-    if constexpr (LANES > 0) {
-      // the CTA's rows' sums are added in their order, through shared memory
-      float* sum = reinterpret_cast<float*>(ring);
-      const int groups = kSmallThreads / width;
-      copy_async_wait<0>();
-      __syncthreads();
+  if (p.partials != nullptr) {
+    const int64_t H = int64_t(groups) * 8;
+    float* out = p.partials + int64_t(unit) * kSums * H;
+    auto write = [&](int which, const Eight (&v)[CPL]) {
+      if constexpr (LANES > 0) {
+        // the CTA's rows' sums are added in their order, through shared memory
+        float* sum = reinterpret_cast<float*>(ring);
+        copy_async_wait<0>();
+        __syncthreads();
 #pragma unroll
-      for (int c = 0; c < CPL; ++c)
+        for (int c = 0; c < CPL; ++c)
+          store_group<true>(reinterpret_cast<uint4*>(sum + (((tid / width) * CPL + c) * width + lane) * 8), v[c]);
+        __syncthreads();
+        for (int col = tid; col < H; col += kSmallThreads) {
+          float x = sum[col];
+          for (int i = 1; i < per_cta; ++i) x = __fadd_rn(x, sum[i * CPL * width * 8 + col]);
+          out[which * H + col] = x;
+        }
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[((tid / width) * CPL + c) * width * 8 + lane * 8 + i] = v[c][i];
-      __syncthreads();
-      for (int col = tid; col < H; col += kSmallThreads) {
-        const int c = col / (width * 8), at = col % (width * 8);
-        float x = sum[c * width * 8 + at];
-        for (int w = 1; w < groups; ++w) x = __fadd_rn(x, sum[(w * CPL + c) * width * 8 + at]);
-        part[k * H + col] = x;
+        for (int c = 0; c < CPL; ++c) {
+          const int g = g0 + c * width;
+          if (g < groups) store_group<true>(reinterpret_cast<uint4*>(out + which * H) + 2 * g, v[c]);
+        }
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        const int g = g0 + lane + c * width;
-        if (g < p.f.groups) store_group<true>(reinterpret_cast<uint4*>(part + k * H) + 2 * g, v[c]);
-      }
+    };
+    if (p.d_w != nullptr) write(0, dw);
+    if constexpr (kHasY) {
+      if (p.d_wp != nullptr || (channel && p.d_gate != nullptr)) write(1, S);
     }
-  };
-  if (p.d_w != nullptr) write(0, dw);
-  if (p.d_wp != nullptr) write(1, dwp);
-  if (channel && p.d_gate != nullptr) write(2, dg);
+  }
   if constexpr (PAIR) cluster_sync();  // neither CTA's shared memory goes while the other may write to it
 }
 
@@ -311,35 +269,46 @@ constexpr int kJoinParts = kJoinThreads / kJoinCols;   // threads that share a c
 __global__ void __launch_bounds__(kJoinThreads)
     norm_join_kernel(const __grid_constant__ NormGradParams p, int parts) {
   __shared__ float scratch[kJoinParts][kJoinCols];
-  const int which = blockIdx.y;
-  void* out = which == 0 ? p.d_w : which == 1 ? p.d_wp : p.f.gate_kind == LP_GATE_CHANNEL ? p.d_gate : nullptr;
-  if (out == nullptr) return;
+  const bool first = blockIdx.y == 0;
+  void* const d_gate = p.f.gate_kind == LP_GATE_CHANNEL ? p.d_gate : nullptr;
   const int64_t H = int64_t(p.f.groups) * 8;
   const int col = blockIdx.x * kJoinCols + threadIdx.x % kJoinCols, j = threadIdx.x / kJoinCols;
+  if (first ? p.d_w == nullptr : p.d_wp == nullptr && d_gate == nullptr) return;
+  auto value = [&](const void* v) {
+    return p.f.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(v)[col]) : static_cast<const float*>(v)[col];
+  };
   grid_dependency_wait();
   float x = 0.f;
   if (col < H) {
 #pragma unroll 8
-    for (int i = j; i < parts; i += kJoinParts) x = __fadd_rn(x, __ldcg(p.partials + (int64_t(i) * kSums + which) * H + col));
+    for (int i = j; i < parts; i += kJoinParts)
+      x = __fadd_rn(x, __ldcg(p.partials + (int64_t(i) * kSums + blockIdx.y) * H + col));
   }
   scratch[j][threadIdx.x % kJoinCols] = x;
   __syncthreads();
   if (j != 0 || col >= H) return;
 #pragma unroll
   for (int k = 1; k < kJoinParts; ++k) x = __fadd_rn(x, scratch[k][threadIdx.x]);
-  if (p.dw_bf16) {
-    static_cast<__nv_bfloat16*>(out)[col] = __float2bfloat16_rn(x);
+  auto write = [&](void* out, float v) {
+    if (out == nullptr) return;
+    if (p.dw_bf16) {
+      static_cast<__nv_bfloat16*>(out)[col] = __float2bfloat16_rn(v);
+    } else {
+      float* o = static_cast<float*>(out) + col;
+      *o = p.accumulate ? __fadd_rn(*o, v) : v;
+    }
+  };
+  if (first) {
+    write(p.d_w, x);
   } else {
-    float* o = static_cast<float*>(out) + col;
-    *o = p.accumulate ? __fadd_rn(*o, x) : x;
+    write(p.d_wp, p.f.gate_kind == LP_GATE_CHANNEL ? x * value(p.f.gate) : x);
+    write(d_gate, p.f.wp != nullptr ? x * __fadd_rn(p.f.offset, value(p.f.wp)) : x);
   }
 }
 
 // ------------------------------------------------------------------ launches
 
-// How a gradient of rows of `groups` groups is laid out over CTAs; parts <= kMostParts.
-constexpr int kMostParts = 8 * kSms;
-
+// How a gradient of rows of `groups` groups is laid out over CTAs.
 struct Layout {
   int threads, per_cta, resident;
   int64_t units(int64_t T) const {  // CTAs, or pairs of them
@@ -382,39 +351,45 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool HF, bool YF, int LANES, int CPL, bool PAIR>
+template <bool HF, bool YF, int LANES, int CPL, bool PAIR, int BRANCH>
 cudaError_t launch_rows(const NormGradParams& params, cudaStream_t s) {
   NormGradParams p = params;
   const Layout l = layout_of<LANES, CPL, PAIR>(p.f.groups);
-  const int units = kUnits<HF> * (1 + (p.d_h_out != nullptr)) +
-                    kUnits<YF> * ((p.f.y != nullptr) + (p.d_norm != nullptr) + (p.f.gate_kind == LP_GATE_FULL));
-  const int64_t stage = int64_t(units) * CPL * l.threads * 16;
-  int depth = int(kShared / (PAIR ? 1 : l.resident) / stage);
-  depth = depth < 1 ? 1 : depth > kMaxDepth ? kMaxDepth : depth;
-  size_t shared = size_t(depth * stage);
+  const int units = CPL * (2 * kUnits<HF> + (BRANCH == kNoBranch ? 1 : BRANCH == kScaled ? 2 : 3) * kUnits<YF>);
+  int depth = kMaxDepth;
+  while (depth > 1 && int64_t(l.resident) * part_units(depth, units) * 16 * l.threads > kShared) --depth;
+  size_t shared = size_t(part_units(depth, units)) * 16 * l.threads;
   if (LANES > 0 && shared < size_t(kSmallThreads) * CPL * 8 * sizeof(float))
     shared = size_t(kSmallThreads) * CPL * 8 * sizeof(float);
   const bool sums = p.d_w != nullptr || p.d_wp != nullptr || (p.f.gate_kind == LP_GATE_CHANNEL && p.d_gate != nullptr);
   if (!sums) p.partials = nullptr;
   const int64_t n = l.units(p.f.T);
-  auto kernel = norm_grad_kernel<HF, YF, LANES, CPL, PAIR>;
   cudaError_t e = cudaSuccess;
-  if (shared > 40 * 1024) e = allow_shared<norm_grad_kernel<HF, YF, LANES, CPL, PAIR>>();
-  if (e == cudaSuccess) e = launch(kernel, dim3(unsigned(PAIR ? 2 * n : n)), l.threads, shared, PAIR, false, s, p, depth);
+  if (shared > 40 * 1024) e = allow_shared<norm_grad_kernel<HF, YF, LANES, CPL, PAIR, BRANCH>>();
+  if (e == cudaSuccess)
+    e = launch(norm_grad_kernel<HF, YF, LANES, CPL, PAIR, BRANCH>, dim3(unsigned(PAIR ? 2 * n : n)), l.threads, shared,
+               PAIR, false, s, p, depth);
   if (e == cudaSuccess && sums)
     e = launch(norm_join_kernel, dim3((p.f.groups * 8 + kJoinCols - 1) / kJoinCols, kSums), kJoinThreads, 0, 0, true, s,
                p, int(n));
   return e;
 }
 
+template <bool HF, bool YF, int BRANCH>
+cudaError_t launch_grad(const NormGradParams& p, cudaStream_t s) {
+  if (p.f.groups <= 8) return launch_rows<HF, YF, 8, 1, false, BRANCH>(p, s);
+  if (p.f.groups <= 16) return launch_rows<HF, YF, 16, 1, false, BRANCH>(p, s);
+  if (p.f.groups <= 32) return launch_rows<HF, YF, 32, 1, false, BRANCH>(p, s);
+  if (p.f.groups <= 64) return launch_rows<HF, YF, 32, 2, false, BRANCH>(p, s);
+  if (p.f.groups <= kPairGroups) return launch_rows<HF, YF, 0, 2, false, BRANCH>(p, s);
+  return launch_rows<HF, YF, 0, 2, true, BRANCH>(p, s);
+}
+
 template <bool HF, bool YF>
 cudaError_t launch_grad(const NormGradParams& p, cudaStream_t s) {
-  if (p.f.groups <= 8) return launch_rows<HF, YF, 8, 1, false>(p, s);
-  if (p.f.groups <= 16) return launch_rows<HF, YF, 16, 1, false>(p, s);
-  if (p.f.groups <= 32) return launch_rows<HF, YF, 32, 1, false>(p, s);
-  if (p.f.groups <= 64) return launch_rows<HF, YF, 32, 2, false>(p, s);
-  if (p.f.groups <= kPairGroups) return launch_rows<HF, YF, 0, 2, false>(p, s);
-  return launch_rows<HF, YF, 0, 2, true>(p, s);
+  if (p.f.y == nullptr) return launch_grad<HF, YF, kNoBranch>(p, s);
+  if (p.f.gate_kind == LP_GATE_FULL || p.f.drop.threshold > 0) return launch_grad<HF, YF, kElementwise>(p, s);
+  return launch_grad<HF, YF, kScaled>(p, s);
 }
 
 }  // namespace
