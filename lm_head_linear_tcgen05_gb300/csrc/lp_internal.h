@@ -336,6 +336,7 @@ struct NormParams {
   float eps, scale, offset, inv_width;
   int32_t gate_kind, post, w_bf16;
   int32_t T, groups;
+  uint64_t wait_limit_ns;
   unsigned int* err;
 };
 

@@ -6,9 +6,11 @@
 // adds the CTAs' in order. Two suffice: d_weight, and S = sum of dropout(D) y / rms(y) (times the gate of the
 // token or element), for of its columns d_post_weight is S times the channel gate and a channel gate's gradient
 // S times the post norm's weight.
-// Bounds: memory, if little enough is issued for each element: as in the forward, columns' weights stay in
-// registers and a thread's part of the next rows is copied to shared memory while it works on the present one,
-// and read from there as often as the row's sums need it.
+// Bounds: what is issued for an element, then memory. So columns' weights stay in registers, the next rows come by
+// bulk copies and are read from shared memory as often as the row's sums need them, and what a call does not have
+// (a post norm, dropout, one of the two gradients) is decided when the kernel is compiled. 8192 x 4096 in bf16 with
+// both norms, a channel gate and dropout: 71 us (5.6 TB/s of 12 bytes an element); copies by each thread (cp.async) in
+// place of bulk ones 143, the cases decided at run time 96.
 #include "lp_rows.cuh"
 
 namespace lp {
@@ -16,16 +18,21 @@ namespace lp {
 namespace {
 
 constexpr int kSmallThreads = 256;
-constexpr int kMaxThreads = 512;
 constexpr int kSums = 2;  // over tokens
 constexpr int kSms = 152;
-constexpr int64_t kShared = 220 * 1024;
+// Bytes of rows on an SM: more than in the forward, for a row takes longer. 20001 x 1032 with an fp32 stream and a full
+// gate: 138 us with 64 KB, 102 with 96, 90 with 128, 85 with 192.
+constexpr int64_t kUnderWay = 192 * 1024;
 constexpr int kPairGroups = 1024;  // rows of more groups belong to a cluster of two CTAs, half of the columns each
+// Of a thread: 16 warps on an SM, whatever the width up to 1024 groups. With 112 or 96 more rows fit, but what spills
+// costs more: 8192 x 4096 with both norms, a gate and dropout 67 us, 112: 82, 96: 102 (112 alone fits two CTAs of
+// 288 threads, but 4104 columns take 93 us with it, 76 without).
+constexpr int kRegisters = 128;
 
 // The sums over the two CTAs of a cluster, each of which writes its own to both. Calls alternate between the
 // halves of `both`.
 template <int N>
-__device__ __forceinline__ void sum_pair(float (&v)[N], float (*both)[2][3], int half) {
+__device__ __forceinline__ void sum_pair(float (&v)[N], float (*both)[2][4], int half) {
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x < 2 * N) {
     const int i = threadIdx.x >> 1;
@@ -41,69 +48,58 @@ __device__ __forceinline__ void sum_pair(float (&v)[N], float (*both)[2][3], int
   for (int i = 0; i < N; ++i) v[i] = __fadd_rn(both[half][0][i], both[half][1][i]);
 }
 
-// As in the forward: nothing joins the stream, y times factors of its row and columns, or of every element too.
-enum Branch { kNoBranch, kScaled, kElementwise };
-
-template <bool HF, bool YF, int LANES, int CPL, bool PAIR, int BRANCH>
-__global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES > 0 ? 2 : 1)
-    norm_grad_kernel(const __grid_constant__ NormGradParams p, int depth) {
-  constexpr bool kHasY = BRANCH != kNoBranch;
-  constexpr int kUH = kUnits<HF> * CPL, kUY = kUnits<YF> * CPL;
-  constexpr int kN = kUH, kD = kN + kUY, kY = kD + kUH, kGate = kY + kUY;  // units of a stage before dn's, dh's, y's, the gate's
-  constexpr int kStage = BRANCH == kNoBranch ? kY : BRANCH == kScaled ? kGate : kGate + kUY;
-  extern __shared__ uint4 ring[];
-  __shared__ CtaSums<3> sums;
-  __shared__ float both[2][2][3];
+// LANES lanes to a row (0: the CTA, or with PAIR two), each with CPL groups of eight columns.
+template <bool HF, bool YF, int LANES, int CPL, bool PAIR, int BRANCH, int CASE>
+__global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__ NormGradParams p, int depth) {
+  constexpr bool kCta = LANES == 0, kHasY = BRANCH != kNoBranch, kAny = CASE == kAnyCase, kFull = BRANCH == kFullGate;
+  extern __shared__ uint4 stages[];
+  __shared__ CtaSums<4> sums;
+  __shared__ RowRing ring;
+  __shared__ float both[2][2][4];
   int half = 0;
-  if constexpr (LANES == 0) sums.clear();
   const int tid = threadIdx.x;
-  const int width = LANES > 0 ? LANES : blockDim.x, lane = LANES > 0 ? tid % (LANES > 0 ? LANES : 1) : tid;
-  const int per_cta = LANES > 0 ? kSmallThreads / (LANES > 0 ? LANES : 1) : 1;
-  const int unit = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x), grid_units = PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
-  const int g0 = (PAIR ? int(blockIdx.x & 1) * (int(blockDim.x) * CPL) : 0) + lane;  // the thread's first group
-  const int T = p.f.T, groups = p.f.groups;
-  const bool has_n = p.d_norm != nullptr, has_d = p.d_h_out != nullptr, post = kHasY && p.f.post;
-  const bool full = BRANCH == kElementwise && p.f.gate_kind == LP_GATE_FULL, drop = BRANCH == kElementwise && p.f.drop.threshold > 0;
-  const bool channel = kHasY && p.f.gate_kind == LP_GATE_CHANNEL, token_gate = kHasY && p.f.gate_kind == LP_GATE_TOKEN;
-  const uint32_t part = smem_u32(ring) + uint32_t(tid) * part_units(depth, kStage) * 16;
+  const int width = kCta ? blockDim.x : LANES, lane = kCta ? tid : tid % (kCta ? 1 : LANES);
+  const int per_cta = kCta ? 1 : kSmallThreads / (kCta ? 1 : LANES);
+  const uint32_t unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, grid_units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t T = p.f.T;
+  const int groups = p.f.groups, room = width * CPL;
+  // the CTA's groups of a row, and the thread's first
+  const int cta_g0 = PAIR ? int(blockIdx.x & 1) * room : 0, g0 = cta_g0 + lane, span = PAIR ? min(groups - cta_g0, room) : groups;
+  const bool has_n = !kAny || p.d_norm != nullptr, has_d = !kAny || p.d_h_out != nullptr;
+  const bool post = kHasY && (kAny ? p.f.post != 0 : CASE == kPostCase);
+  const bool drop = BRANCH == kDropped || (kFull && p.f.drop.threshold > 0);
+  const bool channel = kHasY && !kFull && p.f.gate_kind == LP_GATE_CHANNEL;
+  const bool token_gate = kHasY && !kFull && p.f.gate_kind == LP_GATE_TOKEN;
   const Rows h{(char*)p.f.h, p.f.ld_h}, y{(char*)p.f.y, p.f.ld_y}, z{(char*)p.f.gate, p.f.ld_gate};
   const Rows dn{(char*)p.d_norm, p.ld_d_norm}, dh{(char*)p.d_h_out, p.ld_d_h_out};
-  auto copy_h = [&](const Rows& from, int64_t row, int g, uint32_t to) {
-#pragma unroll
-    for (int i = 0; i < kUnits<HF>; ++i) copy_async16(to + i * 16, from.at<HF>(row, g) + i);
+  // a stage: the CTA's part of the row's h, d_norm, d_h_out, y, gate, one after another, each with room for every
+  // group a thread may ask for
+  const int room_h = room * kUnits<HF>, room_y = room * kUnits<YF>;
+  const int at_n = room_h, at_d = at_n + (has_n ? room_y : 0), at_y = at_d + (has_d ? room_h : 0);
+  const int at_gate = at_y + (kHasY ? room_y : 0), stage_units = at_gate + (kFull ? room_y : 0);
+  auto fetch = [&](uint32_t row, int stage) {
+    const uint32_t bytes_h = span * kUnits<HF> * 16, bytes_y = span * kUnits<YF> * 16;
+    const uint32_t parts_h = 1 + has_d, parts_y = has_n + kHasY + kFull;
+    if (tid != 0 || row >= T || !ring.begin(stage, parts_h * bytes_h + parts_y * bytes_y)) return;
+    uint4* const to = stages + stage * stage_units;
+    uint64_t* const bar = &ring.full[stage];
+    copy_bulk(to, h.at<HF>(row, cta_g0), bytes_h, bar);
+    if (has_n) copy_bulk(to + at_n, dn.at<YF>(row, cta_g0), bytes_y, bar);
+    if (has_d) copy_bulk(to + at_d, dh.at<HF>(row, cta_g0), bytes_h, bar);
+    if constexpr (kHasY) copy_bulk(to + at_y, y.at<YF>(row, cta_g0), bytes_y, bar);
+    if constexpr (kFull) copy_bulk(to + at_gate, z.at<YF>(row, cta_g0), bytes_y, bar);
   };
-  auto copy_y = [&](const Rows& from, int64_t row, int g, uint32_t to) {
-#pragma unroll
-    for (int i = 0; i < kUnits<YF>; ++i) copy_async16(to + i * 16, from.at<YF>(row, g) + i);
+  // the thread's c-th group of a row: from the CTA's stage, or, where a row has a few lanes only, from memory
+  auto read_h = [&](const Rows& m, uint32_t row, const uint4* stage, int section, int c) {
+    return Group<HF>::read(kCta ? stage + section + (lane + c * width) * kUnits<HF> : m.at<HF>(row, g0 + c * width)).unpack();
   };
-  auto fetch = [&](int64_t row, int stage) {
-    const uint32_t to = part + stage * (kStage * 16);
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) {
-      const int g = g0 + c * width;
-      if (row >= T || g >= groups) continue;
-      const uint32_t th = to + c * (kUnits<HF> * 16), ty = to + c * (kUnits<YF> * 16);
-      copy_h(h, row, g, th);
-      if (has_n) copy_y(dn, row, g, ty + kN * 16);
-      if (has_d) copy_h(dh, row, g, th + kD * 16);
-      if constexpr (kHasY) copy_y(y, row, g, ty + kY * 16);
-      if (full) copy_y(z, row, g, ty + kGate * 16);
-    }
+  auto raw_y = [&](const Rows& m, uint32_t row, const uint4* stage, int section, int c) {
+    return Group<YF>::read(kCta ? stage + section + (lane + c * width) * kUnits<YF> : m.at<YF>(row, g0 + c * width));
   };
-  auto read_h = [&](uint32_t at, int first, int c) {
-    Group<HF> v;
-#pragma unroll
-    for (int i = 0; i < kUnits<HF>; ++i) v.v[i] = read_shared16(at + (first + c * kUnits<HF> + i) * 16);
-    return v.unpack();
-  };
-  auto read_y = [&](uint32_t at, int first, int c) {
-    Group<YF> v;
-#pragma unroll
-    for (int i = 0; i < kUnits<YF>; ++i) v.v[i] = read_shared16(at + (first + c * kUnits<YF> + i) * 16);
-    return v.unpack();
-  };
+  // Whether it is to be worked on. A stage holds zeros behind a row, so there it always is.
+  auto has = [&](int c, bool here) { return kCta || (here && g0 + c * width < groups); };
   auto row_sums = [&](auto& v) {
-    if constexpr (LANES > 0) {
+    if constexpr (!kCta) {
       sum_lanes<LANES>(v);
     } else {
       [[maybe_unused]] const int turn = half;
@@ -112,14 +108,23 @@ __global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES
     }
   };
   if constexpr (PAIR) cluster_sync();  // the other CTA has started
-  const int64_t step = int64_t(grid_units) * per_cta;
-  int64_t row = int64_t(unit) * per_cta + (LANES > 0 ? tid / width : 0);
-  int64_t first = LANES > 0 ? row - (tid & 31) / width : row;
-  for (int d = 0; d < depth - 1; ++d) {
-    fetch(row + d * step, d);
-    copy_async_commit();
+  const uint32_t step = grid_units * per_cta;
+  uint32_t row = unit * per_cta + (kCta ? 0 : tid / width);
+  uint32_t first = kCta ? row : row - (tid & 31) / width;
+  if constexpr (kCta) {
+    ring.init();
+    for (int d = 0; d < depth; ++d) {
+      uint4* const stage = stages + d * stage_units;
+      zero_tail(stage, span * kUnits<HF>, room_h);
+      if (has_n) zero_tail(stage + at_n, span * kUnits<YF>, room_y);
+      if (has_d) zero_tail(stage + at_d, span * kUnits<HF>, room_h);
+      if constexpr (kHasY) zero_tail(stage + at_y, span * kUnits<YF>, room_y);
+      if constexpr (kFull) zero_tail(stage + at_gate, span * kUnits<YF>, room_y);
+    }
+    sums.clear();
+    for (int d = 0; d < depth; ++d) fetch(row + d * step, d);
   }
-  const Philox<false> rng(p.f.drop);
+  const Philox rng(p.f.drop);
   Eight w[CPL], before[kHasY ? CPL : 1], dw[CPL], S[kHasY ? CPL : 1];  // before: the columns' factors of y
 #pragma unroll
   for (int c = 0; c < CPL; ++c) {
@@ -131,99 +136,134 @@ __global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES
     if constexpr (kHasY) {
       before[c] = weight_factor(p.f.wp, p.f.w_bf16, p.f.offset, g);
       if (channel) before[c] = before[c] * load_vector(p.f.gate, p.f.w_bf16, g);
+      if (drop) before[c] = before[c] * p.f.drop.factor;
     }
   }
-  for (int stage = 0; first < T; first += step, row += step) {
-    fetch(row + (depth - 1) * step, stage == 0 ? depth - 1 : stage - 1);
-    copy_async_commit();
-    copy_async_oldest(depth);
-    const uint32_t at = part + stage * (kStage * 16);
-    const bool here = row < T;
-    float r = 0.f, k = 0.f, ry = 1.f;
-    if (has_n || post) {
-      uint64_t uu = 0, au = 0, yy = 0;
+  // of a row (whose stage has arrived): the sums of u^2, a u and y^2
+  auto squares = [&](uint32_t of, const uint4* at, bool here, float (&s)[4]) {
+    uint64_t uu = 0, au = 0, yy = 0;
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        if (!here || g0 + c * width >= groups) continue;
-        if (has_n) {
-          const Eight u = read_h(at, 0, c);
-          dot8(uu, u, u);
-          dot8(au, read_y(at, kN, c) * w[c], u);
-        }
-        if (post) {
-          const Eight b = read_y(at, kY, c);
-          dot8(yy, b, b);
-        }
+    for (int c = 0; c < CPL; ++c) {
+      if (!has(c, here)) continue;
+      if (has_n) {
+        const Eight u = read_h(h, of, at, 0, c);
+        dot8(uu, u, u);
+        dot8(au, raw_y(dn, of, at, at_n, c).unpack() * w[c], u);
       }
-      float s[3] = {both_of(uu), both_of(au), both_of(yy)};
-      row_sums(s);
-      r = rsqrtf(__fmaf_rn(s[0], p.f.inv_width, p.f.eps));
-      k = -(r * r * r * (s[1] * p.f.inv_width));
-      if (post) ry = rsqrtf(__fmaf_rn(s[2], p.f.inv_width, p.f.eps));
+      if (post) {
+        const Eight b = raw_y(y, of, at, at_y, c).unpack();
+        dot8(yy, b, b);
+      }
     }
+    s[0] = both_of(uu);
+    s[1] = both_of(au);
+    s[2] = both_of(yy);
+  };
+  // With a second stage the next row's squares are summed together with what this row's post norm needs: one
+  // exchange a row.
+  const bool early = kCta && (!kAny || depth > 1);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};  // the present row's squares, and its sum after the post norm
+  if (early && row < T) {
+    ring.wait(0, 0, p.f.wait_limit_ns, p.f.err);
+    squares(row, stages, true, s);
+    row_sums(s);
+  }
+  uint32_t parity = 0;
+  // where the thread's first group of the row goes, and that of the next
+  uint4* to_h = Rows{(char*)p.d_h, p.ld_d_h}.template at<HF>(row, g0);
+  uint4* to_y = Rows{(char*)p.d_y, p.ld_d_y}.template at<YF>(row, g0);
+  const int64_t by_h = step * (p.ld_d_h / 16), by_y = step * (p.ld_d_y / 16);
+  uint64_t counter = uint64_t(p.f.drop.row_start + row) * uint32_t(groups) + g0;  // the generator's, of that group
+  for (int stage = 0; first < T; first += step, row += step) {
+    const int next = kCta && stage + 1 < depth ? stage + 1 : 0;
+    const uint4* const at = stages + stage * stage_units;
+    const bool here = kCta || row < T;
+    uint4 bits[BRANCH >= kDropped ? CPL : 1];
+    if (drop) {
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) bits[c] = rng.words(counter + c * width);
+      counter += uint64_t(step) * uint32_t(groups);
+    }
+    if (!early) {
+      if constexpr (kCta) ring.wait(stage, parity, p.f.wait_limit_ns, p.f.err);
+      squares(row, at, here, s);
+      s[3] = 0.f;
+      row_sums(s);
+    }
+    const float r = rsqrtf(__fmaf_rn(s[0], p.f.inv_width, p.f.eps)), k = -(s[1] * p.f.inv_width * r * r * r);
+    const float ry = post ? rsqrtf(__fmaf_rn(s[2], p.f.inv_width, p.f.eps)) : 1.f;
     const float token = token_gate && here ? __ldg(static_cast<const float*>(p.f.gate) + row) : 1.f;
+    const float of_S = drop ? ry * token * p.f.drop.factor : ry * token;
     uint64_t cy = 0;  // sum over the row of dropout(D) (full gate) (columns' factors) y
     Eight e[kHasY ? CPL : 1];
+    Group<YF> kept_y[kHasY ? CPL : 1];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
       const int g = g0 + c * width;
-      if (!here || g >= groups) continue;
-      Eight D = has_d ? read_h(at, kD, c) : all_of(0.f);
+      const bool there = g < groups;
+      if (!has(c, here)) continue;
+      Eight D = has_d ? read_h(dh, row, at, at_d, c) : all_of(0.f);
       if (has_n) {
-        const Eight u = read_h(at, 0, c), n = read_y(at, kN, c);
-        D = fma8(u, k, fma8(n * w[c], r, D));
-        dw[c] = fma8(n, u * r, dw[c]);
+        const Eight u = read_h(h, row, at, 0, c), n = raw_y(dn, row, at, at_n, c).unpack() * r;
+        D = fma8(u, k, fma8(n, w[c], D));
+        dw[c] = fma8(n, u, dw[c]);
       }
-      store_group<HF>(Rows{(char*)p.d_h, p.ld_d_h}.template at<HF>(row, g), D * p.f.scale);
+      if (there) store_group<HF>(to_h + c * width * kUnits<HF>, D * p.f.scale);
       if constexpr (kHasY) {
-        const Eight b = read_y(at, kY, c);
-        if constexpr (BRANCH == kElementwise) {
-          uint4 bits;
-          if (drop) {
-            bits = rng.words(uint64_t(p.f.drop.row_start + row) * uint32_t(groups) + g);
-            D = drop8(D, bits, p.f.drop.limit, p.f.drop.factor);
-          }
-          if (full) {
-            if (p.d_gate != nullptr) {
-              Eight q = D * b * (before[c] * ry);
-              if (drop) q = drop8(q, bits, p.f.drop.limit, 1.f);  // where y is not finite
-              store_group<YF>(Rows{(char*)p.d_gate, p.ld_d_gate}.template at<YF>(row, g), q);
-            }
-            D = D * read_y(at, kGate, c);
-            if (drop) D = drop8(D, bits, p.f.drop.limit, 1.f);  // where the gate is not finite
-          }
-          Eight x = b * (ry * token);
-          if (drop) x = drop8(x, bits, p.f.drop.limit, 1.f);
-          S[c] = fma8(D, x, S[c]);
-          e[c] = D * before[c];
-          dot8(cy, e[c], drop ? drop8(b, bits, p.f.drop.limit, 1.f) : b);
-        } else {
-          S[c] = fma8(D, b * (ry * token), S[c]);
-          e[c] = D * before[c];
-          dot8(cy, e[c], b);
+        kept_y[c] = raw_y(y, row, at, at_y, c);
+        Eight b = kept_y[c].unpack();
+        // what is dropped passes on nothing, whatever y and the gate hold there
+        if constexpr (kFull) {
+          Eight x = raw_y(z, row, at, at_gate, c).unpack();
+          if (drop) keep8(bits[c], p.f.drop.limit, D, b, x);
+          if (there && p.d_gate != nullptr)
+            store_group<YF>(Rows{(char*)p.d_gate, p.ld_d_gate}.template at<YF>(row, g), D * b * (before[c] * ry));
+          D = D * x;
         }
-        if (!post) store_group<YF>(Rows{(char*)p.d_y, p.ld_d_y}.template at<YF>(row, g), e[c] * token);
+        if constexpr (BRANCH == kDropped) keep8(bits[c], p.f.drop.limit, D, b);
+        const Eight by = D * b;
+        S[c] = fma8(by, of_S, S[c]);
+        dot8(cy, by, before[c]);
+        e[c] = D * before[c];
+        if (!post && there) store_group<YF>(to_y + c * width * kUnits<YF>, e[c] * token);
       }
+    }
+    float after = 0.f;  // the sum of cy
+    if constexpr (kCta) {
+      float v[4] = {0.f, 0.f, 0.f, both_of(cy)};
+      if (early && row + step < T) {
+        ring.wait(next, next == 0 ? parity ^ 1u : parity, p.f.wait_limit_ns, p.f.err);
+        squares(row + step, stages + next * stage_units, true, v);
+      }
+      row_sums(v);  // and everyone has read the stage
+      fetch(row + depth * step, stage);
+      after = v[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) s[i] = v[i];
+    } else if (post || token_gate) {
+      float v[1] = {both_of(cy)};
+      row_sums(v);
+      after = v[0];
     }
     if constexpr (kHasY) {
-      if (post || token_gate) {
-        float t[1] = {both_of(cy)};
-        row_sums(t);
-        if (token_gate && here && p.d_gate != nullptr && g0 == 0) static_cast<float*>(p.d_gate)[row] = ry * t[0];
-        if (post) {
-          const float ky = -(ry * ry * ry * (token * t[0] * p.f.inv_width));
+      if (token_gate && here && p.d_gate != nullptr && g0 == 0) static_cast<float*>(p.d_gate)[row] = ry * after;
+      if (post) {
+        const float ky = -(ry * ry * ry * (token * after * p.f.inv_width));
 #pragma unroll
-          for (int c = 0; c < CPL; ++c) {
-            const int g = g0 + c * width;
-            if (here && g < groups)
-              store_group<YF>(Rows{(char*)p.d_y, p.ld_d_y}.template at<YF>(row, g),
-                              fma8(read_y(at, kY, c), ky, e[c] * (ry * token)));
-          }
+        for (int c = 0; c < CPL; ++c) {
+          const int g = g0 + c * width;
+          if (here && g < groups)
+            store_group<YF>(to_y + c * width * kUnits<YF>,
+                            fma8(kept_y[c].unpack(), ky, e[c] * (ry * token)));
         }
       }
     }
-    if (++stage == depth) stage = 0;
+    if (next == 0) parity ^= 1u;
+    stage = next;
+    to_h += by_h;
+    to_y += by_y;
   }
+  if constexpr (kCta) ring.drain();
   grid_launch_dependents();
   if (p.partials != nullptr) {
     const int64_t H = int64_t(groups) * 8;
@@ -231,9 +271,8 @@ __global__ void __launch_bounds__(LANES > 0 ? kSmallThreads : kMaxThreads, LANES
     auto write = [&](int which, const Eight (&v)[CPL]) {
       if constexpr (LANES > 0) {
         // the CTA's rows' sums are added in their order, through shared memory
-        float* sum = reinterpret_cast<float*>(ring);
-        copy_async_wait<0>();
-        __syncthreads();
+        float* sum = reinterpret_cast<float*>(stages);
+        __syncthreads();  // the sum before has been read
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
           store_group<true>(reinterpret_cast<uint4*>(sum + (((tid / width) * CPL + c) * width + lane) * 8), v[c]);
@@ -308,21 +347,26 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // ------------------------------------------------------------------ launches
 
-// How a gradient of rows of `groups` groups is laid out over CTAs.
+// How a gradient of rows of `groups` groups is laid out over CTAs: lanes and groups a lane as the kernel has them.
 struct Layout {
-  int threads, per_cta, resident;
+  int lanes, pair, threads, per_cta, resident;
   int64_t units(int64_t T) const {  // CTAs, or pairs of them
     const int64_t rows = (T + per_cta - 1) / per_cta;
-    return rows < int64_t(kSms) * resident ? rows : int64_t(kSms) * resident;
+    const int64_t most = int64_t(kSms) * resident / (1 + pair);
+    return rows < most ? rows : most;
   }
 };
 
-template <int LANES, int CPL, bool PAIR>
 Layout layout_of(int groups) {
-  const int cta_groups = PAIR ? (groups + 1) / 2 : groups;
-  const int threads = LANES > 0 ? kSmallThreads : (cta_groups + 32 * CPL - 1) / (32 * CPL) * 32;
-  const int resident = PAIR ? 1 : 512 / threads;  // 128 registers a thread
-  return Layout{threads, LANES > 0 ? kSmallThreads / (LANES > 0 ? LANES : 1) : 1, resident < 1 ? 1 : resident > 8 ? 8 : resident};
+  Layout l;
+  l.lanes = groups <= 8 ? 8 : groups <= 32 ? 32 : 0;
+  l.pair = groups > kPairGroups;
+  const int cta_groups = l.pair ? (groups + 1) / 2 : groups;
+  l.threads = l.lanes > 0 ? kSmallThreads : (cta_groups + 63) / 64 * 32;
+  l.per_cta = l.lanes > 0 ? kSmallThreads / l.lanes : 1;
+  l.resident = 65536 / kRegisters / l.threads;
+  l.resident = l.resident < 1 ? 1 : l.resident > 16 ? 16 : l.resident;
+  return l;
 }
 
 template <typename... P, typename... A>
@@ -351,58 +395,63 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool HF, bool YF, int LANES, int CPL, bool PAIR, int BRANCH>
-cudaError_t launch_rows(const NormGradParams& params, cudaStream_t s) {
-  NormGradParams p = params;
-  const Layout l = layout_of<LANES, CPL, PAIR>(p.f.groups);
-  const int units = CPL * (2 * kUnits<HF> + (BRANCH == kNoBranch ? 1 : BRANCH == kScaled ? 2 : 3) * kUnits<YF>);
-  int depth = kMaxDepth;
-  while (depth > 1 && int64_t(l.resident) * part_units(depth, units) * 16 * l.threads > kShared) --depth;
-  size_t shared = size_t(part_units(depth, units)) * 16 * l.threads;
-  if (LANES > 0 && shared < size_t(kSmallThreads) * CPL * 8 * sizeof(float))
-    shared = size_t(kSmallThreads) * CPL * 8 * sizeof(float);
-  const bool sums = p.d_w != nullptr || p.d_wp != nullptr || (p.f.gate_kind == LP_GATE_CHANNEL && p.d_gate != nullptr);
-  if (!sums) p.partials = nullptr;
-  const int64_t n = l.units(p.f.T);
-  cudaError_t e = cudaSuccess;
-  if (shared > 40 * 1024) e = allow_shared<norm_grad_kernel<HF, YF, LANES, CPL, PAIR, BRANCH>>();
-  if (e == cudaSuccess)
-    e = launch(norm_grad_kernel<HF, YF, LANES, CPL, PAIR, BRANCH>, dim3(unsigned(PAIR ? 2 * n : n)), l.threads, shared,
-               PAIR, false, s, p, depth);
-  if (e == cudaSuccess && sums)
-    e = launch(norm_join_kernel, dim3((p.f.groups * 8 + kJoinCols - 1) / kJoinCols, kSums), kJoinThreads, 0, 0, true, s,
-               p, int(n));
-  return e;
+template <bool HF, bool YF, int LANES, int CPL, bool PAIR, int BRANCH, int CASE>
+cudaError_t launch_case(const NormGradParams& p, const Layout& l, const RowStages& r, cudaStream_t s) {
+  constexpr auto kernel = norm_grad_kernel<HF, YF, LANES, CPL, PAIR, BRANCH, CASE>;
+  const cudaError_t e = LANES == 0 ? allow_shared<kernel>() : cudaSuccess;
+  return e != cudaSuccess ? e
+                          : launch(kernel, dim3(unsigned((PAIR ? 2 : 1) * l.units(p.f.T))), l.threads, r.shared, PAIR,
+                                   false, s, p, r.depth);
+}
+
+template <bool HF, bool YF, bool PAIR, int BRANCH>
+cudaError_t launch_wide(const NormGradParams& p, bool any, const Layout& l, const RowStages& r, cudaStream_t s) {
+  if (any) return launch_case<HF, YF, 0, 2, PAIR, BRANCH, kAnyCase>(p, l, r, s);
+  if constexpr (BRANCH != kNoBranch)
+    if (p.f.post) return launch_case<HF, YF, 0, 2, PAIR, BRANCH, kPostCase>(p, l, r, s);
+  return launch_case<HF, YF, 0, 2, PAIR, BRANCH, kPlainCase>(p, l, r, s);
 }
 
 template <bool HF, bool YF, int BRANCH>
-cudaError_t launch_grad(const NormGradParams& p, cudaStream_t s) {
-  if (p.f.groups <= 8) return launch_rows<HF, YF, 8, 1, false, BRANCH>(p, s);
-  if (p.f.groups <= 16) return launch_rows<HF, YF, 16, 1, false, BRANCH>(p, s);
-  if (p.f.groups <= 32) return launch_rows<HF, YF, 32, 1, false, BRANCH>(p, s);
-  if (p.f.groups <= 64) return launch_rows<HF, YF, 32, 2, false, BRANCH>(p, s);
-  if (p.f.groups <= kPairGroups) return launch_rows<HF, YF, 0, 2, false, BRANCH>(p, s);
-  return launch_rows<HF, YF, 0, 2, true, BRANCH>(p, s);
+cudaError_t launch_grad(const NormGradParams& params, cudaStream_t s) {
+  NormGradParams p = params;
+  p.f.wait_limit_ns = wait_limit_ns();
+  const bool sums = p.d_w != nullptr || p.d_wp != nullptr || (p.f.gate_kind == LP_GATE_CHANNEL && p.d_gate != nullptr);
+  if (!sums) p.partials = nullptr;
+  Layout l = layout_of(p.f.groups);
+  cudaError_t e;
+  if (l.lanes > 0) {
+    const RowStages r{l.resident, 1, size_t(kSmallThreads) * 8 * sizeof(float)};  // the sums over the CTA's rows
+    e = l.lanes == 8 ? launch_case<HF, YF, 8, 1, false, BRANCH, kAnyCase>(p, l, r, s)
+                     : launch_case<HF, YF, 32, 1, false, BRANCH, kAnyCase>(p, l, r, s);
+  } else {
+    const int64_t units = (1 + (p.d_h_out != nullptr)) * kUnits<HF> +
+                          ((p.d_norm != nullptr) + (BRANCH != kNoBranch) + (BRANCH == kFullGate)) * kUnits<YF>;
+    const RowStages r = row_stages(units * 16 * 2 * l.threads, l.resident, kUnderWay);
+    l.resident = r.ctas;
+    const bool any = p.d_norm == nullptr || p.d_h_out == nullptr || r.depth == 1;
+    e = l.pair ? launch_wide<HF, YF, true, BRANCH>(p, any, l, r, s) : launch_wide<HF, YF, false, BRANCH>(p, any, l, r, s);
+  }
+  if (e == cudaSuccess && sums)
+    e = launch(norm_join_kernel, dim3((p.f.groups * 8 + kJoinCols - 1) / kJoinCols, kSums), kJoinThreads, 0, 0, true, s,
+               p, int(l.units(p.f.T)));
+  return e;
 }
 
 template <bool HF, bool YF>
 cudaError_t launch_grad(const NormGradParams& p, cudaStream_t s) {
-  if (p.f.y == nullptr) return launch_grad<HF, YF, kNoBranch>(p, s);
-  if (p.f.gate_kind == LP_GATE_FULL || p.f.drop.threshold > 0) return launch_grad<HF, YF, kElementwise>(p, s);
-  return launch_grad<HF, YF, kScaled>(p, s);
+  switch (branch_of(p.f)) {
+    case kNoBranch: return launch_grad<HF, YF, kNoBranch>(p, s);
+    case kScaled: return launch_grad<HF, YF, kScaled>(p, s);
+    case kDropped: return launch_grad<HF, YF, kDropped>(p, s);
+    default: return launch_grad<HF, YF, kFullGate>(p, s);
+  }
 }
 
 }  // namespace
 
 size_t norm_backward_ws_bytes(int64_t T, int64_t H) {
-  const int groups = int(H / 8);
-  const Layout l = groups <= 8    ? layout_of<8, 1, false>(groups)
-                   : groups <= 16 ? layout_of<16, 1, false>(groups)
-                   : groups <= 32 ? layout_of<32, 1, false>(groups)
-                   : groups <= 64 ? layout_of<32, 2, false>(groups)
-                   : groups <= kPairGroups ? layout_of<0, 2, false>(groups)
-                                           : layout_of<0, 2, true>(groups);
-  return size_t(l.units(T)) * kSums * size_t(H) * sizeof(float);
+  return size_t(layout_of(int(H / 8)).units(T)) * kSums * size_t(H) * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_backward(const NormGradParams& p, bool h_f32, bool y_f32, cudaStream_t s) {

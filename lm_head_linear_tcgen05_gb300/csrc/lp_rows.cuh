@@ -57,6 +57,19 @@ constexpr int kUnits = F32 ? 2 : 1;
 template <bool F32>
 struct Group {
   uint4 v[kUnits<F32>];
+  // not through the read-only path: a call's output may be its input
+  static __device__ __forceinline__ Group read(const uint4* p) {
+    Group g;
+#pragma unroll
+    for (int i = 0; i < kUnits<F32>; ++i) g.v[i] = p[i];
+    return g;
+  }
+  static __device__ __forceinline__ Group zero() {
+    Group g;
+#pragma unroll
+    for (int i = 0; i < kUnits<F32>; ++i) g.v[i] = make_uint4(0u, 0u, 0u, 0u);
+    return g;
+  }
   __device__ __forceinline__ Eight unpack() const {
     if constexpr (F32) {
       return Eight{{pack2(__uint_as_float(v[0].x), __uint_as_float(v[0].y)),
@@ -121,37 +134,73 @@ __device__ __forceinline__ Eight weight_factor(const void* w, bool bf16, float o
   return w != nullptr ? load_vector(w, bf16, g) + all_of(offset) : all_of(1.f);
 }
 
+// What joins the stream, as the kernels are compiled for it: nothing; y times factors of its row and columns; that
+// with dropout; with a factor of every element, and perhaps dropout.
+enum Branch { kNoBranch, kScaled, kDropped, kFullGate };
+
+inline Branch branch_of(const NormParams& p) {
+  if (p.y == nullptr) return kNoBranch;
+  return p.gate_kind == LP_GATE_FULL ? kFullGate : p.drop.threshold > 0 ? kDropped : kScaled;
+}
+
+// What else they are compiled for: anything, decided as they run; or the whole work without or with a post norm, on
+// rows with two stages at least. Deciding for every group costs a fifth of the instructions.
+enum Case { kAnyCase, kPlainCase, kPostCase };
+
 // ------------------------------------------------------------------ rows in flight
 
-__device__ __forceinline__ void copy_async16(uint32_t shared, const void* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared), "l"(global) : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-// until the oldest of `depth` groups has arrived
-__device__ __forceinline__ void copy_async_oldest(int depth) {
-  if (depth == 3)
-    copy_async_wait<2>();
-  else if (depth == 2)
-    copy_async_wait<1>();
-  else
-    copy_async_wait<0>();
+// Contiguous bytes of global memory to shared memory; both addresses and the size are multiples of 16.
+__device__ __forceinline__ void copy_bulk(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(to)),
+               "l"(from), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
-__device__ __forceinline__ uint4 read_shared16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
+// Zeroes the end of a part of a stage, which no copy writes: there it is read as columns that are 0.
+__device__ __forceinline__ void zero_tail(uint4* part, int from, int to) {
+  for (int i = from + int(threadIdx.x); i < to; i += blockDim.x) part[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// A thread's own part of the rows in flight: `depth` stages of UNITS 16-byte units, in shared memory that only
-// this thread copies to and reads, so that its own wait is all that is needed. The parts lie an odd number of
-// units apart, which spreads the threads over the banks.
-constexpr int kMaxDepth = 3;  // rows in flight, the present one among them
-__host__ __device__ inline int part_units(int depth, int units) { return (depth * units) | 1; }
+constexpr int kMaxDepth = 3;  // rows that a CTA has in shared memory or under way
+
+// The stages of a CTA's rows in shared memory, each filled by bulk copies that one thread asks for. Rows of 8 KB read
+// this way, 64 KB of them under way on an SM, come at the rate of a plain copy; the same through cp.async, 16 bytes
+// a thread, at 0.7 of it (two inputs and two outputs of 16384 x 4096, 83 and 116 us, any depth).
+struct RowRing {
+  uint64_t full[kMaxDepth];
+  uint32_t fills[kMaxDepth];  // the first thread's: how often a stage has been filled or is being filled
+  int abort;
+  __device__ __forceinline__ void init() {  // a barrier of the CTA has to follow
+    if (threadIdx.x != 0) return;
+#pragma unroll
+    for (int i = 0; i < kMaxDepth; ++i) {
+      mbar_init(&full[i], 1);
+      fills[i] = 0;
+    }
+    abort = 0;
+    fence_barrier_init();
+  }
+  // announces copies of so many bytes in all; false after a wait has given up: then none may follow
+  __device__ __forceinline__ bool begin(int stage, uint32_t bytes) {
+    if (*const_cast<const volatile int*>(&abort) != 0) return false;
+    ++fills[stage];
+    mbar_arrive_expect_tx(&full[stage], bytes);
+    return true;
+  }
+  // until the stage's fill of this parity (0 for the first, 1 for the second, 0 for the third, ...) has arrived.
+  // Past the wait limit the error is recorded and the CTA goes on to its end with what the stage holds.
+  __device__ __forceinline__ void wait(int stage, uint32_t parity, uint64_t limit_ns, unsigned int* err) {
+    mbar_wait(&full[stage], parity, &abort, limit_ns, err);
+  }
+  // after giving up: until the copies under way have arrived
+  __device__ __forceinline__ void drain() {
+    if (threadIdx.x != 0 || *const_cast<const volatile int*>(&abort) == 0) return;
+    const uint64_t deadline = global_timer_ns() + kDrainLimitNs;
+    for (int i = 0; i < kMaxDepth; ++i)
+      if (fills[i] > 0) drain_until(&full[i], (fills[i] - 1) & 1u, deadline);
+  }
+};
 
 // ------------------------------------------------------------------ sums over a row
 
@@ -164,10 +213,31 @@ __device__ __forceinline__ void sum_lanes(float (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], off));
 }
 
+// The same over a warp, but each sum ends in 32 / N lanes only: returns sum lane / (32 / N). 18 instructions for four
+// sums instead of 40. N is 1, 2 or 4.
+template <int N>
+__device__ __forceinline__ float scatter_sums(const float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  float x = v[0];
+  if constexpr (N == 4) {
+    const bool up = (lane & 16) != 0, odd = (lane & 8) != 0;
+    const float a = __fadd_rn(up ? v[2] : v[0], __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16));
+    const float b = __fadd_rn(up ? v[3] : v[1], __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16));
+    x = __fadd_rn(odd ? b : a, __shfl_xor_sync(0xffffffffu, odd ? a : b, 8));
+  } else if constexpr (N == 2) {
+    const bool up = (lane & 16) != 0;
+    x = __fadd_rn(up ? v[1] : v[0], __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16));
+  }
+#pragma unroll
+  for (int off = 16 / N; off >= 1; off >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
+}
+
 constexpr int kMostWarps = 16;
 
-// N sums over the CTA, every thread gets them, in an order set by its number of warps. `scratch` starts zeroed; calls
-// alternate between its halves, so that one barrier a call is enough.
+// Up to N sums over the CTA, every thread gets them, in an order set by its number of warps. Calls alternate between
+// the halves, so that one barrier a call is enough. The warps' sums are added across lanes too: a row's exchange costs
+// what a thread issues for it, and reading them all in every thread is 46 instructions for four sums of 8 warps, not 12.
 template <int N>
 struct __align__(16) CtaSums {
   float at[2][N][kMostWarps];
@@ -177,21 +247,24 @@ struct __align__(16) CtaSums {
   }
   template <int M>
   __device__ __forceinline__ void add(float (&v)[M], int& half) {
-    sum_lanes<32>(v);
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-      for (int i = 0; i < M; ++i) at[half][i][threadIdx.x >> 5] = v[i];
+    constexpr int kLanes = 32 / M;
+    const int lane = threadIdx.x & 31, sum = lane / kLanes;
+    const float mine = scatter_sums(v);
+    if (lane % kLanes == 0) at[half][sum][threadIdx.x >> 5] = mine;
     __syncthreads();
-    const int fours = (blockDim.x + 127) >> 7;
+    float x;
+    if constexpr (M == 4) {
+      const float2 two = reinterpret_cast<const float2*>(at[half][sum])[lane % kLanes];
+      x = __fadd_rn(two.x, two.y);
+    } else {
+      x = at[half][sum][lane % kMostWarps];
+    }
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      const float4* p = reinterpret_cast<const float4*>(at[half][i]);
-      float4 s = p[0];
-      for (int w = 1; w < fours; ++w) {
-        const float4 x = p[w];
-        s = make_float4(__fadd_rn(s.x, x.x), __fadd_rn(s.y, x.y), __fadd_rn(s.z, x.z), __fadd_rn(s.w, x.w));
-      }
-      v[i] = __fadd_rn(__fadd_rn(s.x, s.y), __fadd_rn(s.z, s.w));
+    for (int off = M == 4 ? 4 : 8; off >= 1; off >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, off));
+    v[0] = x;
+    if constexpr (M > 1) {
+#pragma unroll
+      for (int i = 0; i < M; ++i) v[i] = __shfl_sync(0xffffffffu, x, i * kLanes);
     }
     half ^= 1;
   }
@@ -212,18 +285,38 @@ inline cudaError_t allow_shared() {
   return e;
 }
 
+// How many CTAs an SM holds for rows of so many bytes, and with how many stages each.
+struct RowStages {
+  int ctas, depth;
+  size_t shared;
+};
+
+constexpr int64_t kRowsShared = 220 * 1024;  // of an SM, for stages
+// As many CTAs as the registers allow and two stages each, fewer CTAs if the stages would be more than `aim` bytes;
+// more stages if there is room below it.
+inline RowStages row_stages(int64_t stage, int most_ctas, int64_t aim) {
+  RowStages r;
+  r.ctas = most_ctas < 1 ? 1 : most_ctas > 16 ? 16 : most_ctas;
+  r.depth = 2;
+  while (r.ctas > 2 && r.ctas * r.depth * stage > aim) --r.ctas;
+  if (r.ctas * r.depth * stage > kRowsShared) r.ctas = 1;
+  if (r.depth * stage > kRowsShared) r.depth = 1;
+  while (r.depth < kMaxDepth && r.ctas * (r.depth + 1) * stage <= aim) ++r.depth;
+  r.shared = size_t(r.depth * stage);
+  return r;
+}
+
 // ------------------------------------------------------------------ dropout
 
 // Philox4x32-10, the counter-based generator of Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy
-// as 1, 2, 3" (SC 2011), with the multipliers and key increments given there. HOST_KEYS: the ten rounds' keys come
-// with the call, an operand of the rounds' exclusive ors that costs nothing (without device-side seeds).
-template <bool HOST_KEYS>
+// as 1, 2, 3" (SC 2011), with the multipliers and key increments given there. The ten rounds' keys come with the
+// call, an operand of the rounds' exclusive ors that costs nothing, unless device-side seeds change them.
 struct Philox {
   const DropoutParams& d;
-  uint32_t k0 = 0, k1 = 0, c2, c3;
+  uint32_t k0, k1, c2, c3;
   __device__ __forceinline__ explicit Philox(const DropoutParams& drop) : d(drop) {
     uint64_t seed = d.seed, offset = d.offset;
-    if (!HOST_KEYS && d.rng != nullptr) {
+    if (d.rng != nullptr) {
       seed += __ldg(d.rng);
       offset += __ldg(d.rng + 1);
     }
@@ -232,37 +325,41 @@ struct Philox {
     c2 = uint32_t(offset);
     c3 = uint32_t(offset >> 32);
   }
+  static __device__ __forceinline__ void round(uint4& x, uint32_t a, uint32_t b) {
+    const uint64_t p = uint64_t(0xD2511F53u) * x.x, q = uint64_t(0xCD9E8D57u) * x.z;
+    x = make_uint4(uint32_t(q >> 32) ^ x.y ^ a, uint32_t(q), uint32_t(p >> 32) ^ x.w ^ b, uint32_t(p));
+  }
   __device__ __forceinline__ uint4 words(uint64_t counter) const {
-    uint32_t x0 = uint32_t(counter), x1 = uint32_t(counter >> 32), x2 = c2, x3 = c3, a = k0, b = k1;
+    uint4 x = make_uint4(uint32_t(counter), uint32_t(counter >> 32), c2, c3);
+    if (d.rng == nullptr) {
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
-      const uint64_t p = uint64_t(0xD2511F53u) * x0, q = uint64_t(0xCD9E8D57u) * x2;
-      x0 = uint32_t(q >> 32) ^ x1 ^ (HOST_KEYS ? d.keys[2 * r] : a);
-      x1 = uint32_t(q);
-      x2 = uint32_t(p >> 32) ^ x3 ^ (HOST_KEYS ? d.keys[2 * r + 1] : b);
-      x3 = uint32_t(p);
-      a += kPhiloxStep0;
-      b += kPhiloxStep1;
+      for (int r = 0; r < 10; ++r) round(x, d.keys[2 * r], d.keys[2 * r + 1]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 10; ++r) round(x, k0 + r * kPhiloxStep0, k1 + r * kPhiloxStep1);
     }
-    return make_uint4(x0, x1, x2, x3);
+    return x;
   }
 };
 
-// A group after dropout by the four words of its counter: element j has the j-th 16 bits and is dropped where they are
+// Dropout of a group by the four words of its counter: element j has the j-th 16 bits and is dropped where they are
 // below the threshold, that is, where they, as the high half of a word, are at most `limit` = threshold 2^16 - 1.
 // 16 bits because the generator, not the memory, would bound dropout with 32 (a group would need two counters).
-// What is dropped becomes 0 whatever it was.
-__device__ __forceinline__ Eight drop8(const Eight& e, const uint4& words, uint32_t limit, float factor) {
+// What is dropped becomes 0 whatever it was; what is kept stays, the factor 1 / (1 - p) is the caller's. With several
+// groups each comparison is made once for all of them.
+template <typename... E>
+__device__ __forceinline__ void keep8(const uint4& words, uint32_t limit, E&... e) {
   const uint32_t w[4] = {words.x, words.y, words.z, words.w};
-  const Eight s = e * factor;
-  Eight r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    unpack2(s.v[i], lo, hi);
-    r.v[i] = pack2((w[i] << 16) > limit ? lo : 0.f, w[i] > limit ? hi : 0.f);
+    const bool first = (w[i] << 16) > limit, second = w[i] > limit;
+    auto keep = [&](Eight& x) {
+      float lo, hi;
+      unpack2(x.v[i], lo, hi);
+      x.v[i] = pack2(first ? lo : 0.f, second ? hi : 0.f);
+    };
+    (keep(e), ...);
   }
-  return r;
 }
 
 }  // namespace lp
