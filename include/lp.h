@@ -749,8 +749,8 @@ typedef struct {
  *   d_y    = e,  or with post_norm  q a' - y q^3 mean(a' y),  a' = e (o + post_weight),
  *            q = 1 / sqrt(mean y^2 + eps)
  *   d_weight = sum_t d_norm u r,   d_post_weight = sum_t e y q
- * Rows depend on their own inputs alone; the sums over tokens have an order fixed by T and H, so
- * results are bitwise the same from run to run. T = 0 writes zeros to the three sums (nothing
+ * Rows depend on their own inputs alone; the sums over tokens have an order fixed by T, H, the types
+ * and the options, so results are bitwise the same from run to run. T = 0 writes zeros to the three sums (nothing
  * when accumulating). Workspace: lp_norm_workspace_size(T, H). */
 LP_API lp_status lp_residual_norm_backward(int64_t T, int64_t H, const lp_norm_inputs* in, const lp_norm_options* opts,
                                            const lp_norm_grads* grads, void* workspace, size_t ws_bytes,
@@ -772,11 +772,11 @@ typedef enum {
  *   logits      [T, E] of type options.logits_dtype, row stride ld_logits >= E (any alignment
  *               of the type; rows on 16-byte boundaries are faster), 1 <= E <= LP_MAX_EXPERTS
  *   ids         int32 [T, K], the experts that each token went to: [0, E), or -1 for a slot
- *               that was not used; 1 <= K <= LP_MAX_EXPERT_SLOTS, T K < 2^31
+ *               that was not used; 1 <= K <= LP_MAX_EXPERT_SLOTS, T K <= 2^30
  *   mask        uint8 [T], nonzero = the token counts; NULL keeps every token. What logits and
  *               ids hold where the mask is zero has no effect
  *   cu_seqlens  int32 [n_seqs + 1], ascending from 0 to T: the balance is taken within each
- *               sequence; NULL: over the batch
+ *               sequence, n_seqs E <= 2^30; NULL: over the batch
  *   upstream    device fp32 [1], the gradient of what follows with respect to the loss; NULL: 1 */
 typedef struct {
   const void* logits;

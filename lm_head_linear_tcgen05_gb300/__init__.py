@@ -16,6 +16,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
 
@@ -164,44 +165,6 @@ class _PreferenceOutputs(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in ("metrics", "counts", "margins", "grad_logp")]
 
 
-class _NormInputs(ctypes.Structure):
-    _fields_ = ([(k, ctypes.c_void_p) for k in ("h", "y", "weight", "post_weight", "gate", "rng")]
-                + [(k, ctypes.c_int64) for k in ("ld_h", "ld_y", "ld_gate")])
-
-
-class _NormOptions(ctypes.Structure):
-    _fields_ = ([(k, ctypes.c_float) for k in ("eps", "residual_scale", "weight_offset", "dropout")]
-                + [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("row_start", ctypes.c_int64)]
-                + [(k, ctypes.c_int32) for k in ("h_dtype", "y_dtype", "w_dtype", "gate_kind", "post_norm")])
-
-
-class _NormOutputs(ctypes.Structure):
-    _fields_ = [("h_out", ctypes.c_void_p), ("norm", ctypes.c_void_p), ("ld_h_out", ctypes.c_int64),
-                ("ld_norm", ctypes.c_int64)]
-
-
-class _NormGrads(ctypes.Structure):
-    _fields_ = ([(k, ctypes.c_void_p) for k in ("d_norm", "d_h_out", "d_h", "d_y", "d_gate", "d_weight",
-                                                "d_post_weight")]
-                + [(k, ctypes.c_int64) for k in ("ld_d_norm", "ld_d_h_out", "ld_d_h", "ld_d_y", "ld_d_gate")]
-                + [("dw_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)])
-
-
-class _BalanceInputs(ctypes.Structure):
-    _fields_ = ([(k, ctypes.c_void_p) for k in ("logits", "ids", "mask", "cu_seqlens", "upstream")]
-                + [("ld_logits", ctypes.c_int64), ("n_seqs", ctypes.c_int64)])
-
-
-class _BalanceOptions(ctypes.Structure):
-    _fields_ = ([("coef", ctypes.c_float), ("z_coef", ctypes.c_float)]
-                + [(k, ctypes.c_int32) for k in ("score", "logits_dtype", "grad_dtype")])
-
-
-class _BalanceOutputs(ctypes.Structure):
-    _fields_ = ([(k, ctypes.c_void_p) for k in ("metrics", "expert_counts", "counts", "grad_logits")]
-                + [("ld_grad", ctypes.c_int64)])
-
-
 _lib = None
 
 
@@ -256,11 +219,12 @@ def lib() -> ctypes.CDLL:
                                      vp]
     u64 = ctypes.c_uint64
     L.lp_dropout.argtypes = [vp, i64, i64, i64, ctypes.c_int, f32, u64, u64, i64, vp, vp, i64, vp]
-    L.lp_residual_norm.argtypes = [i64, i64, P(_NormInputs), P(_NormOptions), P(_NormOutputs), vp]
-    L.lp_residual_norm_backward.argtypes = [i64, i64, P(_NormInputs), P(_NormOptions), P(_NormGrads), vp, sz, vp]
+    packed = ctypes.c_char_p                # a structure of the call as bytes
+    L.lp_residual_norm.argtypes = [i64, i64, packed, packed, packed, vp]
+    L.lp_residual_norm_backward.argtypes = [i64, i64, packed, packed, packed, vp, sz, vp]
     L.lp_norm_workspace_size.argtypes = [i64, i64]
     L.lp_norm_workspace_size.restype = sz
-    L.lp_balance_loss.argtypes = [i64, i64, i64, P(_BalanceInputs), P(_BalanceOptions), P(_BalanceOutputs), vp, sz, vp]
+    L.lp_balance_loss.argtypes = [i64, i64, i64, packed, packed, packed, vp, sz, vp]
     L.lp_balance_workspace_size.argtypes = [i64, i64, i64, i64]
     L.lp_balance_workspace_size.restype = sz
     L.lp_get_device_error.argtypes = [vp]
@@ -1157,6 +1121,39 @@ def _matrix(t: torch.Tensor, name: str, device: Optional[int] = None):
 
 _U64 = (1 << 64) - 1
 
+# lp_norm_inputs, lp_norm_options, lp_norm_outputs, lp_norm_grads and their like as bytes, which are made in a third of the time of
+# a ctypes structure; a call of a small batch is bound by what happens before its launch.
+_NORM_INPUTS = struct.Struct("@6P3q")
+_NORM_OPTIONS = struct.Struct("@4f2Qq5i4x")
+_NORM_OUTPUTS = struct.Struct("@2P2q")
+_NORM_GRADS = struct.Struct("@7P5q2i")
+_BALANCE_INPUTS = struct.Struct("@5P2q")
+_BALANCE_OPTIONS = struct.Struct("@2f3i")
+_BALANCE_OUTPUTS = struct.Struct("@4Pq")
+
+
+_NOTHING: dict = {}
+
+
+def _address(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _pack(form: struct.Struct, *values) -> bytes:
+    try:
+        return form.pack(*values)
+    except struct.error as e:
+        raise TypeError(f"an option has the wrong type or is out of range: {e}") from None
+
+
+def _rows_like(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
+    """_rows for the matrix that is as it should be, at once."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device and shape[0] > 1:
+        stride = t.stride()
+        if stride[1] == 1:
+            return stride[0]
+    return _rows(t, name, dtype, shape[0], shape[1], device)
+
 
 def _rng(rng: Optional[torch.Tensor], device: int) -> Optional[int]:
     if rng is None:
@@ -1188,22 +1185,22 @@ def _norm_call(h, y, weight, post_norm, post_weight, gate, residual_scale, eps, 
                row_start, rng, y_dtype):
     """Checks what the residual norm and its gradient share: (T, H, device index, inputs, options, weights' dtype)."""
     T, H, h_dtype, ld_h = _matrix(h, "h")
-    d = h.get_device()
-    ld_y = 0
+    d, shape = h.get_device(), h.shape
+    ld_y, at_y = 0, 0
     if y is not None:
         if not isinstance(y, torch.Tensor) or y.dtype not in _LP_DTYPES:
             raise TypeError("y must be an fp32 or bf16 CUDA tensor")
-        ld_y = _rows(y, "y", y.dtype, T, H, d)
         y_dtype = y.dtype
+        ld_y, at_y = _rows_like(y, "y", y_dtype, shape, d), y.data_ptr()
     if y_dtype not in _LP_DTYPES:
         raise TypeError("the norm's type must be torch.float32 or torch.bfloat16")
-    kind, ld_gate, w_dtype = LP_GATE_NONE, 0, None
+    kind, ld_gate, w_dtype, at_gate = LP_GATE_NONE, 0, None, 0
     if gate is not None:
         if not isinstance(gate, torch.Tensor):
             raise TypeError("gate must be a torch.Tensor")
         if gate.dim() == 1:
             kind, w_dtype = LP_GATE_CHANNEL, gate.dtype
-            _vector(gate, "gate", gate.dtype, H, d)
+            _vector(gate, "gate", w_dtype, H, d)
         elif gate.dim() == 2 and gate.shape[1] == 1 and gate.shape[0] == T:
             kind = LP_GATE_TOKEN
             if gate.dtype is not torch.float32 or not gate.is_contiguous():
@@ -1211,19 +1208,24 @@ def _norm_call(h, y, weight, post_norm, post_weight, gate, residual_scale, eps, 
             _on_device(gate, "gate", d)
         else:
             kind = LP_GATE_FULL
-            ld_gate = _rows(gate, "gate", y_dtype, T, H, d)
-    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
-        if t is not None:
-            w_dtype = getattr(t, "dtype", None) if w_dtype is None else w_dtype
-            _vector(t, name, w_dtype, H, d)
+            ld_gate = _rows_like(gate, "gate", y_dtype, shape, d)
+        at_gate = gate.data_ptr()
+    at_w = at_wp = 0
+    if weight is not None:
+        w_dtype = getattr(weight, "dtype", None) if w_dtype is None else w_dtype
+        at_w = _vector(weight, "weight", w_dtype, H, d)
+    if post_weight is not None:
+        w_dtype = getattr(post_weight, "dtype", None) if w_dtype is None else w_dtype
+        at_wp = _vector(post_weight, "post_weight", w_dtype, H, d)
     if w_dtype is None:
         w_dtype = torch.float32
-    if w_dtype not in _LP_DTYPES:
+    elif w_dtype not in _LP_DTYPES:
         raise TypeError("weights must be torch.float32 or torch.bfloat16")
-    ci = _NormInputs(h.data_ptr(), _ptr(y), _ptr(weight), _ptr(post_weight), _ptr(gate), _rng(rng, d), ld_h, ld_y, ld_gate)
-    co = _NormOptions(eps, residual_scale, weight_offset, dropout, seed & _U64, offset & _U64, row_start, h_dtype,
-                      _LP_DTYPES[y_dtype], _LP_DTYPES[w_dtype], kind, 1 if post_norm else 0)
-    return T, H, d, ci, co, y_dtype
+    ci = _NORM_INPUTS.pack(h.data_ptr(), at_y, at_w, at_wp, at_gate, 0 if rng is None else _rng(rng, d), ld_h, ld_y,
+                           ld_gate)
+    co = _pack(_NORM_OPTIONS, eps, residual_scale, weight_offset, dropout, seed & _U64, offset & _U64, row_start,
+               h_dtype, _LP_DTYPES[y_dtype], _LP_DTYPES[w_dtype], kind, 1 if post_norm else 0)
+    return T, H, d, ci, co, y_dtype, kind
 
 
 def lp_residual_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
@@ -1244,12 +1246,12 @@ def lp_residual_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, weight: 
     "h_out" (h itself is allowed) and "norm"."""
     if norm_dtype is None and y is None:
         norm_dtype = getattr(h, "dtype", None)
-    T, H, d, ci, co, y_dtype = _norm_call(h, y, weight, post_norm, post_weight, gate, residual_scale, eps, weight_offset,
-                                          dropout, seed, offset, row_start, rng, norm_dtype)
+    T, H, d, ci, co, y_dtype, _ = _norm_call(h, y, weight, post_norm, post_weight, gate, residual_scale, eps,
+                                             weight_offset, dropout, seed, offset, row_start, rng, norm_dtype)
     if norm_dtype is not None and norm_dtype is not y_dtype:
         raise TypeError(f"the norm has y's type, {y_dtype}")
     dev, h_out, n, ld_h_out, ld_n = h.device, None, None, H, H
-    given = {} if out is None else out
+    given = _NOTHING if out is None else out
     if y is not None:
         h_out = given.get("h_out")
         if h_out is None:
@@ -1266,10 +1268,11 @@ def lp_residual_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, weight: 
             ld_n = _rows(n, "out['norm']", y_dtype, T, H, d)
     elif given.get("norm") is not None:
         raise ValueError("out['norm'] needs norm=True")
-    cr = _NormOutputs(_ptr(h_out), _ptr(n), ld_h_out, ld_n)
+    cr = _NORM_OUTPUTS.pack(0 if h_out is None else h_out.data_ptr(), 0 if n is None else n.data_ptr(), ld_h_out, ld_n)
     with _on(dev):
-        st = lib().lp_residual_norm(T, H, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), _raw_stream(dev))
-    _raise(st, "lp_residual_norm")
+        st = lib().lp_residual_norm(T, H, ci, co, cr, _raw_stream(dev))
+    if st != LP_OK:
+        _raise(st, "lp_residual_norm")
     return (h if y is None else h_out), n
 
 
@@ -1292,65 +1295,62 @@ def lp_residual_norm_backward(h_out: torch.Tensor, y: Optional[torch.Tensor], d_
     the fp32 [H] sums held by ``out``, which may also hold any of the other results (d_h may be d_h_out, d_y may be
     d_norm). ``weight_grad=False`` and ``gate_grad=False`` leave those gradients out."""
     y_dtype = d_norm.dtype if isinstance(d_norm, torch.Tensor) else getattr(h_out, "dtype", None)
-    T, H, d, ci, co, y_dtype = _norm_call(h_out, y, weight, post_norm, post_weight, gate, residual_scale, eps,
-                                          weight_offset, dropout, seed, offset, row_start, rng, y_dtype)
+    T, H, d, ci, co, y_dtype, kind = _norm_call(h_out, y, weight, post_norm, post_weight, gate, residual_scale, eps,
+                                                weight_offset, dropout, seed, offset, row_start, rng, y_dtype)
     if dw_dtype not in _LP_DTYPES:
         raise TypeError("dw_dtype must be torch.float32 or torch.bfloat16")
-    ld_dn = 0 if d_norm is None else _rows(d_norm, "d_norm", y_dtype, T, H, d)
-    ld_dh = 0 if d_h_out is None else _rows(d_h_out, "d_h_out", h_out.dtype, T, H, d)
-    dev, given = h_out.device, {} if out is None else out
-    r = dict.fromkeys(("d_h", "d_y", "d_weight", "d_post_weight", "d_gate"))
+    shape, h_dtype = h_out.shape, h_out.dtype
+    ld_dn = 0 if d_norm is None else _rows_like(d_norm, "d_norm", y_dtype, shape, d)
+    ld_dh = 0 if d_h_out is None else _rows_like(d_h_out, "d_h_out", h_dtype, shape, d)
+    dev, given = h_out.device, _NOTHING if out is None else out
 
     def rows(name, dtype):
         t = given.get(name)
         if t is None:
-            r[name] = torch.empty((T, H), dtype=dtype, device=dev)
-            return H
-        r[name] = t
-        return _rows(t, f"out[{name!r}]", dtype, T, H, d)
+            return torch.empty((T, H), dtype=dtype, device=dev), H
+        return t, _rows_like(t, f"out[{name!r}]", dtype, shape, d)
 
     def vector(name):
         t = given.get(name)
         if t is None:
             if accumulate:
                 raise ValueError(f"accumulate=True adds into the caller's {name}: pass it in out")
-            t = torch.empty(H, dtype=dw_dtype, device=dev)
+            return torch.empty(H, dtype=dw_dtype, device=dev)
         _vector(t, f"out[{name!r}]", dw_dtype, H, d)
-        r[name] = t
+        return t
 
-    ld_out = rows("d_h", h_out.dtype)
-    ld_y = rows("d_y", y_dtype) if y is not None else 0
-    ld_gate = 0
-    if weight is not None and d_norm is not None and weight_grad:
-        vector("d_weight")
-    if post_weight is not None and weight_grad:
-        vector("d_post_weight")
+    d_h, ld_out = rows("d_h", h_dtype)
+    d_y, ld_y = (None, 0) if y is None else rows("d_y", y_dtype)
+    d_w = vector("d_weight") if weight is not None and d_norm is not None and weight_grad else None
+    d_wp = vector("d_post_weight") if post_weight is not None and weight_grad else None
+    d_gate, ld_gate = None, 0
     if gate is not None and gate_grad:
-        if co.gate_kind == LP_GATE_CHANNEL:
-            vector("d_gate")
-        elif co.gate_kind == LP_GATE_FULL:
-            ld_gate = rows("d_gate", y_dtype)
+        if kind == LP_GATE_CHANNEL:
+            d_gate = vector("d_gate")
+        elif kind == LP_GATE_FULL:
+            d_gate, ld_gate = rows("d_gate", y_dtype)
         else:
-            t = given.get("d_gate")
-            if t is None:
-                t = torch.empty((T, 1), dtype=torch.float32, device=dev)
-            _check(t, "out['d_gate']", torch.float32, 2)
-            _shape(t, "out['d_gate']", (T, 1))
-            _on_device(t, "out['d_gate']", d)
-            r["d_gate"] = t
+            d_gate = given.get("d_gate")
+            if d_gate is None:
+                d_gate = torch.empty((T, 1), dtype=torch.float32, device=dev)
+            else:
+                _check(d_gate, "out['d_gate']", torch.float32, 2)
+                _shape(d_gate, "out['d_gate']", (T, 1))
+                _on_device(d_gate, "out['d_gate']", d)
+    r = {"d_h": d_h, "d_y": d_y, "d_weight": d_w, "d_post_weight": d_wp, "d_gate": d_gate}
     for name in given:
         if given[name] is not None and r.get(name) is None:
             raise ValueError(f"out[{name!r}] is not a gradient of this call")
-    cg = _NormGrads(_ptr(d_norm), _ptr(d_h_out), _ptr(r["d_h"]), _ptr(r["d_y"]), _ptr(r["d_gate"]), _ptr(r["d_weight"]),
-                    _ptr(r["d_post_weight"]), ld_dn, ld_dh, ld_out, ld_y, ld_gate, _LP_DTYPES[dw_dtype],
-                    1 if accumulate else 0)
+    cg = _NORM_GRADS.pack(_address(d_norm), _address(d_h_out), d_h.data_ptr(), _address(d_y), _address(d_gate),
+                          _address(d_w), _address(d_wp), ld_dn, ld_dh, ld_out, ld_y, ld_gate, _LP_DTYPES[dw_dtype],
+                          1 if accumulate else 0)
     L = lib()
-    sums = r["d_weight"] is not None or r["d_post_weight"] is not None or co.gate_kind == LP_GATE_CHANNEL
+    sums = d_w is not None or d_wp is not None or (kind == LP_GATE_CHANNEL and d_gate is not None)
     with _on(dev):
         at, wsb, _kept = _scratch(L.lp_norm_workspace_size(T, H) if sums else 0, dev, workspace)
-        st = L.lp_residual_norm_backward(T, H, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cg), at, wsb,
-                                         _raw_stream(dev))
-    _raise(st, "lp_residual_norm_backward")
+        st = L.lp_residual_norm_backward(T, H, ci, co, cg, at, wsb, _raw_stream(dev))
+    if st != LP_OK:
+        _raise(st, "lp_residual_norm_backward")
     return r
 
 
@@ -1410,12 +1410,14 @@ def lp_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float = 1.0, 
     m = torch.empty(len(BALANCE_METRICS), dtype=torch.float32, device=dev) if metrics else None
     experts = torch.empty(E, dtype=torch.int64, device=dev) if metrics else None
     c = torch.empty(2, dtype=torch.int64, device=dev) if metrics else None
-    ci = _BalanceInputs(logits.data_ptr(), ids.data_ptr(), _mask_bytes(mask, T, d), cu, _upstream(upstream, d), ld, S)
-    co = _BalanceOptions(coef, z_coef, LP_SCORES[score], _LP_DTYPES[logits.dtype], _LP_DTYPES[grad_dtype])
-    cr = _BalanceOutputs(_ptr(m), _ptr(experts), _ptr(c), _ptr(g), ld_g)
+    ci = _BALANCE_INPUTS.pack(logits.data_ptr(), ids.data_ptr(), _mask_bytes(mask, T, d) or 0, cu or 0,
+                              _upstream(upstream, d) or 0, ld, S)
+    co = _pack(_BALANCE_OPTIONS, coef, z_coef, LP_SCORES[score], _LP_DTYPES[logits.dtype], _LP_DTYPES[grad_dtype])
+    cr = _BALANCE_OUTPUTS.pack(_address(m), _address(experts), _address(c), _address(g), ld_g)
     L = lib()
     with _on(dev):
         at, wsb, _kept = _scratch(L.lp_balance_workspace_size(T, E, K, S), dev, workspace)
-        st = L.lp_balance_loss(T, E, K, ctypes.byref(ci), ctypes.byref(co), ctypes.byref(cr), at, wsb, _raw_stream(dev))
-    _raise(st, "lp_balance_loss")
+        st = L.lp_balance_loss(T, E, K, ci, co, cr, at, wsb, _raw_stream(dev))
+    if st != LP_OK:
+        _raise(st, "lp_balance_loss")
     return LossOutputs(metrics=m, expert_counts=experts, counts=c, grad_logits=g)

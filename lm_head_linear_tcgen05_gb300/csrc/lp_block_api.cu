@@ -18,6 +18,8 @@ bool known_dtype(int32_t d) { return d == LP_DTYPE_F32 || d == LP_DTYPE_BF16; }
 
 int64_t size_of(int32_t dtype) { return dtype == LP_DTYPE_BF16 ? 2 : 4; }
 
+constexpr int64_t kMostSlots = int64_t(1) << 30;  // of a batch; entries of a table by sequence: 32-bit indexes with room for a step
+
 bool flag(int32_t f) { return f == 0 || f == 1; }
 
 // rows of [T, H] at stride ld that start on 16-byte boundaries
@@ -210,7 +212,7 @@ lp_status lp_residual_norm_backward(int64_t T, int64_t H, const lp_norm_inputs* 
 
 size_t lp_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t n_seqs) {
   if (!valid_rows(T) || !valid_rows(n_seqs) || T == 0 || E < 1 || E > LP_MAX_EXPERTS || K < 1 ||
-      K > LP_MAX_EXPERT_SLOTS || T * K > int64_t(INT32_MAX) || n_seqs * E > int64_t(INT32_MAX))
+      K > LP_MAX_EXPERT_SLOTS || T * K > kMostSlots || n_seqs * E > kMostSlots)
     return 0;
   return balance_ws_bytes(T, E, K, n_seqs);
 }
@@ -218,7 +220,7 @@ size_t lp_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t n_seqs
 lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balance_inputs* in, const lp_balance_options* opts,
                           const lp_balance_outputs* out, void* workspace, size_t ws_bytes, lp_stream_t stream) {
   if (in == nullptr || opts == nullptr || out == nullptr || !valid_rows(T) || E < 1 || E > LP_MAX_EXPERTS || K < 1 ||
-      K > LP_MAX_EXPERT_SLOTS || T * K > int64_t(INT32_MAX))
+      K > LP_MAX_EXPERT_SLOTS || T * K > kMostSlots)
     return LP_ERR_INVALID_ARG;
   if (!std::isfinite(opts->coef) || !std::isfinite(opts->z_coef) || !known_dtype(opts->logits_dtype) ||
       !known_dtype(opts->grad_dtype) || opts->score < LP_SCORE_SOFTMAX || opts->score > LP_SCORE_SIGMOID ||
@@ -227,7 +229,7 @@ lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balance_inpu
   if (out->metrics == nullptr && out->expert_counts == nullptr && out->counts == nullptr && out->grad_logits == nullptr)
     return LP_ERR_INVALID_ARG;
   const int64_t n_seqs = in->cu_seqlens != nullptr ? in->n_seqs : 0;
-  if (!valid_rows(n_seqs) || n_seqs * E > int64_t(INT32_MAX)) return LP_ERR_INVALID_ARG;
+  if (!valid_rows(n_seqs) || n_seqs * E > kMostSlots) return LP_ERR_INVALID_ARG;
   if (!aligned(in->upstream, 4) || !aligned(in->cu_seqlens, 4) || !aligned(out->metrics, 4) ||
       !aligned(out->expert_counts, 8) || !aligned(out->counts, 8))
     return LP_ERR_ALIGNMENT;

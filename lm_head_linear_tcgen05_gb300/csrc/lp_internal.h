@@ -366,6 +366,7 @@ struct BalanceParams {
 
 size_t balance_ws_bytes(int64_t T, int64_t E, int64_t K, int64_t n_seqs);
 cudaError_t launch_balance_loss(const BalanceParams& p, bool logits_f32, cudaStream_t s);
+cudaError_t launch_balance_loss_bf16(const BalanceParams& p, cudaStream_t s);
 
 // Argument checks and per-device state shared by the translation units of the C ABI.
 lp_status check_partition(const lp_vocab_partition* part, Shards* sh);
