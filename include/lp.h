@@ -688,7 +688,8 @@ typedef struct {
 /* Outputs of lp_residual_norm, device pointers.
  *   h_out  the stream after the block [T, H] of type h_dtype; required with y, NULL without.
  *          May be h (with the same stride)
- *   norm   its norm [T, H] of type y_dtype; NULL: not wanted. May be y (with the same stride)
+ *   norm   its norm [T, H] of type y_dtype; NULL: not wanted (weight is NULL then). May be y (with
+ *          the same stride)
  * No other overlaps. */
 typedef struct {
   void* h_out;
@@ -826,8 +827,8 @@ typedef struct {
  * are not kept get zero gradients; a batch that keeps none has loss 0. A token whose logits are all
  * -inf has p = 0 (and no z term). An id outside {-1} U [0, E) of a kept token records
  * LP_ERR_EXPERT_OUT_OF_RANGE and counts for no expert. Offsets that do not ascend from 0 to T
- * record LP_ERR_SEQ_OFFSETS; metrics are then NaN and gradients zero. Sums have a fixed order:
- * results are bitwise the same from run to run. T = 0 gives loss 0.
+ * record LP_ERR_SEQ_OFFSETS; metrics are then NaN and gradients zero. Sums have an order fixed by
+ * sizes, types and alignments: results are bitwise the same from run to run. T = 0 gives loss 0.
  * Workspace: lp_balance_workspace_size(T, E, K, n_seqs), n_seqs = 0 without cu_seqlens. */
 LP_API lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balance_inputs* in,
                                  const lp_balance_options* opts, const lp_balance_outputs* out, void* workspace,

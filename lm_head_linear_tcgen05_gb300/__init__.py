@@ -1242,7 +1242,7 @@ def lp_residual_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, weight: 
 
     h: the residual stream, bf16 or fp32 [T, H]; y: the block's output [T, H] (None: (h, the norm of h)); weights
     [H], all of one type, None for none; ``gate``: [H], fp32 [T, 1] or [T, H] of y's type. norm has y's type (without
-    y: ``norm_dtype``, default h's); ``norm=False`` leaves it out. Dropout as in lp_dropout. ``out`` may hold
+    y: ``norm_dtype``, default h's); ``norm=False`` leaves it out (then without weight). Dropout as in lp_dropout. ``out`` may hold
     "h_out" (h itself is allowed) and "norm"."""
     if norm_dtype is None and y is None:
         norm_dtype = getattr(h, "dtype", None)

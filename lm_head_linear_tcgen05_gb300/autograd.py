@@ -14,13 +14,14 @@ wrappers only route tensors between the two calls.
     logp, entropy = linear_logp(X, [W], None, part, y, tau)
     (logp * advantages).sum().backward()       # X.grad, W.grad
 
-The operator's neighbours in a training step have wrappers of the same kind: embedding,
-policy_loss and preference_loss.
+The operator's neighbours in a training step have wrappers of the same kind: embedding, dropout,
+residual_norm, balance_loss, policy_loss and preference_loss.
 
-    X = block(embedding(ids, [W], part))
+    h = dropout(embedding(ids, [W], part), 0.1, seed)
+    h, X = residual_norm(h, block(h), weight=norm_weight, dropout=0.1, seed=seed, offset=1)
     logp, entropy = linear_logp(X, [W], None, part, y, tau)
     loss, metrics, counts = policy_loss(logp, old_logp, advantages, entropy=entropy, entropy_coef=1e-3)
-    loss.backward()
+    (loss + balance_loss(router_logits, experts, coef=1e-2)[0]).backward()
 """
 from __future__ import annotations
 
@@ -29,8 +30,9 @@ from typing import Optional, Sequence
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (lp_backward_ex, lp_backward_from_logits, lp_embedding, lp_embedding_backward, lp_forward,
-               lp_forward_from_logits, lp_policy_loss, lp_preference_loss)
+from . import (lp_backward_ex, lp_backward_from_logits, lp_balance_loss, lp_dropout, lp_embedding, lp_embedding_backward,
+               lp_forward, lp_forward_from_logits, lp_policy_loss, lp_preference_loss, lp_residual_norm,
+               lp_residual_norm_backward)
 
 
 def _zeros_like_rows(ref: torch.Tensor) -> torch.Tensor:
@@ -119,6 +121,14 @@ def linear_logp_from_logits(logits: Sequence[torch.Tensor], part, y: torch.Tenso
     return logp, entropy
 
 
+def _rows_taken(g: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """A gradient of [T, H]; one that was broadcast or transposed has rows the library does not take."""
+    if g is not None and (g.stride(1) != 1 or (g.stride(0) * g.element_size()) % 16 != 0 or g.data_ptr() % 16 != 0
+                          or g.stride(0) < g.shape[1]):
+        g = g.clone(memory_format=torch.contiguous_format)
+    return g
+
+
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, part, scale, out_dtype, *W):
@@ -132,10 +142,7 @@ class _Embedding(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g):
         (ids,) = ctx.saved_tensors
-        # a gradient that was broadcast or transposed has rows the library does not take
-        if g.stride(1) != 1 or (g.stride(0) * g.element_size()) % 16 != 0 or g.data_ptr() % 16 != 0 \
-                or g.stride(0) < g.shape[1]:
-            g = g.clone(memory_format=torch.contiguous_format)
+        g = _rows_taken(g)
         dW = lp_embedding_backward(ids, g, ctx.part, scale=ctx.scale, dw_dtype=ctx.dtype)
         return (None, None, None, None, *[d if ctx.needs_input_grad[4 + k] else None for k, d in enumerate(dW)])
 
@@ -148,9 +155,94 @@ def embedding(ids: torch.Tensor, W: Sequence[torch.Tensor], part, scale: float =
     return _Embedding.apply(ids, part, float(scale), out_dtype, *W)
 
 
-def _check_options(function, options):
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, row_start, rng):
+        ctx.options = (p, seed, offset, row_start)
+        ctx.save_for_backward(rng)
+        return lp_dropout(x, p, seed, offset=offset, row_start=row_start, rng=rng)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        p, seed, offset, row_start = ctx.options
+        (rng,) = ctx.saved_tensors
+        return (lp_dropout(_rows_taken(g), p, seed, offset=offset, row_start=row_start, rng=rng),) + (None,) * 5
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, row_start: int = 0,
+            rng: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """lp_dropout with autograd. No mask is kept: the backward makes the same bits again, from ``rng`` too, which
+    must not change before it has run."""
+    return _Dropout.apply(x, float(p), int(seed), int(offset), int(row_start), rng)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, y, weight, post_weight, gate, rng, options):
+        h_out, norm = lp_residual_norm(h, y, weight=weight, post_weight=post_weight, gate=gate, rng=rng, **options)
+        ctx.options = {k: v for k, v in options.items() if k not in ("norm", "norm_dtype")}
+        ctx.save_for_backward(h_out, y, weight, post_weight, gate, rng)
+        ctx.set_materialize_grads(False)
+        return (None, norm) if y is None else (h_out, norm)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_h, g_norm):
+        if g_h is None and g_norm is None:
+            return (None,) * 7
+        h_out, y, weight, post_weight, gate, rng = ctx.saved_tensors
+        _, want_y, want_w, want_wp, want_gate, _, _ = ctx.needs_input_grad
+        vectors = [t for t in (weight, post_weight, gate) if t is not None and t.dim() == 1]
+        r = lp_residual_norm_backward(h_out, y, _rows_taken(g_norm), _rows_taken(g_h), weight=weight,
+                                      post_weight=post_weight, gate=gate, rng=rng, gate_grad=want_gate,
+                                      dw_dtype=vectors[0].dtype if vectors else torch.float32,
+                                      weight_grad=want_w or want_wp, **ctx.options)
+        return (r["d_h"] if ctx.needs_input_grad[0] else None, r["d_y"] if want_y else None,
+                r["d_weight"] if want_w else None, r["d_post_weight"] if want_wp else None, r["d_gate"], None, None)
+
+
+def residual_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                  post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  rng: Optional[torch.Tensor] = None, **options):
+    """lp_residual_norm with autograd: returns (h_out, norm), both differentiable with respect to h, y, the weights
+    and the gate (without y: (h, the norm of h)). ``options`` are those of lp_residual_norm (post_norm, residual_scale,
+    eps, weight_offset, dropout, seed, offset, row_start, norm, norm_dtype). The backward reads h_out, not h, and
+    makes dropout's bits again. Gradients have the types of what they are of; for fp32 sums beside bf16 weights,
+    or added to earlier ones, call lp_residual_norm_backward."""
+    if "out" in options:
+        raise TypeError("out is not an option of residual_norm under autograd, whose outputs are its own")
+    h_out, norm = _ResidualNorm.apply(h, y, weight, post_weight, gate, rng, options)
+    return (h if y is None else h_out), norm
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, options):
+        out = lp_balance_loss(logits, ids, grads=False, **options)
+        _save(ctx, (logits, ids), options)
+        ctx.mark_non_differentiable(out["metrics"], out["expert_counts"], out["counts"])
+        return out["metrics"][0].clone(), out["metrics"], out["expert_counts"], out["counts"]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g, _g_metrics, _g_experts, _g_counts):
+        (logits, ids), options = _saved(ctx, 2)
+        out = lp_balance_loss(logits, ids, metrics=False, upstream=g.to(torch.float32), **options)
+        return out["grad_logits"], None, None
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, **options):
+    """lp_balance_loss with autograd: returns (loss, metrics, expert_counts, counts), the loss differentiable with
+    respect to logits (the counts are not differentiated). ``options`` are those of lp_balance_loss (coef,
+    z_coef, score, mask, cu_seqlens, workspace)."""
+    _check_options("balance_loss", options, "out", "grad_dtype")
+    return _BalanceLoss.apply(logits, ids, options)
+
+
+def _check_options(function, options, *more):
     """Refuses the options of the library call that the wrapper gives itself."""
-    for name in ("upstream", "grads", "metrics"):
+    for name in ("upstream", "grads", "metrics") + more:
         if name in options:
             raise TypeError(f"{name} is not an option of {function} under autograd, which sets it")
 

@@ -510,11 +510,11 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
         uint64_t x[kPairs];
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) x[k] = again.pair(k);
-        const float top = highest(x), base = top != -INFINITY ? top * kLog2e : 0.f, was = total, was_d = d;
+        const float top = highest(x), base = top != -INFINITY ? top : 0.f, was = total, was_d = d;
         sum = dot = 0;
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
-          x[k] = ex2_pair(fma2(x[k], both(kLog2e), both(-base)));
+          x[k] = ex2_pair(mul2(add2(x[k], both(-base)), both(kLog2e)));
           add(x[k], k);
           q[k] = vanish ? x[k] : q[k];
         }
@@ -527,14 +527,15 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
     } else {
       const float top = highest(q);
       const bool some = top != -INFINITY;  // NaN is passed on by the exponentials
-      const float base = some ? top * kLog2e : 0.f;
+      const float base = some ? top : 0.f;
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) {
-        q[k] = ex2_pair(fma2(q[k], both(kLog2e), both(-base)));
+        // the difference first: a row of the type's lowest value has a base that times log2 e would overflow
+        q[k] = ex2_pair(mul2(add2(q[k], both(-base)), both(kLog2e)));
         add(q[k], k);
       }
       over_lanes();
-      if (some) lse = kLn2 * (base + lg2_ftz(total));
+      if (some) lse = __fmaf_rn(kLn2, lg2_ftz(total), base);
     }
     const float inv = total == 0.f ? 0.f : rcp_ftz(total);  // NaN stays
     d *= inv;

@@ -248,7 +248,7 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
     if constexpr (kHasY) {
       if (token_gate && here && p.d_gate != nullptr && g0 == 0) static_cast<float*>(p.d_gate)[row] = ry * after;
       if (post) {
-        const float ky = -(ry * ry * ry * (token * after * p.f.inv_width));
+        const float ky = -(token * after * p.f.inv_width * ry * ry * ry);  // in this order: ry^3 alone may overflow
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
           const int g = g0 + c * width;
