@@ -233,6 +233,12 @@ __device__ __forceinline__ int count_sequences(const BalanceParams& p, int a, in
   return tokens;
 }
 
+// Zeroes what the sequences' counts are added to; the count stage starts beside it.
+__global__ void __launch_bounds__(kThreads) balance_zero_kernel(uint4* at, unsigned n) {
+  grid_launch_dependents();
+  for (unsigned i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) at[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __grid_constant__ BalanceParams p, const BalanceWs ws) {
   __shared__ int hist[LP_MAX_EXPERTS], all[LP_MAX_EXPERTS], part[kCountThreads / 32], kept;
   grid_launch_dependents();
@@ -245,7 +251,9 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
   if (p.n_seqs == 0) {
     tokens = cta_sum<kCountThreads>(count_slots<kCountThreads>(p, all, a, b), part);
   } else {
-    if (bad_offsets<kCountThreads>(p, cta, ctas)) atomicOr(&ws.totals->bad, 1);
+    const bool bad = bad_offsets<kCountThreads>(p, cta, ctas);
+    grid_dependency_wait();
+    if (bad) atomicOr(&ws.totals->bad, 1);
     tokens = count_sequences<kCountThreads>(p, a, b, all, hist, ws.kept, ws.by_seq, &ws.totals->seqs, part);
   }
   if (threadIdx.x == 0) {
@@ -311,11 +319,20 @@ struct Raw {
       w[v] = F32 ? static_cast<const uint32_t*>(row)[e] : uint32_t(static_cast<const uint16_t*>(row)[e]) << 16;
     }
   }
-  __device__ __forceinline__ uint64_t pair(int i) const {  // elements 2 i and 2 i + 1
-    if constexpr (F32 || !kWide)
+  // Elements 2 i and 2 i + 1. FLOOR: bf16 logits at least -69 (e^69 is nearly 2^100), NaN stays.
+  template <bool FLOOR>
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (F32) {
       return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-    else
-      return pack2(bf16_lo(w[i]), bf16_hi(w[i]));
+    } else if constexpr (!kWide) {  // each in the high half of a word
+      uint32_t x = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+      if constexpr (FLOOR) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xc28ac28au));
+      return pack2(bf16_lo(x), bf16_hi(x));
+    } else {
+      uint32_t x = w[i];
+      if constexpr (FLOOR) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xc28ac28au));
+      return pack2(bf16_lo(x), bf16_hi(x));
+    }
   }
 };
 
@@ -383,14 +400,16 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
   constexpr int kPairs = N / 2, kPerWarp = 32 / LANES;
   const int tid = threadIdx.x, sub = tid % LANES, E = p.E, S = p.n_seqs;
   const int warps = ctas * kWarps;
-  const int steps = (p.T + kPerWarp - 1) / kPerWarp, per = (steps + warps - 1) / warps;
-  const int64_t first = (int64_t(cta) * kWarps + (tid >> 5)) * per * kPerWarp;  // of the warp
-  int64_t t = first + (tid & 31) / LANES;
-  const char* row = static_cast<const char*>(p.in.logits) + t * p.in.ld_logits * (LF ? 4 : 2);
+  const int steps = (p.T - 1) / kPerWarp + 1, per = (steps - 1) / warps + 1;
+  const int first = min((cta * kWarps + (tid >> 5)) * per, steps) * kPerWarp;  // of the warp
+  const int end = min(first + per * kPerWarp, p.T);                            // of its tokens; the last may lack some
+  int t = first + (tid & 31) / LANES;
+  const char* row = static_cast<const char*>(p.in.logits) + int64_t(t) * p.in.ld_logits * (LF ? 4 : 2);
   const int64_t by_row = p.in.ld_logits * kPerWarp * (LF ? 4 : 2);
-  char* grad = static_cast<char*>(p.out.grad_logits) + t * p.out.ld_grad * (p.grad_f32 ? 4 : 2);
-  const int64_t by_grad = p.out.ld_grad * kPerWarp * (p.grad_f32 ? 4 : 2);
-  auto kept = [&](int64_t at) { return at < p.T && kept_token(p.in.mask, int(at)); };
+  const bool grad_f32 = p.grad_f32, want_grad = p.out.grad_logits != nullptr;
+  char* grad = static_cast<char*>(p.out.grad_logits) + int64_t(t) * p.out.ld_grad * (grad_f32 ? 4 : 2);
+  const int64_t by_grad = p.out.ld_grad * kPerWarp * (grad_f32 ? 4 : 2);
+  auto kept = [&](int at) { return at < end && kept_token(p.in.mask, at); };
   uint32_t has = 0;  // the lane's accesses that lie in a row
 #pragma unroll
   for (int v = 0; v < N / VE; ++v) has |= uint32_t((sub + v * LANES) * VE < E) << v;
@@ -402,17 +421,19 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
       to.template load<false>(from, read, has, sub, LANES);
   };
   Raw<LF, VE, N> raw;
-  bool mine = kept(t), following = per > 1 && kept(t + kPerWarp);  // the tokens of raw and of the step after are kept
+  bool mine = kept(t), following = kept(t + kPerWarp);  // the tokens of raw and of the step after are kept
   load_row(raw, row, mine);
   int seq = 0, next = p.T;  // the token's sequence, and where it ends; at first, of the warp's first token
-  if (S > 0 && first < p.T) {
-    seq = sequence_by_warp(p.in.cu_seqlens, 0, S - 1, int(first));
+  if (S > 0 && first < end) {
+    seq = sequence_by_warp(p.in.cu_seqlens, 0, S - 1, first);
     next = -1;
   }
   const Found found = count();
   const float inv_n = found.tokens > 0 ? 1.f / float(found.tokens) : 0.f;
   const float up = p.in.upstream != nullptr ? __ldg(p.in.upstream) : 1.f;
-  if (found.bad) {
+  const float of_balance = up * p.coef, of_z = p.z_coef != 0.f ? up * p.z_coef * 2.f * inv_n : 0.f;
+  const bool sound = !found.bad;
+  if (!sound) {
     mine = following = false;
     load_row(raw, row, false);
   }
@@ -439,21 +460,21 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
   }
   float balance = 0.f, zsum = 0.f;
 #pragma unroll 1
-  for (int i = 0; i < per; ++i, t += kPerWarp) {
+  for (int first_t = first; first_t < end; first_t += kPerWarp, t += kPerWarp) {
     const bool keep = mine;
     uint64_t q[kPairs];
 #pragma unroll
-    for (int k = 0; k < kPairs; ++k) q[k] = raw.pair(k);
+    for (int k = 0; k < kPairs; ++k) q[k] = raw.template pair<SIGMOID>(k);
     row += by_row;
     mine = following;
-    if (i + 1 < per) load_row(raw, row, mine);
-    following = i + 2 < per && !found.bad && kept(t + 2 * kPerWarp);
+    if (first_t + kPerWarp < end) load_row(raw, row, mine);
+    following = sound && kept(t + 2 * kPerWarp);
     if (S > 0 && keep && t >= next) {
       // the one after, or, over empty ones, by search
       if (next >= 0 && seq < S - 1) ++seq;
       next = seq == S - 1 ? p.T : __ldg(p.in.cu_seqlens + seq + 1);
       if (t >= next) {
-        seq = sequence_in(p.in.cu_seqlens, seq, S - 1, int(t));
+        seq = sequence_in(p.in.cu_seqlens, seq, S - 1, t);
         next = seq == S - 1 ? p.T : __ldg(p.in.cu_seqlens + seq + 1);
       }
       const int n = found.kept[seq];
@@ -493,8 +514,10 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
         // x = e^-l up to 2^100 (s is below kTiny long before), s = 1 / (1 + x), 1 - s = x s
         float lo, hi;
         unpack2(mul2(q[k], both(-kLog2e)), lo, hi);
-        asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(100.f));
-        asm("min.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(100.f));
+        if constexpr (LF) {
+          asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(100.f));
+          asm("min.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(100.f));
+        }
         const uint64_t x = pack2(hw_ex2(lo), hw_ex2(hi));
         unpack2(add2(x, both(1.f)), lo, hi);
         const uint64_t score = pack2(rcp_ftz(lo), rcp_ftz(hi));
@@ -509,7 +532,7 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
         load_row(again, row - by_row, vanish);
         uint64_t x[kPairs];
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) x[k] = again.pair(k);
+        for (int k = 0; k < kPairs; ++k) x[k] = again.template pair<false>(k);
         const float top = highest(x), base = top != -INFINITY ? top : 0.f, was = total, was_d = d;
         sum = dot = 0;
 #pragma unroll
@@ -543,13 +566,13 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
       balance = __fmaf_rn(w, __fmaf_rn(total, inv, d), balance);
       zsum = __fmaf_rn(lse, lse * inv_n, zsum);
     }
-    if (t < p.T && p.out.grad_logits != nullptr) {
+    if (want_grad && t < end) {
       // q (a (f - d) + z) as q (a f + b); a token that is not kept has a = b = 0
-      const float a = keep ? up * p.coef * w * inv : 0.f;
-      const float b = (keep && p.z_coef != 0.f ? up * p.z_coef * 2.f * lse * inv_n * inv : 0.f) - a * d;
+      const float scale = keep ? inv : 0.f, a = of_balance * w * scale;
+      const float b = __fmaf_rn(-a, d, of_z != 0.f ? of_z * lse * scale : 0.f);
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) q[k] = mul2(q[k], fma2(f[k], both(a), both(b)));
-      if (p.grad_f32)
+      if (grad_f32)
         store_grads<true, VE, N>(grad, has, sub, LANES, q);
       else
         store_grads<false, VE, N>(grad, has, sub, LANES, q);
@@ -747,15 +770,20 @@ cudaError_t launch_stages(const BalanceParams& p, cudaStream_t s) {
     return launch(balance_cluster_kernel<LF, SIGMOID, VE, LANES, N>, kCluster, kThreads, true, false, s, p);
   size_t bytes;
   const BalanceWs ws = carve(p.workspace, p.E, p.n_seqs, &bytes);
-  cudaError_t e = p.n_seqs > 0 ? cudaMemsetAsync(ws.totals, 0, ws.zero_bytes, s) : cudaSuccess;
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (p.n_seqs > 0) {
+    const size_t n = ws.zero_bytes / sizeof(uint4), ctas = (n + kThreads - 1) / kThreads;
+    e = launch(balance_zero_kernel, int(ctas < 2 * kSms ? ctas : 2 * kSms), kThreads, false, false, s,
+               reinterpret_cast<uint4*>(ws.totals), unsigned(n));
+    if (e != cudaSuccess) return e;
+  }
   const int64_t some = (int64_t(p.T) * p.K + 16383) / 16384;
   const int clusters = int(some < kCountClusters ? some : kCountClusters);
-  if ((e = launch(balance_count_kernel, clusters * kCluster, kCountThreads, true, false, s, p, ws)) != cudaSuccess) return e;
+  e = launch(balance_count_kernel, clusters * kCluster, kCountThreads, true, p.n_seqs > 0, s, p, ws);
+  if (e != cudaSuccess) return e;
   const int64_t per_cta = int64_t(kWarps) * (32 / LANES), ctas = (p.T + per_cta - 1) / per_cta;
-  return launch(balance_token_kernel<LF, SIGMOID, VE, LANES, N>, int(ctas < kTokenCtas ? ctas : kTokenCtas), kThreads, false,
-                true,
-                s, p, ws, clusters);
+  return launch(balance_token_kernel<LF, SIGMOID, VE, LANES, N>, int(ctas < kTokenCtas ? ctas : kTokenCtas), kThreads,
+                false, true, s, p, ws, clusters);
 }
 
 // Lanes of a token: as few as leave a lane 16 logits, but four. (With 32 bf16 logits a lane, 131071 x 256 take 51 us,
