@@ -757,7 +757,8 @@ LP_API lp_status lp_residual_norm_backward(int64_t T, int64_t H, const lp_norm_i
                                            const lp_norm_grads* grads, void* workspace, size_t ws_bytes,
                                            lp_stream_t stream);
 
-/* Bytes of device scratch of lp_residual_norm_backward; 0 for invalid arguments. */
+/* Bytes of device scratch of lp_residual_norm_backward; 0 for short batches, and for invalid
+ * arguments. */
 LP_API size_t lp_norm_workspace_size(int64_t T, int64_t H);
 
 #define LP_MAX_EXPERTS 1024
@@ -834,7 +835,7 @@ LP_API lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balan
                                  const lp_balance_options* opts, const lp_balance_outputs* out, void* workspace,
                                  size_t ws_bytes, lp_stream_t stream);
 
-/* Bytes of device scratch of lp_balance_loss; 0 for invalid arguments. */
+/* Bytes of device scratch of lp_balance_loss; 0 for short batches, and for invalid arguments. */
 LP_API size_t lp_balance_workspace_size(int64_t T, int64_t E, int64_t K, int64_t n_seqs);
 
 /* Synchronises `stream`, returns the first device-side error recorded on the

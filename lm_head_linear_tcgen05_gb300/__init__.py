@@ -817,7 +817,7 @@ _SAME_DEVICE = contextlib.nullcontext()
 
 
 def _on(dev: torch.device):
-    return _SAME_DEVICE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _SAME_DEVICE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _raw_stream(dev: torch.device) -> int:
@@ -1184,13 +1184,19 @@ def lp_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, row_start:
 def _norm_call(h, y, weight, post_norm, post_weight, gate, residual_scale, eps, weight_offset, dropout, seed, offset,
                row_start, rng, y_dtype):
     """Checks what the residual norm and its gradient share: (T, H, device index, inputs, options, weights' dtype)."""
-    T, H, h_dtype, ld_h = _matrix(h, "h")
-    d, shape = h.get_device(), h.shape
-    ld_y, at_y = 0, 0
+    h_dtype = _LP_DTYPES.get(h.dtype) if type(h) is torch.Tensor and h.dim() == 2 else None
+    d = -1 if h_dtype is None else h.get_device()
+    if d >= 0 and h.shape[0] > 1 and h.stride(1) == 1:
+        shape, ld_h = h.shape, h.stride(0)
+        T, H = shape
+    else:
+        T, H, h_dtype, ld_h = _matrix(h, "h")
+        d, shape = h.get_device(), h.shape
+    ld_y = at_y = 0
     if y is not None:
-        if not isinstance(y, torch.Tensor) or y.dtype not in _LP_DTYPES:
+        y_dtype = getattr(y, "dtype", None)
+        if y_dtype not in _LP_DTYPES:
             raise TypeError("y must be an fp32 or bf16 CUDA tensor")
-        y_dtype = y.dtype
         ld_y, at_y = _rows_like(y, "y", y_dtype, shape, d), y.data_ptr()
     if y_dtype not in _LP_DTYPES:
         raise TypeError("the norm's type must be torch.float32 or torch.bfloat16")
@@ -1378,11 +1384,13 @@ def lp_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float = 1.0, 
     d, dev = logits.get_device(), logits.device
     if T > 0 and E > 1 and logits.stride(1) != 1:
         raise ValueError("logits must have unit column stride")
-    _check(ids, "ids", torch.int32, 2)
-    _on_device(ids, "ids", d)
-    if ids.shape[0] != T:
-        raise ValueError(f"ids must have {T} rows, got {ids.shape[0]}")
-    K = ids.shape[1]
+    if not (type(ids) is torch.Tensor and ids.dtype is torch.int32 and ids.dim() == 2 and ids.get_device() == d
+            and ids.is_contiguous()):
+        _check(ids, "ids", torch.int32, 2)
+        _on_device(ids, "ids", d)
+    rows, K = ids.shape
+    if rows != T:
+        raise ValueError(f"ids must have {T} rows, got {rows}")
     if score not in LP_SCORES:
         raise ValueError(f"score is one of {tuple(LP_SCORES)}")
     S, cu = 0, None

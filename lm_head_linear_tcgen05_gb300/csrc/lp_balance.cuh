@@ -68,14 +68,6 @@ __host__ __device__ inline BalanceWs carve(void* base, int64_t E, int64_t n_seqs
   return w;
 }
 
-// The generic address of another cluster CTA's shared variable.
-template <typename V>
-__device__ __forceinline__ V* of_cta(V* mine, uint32_t rank) {
-  uint64_t a;
-  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(mine)), "r"(rank));
-  return reinterpret_cast<V*>(a);
-}
-
 // Index of the sequence that holds token t, searched in [lo, hi]; within them whatever the offsets hold.
 __device__ __forceinline__ int sequence_in(const int32_t* cu, int lo, int hi, int t) {
 #pragma unroll 1

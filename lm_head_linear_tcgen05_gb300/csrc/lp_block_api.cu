@@ -185,7 +185,8 @@ lp_status lp_residual_norm_backward(int64_t T, int64_t H, const lp_norm_inputs* 
   if (st != LP_OK) return st;
   if (opts->gate_kind == LP_GATE_TOKEN && !aligned(g->d_gate, 4)) return LP_ERR_ALIGNMENT;
   if (sums[0] != nullptr || sums[1] != nullptr || sums[2] != nullptr) {
-    if (workspace == nullptr || ws_bytes < norm_backward_ws_bytes(T, H)) return LP_ERR_WORKSPACE_TOO_SMALL;
+    const size_t need = norm_backward_ws_bytes(T, H);
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LP_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 16)) return LP_ERR_ALIGNMENT;
     p.partials = static_cast<float*>(workspace);
   }

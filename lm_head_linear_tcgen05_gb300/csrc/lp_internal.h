@@ -346,7 +346,8 @@ struct NormGradParams {
   void *d_h, *d_y, *d_gate, *d_w, *d_wp; // d_gate: by kind
   int64_t ld_d_norm, ld_d_h_out, ld_d_h, ld_d_y, ld_d_gate;
   int32_t accumulate, dw_bf16;
-  float* partials;                       // [parts][sums][H]
+  int32_t one_cluster;                   // the launch's one cluster adds the sums over tokens
+  float* partials;                       // [parts][sums][H], otherwise
 };
 
 size_t norm_backward_ws_bytes(int64_t T, int64_t H);

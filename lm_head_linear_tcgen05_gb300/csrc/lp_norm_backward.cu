@@ -19,6 +19,8 @@ namespace {
 
 constexpr int kSmallThreads = 256;
 constexpr int kSums = 2;  // over tokens
+constexpr int kCluster = 8;
+constexpr int kRowsOfOne = 3;  // rows of a CTA, where one cluster takes a batch
 constexpr int kSms = 152;
 // Bytes of rows on an SM: more than in the forward, for a row takes longer. 20001 x 1032 with an fp32 stream and a full
 // gate: 138 us with 64 KB, 102 with 96, 90 with 128, 85 with 192.
@@ -46,6 +48,29 @@ __device__ __forceinline__ void sum_pair(float (&v)[N], float (*both)[2][4], int
   cluster_sync();
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __fadd_rn(both[half][0][i], both[half][1][i]);
+}
+
+// The gradients of column col from one of the two sums over tokens.
+__device__ __forceinline__ void write_sum(const NormGradParams& p, int which, int64_t col, float x) {
+  auto value = [&](const void* v) {
+    return p.f.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(v)[col]) : static_cast<const float*>(v)[col];
+  };
+  auto write = [&](void* out, float v) {
+    if (out == nullptr) return;
+    if (p.dw_bf16) {
+      static_cast<__nv_bfloat16*>(out)[col] = __float2bfloat16_rn(v);
+    } else {
+      float* o = static_cast<float*>(out) + col;
+      *o = p.accumulate ? __fadd_rn(*o, v) : v;
+    }
+  };
+  if (which == 0) {
+    write(p.d_w, x);
+  } else {
+    const bool channel = p.f.gate_kind == LP_GATE_CHANNEL;
+    write(p.d_wp, channel ? x * value(p.f.gate) : x);
+    if (channel) write(p.d_gate, p.f.wp != nullptr ? x * __fadd_rn(p.f.offset, value(p.f.wp)) : x);
+  }
 }
 
 // LANES lanes to a row (0: the CTA, or with PAIR two), each with CPL groups of eight columns.
@@ -265,9 +290,13 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
   }
   if constexpr (kCta) ring.drain();
   grid_launch_dependents();
-  if (p.partials != nullptr) {
+  const bool sum_w = p.d_w != nullptr, sum_S = kHasY && (p.d_wp != nullptr || (channel && p.d_gate != nullptr));
+  if (sum_w || sum_S) {
     const int64_t H = int64_t(groups) * 8;
-    float* out = p.partials + int64_t(unit) * kSums * H;
+    // to memory for the second kernel, or, from a batch that one cluster has, to shared memory behind the scratch
+    float* const own = reinterpret_cast<float*>(stages) + (kCta ? 0 : kSmallThreads * CPL * 8);
+    float* const out = p.one_cluster ? own : p.partials + int64_t(unit) * kSums * H;
+    if (kCta && p.one_cluster) __syncthreads();  // the stages have been read
     auto write = [&](int which, const Eight (&v)[CPL]) {
       if constexpr (LANES > 0) {
         // the CTA's rows' sums are added in their order, through shared memory
@@ -290,9 +319,19 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
         }
       }
     };
-    if (p.d_w != nullptr) write(0, dw);
+    if (sum_w) write(0, dw);
     if constexpr (kHasY) {
-      if (p.d_wp != nullptr || (channel && p.d_gate != nullptr)) write(1, S);
+      if (sum_S) write(1, S);
+    }
+    if (!PAIR && p.one_cluster) {
+      cluster_sync();
+      for (int which = sum_w ? 0 : 1; which < (sum_S ? 2 : 1); ++which)
+        for (int col = blockIdx.x * blockDim.x + tid; col < H; col += gridDim.x * blockDim.x) {
+          float x = of_cta(out, 0)[which * H + col];
+          for (uint32_t r = 1; r < gridDim.x; ++r) x = __fadd_rn(x, of_cta(out, r)[which * H + col]);
+          write_sum(p, which, col, x);
+        }
+      cluster_sync();  // no CTA's shared memory goes while another reads it
     }
   }
   if constexpr (PAIR) cluster_sync();  // neither CTA's shared memory goes while the other may write to it
@@ -313,9 +352,6 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t H = int64_t(p.f.groups) * 8;
   const int col = blockIdx.x * kJoinCols + threadIdx.x % kJoinCols, j = threadIdx.x / kJoinCols;
   if (first ? p.d_w == nullptr : p.d_wp == nullptr && d_gate == nullptr) return;
-  auto value = [&](const void* v) {
-    return p.f.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(v)[col]) : static_cast<const float*>(v)[col];
-  };
   grid_dependency_wait();
   float x = 0.f;
   if (col < H) {
@@ -328,21 +364,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (j != 0 || col >= H) return;
 #pragma unroll
   for (int k = 1; k < kJoinParts; ++k) x = __fadd_rn(x, scratch[k][threadIdx.x]);
-  auto write = [&](void* out, float v) {
-    if (out == nullptr) return;
-    if (p.dw_bf16) {
-      static_cast<__nv_bfloat16*>(out)[col] = __float2bfloat16_rn(v);
-    } else {
-      float* o = static_cast<float*>(out) + col;
-      *o = p.accumulate ? __fadd_rn(*o, v) : v;
-    }
-  };
-  if (first) {
-    write(p.d_w, x);
-  } else {
-    write(p.d_wp, p.f.gate_kind == LP_GATE_CHANNEL ? x * value(p.f.gate) : x);
-    write(d_gate, p.f.wp != nullptr ? x * __fadd_rn(p.f.offset, value(p.f.wp)) : x);
-  }
+  write_sum(p, blockIdx.y, col, x);
 }
 
 // ------------------------------------------------------------------ launches
@@ -350,8 +372,12 @@ __global__ void __launch_bounds__(kJoinThreads)
 // How a gradient of rows of `groups` groups is laid out over CTAs: lanes and groups a lane as the kernel has them.
 struct Layout {
   int lanes, pair, threads, per_cta, resident;
+  // Whether one cluster takes the whole batch and adds its CTAs' sums itself: a short one, for which the second
+  // launch and the workspace cost more than the rows.
+  bool one_cluster(int64_t T) const { return !pair && T <= kCluster * (lanes > 0 ? per_cta : kRowsOfOne); }
   int64_t units(int64_t T) const {  // CTAs, or pairs of them
     const int64_t rows = (T + per_cta - 1) / per_cta;
+    if (one_cluster(T)) return rows < kCluster ? rows : kCluster;
     const int64_t most = int64_t(kSms) * resident / (1 + pair);
     return rows < most ? rows : most;
   }
@@ -370,7 +396,7 @@ Layout layout_of(int groups) {
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, int pair, bool after, cudaStream_t s,
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, int cluster, bool after, cudaStream_t s,
                    const A&... args) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
@@ -379,9 +405,9 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, 
   cfg.dynamicSmemBytes = shared;
   cfg.stream = s;
   cfg.attrs = attr;
-  if (pair) {
+  if (cluster > 0) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = 2;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
     attr[cfg.numAttrs].val.clusterDim.y = 1;
     attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
@@ -398,10 +424,16 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, 
 template <bool HF, bool YF, int LANES, int CPL, bool PAIR, int BRANCH, int CASE>
 cudaError_t launch_case(const NormGradParams& p, const Layout& l, const RowStages& r, cudaStream_t s) {
   constexpr auto kernel = norm_grad_kernel<HF, YF, LANES, CPL, PAIR, BRANCH, CASE>;
-  const cudaError_t e = LANES == 0 ? allow_shared<kernel>() : cudaSuccess;
-  return e != cudaSuccess ? e
-                          : launch(kernel, dim3(unsigned((PAIR ? 2 : 1) * l.units(p.f.T))), l.threads, r.shared, PAIR,
-                                   false, s, p, r.depth);
+  cudaError_t e = LANES == 0 ? allow_shared<kernel>() : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  const int64_t units = l.units(p.f.T);
+  size_t shared = r.shared;
+  if (p.one_cluster) {  // the sums, in the stages' place or behind the scratch
+    const size_t sums = size_t(kSums) * p.f.groups * 8 * sizeof(float);
+    shared = LANES > 0 ? shared + sums : shared > sums ? shared : sums;
+  }
+  return launch(kernel, dim3(unsigned((PAIR ? 2 : 1) * units)), l.threads, shared, p.one_cluster ? int(units) : PAIR ? 2 : 0,
+                false, s, p, r.depth);
 }
 
 template <bool HF, bool YF, bool PAIR, int BRANCH>
@@ -417,8 +449,8 @@ cudaError_t launch_grad(const NormGradParams& params, cudaStream_t s) {
   NormGradParams p = params;
   p.f.wait_limit_ns = wait_limit_ns();
   const bool sums = p.d_w != nullptr || p.d_wp != nullptr || (p.f.gate_kind == LP_GATE_CHANNEL && p.d_gate != nullptr);
-  if (!sums) p.partials = nullptr;
   Layout l = layout_of(p.f.groups);
+  p.one_cluster = sums && l.one_cluster(p.f.T);
   cudaError_t e;
   if (l.lanes > 0) {
     const RowStages r{l.resident, 1, size_t(kSmallThreads) * 8 * sizeof(float)};  // the sums over the CTA's rows
@@ -432,7 +464,7 @@ cudaError_t launch_grad(const NormGradParams& params, cudaStream_t s) {
     const bool any = p.d_norm == nullptr || p.d_h_out == nullptr || r.depth == 1;
     e = l.pair ? launch_wide<HF, YF, true, BRANCH>(p, any, l, r, s) : launch_wide<HF, YF, false, BRANCH>(p, any, l, r, s);
   }
-  if (e == cudaSuccess && sums)
+  if (e == cudaSuccess && sums && !p.one_cluster)
     e = launch(norm_join_kernel, dim3((p.f.groups * 8 + kJoinCols - 1) / kJoinCols, kSums), kJoinThreads, 0, 0, true, s,
                p, int(l.units(p.f.T)));
   return e;
@@ -451,7 +483,8 @@ cudaError_t launch_grad(const NormGradParams& p, cudaStream_t s) {
 }  // namespace
 
 size_t norm_backward_ws_bytes(int64_t T, int64_t H) {
-  return size_t(layout_of(int(H / 8)).units(T)) * kSums * size_t(H) * sizeof(float);
+  const Layout l = layout_of(int(H / 8));
+  return l.one_cluster(T) ? 0 : size_t(l.units(T)) * kSums * size_t(H) * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_backward(const NormGradParams& p, bool h_f32, bool y_f32, cudaStream_t s) {

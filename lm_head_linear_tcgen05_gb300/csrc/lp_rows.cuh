@@ -270,6 +270,14 @@ struct __align__(16) CtaSums {
   }
 };
 
+// The generic address of another cluster CTA's shared variable.
+template <typename V>
+__device__ __forceinline__ V* of_cta(V* mine, uint32_t rank) {
+  uint64_t a;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(mine)), "r"(rank));
+  return reinterpret_cast<V*>(a);
+}
+
 // Lets KERNEL be launched with as much dynamic shared memory as an SM has for it; asked for once per device.
 constexpr int kMostShared = 224 * 1024;  // beside 3 KB that a kernel declares itself
 template <auto KERNEL>

@@ -104,10 +104,10 @@ def test_residual_norm_refuses(lp):
 
 @no_gpu
 def test_residual_norm_backward_refuses(lp):
-    need = lp.lp_norm_workspace_size(100, 64)
+    need = lp.lp_norm_workspace_size(1000, 64)
     assert need > 0
 
-    def call(T=100, H=64, ws=A, wsb=need, grads=True, d_norm=A, d_h_out=A, d_h=A, d_y=A, d_gate=None, d_weight=A, d_post=None,
+    def call(T=1000, H=64, ws=A, wsb=need, grads=True, d_norm=A, d_h_out=A, d_h=A, d_y=A, d_gate=None, d_weight=A, d_post=None,
              ld=(64,) * 5, dw=0, acc=0, **kw):
         ci, co = _packed(lp, kw)
         cg = lp._NORM_GRADS.pack(*(v or 0 for v in (d_norm, d_h_out, d_h, d_y, d_gate, d_weight, d_post)), *ld, dw, acc)
@@ -125,7 +125,7 @@ def test_residual_norm_backward_refuses(lp):
                       dict(ld=(68, 64, 64, 64, 64)), dict(kind=2, gate=A, d_gate=A + 2), dict(kind=3, gate=A, d_gate=A + 8)):
         assert call(**bad) == ALIGN, bad
     assert call(wsb=need - 1) == WORKSPACE and call(ws=None) == WORKSPACE
-    assert call(kind=1, gate=A, d_gate=A, d_weight=None, ws=None) == WORKSPACE
+    assert call(kind=1, gate=A, d_gate=A, d_weight=None, ws=None) == WORKSPACE and call(T=100, ws=None, wsb=0) == DEVICE
     empty = dict(T=0, h=None, y=None, d_norm=None, d_h_out=None, d_h=None, d_y=None, ws=None, wsb=0)
     assert call(**empty) == DEVICE and call(**empty, acc=1) == OK and call(**dict(empty, d_weight=None)) == OK
 
@@ -159,8 +159,11 @@ def test_balance_loss_refuses(lp):
 
 def test_workspace_sizes(lp):
     assert lp.lp_norm_workspace_size(0, 64) == 0 and lp.lp_norm_workspace_size(8, 60) == 0 and lp.lp_norm_workspace_size(8, 16392) == 0
+    # a short batch belongs to one cluster, which needs none
+    for H, most in ((8, 256), (64, 256), (72, 64), (256, 64), (264, 24), (8192, 24)):
+        assert lp.lp_norm_workspace_size(most, H) == 0 and lp.lp_norm_workspace_size(most + 1, H) > 0
     for H in (8, 64, 256, 264, 4096, 8192, 8200, 16384):
-        sizes = [lp.lp_norm_workspace_size(T, H) for T in (1, 100, 10 ** 4, 10 ** 6, 10 ** 9)]
+        sizes = [lp.lp_norm_workspace_size(T, H) for T in (300, 2000, 10 ** 4, 10 ** 6, 10 ** 9)]
         assert sizes[0] > 0 and sizes == sorted(sizes) and sizes[-1] <= 2 * 4 * H * 152 * 16
     size = lp.lp_balance_workspace_size
     # a short batch runs in one launch, which needs none

@@ -51,7 +51,7 @@ def case(T, H, stream, branch, post, gate, seed, pad=0, wdt=None, weights=True, 
 
 SHAPES = [(1, 8), (3, 64), (2, 72), (37, 128), (6, 200), (5, 256), (7, 264), (3, 520), (9, 1032), (2, 2048), (4, 4096),
           (3, 4104), (2, 8192), (3, 8200), (2, 12296), (3, 16384), (700, 64), (1300, 264), (650, 1032), (400, 4096),
-          (333, 8200)]
+          (333, 8200), (256, 64), (257, 64), (64, 256), (65, 256), (24, 1032), (25, 1032), (20, 8192)]
 
 
 def combos():
@@ -456,8 +456,10 @@ def test_refusals_of_the_binding(lp):
     with pytest.raises(ValueError):
         lp.lp_residual_norm_backward(h, y, h, h, out=dict(d_gate=z))
     small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    lp.lp_residual_norm_backward(h, y, h, h, weight=w, workspace=small)          # a short batch needs none
+    long = torch.zeros(300, 64, dtype=BF, device="cuda")
     with pytest.raises(lp.LPError):
-        lp.lp_residual_norm_backward(h, y, h, h, weight=w, workspace=small)
+        lp.lp_residual_norm_backward(long, long, long, long, weight=w, workspace=small)
     for kw in (dict(p=float("nan")), dict(p=2.0), dict(p=0.5, row_start=-2)):
         with pytest.raises(lp.LPError):
             lp.lp_dropout(h, seed=1, **kw)
