@@ -9,7 +9,7 @@
 // Bounds: what is issued for an element, then memory. So columns' weights stay in registers, the next rows come by
 // bulk copies and are read from shared memory as often as the row's sums need them, and what a call does not have
 // (a post norm, dropout, one of the two gradients) is decided when the kernel is compiled. 8192 x 4096 in bf16 with
-// both norms, a channel gate and dropout: 71 us (5.6 TB/s of 12 bytes an element); copies by each thread (cp.async) in
+// both norms, a channel gate and dropout: 70 us (5.8 TB/s of 12 bytes an element); copies by each thread (cp.async) in
 // place of bulk ones 143, the cases decided at run time 96.
 #include "lp_rows.cuh"
 
@@ -295,8 +295,9 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
     const int64_t H = int64_t(groups) * 8;
     // to memory for the second kernel, or, from a batch that one cluster has, to shared memory behind the scratch
     float* const own = reinterpret_cast<float*>(stages) + (kCta ? 0 : kSmallThreads * CPL * 8);
-    float* const out = p.one_cluster ? own : p.partials + int64_t(unit) * kSums * H;
-    if (kCta && p.one_cluster) __syncthreads();  // the stages have been read
+    const bool one = kAny && !PAIR && p.one_cluster;
+    float* const out = one ? own : p.partials + int64_t(unit) * kSums * H;
+    if (kCta && one) __syncthreads();  // the stages have been read
     auto write = [&](int which, const Eight (&v)[CPL]) {
       if constexpr (LANES > 0) {
         // the CTA's rows' sums are added in their order, through shared memory
@@ -323,7 +324,7 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
     if constexpr (kHasY) {
       if (sum_S) write(1, S);
     }
-    if (!PAIR && p.one_cluster) {
+    if (one) {
       cluster_sync();
       for (int which = sum_w ? 0 : 1; which < (sum_S ? 2 : 1); ++which)
         for (int col = blockIdx.x * blockDim.x + tid; col < H; col += gridDim.x * blockDim.x) {
@@ -339,11 +340,11 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
 
 // ------------------------------------------------------------------ the CTAs' sums
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 1024;  // 20001 x 1032 with 256: 4 us more
 constexpr int kJoinCols = 32;                          // columns of a CTA
 constexpr int kJoinParts = kJoinThreads / kJoinCols;   // threads that share a column
 
-// One sum's 32 columns: thread (i, j) adds the parts j, j + 8, ... of column i, then one adds those eight.
+// One sum's 32 columns: thread (i, j) adds the parts j, j + kJoinParts, ... of column i, then one adds those.
 __global__ void __launch_bounds__(kJoinThreads)
     norm_join_kernel(const __grid_constant__ NormGradParams p, int parts) {
   __shared__ float scratch[kJoinParts][kJoinCols];
@@ -461,7 +462,7 @@ cudaError_t launch_grad(const NormGradParams& params, cudaStream_t s) {
                           ((p.d_norm != nullptr) + (BRANCH != kNoBranch) + (BRANCH == kFullGate)) * kUnits<YF>;
     const RowStages r = row_stages(units * 16 * 2 * l.threads, l.resident, kUnderWay);
     l.resident = r.ctas;
-    const bool any = p.d_norm == nullptr || p.d_h_out == nullptr || r.depth == 1;
+    const bool any = p.d_norm == nullptr || p.d_h_out == nullptr || r.depth == 1 || p.one_cluster;
     e = l.pair ? launch_wide<HF, YF, true, BRANCH>(p, any, l, r, s) : launch_wide<HF, YF, false, BRANCH>(p, any, l, r, s);
   }
   if (e == cudaSuccess && sums && !p.one_cluster)
