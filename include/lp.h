@@ -704,7 +704,9 @@ typedef struct {
  *   h_out = R h + dropout(gate b)
  *   norm  = h_out / sqrt(mean h_out^2 + eps) (o + weight)
  * in fp32, each output rounded once: the norm is of the unrounded sum. A row's results depend on
- * that row alone, and on its number where there is dropout. Needs no workspace. */
+ * that row alone, and on its number where there is dropout. Needs no workspace. Rows come by bulk
+ * copies: one that does not arrive within the wait limit records LP_ERR_DEVICE_TIMEOUT, and what is
+ * written then is undefined (as in the gradient). */
 LP_API lp_status lp_residual_norm(int64_t T, int64_t H, const lp_norm_inputs* in, const lp_norm_options* opts,
                                   const lp_norm_outputs* out, lp_stream_t stream);
 
