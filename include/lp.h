@@ -851,7 +851,7 @@ LP_API lp_status lp_get_device_error(lp_stream_t stream);
  * result with lp_get_device_error(). Nothing hangs and nothing faults. */
 LP_API lp_status lp_selftest_wait_timeout(uint64_t limit_ns, lp_stream_t stream);
 
-/* The time limit of every pipeline wait of the GEMM kernels launched after this call, in
+/* The time limit of every pipeline wait of the GEMM and norm kernels launched after this call, in
  * nanoseconds (1 us .. 10 s; 0 restores the default of 2 s), for the whole process. A wait
  * that runs past it gives up: the kernel records LP_ERR_DEVICE_TIMEOUT, lets the copies and
  * MMAs it already started finish, frees its tensor memory and returns, leaving the context

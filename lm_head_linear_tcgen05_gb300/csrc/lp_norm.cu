@@ -3,7 +3,7 @@
 //
 // Per row of H columns (groups of eight): b = y or its norm, u = R h + dropout(gate b), norm = u rsqrt(mean u^2 +
 // eps) w. A thread takes the same columns of every row it works on and keeps them in registers between the
-// sums, so each input is read once and each output written once. Rows of up to 512 columns belong to part of a
+// sums, so each input is read once and each output written once. Rows of up to 256 columns belong to part of a
 // warp or a whole one, wider ones to a CTA; which depends on H and the types alone, and so does the order of a
 // row's sums: its bits do not depend on the batch.
 // Bounds: memory, if little enough is issued for each element. So CTAs stay for many rows, with their columns'
@@ -94,7 +94,20 @@ __global__ void __maxnreg__((kRegisters<CPL, BRANCH>)) norm_kernel(const __grid_
   };
   // Whether the thread's c-th group is to be worked on. A stage holds zeros behind a row, so there it always is.
   auto has = [&](int c, bool here) { return kCta || (here && lane + c * width < groups); };
-  Group<YF> raw_y[kHasY && !kCta ? CPL : 1];  // a warp's rows come straight from memory
+  // a warp's rows come straight from memory, the next one's while the present one is worked on
+  constexpr int kDirect = kCta ? 1 : CPL;
+  [[maybe_unused]] Group<HF> ahead_h[kDirect];
+  [[maybe_unused]] Group<YF> raw_y[kDirect], raw_z[kDirect], ahead_y[kDirect], ahead_z[kDirect];
+  auto load_ahead = [&](uint32_t of) {
+#pragma unroll
+    for (int c = 0; c < kDirect; ++c) {
+      const int g = lane + c * width;
+      if (of >= T || g >= groups) continue;
+      ahead_h[c] = Group<HF>::read(h.at<HF>(of, g));
+      if constexpr (kHasY) ahead_y[c] = Group<YF>::read(y.at<YF>(of, g));
+      if constexpr (kFull) ahead_z[c] = Group<YF>::read(z.at<YF>(of, g));
+    }
+  };
   auto read_y = [&](const uint4* at, int c) {
     if constexpr (kCta)
       return Group<YF>::read(at + at_y + (lane + c * width) * kUnits<YF>).unpack();
@@ -123,6 +136,7 @@ __global__ void __maxnreg__((kRegisters<CPL, BRANCH>)) norm_kernel(const __grid_
     row_sums(s);
     mean_y = s[0];
   }
+  if constexpr (!kCta) load_ahead(row);
   uint32_t parity = 0;
   // where the thread's first group of the row goes, and that of the next; the generator's counter of that group
   uint4* to_h = Rows{(char*)p.h_out, p.ld_h_out}.template at<HF>(row, lane);
@@ -147,13 +161,11 @@ __global__ void __maxnreg__((kRegisters<CPL, BRANCH>)) norm_kernel(const __grid_
     } else {
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
-        const int g = lane + c * width;
-        u[c] = all_of(0.f);
-        if constexpr (kHasY) raw_y[c] = Group<YF>::zero();
-        if (!has(c, here)) continue;
-        u[c] = Group<HF>::read(h.at<HF>(row, g)).unpack();
-        if constexpr (kHasY) raw_y[c] = Group<YF>::read(y.at<YF>(row, g));
+        u[c] = ahead_h[c].unpack();
+        if constexpr (kHasY) raw_y[c] = ahead_y[c];
+        if constexpr (kFull) raw_z[c] = ahead_z[c];
       }
+      load_ahead(row + step);
     }
     float mult = 1.f;  // the row's factor of y
     if constexpr (kHasY) {
@@ -174,7 +186,7 @@ __global__ void __maxnreg__((kRegisters<CPL, BRANCH>)) norm_kernel(const __grid_
       if (!has(c, here)) continue;
       if constexpr (kHasY) {
         Eight b = read_y(at, c) * (before[c] * mult);
-        if constexpr (kFull) b = b * Group<YF>::read(kCta ? at + at_gate + g * kUnits<YF> : z.at<YF>(row, g)).unpack();
+        if constexpr (kFull) b = b * (kCta ? Group<YF>::read(at + at_gate + g * kUnits<YF>) : raw_z[kCta ? 0 : c]).unpack();
         if (drop) keep8(bits[c], p.drop.limit, b);
         u[c] = fma8(u[c], p.scale, b);
         if (g < groups) store_group<HF>(to_h + c * width * kUnits<HF>, u[c]);
@@ -249,6 +261,7 @@ cudaError_t launch_rows(const NormParams& p, cudaStream_t s) {
 template <bool HF, bool YF, int BRANCH>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   if (p.groups <= 8) return launch_rows<HF, YF, 8, 1, BRANCH>(p, s);
+  if (p.groups <= 16) return launch_rows<HF, YF, 16, 1, BRANCH>(p, s);
   if (p.groups <= 32) return launch_rows<HF, YF, 32, 1, BRANCH>(p, s);
   if (p.groups <= 2 * kMostThreads) return launch_rows<HF, YF, 0, 2, BRANCH>(p, s);
   return launch_rows<HF, YF, 0, 4, BRANCH>(p, s);

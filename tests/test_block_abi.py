@@ -160,7 +160,7 @@ def test_balance_loss_refuses(lp):
 def test_workspace_sizes(lp):
     assert lp.lp_norm_workspace_size(0, 64) == 0 and lp.lp_norm_workspace_size(8, 60) == 0 and lp.lp_norm_workspace_size(8, 16392) == 0
     # a short batch belongs to one cluster, which needs none
-    for H, most in ((8, 256), (64, 256), (72, 64), (256, 64), (264, 24), (8192, 24)):
+    for H, most in ((8, 256), (64, 256), (72, 128), (136, 64), (256, 64), (264, 24), (8192, 24)):
         assert lp.lp_norm_workspace_size(most, H) == 0 and lp.lp_norm_workspace_size(most + 1, H) > 0
     for H in (8, 64, 256, 264, 4096, 8192, 8200, 16384):
         sizes = [lp.lp_norm_workspace_size(T, H) for T in (300, 2000, 10 ** 4, 10 ** 6, 10 ** 9)]

@@ -51,7 +51,7 @@ def case(T, H, stream, branch, post, gate, seed, pad=0, wdt=None, weights=True, 
 
 SHAPES = [(1, 8), (3, 64), (2, 72), (37, 128), (6, 200), (5, 256), (7, 264), (3, 520), (9, 1032), (2, 2048), (4, 4096),
           (3, 4104), (2, 8192), (3, 8200), (2, 12296), (3, 16384), (700, 64), (1300, 264), (650, 1032), (400, 4096),
-          (333, 8200), (256, 64), (257, 64), (64, 256), (65, 256), (24, 1032), (25, 1032), (20, 8192)]
+          (333, 8200), (256, 64), (257, 64), (64, 256), (65, 256), (24, 1032), (25, 1032), (20, 8192), (2500, 72), (3000, 136), (5001, 64)]
 
 
 def combos():
@@ -466,3 +466,26 @@ def test_refusals_of_the_binding(lp):
     with pytest.raises(TypeError):
         lp.lp_dropout(h, 0.5, 1, rng=torch.zeros(2, dtype=torch.int32, device="cuda"))
     assert lp.lp_get_device_error() == 0
+
+
+@pytest.mark.parametrize("limit", [1000, 20000])
+@pytest.mark.parametrize("T,H", [(2000, 4096), (700, 8200), (20, 1032)])
+def test_waits_that_run_out_are_recorded(lp, limit, T, H):
+    """With a limit that few copies meet the call ends with LP_ERR_DEVICE_TIMEOUT, or in time; the next one, with the
+    usual limit, is as if it had not been."""
+    h, y, w, wp, z, gen = case(T, H, BF, BF, True, "channel", 7)
+    o = dict(weight=w, post_norm=True, post_weight=wp, gate=z, dropout=0.1)
+    dn, dh = rows(T, H, BF, gen), rows(T, H, BF, gen)
+    both = lambda: (lp.lp_residual_norm(h, y, **o), lp.lp_residual_norm_backward(h, y, dn, dh, **o))  # noqa: E731
+    want = both()
+    assert lp.lp_get_device_error() == 0
+    try:
+        lp.lp_set_wait_limit(limit)
+        both()
+        assert lp.lp_get_device_error() in (0, 7)
+    finally:
+        lp.lp_set_wait_limit(0)
+    got = both()
+    assert lp.lp_get_device_error() == 0
+    assert torch.equal(got[0][0], want[0][0]) and torch.equal(got[0][1], want[0][1])
+    assert all(v is None or torch.equal(v, want[1][k]) for k, v in got[1].items())
