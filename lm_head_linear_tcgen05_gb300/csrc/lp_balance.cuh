@@ -27,7 +27,7 @@ constexpr int kCluster = 8;
 constexpr int kCountClusters = kSms / kCluster;
 constexpr int kTokenResident = 2;  // CTAs of the token stage on an SM; three spill, and are no faster
 constexpr int kTokenCtas = kTokenResident * kSms;
-constexpr int kFewSequences = 8;  // sequences of a CTA's tokens that are counted one by one in shared memory
+constexpr int kFewSequences = 8;  // sequences of a CTA's tokens that are counted in shared memory first
 // The one-launch form takes batches of up to this many logits, slots and (sequences x experts).
 constexpr int64_t kOneLogits = 1 << 18;
 constexpr int64_t kOneSlots = 1 << 15;
@@ -176,53 +176,86 @@ __device__ __forceinline__ bool bad_offsets(const BalanceParams& p, int cta, int
   return bad;
 }
 
-// The tokens [a, b) of a CTA by sequence: kept[s] and by_seq[s][E] (global memory, or the CTA's shared memory,
-// zeroed), all[E] (shared). Returns the kept tokens, to every thread.
-template <int THREADS>
-__device__ __forceinline__ int count_sequences(const BalanceParams& p, int a, int b, int* all, int* hist, int* kept,
-                                               int* by_seq, int* seqs, int (&part)[THREADS / 32]) {
+// A CTA's counts by sequence on their way to the tables: of a few sequences, ENTRIES slots' counts in all.
+template <int ENTRIES>
+struct LocalCounts {
+  static constexpr int kEntries = ENTRIES;
+  int slots[ENTRIES], kept[kFewSequences], ends[kFewSequences], first, last;
+};
+
+// The tokens [a, b) of a CTA by sequence, added to kept[s] and by_seq[s][E] (global memory, or the CTA's shared memory,
+// zeroed once ready() returns) and all[E] (shared). Returns the kept tokens, to every thread.
+template <int THREADS, typename L, typename R>
+__device__ __forceinline__ int count_sequences(const BalanceParams& p, int a, int b, int* all, L& local, int* kept,
+                                               int* by_seq, int* seqs, int (&part)[THREADS / 32], const R& ready) {
   const int32_t* cu = p.in.cu_seqlens;
+  const int tid = threadIdx.x, E = p.E;
   if (a >= b) return 0;
-  const int s0 = sequence_by_warp(cu, 0, p.n_seqs - 1, a), s1 = sequence_by_warp(cu, s0, p.n_seqs - 1, b - 1);
-  if (s1 - s0 >= kFewSequences) {
-    const bool vec = vector_ids(p);
+  // the first and the last sequence, searched at the same time
+  if (tid < 64) {
+    const int s = sequence_by_warp(cu, 0, p.n_seqs - 1, tid < 32 ? a : b - 1);
+    if (tid == 0) local.first = s;
+    if (tid == 32) local.last = s;
+  }
+  __syncthreads();
+  const int s0 = local.first, n_local = max(local.last, s0) - s0 + 1;
+  const bool vec = vector_ids(p), few = n_local <= kFewSequences && n_local * E <= L::kEntries;
+  bool wrong = false;
+  int n = 0;
+  if (!few) {
     // many short sequences: a thread per token, straight to the table
-    int n = 0;
-    bool wrong = false;
+    ready();
 #pragma unroll 1
-    for (int t = a + int(threadIdx.x); t < b; t += THREADS) {
+    for (int t = a + tid; t < b; t += THREADS) {
       if (!kept_token(p.in.mask, t)) continue;
-      const int s = sequence_in(cu, s0, s1, t);
+      const int s = sequence_in(cu, s0, s0 + n_local - 1, t);
       ++n;
       if (atomicAdd(kept + s, 1) == 0 && seqs != nullptr) atomicAdd(seqs, 1);
       each_slot(p, t, vec, [&](int e) {
-        wrong |= count_slot(all, e, p.E);
-        if (unsigned(e) < unsigned(p.E)) atomicAdd(by_seq + int64_t(s) * p.E + e, 1);
+        wrong |= count_slot(all, e, E);
+        if (unsigned(e) < unsigned(E)) atomicAdd(by_seq + int64_t(s) * E + e, 1);
       });
     }
     if (wrong) record_error(p.err, LP_ERR_EXPERT_OUT_OF_RANGE);
     return cta_sum<THREADS>(n, part);
   }
-  int from = a, tokens = 0;
 #pragma unroll 1
-  for (int s = s0; s <= s1; ++s) {
-    const int to = s == s1 ? b : min(max(__ldg(cu + s + 1), from), b);
-    if (to == from) continue;
-    const int n = cta_sum<THREADS>(count_slots<THREADS>(p, hist, from, to), part);
-#pragma unroll 1
-    for (int e = threadIdx.x; e < p.E; e += THREADS) {
-      const int c = hist[e];
-      if (c == 0) continue;
-      hist[e] = 0;
-      all[e] += c;
-      atomicAdd(by_seq + int64_t(s) * p.E + e, c);
-    }
-    if (threadIdx.x == 0 && n > 0 && atomicAdd(kept + s, n) == 0 && seqs != nullptr) atomicAdd(seqs, 1);
-    tokens += n;
-    __syncthreads();
-    from = to;
+  for (int i = tid; i < n_local * E; i += THREADS) local.slots[i] = 0;
+  if (tid < kFewSequences) {
+    local.kept[tid] = 0;
+    local.ends[tid] = tid < n_local - 1 ? __ldg(cu + s0 + tid + 1) : INT32_MAX;
   }
-  return tokens;
+  __syncthreads();
+#pragma unroll 1
+  for (int t = a + tid; t < b; t += THREADS) {
+    const bool keep = kept_token(p.in.mask, t);
+    int l = 0;
+#pragma unroll 1
+    while (l < n_local - 1 && local.ends[l] <= t) ++l;
+    if (keep) atomicAdd(&local.kept[l], 1);
+    each_slot(p, t, vec, [&](int e) {
+      if (keep) wrong |= count_slot(local.slots + l * E, e, E);
+    });
+  }
+  if (wrong) record_error(p.err, LP_ERR_EXPERT_OUT_OF_RANGE);
+  __syncthreads();
+  ready();
+#pragma unroll 1
+  for (int e = tid; e < E; e += THREADS) {
+    int sum = 0;
+#pragma unroll 1
+    for (int l = 0; l < n_local; ++l) {
+      const int c = local.slots[l * E + e];
+      if (c > 0) atomicAdd(by_seq + int64_t(s0 + l) * E + e, c);
+      sum += c;
+    }
+    all[e] += sum;
+  }
+  if (tid < n_local && local.kept[tid] > 0 && atomicAdd(kept + s0 + tid, local.kept[tid]) == 0 && seqs != nullptr)
+    atomicAdd(seqs, 1);
+#pragma unroll 1
+  for (int l = 0; l < n_local; ++l) n += local.kept[l];
+  return n;
 }
 
 // Zeroes what the sequences' counts are added to; the count stage starts beside it.
@@ -232,21 +265,23 @@ __global__ void __launch_bounds__(kThreads) balance_zero_kernel(uint4* at, unsig
 }
 
 __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __grid_constant__ BalanceParams p, const BalanceWs ws) {
-  __shared__ int hist[LP_MAX_EXPERTS], all[LP_MAX_EXPERTS], part[kCountThreads / 32], kept;
+  __shared__ int all[LP_MAX_EXPERTS], part[kCountThreads / 32], kept;
+  __shared__ LocalCounts<4 * LP_MAX_EXPERTS> local;
   grid_launch_dependents();
   const int ctas = gridDim.x, cta = blockIdx.x, cluster = cta / kCluster;
   const int per = (p.T + ctas - 1) / ctas, a = min(p.T, cta * per), b = min(p.T, a + per);
 #pragma unroll 1
-  for (int e = threadIdx.x; e < p.E; e += kCountThreads) all[e] = hist[e] = 0;
+  for (int e = threadIdx.x; e < p.E; e += kCountThreads) all[e] = 0;
   __syncthreads();
   int tokens;
   if (p.n_seqs == 0) {
     tokens = cta_sum<kCountThreads>(count_slots<kCountThreads>(p, all, a, b), part);
   } else {
     const bool bad = bad_offsets<kCountThreads>(p, cta, ctas);
+    tokens = count_sequences<kCountThreads>(p, a, b, all, local, ws.kept, ws.by_seq, &ws.totals->seqs, part,
+                                            [] { grid_dependency_wait(); });
     grid_dependency_wait();
     if (bad) atomicOr(&ws.totals->bad, 1);
-    tokens = count_sequences<kCountThreads>(p, a, b, all, hist, ws.kept, ws.by_seq, &ws.totals->seqs, part);
   }
   if (threadIdx.x == 0) {
     kept = tokens;
@@ -671,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : kTokenResident)
 // All stages by one cluster. Every CTA counts its tokens into a table of its own; then each adds the cluster's.
 template <bool LF, bool SIGMOID, int VE, int LANES, int N>
 __global__ void __launch_bounds__(kThreads) balance_cluster_kernel(const __grid_constant__ BalanceParams p) {
-  __shared__ int own[kOneTable], table[kOneTable], all[LP_MAX_EXPERTS], hist[LP_MAX_EXPERTS], total[LP_MAX_EXPERTS];
+  __shared__ int own[kOneTable], table[kOneTable], all[LP_MAX_EXPERTS], total[LP_MAX_EXPERTS];
+  __shared__ LocalCounts<LP_MAX_EXPERTS> local;
   __shared__ int own_kept[kOneTable], kept[kOneTable], part_i[kWarps], peak[kWarps], own_tokens, own_bad, seqs;
   __shared__ float2 part[kWarps], sum;
   const int cta = blockIdx.x, S = p.n_seqs;
@@ -679,7 +715,7 @@ __global__ void __launch_bounds__(kThreads) balance_cluster_kernel(const __grid_
   auto count = [&]() {
     const int per = (p.T + kCluster - 1) / kCluster, a = min(p.T, cta * per), b = min(p.T, a + per);
 #pragma unroll 1
-    for (int e = threadIdx.x; e < p.E; e += kThreads) all[e] = hist[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += kThreads) all[e] = 0;
 #pragma unroll 1
     for (int i = threadIdx.x; i < S * p.E; i += kThreads) own[i] = 0;
 #pragma unroll 1
@@ -691,7 +727,7 @@ __global__ void __launch_bounds__(kThreads) balance_cluster_kernel(const __grid_
       tokens = cta_sum<kThreads>(count_slots<kThreads>(p, all, a, b), part_i);
     } else {
       if (bad_offsets<kThreads>(p, cta, kCluster)) atomicOr(&own_bad, 1);
-      tokens = count_sequences<kThreads>(p, a, b, all, hist, own_kept, own, nullptr, part_i);
+      tokens = count_sequences<kThreads>(p, a, b, all, local, own_kept, own, nullptr, part_i, [] {});
     }
     if (threadIdx.x == 0) own_tokens = tokens;
     cluster_sync();
