@@ -11,6 +11,7 @@
 // a token costs besides its logits (sums over its lanes, its weight) is spread over many of them, and a lane
 // keeps its experts' f in registers until the sequence changes. A short one by its launches and their dependent
 // steps: one cluster runs the three stages in one launch, what passes between them in its shared memory.
+// 65536 tokens over 128 experts in fp32: 19 us, 6 of them the counts', 3.6 TB/s of logits and gradient in all.
 #pragma once
 
 #include "lp_rows.cuh"
@@ -28,7 +29,8 @@ constexpr int kCountClusters = kSms / kCluster;
 constexpr int kTokenResident = 2;  // CTAs of the token stage on an SM; three spill, and are no faster
 constexpr int kTokenCtas = kTokenResident * kSms;
 constexpr int kFewSequences = 8;  // sequences of a CTA's tokens that are counted in shared memory first
-// The one-launch form takes batches of up to this many logits, slots and (sequences x experts).
+// The one-launch form takes batches of up to this many logits, slots and (sequences x experts). At 4096 x 64, the most,
+// its GPU time is 10 us where the other's is 7, but a call takes 20 us and not 27, without a workspace and a launch.
 constexpr int64_t kOneLogits = 1 << 18;
 constexpr int64_t kOneSlots = 1 << 15;
 constexpr int kOneTable = 2048;
@@ -814,8 +816,8 @@ cudaError_t launch_stages(const BalanceParams& p, cudaStream_t s) {
                 false, true, s, p, ws, clusters);
 }
 
-// Lanes of a token: as few as leave a lane 16 logits, but four. (With 32 bf16 logits a lane, 131071 x 256 take 51 us,
-// 47 with 16: a step has fewer instructions for each logit, but less else to do while it waits for its sums.)
+// Lanes of a token: as few as leave a lane 16 logits, but four. (131071 x 256 in bf16: 47 us with 16, 51 with
+// 32, where a step has fewer instructions for each logit but less else to do while it waits for its sums.)
 template <bool LF, bool SIGMOID, int VE>
 cudaError_t launch_widths(const BalanceParams& p, cudaStream_t s) {
   constexpr int kFewest = VE > 4 ? VE : 4;
