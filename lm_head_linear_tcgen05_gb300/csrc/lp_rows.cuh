@@ -1,5 +1,5 @@
 // lp_rows.cuh - what the kernels over hidden-state rows share: eight neighbouring elements as the unit of every
-// access, sums over a row, asynchronous copies into a thread's own part of shared memory, and dropout's bits.
+// access, sums over a row, a CTA's next rows under way to its shared memory, and dropout's bits.
 #pragma once
 
 #include <atomic>
