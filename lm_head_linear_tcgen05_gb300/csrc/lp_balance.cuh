@@ -596,9 +596,10 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
       zsum = __fmaf_rn(lse, lse * inv_n, zsum);
     }
     if (want_grad && t < end) {
-      // q (a (f - d) + z) as q (a f + b); a token that is not kept has a = b = 0
-      const float scale = keep ? inv : 0.f, a = of_balance * w * scale;
-      const float b = __fmaf_rn(-a, d, of_z != 0.f ? of_z * lse * scale : 0.f);
+      // q (a (f - d) + z) as q (a f + b); a token that is not kept has a = b = 0, by choice and not by a product, which
+      // would be NaN where upstream is not finite
+      const float a = keep ? of_balance * w * inv : 0.f;
+      const float b = keep ? __fmaf_rn(-a, d, of_z != 0.f ? of_z * lse * inv : 0.f) : 0.f;
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) q[k] = mul2(q[k], fma2(f[k], both(a), both(b)));
       if (grad_f32)

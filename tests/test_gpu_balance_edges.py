@@ -1,0 +1,48 @@
+"""lp_balance_loss where its inputs leave the ordinary range: gradients from upstream that are not finite, experts out of
+reach under sigmoid scores, counts past 24 bits. Definition and bounds are block_ref.py's."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import block_ref as ref  # noqa: E402
+
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lp():
+    from lm_head_linear_tcgen05_gb300 import _build
+    _build.build()
+    import lm_head_linear_tcgen05_gb300 as mod
+    assert mod.lp_device_supported()
+    torch.cuda.set_device(0)
+    return mod
+
+
+def make(T, E, K, dtype, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    logits = torch.empty((T, E), dtype=dtype, device="cuda").normal_(0.0, 1.5, generator=gen)
+    ids = torch.randint(0, E, (T, K), device="cuda", generator=gen, dtype=torch.int32)
+    return logits, ids, (torch.rand(T, device="cuda", generator=gen) < 0.7).to(torch.uint8)
+
+
+def offsets(*cu):
+    return torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("T", [24, 9000])               # one launch, several
+@pytest.mark.parametrize("dtype,E,score,z", [(F32, 64, "softmax", 0.1), (BF, 64, "sigmoid", 0.0), (F32, 37, "softmax", 0.0)])
+@pytest.mark.parametrize("up,coef", [(INF, 1.0), (-INF, 1.0), (NAN, 1.0), (3e38, 1e6)])
+def test_what_is_not_kept_has_a_zero_gradient_whatever_is_upstream(lp, T, dtype, E, score, z, up, coef):
+    logits, ids, mask = make(T, E, 4, dtype, T + E)
+    o = dict(coef=coef, z_coef=z, score=score, mask=mask, upstream=torch.tensor([up], device="cuda"))
+    for cu in (None, offsets(0, T // 3, T)):
+        got = lp.lp_balance_loss(logits, ids, cu_seqlens=cu, **o)
+        assert lp.lp_get_device_error() == 0
+        assert bool((got["grad_logits"][mask == 0] == 0).all()) and bool(torch.isfinite(got["metrics"]).all())
+        assert not bool(torch.isfinite(got["grad_logits"][mask != 0]).all())
+    got = lp.lp_balance_loss(logits, ids, cu_seqlens=offsets(0, T // 2, T // 3, T), **o)
+    assert lp.lp_get_device_error() == 12                 # gradients are zero, all of them
+    assert bool((got["grad_logits"] == 0).all()) and bool(torch.isnan(got["metrics"]).all())
