@@ -46,3 +46,29 @@ def test_what_is_not_kept_has_a_zero_gradient_whatever_is_upstream(lp, T, dtype,
     got = lp.lp_balance_loss(logits, ids, cu_seqlens=offsets(0, T // 2, T // 3, T), **o)
     assert lp.lp_get_device_error() == 12                 # gradients are zero, all of them
     assert bool((got["grad_logits"] == 0).all()) and bool(torch.isnan(got["metrics"]).all())
+
+
+@pytest.mark.parametrize("by_sequence", [False, True])
+def test_even_loads_past_24_bits_have_no_gradient(lp, by_sequence):
+    """K N = 3 * 5592407 is odd and past 2^24, so no fp32 number; c E is the same number."""
+    T = 5592407
+    logits, _, _ = make(T, 3, 3, F32, 1)
+    ids = torch.arange(3, device="cuda", dtype=torch.int32).repeat(T, 1)
+    out = lp.lp_balance_loss(logits, ids, cu_seqlens=offsets(0, T) if by_sequence else None)
+    assert lp.lp_get_device_error() == 0
+    assert out["expert_counts"].tolist() == [T] * 3 and float(out["grad_logits"].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("by_sequence", [False, True])
+@pytest.mark.parametrize("T,K,E", [(1000003, 63, 3), (1000003, 64, 2)])
+def test_counts_past_24_bits(lp, T, K, E, by_sequence):
+    """Experts named about evenly, each more than 2^24 times: f - 1 is some 1e-4, of which a count rounded to fp32 would
+    leave three digits."""
+    logits, ids, _ = make(T, E, K, F32, 2)
+    cu = offsets(0, T) if by_sequence else None
+    out = lp.lp_balance_loss(logits, ids, coef=0.7, cu_seqlens=cu)
+    metrics, experts, counts, grad, m_tol, g_tol = ref.balance(logits, ids, 0.7, cu=cu)
+    assert int(experts.min()) > 1 << 24 and torch.equal(out["expert_counts"], experts) and torch.equal(out["counts"], counts)
+    assert bool(((out["metrics"].double() - metrics).abs() <= m_tol + ref.U * metrics.abs()).all())
+    assert bool(((out["grad_logits"].double() - grad).abs() <= g_tol + ref.U * (grad.abs() + g_tol) + 1e-37).all())
+    assert lp.lp_get_device_error() == 0
