@@ -348,18 +348,18 @@ struct Raw {
       w[v] = F32 ? static_cast<const uint32_t*>(row)[e] : uint32_t(static_cast<const uint16_t*>(row)[e]) << 16;
     }
   }
-  // Elements 2 i and 2 i + 1. FLOOR: bf16 logits at least -69 (e^69 is nearly 2^100), NaN stays.
+  // Elements 2 i and 2 i + 1. FLOOR: bf16 logits at least -88 (e^88 is 2^126.96), NaN stays.
   template <bool FLOOR>
   __device__ __forceinline__ uint64_t pair(int i) const {
     if constexpr (F32) {
       return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else if constexpr (!kWide) {  // each in the high half of a word
       uint32_t x = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
-      if constexpr (FLOOR) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xc28ac28au));
+      if constexpr (FLOOR) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xc2b0c2b0u));
       return pack2(bf16_lo(x), bf16_hi(x));
     } else {
       uint32_t x = w[i];
-      if constexpr (FLOOR) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xc28ac28au));
+      if constexpr (FLOOR) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0xc2b0c2b0u));
       return pack2(bf16_lo(x), bf16_hi(x));
     }
   }
@@ -544,12 +544,13 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
       constexpr float kTiny = 1e-20f;
 #pragma unroll
       for (int k = 0; k < kPairs; ++k) {
-        // x = e^-l up to 2^100 (s is below kTiny long before), s = 1 / (1 + x), 1 - s = x s
+        // x = e^-l up to 2^127 (2^126.96 in bf16), s = 1 / (1 + x), 1 - s = x s: from 2^126 on s is 0, as for a logit of
+        // -inf, and x s no 0 inf
         float lo, hi;
         unpack2(mul2(q[k], both(-kLog2e)), lo, hi);
         if constexpr (LF) {
-          asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(100.f));
-          asm("min.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(100.f));
+          asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(127.f));
+          asm("min.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(127.f));
         }
         const uint64_t x = pack2(hw_ex2(lo), hw_ex2(hi));
         unpack2(add2(x, both(1.f)), lo, hi);

@@ -72,3 +72,22 @@ def test_counts_past_24_bits(lp, T, K, E, by_sequence):
     assert bool(((out["metrics"].double() - metrics).abs() <= m_tol + ref.U * metrics.abs()).all())
     assert bool(((out["grad_logits"].double() - grad).abs() <= g_tol + ref.U * (grad.abs() + g_tol) + 1e-37).all())
     assert lp.lp_get_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [24, 9000])
+@pytest.mark.parametrize("dtype,E", [(F32, 64), (BF, 64), (F32, 37), (BF, 37), (F32, 260)])
+def test_a_sigmoid_score_of_minus_infinity_is_zero(lp, T, dtype, E):
+    """1 / (1 + e^inf) = 0: such an expert has no probability and no gradient, however small the others' scores are."""
+    logits, ids, _ = make(T, E, 4, dtype, T + E)
+    logits[:, 3:7] = -INF
+    logits[1, :] -= 44.0                                  # scores of about e^-44: their sum is above what is rescaled
+    logits[2, :] -= 80.0                                  # below it
+    logits[3, :] = -INF
+    out = lp.lp_balance_loss(logits, ids, coef=0.5, score="sigmoid")
+    assert lp.lp_get_device_error() == 0
+    gone = logits == -INF
+    assert bool((out["grad_logits"][gone] == 0).all())
+    metrics, _, _, grad, m_tol, g_tol = ref.balance(logits, ids, 0.5, 0.0, "sigmoid")
+    got = out["grad_logits"]
+    assert bool(((got.double() - grad).abs() <= g_tol + ref.HALF_STEP[dtype] * (grad.abs() + g_tol) + 1e-37).all())
+    assert bool(((out["metrics"].double() - metrics).abs() <= m_tol + ref.U * metrics.abs() + 1e-37).all())
