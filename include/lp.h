@@ -855,8 +855,11 @@ LP_API lp_status lp_selftest_wait_timeout(uint64_t limit_ns, lp_stream_t stream)
  * nanoseconds (1 us .. 10 s; 0 restores the default of 2 s), for the whole process. A wait
  * that runs past it gives up: the kernel records LP_ERR_DEVICE_TIMEOUT, lets the copies and
  * MMAs it already started finish, frees its tensor memory and returns, leaving the context
- * usable and the call's outputs undefined. Failure detection is tested by setting a limit
- * too short for any wait to be met. Returns LP_ERR_INVALID_ARG outside the range. */
+ * usable and the call's outputs undefined. The limit holds to within one suspension of the waiting
+ * thread by the hardware, which is longer than a row of the norm kernels takes to arrive; their waits
+ * keep a limit of microseconds in the bounds-checked build only, which polls. Failure detection is
+ * tested by setting a limit too short for any wait to be met. Returns LP_ERR_INVALID_ARG outside
+ * the range. */
 LP_API lp_status lp_set_wait_limit(uint64_t limit_ns);
 
 /* 1 if this library was built with device-side bounds checks (LP_DEBUG_BOUNDS=1), else 0.

@@ -95,17 +95,32 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without suspending the thread.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits for the phase of `bar` with the given parity to complete. Gives up (returns
 // false) when `*abort` is raised by another role or when `limit_ns` has elapsed; in
 // the latter case it raises `*abort` and records LP_ERR_DEVICE_TIMEOUT. Each try_wait may
 // suspend the thread for a while in hardware, so the flag and the clock are checked after
-// every unsuccessful try: the limit holds to within one suspension.
+// every unsuccessful try: the limit holds to within one suspension. POLL: never suspended.
+template <bool POLL = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint64_t limit_ns, unsigned int* err) {
-  if (mbar_test(bar, parity)) return true;
+  auto test = [&] { return POLL ? mbar_poll(bar, parity) : mbar_test(bar, parity); };
+  if (test()) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
-    if (mbar_test(bar, parity)) return true;
+    if (test()) return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > limit_ns) {
       *abort = 1;

@@ -189,9 +189,11 @@ struct RowRing {
     return true;
   }
   // until the stage's fill of this parity (0 for the first, 1 for the second, 0 for the third, ...) has arrived.
-  // Past the wait limit the error is recorded and the CTA goes on to its end with what the stage holds.
+  // Past the wait limit the error is recorded and the CTA goes on to its end with what the stage holds. A suspended
+  // thread sleeps through any copy, however short the limit (nothing gave up at 1 us, nor when the try asked for a
+  // shorter suspension, which cost 1 %), so the bounds-checked build polls: there a test can make a wait run out.
   __device__ __forceinline__ void wait(int stage, uint32_t parity, uint64_t limit_ns, unsigned int* err) {
-    mbar_wait(&full[stage], parity, &abort, limit_ns, err);
+    mbar_wait<LP_DEBUG_BOUNDS != 0>(&full[stage], parity, &abort, limit_ns, err);
   }
   // after giving up: until the copies under way have arrived
   __device__ __forceinline__ void drain() {
