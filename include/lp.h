@@ -869,13 +869,17 @@ LP_API lp_status lp_set_wait_limit(uint64_t limit_ns);
  * and gradient kernels and in the epilogues of the tensor-core GEMMs (bias reads, the
  * forward's statistics, G, dW and dX stores) - is compared with the extent of its buffer
  * as the host computed it, before the access; a failed comparison records LP_ERR_BOUNDS in
- * the device error word and skips the access instead of touching memory. TMA copies are
- * bounded by their tensor maps. Results are otherwise bitwise those of the regular build,
+ * the device error word and skips the access instead of touching memory. Tiled TMA copies are
+ * bounded by their tensor maps. In the kernels of the norms, dropout and the balance loss the
+ * compared ones are: the norms' row copies and their stages, row stores, the sums over tokens in the
+ * workspace or shared memory; dropout's rows; the balance loss's ids, logits and gradient rows,
+ * the entries of its tables by sequence, and what it writes to the workspace. Results are otherwise bitwise those of the regular build,
  * which compiles the checks away. */
 LP_API int lp_debug_bounds_build(void);
 
 /* Self-test of the bounds checks: one thread checks an index equal to its extent, and asks
- * for the gradient row after a table's last. A bounds-checked build in which both are noticed
+ * for the gradient row after a table's last, the sequence after a batch's last, a buffer's end and one
+ * byte more, and shared memory that the launch has not. A bounds-checked build in which all are noticed
  * records LP_ERR_BOUNDS (read it with lp_get_device_error()); the regular build records
  * nothing. No buffer is accessed either way. */
 LP_API lp_status lp_selftest_bounds(lp_stream_t stream);

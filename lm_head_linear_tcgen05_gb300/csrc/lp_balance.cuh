@@ -97,6 +97,10 @@ __device__ __forceinline__ int sequence_by_warp(const int32_t* cu, int lo, int h
   return lo;
 }
 
+__device__ __forceinline__ bool in_workspace(const BalanceParams& p, const void* at, int64_t n) {
+  return in_buffer(p.workspace, p.ws_bytes, at, n, p.err);
+}
+
 __device__ __forceinline__ bool kept_token(const uint8_t* mask, int t) { return mask == nullptr || __ldg(mask + t) != 0; }
 
 template <int THREADS>
@@ -123,6 +127,7 @@ __device__ __forceinline__ bool count_slot(int* hist, int e, int E) {
 template <typename F>
 __device__ __forceinline__ void each_slot(const BalanceParams& p, int t, bool vec, const F& f) {
   const int32_t* ids = p.in.ids + int64_t(t) * p.K;
+  if (!in_bounds(unsigned(t) < unsigned(p.T) && (!vec || p.K % 4 == 0), p.err)) return;
   if (vec) {
 #pragma unroll 1
     for (int k = 0; k < p.K; k += 8) {
@@ -211,6 +216,7 @@ __device__ __forceinline__ int count_sequences(const BalanceParams& p, int a, in
     for (int t = a + tid; t < b; t += THREADS) {
       if (!kept_token(p.in.mask, t)) continue;
       const int s = sequence_in(cu, s0, s0 + n_local - 1, t);
+      if (!has_sequence(s, p.n_seqs, p.err)) continue;
       ++n;
       if (atomicAdd(kept + s, 1) == 0 && seqs != nullptr) atomicAdd(seqs, 1);
       each_slot(p, t, vec, [&](int e) {
@@ -234,6 +240,7 @@ __device__ __forceinline__ int count_sequences(const BalanceParams& p, int a, in
     int l = 0;
 #pragma unroll 1
     while (l < n_local - 1 && local.ends[l] <= t) ++l;
+    if (!in_bounds(l < kFewSequences && (l + 1) * E <= L::kEntries, p.err)) continue;
     if (keep) atomicAdd(&local.kept[l], 1);
     each_slot(p, t, vec, [&](int e) {
       if (keep) wrong |= count_slot(local.slots + l * E, e, E);
@@ -247,13 +254,15 @@ __device__ __forceinline__ int count_sequences(const BalanceParams& p, int a, in
     int sum = 0;
 #pragma unroll 1
     for (int l = 0; l < n_local; ++l) {
+      if (!has_sequence(s0 + l, p.n_seqs, p.err)) continue;
       const int c = local.slots[l * E + e];
       if (c > 0) atomicAdd(by_seq + int64_t(s0 + l) * E + e, c);
       sum += c;
     }
     all[e] += sum;
   }
-  if (tid < n_local && local.kept[tid] > 0 && atomicAdd(kept + s0 + tid, local.kept[tid]) == 0 && seqs != nullptr)
+  if (tid < n_local && local.kept[tid] > 0 && has_sequence(s0 + tid, p.n_seqs, p.err) &&
+      atomicAdd(kept + s0 + tid, local.kept[tid]) == 0 && seqs != nullptr)
     atomicAdd(seqs, 1);
 #pragma unroll 1
   for (int l = 0; l < n_local; ++l) n += local.kept[l];
@@ -261,9 +270,10 @@ __device__ __forceinline__ int count_sequences(const BalanceParams& p, int a, in
 }
 
 // Zeroes what the sequences' counts are added to; the count stage starts beside it.
-__global__ void __launch_bounds__(kThreads) balance_zero_kernel(uint4* at, unsigned n) {
+__global__ void __launch_bounds__(kThreads) balance_zero_kernel(const __grid_constant__ BalanceParams p, uint4* at, unsigned n) {
   grid_launch_dependents();
-  for (unsigned i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) at[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (unsigned i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads)
+    if (in_workspace(p, at + i, sizeof(uint4))) at[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __grid_constant__ BalanceParams p, const BalanceWs ws) {
@@ -296,7 +306,8 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
     int c = 0;
 #pragma unroll
     for (uint32_t r = 0; r < kCluster; ++r) c += e < p.E ? of_cta(all, r)[e] : *of_cta(&kept, r);
-    ws.experts[cluster * (p.E + 1) + e] = c;
+    int32_t* const to = ws.experts + cluster * (p.E + 1) + e;
+    if (in_bounds(cluster < kCountClusters, p.err) && in_workspace(p, to, sizeof(int32_t))) *to = c;
   }
   cluster_sync();
 }
@@ -443,7 +454,10 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
 #pragma unroll
   for (int v = 0; v < N / VE; ++v) has |= uint32_t((sub + v * LANES) * VE < E) << v;
   const bool exact = VE > 1 && E == LANES * N;
-  auto load_row = [&](Raw<LF, VE, N>& to, const void* from, bool read) {
+  // the logits of token `of`, at `from`
+  auto load_row = [&](Raw<LF, VE, N>& to, const char* from, int of, bool read) {
+    read = read && in_bounds(of < p.T && from - static_cast<const char*>(p.in.logits) ==
+                                             int64_t(of) * p.in.ld_logits * (LF ? 4 : 2), p.err);
     if (exact)
       to.template load<true>(from, read, has, sub, LANES);
     else
@@ -451,7 +465,7 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
   };
   Raw<LF, VE, N> raw;
   bool mine = kept(t), following = kept(t + kPerWarp);  // the tokens of raw and of the step after are kept
-  load_row(raw, row, mine);
+  load_row(raw, row, t, mine);
   int seq = 0, next = p.T;  // the token's sequence, and where it ends; at first, of the warp's first token
   if (S > 0 && first < end) {
     seq = sequence_by_warp(p.in.cu_seqlens, 0, S - 1, first);
@@ -464,7 +478,7 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
   const bool sound = !found.bad;
   if (!sound) {
     mine = following = false;
-    load_row(raw, row, false);
+    load_row(raw, row, t, false);
   }
   uint64_t f[kPairs];
   float w = inv_n;
@@ -500,7 +514,7 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
     for (int k = 0; k < kPairs; ++k) q[k] = raw.template pair<SIGMOID>(k);
     row += by_row;
     mine = following;
-    if (first_t + kPerWarp < end) load_row(raw, row, mine);
+    if (first_t + kPerWarp < end) load_row(raw, row, t + kPerWarp, mine);
     following = sound && kept(t + 2 * kPerWarp);
     if (S > 0 && keep && t >= next) {
       // the one after, or, over empty ones, by search
@@ -510,9 +524,11 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
         seq = sequence_in(p.in.cu_seqlens, seq, S - 1, t);
         next = seq == S - 1 ? p.T : __ldg(p.in.cu_seqlens + seq + 1);
       }
-      const int n = found.kept[seq];
-      w = 1.f / (float(n) * float(found.seqs));
-      shares(found.by_seq + int64_t(seq) * E, n);
+      if (has_sequence(seq, S, p.err)) {
+        const int n = found.kept[seq];
+        w = 1.f / (float(n) * float(found.seqs));
+        shares(found.by_seq + int64_t(seq) * E, n);
+      }
     }
     // From the logits in q: their scores (softmax: times the sum), the sum of these and of their products with f - 1,
     // and, in q, what the gradient has of each: the score, for sigmoid s (1 - s).
@@ -563,7 +579,7 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
       const bool vanish = keep && total < kTiny;
       if (__any_sync(0xffffffffu, vanish)) {
         Raw<LF, VE, N> again;
-        load_row(again, row - by_row, vanish);
+        load_row(again, row - by_row, t, vanish);
         uint64_t x[kPairs];
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) x[k] = again.template pair<false>(k);
@@ -600,7 +616,9 @@ __device__ __forceinline__ float2 token_stage(const BalanceParams& p, int cta, i
       balance = __fmaf_rn(w, __fmaf_rn(total, inv, d), balance);
       zsum = __fmaf_rn(lse, lse * inv_n, zsum);
     }
-    if (want_grad && t < end) {
+    if (want_grad && t < end &&
+        in_bounds(t < p.T && E % (VE < 2 ? 1 : VE) == 0 && grad - static_cast<char*>(p.out.grad_logits) ==
+                      int64_t(t) * p.out.ld_grad * (grad_f32 ? 4 : 2), p.err)) {
       // q (a (f - d) + z) as q (a f + b); a token that is not kept has a = b = 0, by choice and not by a product, which
       // would be NaN where upstream is not finite
       const float a = keep ? of_balance * w * inv : 0.f;
@@ -701,7 +719,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : kTokenResident)
   };
   const float2 s = token_stage<LF, SIGMOID, VE, LANES, N>(p, blockIdx.x, gridDim.x, count, part);
   if (threadIdx.x == 0) {
-    ws.sums[blockIdx.x] = s;
+    if (in_bounds(blockIdx.x < kTokenCtas, p.err) && in_workspace(p, ws.sums + blockIdx.x, sizeof(float2)))
+      ws.sums[blockIdx.x] = s;
     __threadfence();
     is_last = atomicAdd(ws.done, 1u) == gridDim.x - 1;
   }
@@ -719,6 +738,7 @@ __global__ void __launch_bounds__(kThreads) balance_cluster_kernel(const __grid_
   __shared__ int own_kept[kOneTable], kept[kOneTable], part_i[kWarps], peak[kWarps], own_tokens, own_bad, seqs;
   __shared__ float2 part[kWarps], sum;
   const int cta = blockIdx.x, S = p.n_seqs;
+  if (!in_bounds(S * p.E <= kOneTable && gridDim.x == kCluster, p.err)) return;
   Found found{};
   auto count = [&]() {
     const int per = (p.T + kCluster - 1) / kCluster, a = min(p.T, cta * per), b = min(p.T, a + per);
@@ -810,7 +830,7 @@ cudaError_t launch_stages(const BalanceParams& p, cudaStream_t s) {
   if (p.n_seqs > 0) {
     const size_t n = ws.zero_bytes / sizeof(uint4), ctas = (n + kThreads - 1) / kThreads;
     e = launch(balance_zero_kernel, int(ctas < 2 * kSms ? ctas : 2 * kSms), kThreads, false, false, s,
-               reinterpret_cast<uint4*>(ws.totals), unsigned(n));
+               p, reinterpret_cast<uint4*>(ws.totals), unsigned(n));
     if (e != cudaSuccess) return e;
   }
   const int64_t some = (int64_t(p.T) * p.K + 16383) / 16384;

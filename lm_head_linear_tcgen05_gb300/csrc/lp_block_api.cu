@@ -189,6 +189,7 @@ lp_status lp_residual_norm_backward(int64_t T, int64_t H, const lp_norm_inputs* 
     if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LP_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 16)) return LP_ERR_ALIGNMENT;
     p.partials = static_cast<float*>(workspace);
+    p.ws_bytes = int64_t(ws_bytes);
   }
   if ((st = device_error_word(&p.f.err)) != LP_OK) return st;
   p.d_norm = g->d_norm;
@@ -267,6 +268,7 @@ lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balance_inpu
   p.K = int32_t(K);
   p.n_seqs = int32_t(n_seqs);
   p.workspace = workspace;
+  p.ws_bytes = int64_t(ws_bytes);
   p.grad_f32 = opts->grad_dtype == LP_DTYPE_F32;
   return launch_balance_loss(p, opts->logits_dtype == LP_DTYPE_F32, s) == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }

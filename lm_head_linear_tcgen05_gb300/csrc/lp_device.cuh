@@ -61,6 +61,24 @@ __device__ __forceinline__ bool in_bounds(bool ok, unsigned int* err) {
 #endif
 }
 
+// Whether n bytes at `at` lie in the `size` bytes of a buffer.
+__device__ __forceinline__ bool in_buffer(const void* base, int64_t size, const void* at, int64_t n, unsigned int* err) {
+  const int64_t from = static_cast<const char*>(at) - static_cast<const char*>(base);
+  return in_bounds(from >= 0 && n <= size - from, err);
+}
+
+// Whether a batch of n_seqs sequences has one of number s.
+__device__ __forceinline__ bool has_sequence(int s, int n_seqs, unsigned int* err) {
+  return in_bounds(unsigned(s) < unsigned(n_seqs), err);
+}
+
+// Whether the first `bytes` of the launch's dynamic shared memory are there.
+__device__ __forceinline__ bool in_shared(int64_t bytes, unsigned int* err) {
+  uint32_t size;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(size));
+  return in_bounds(bytes <= int64_t(size), err);
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 

@@ -979,17 +979,24 @@ cudaError_t launch_embedding(const EmbeddingParams& p, bool w_bf16, bool y_bf16,
 
 namespace {
 
-// One thread checks an index equal to its extent, and asks for the row after a table's last; each has to record
+// One thread checks an index equal to its extent, and asks for the row after a table's last, a batch's sequence after
+// its last, the last bytes of a buffer and one more, and shared memory that the launch does not have; each has to record
 // LP_ERR_BOUNDS in a word of its own for the kernel to record it. Touches no memory but its own.
 __global__ void bounds_selftest_kernel(EmbeddingGradParams p, int64_t extent, unsigned int* err) {
-  __shared__ unsigned int seen[2];
+  constexpr int kChecks = 5;
+  __shared__ unsigned int seen[kChecks];
   if (threadIdx.x != 0) return;
-  seen[0] = seen[1] = 0u;
+  for (int i = 0; i < kChecks; ++i) seen[i] = 0u;
   (void)in_bounds(extent < extent, seen);
   p.err = seen + 1;
   int64_t off;
   const bool written = dw_row(p, p.row_start[p.n_shards], &off) != nullptr;
-  if (seen[0] == LP_ERR_BOUNDS && seen[1] == LP_ERR_BOUNDS && !written) record_error(err, LP_ERR_BOUNDS);
+  (void)has_sequence(int(extent), int(extent), seen + 2);
+  (void)in_buffer(seen, sizeof(seen), seen + 1, sizeof(seen) - sizeof(seen[0]) + 1, seen + 3);
+  (void)in_shared(extent, seen + 4);
+  bool all = !written;
+  for (int i = 0; i < kChecks; ++i) all &= seen[i] == LP_ERR_BOUNDS;
+  if (all) record_error(err, LP_ERR_BOUNDS);
 }
 
 }  // namespace

@@ -348,6 +348,7 @@ struct NormGradParams {
   int32_t accumulate, dw_bf16;
   int32_t one_cluster;                   // the launch's one cluster adds the sums over tokens
   float* partials;                       // [parts][sums][H], otherwise
+  int64_t ws_bytes;                      // there (the extent the bounds-checked build compares with)
 };
 
 size_t norm_backward_ws_bytes(int64_t T, int64_t H);
@@ -362,6 +363,7 @@ struct BalanceParams {
   int32_t T, E, K, n_seqs;               // n_seqs 0: over the whole batch
   int32_t score, grad_f32;
   void* workspace;
+  int64_t ws_bytes;                      // the extent the bounds-checked build compares with
   unsigned int* err;
 };
 

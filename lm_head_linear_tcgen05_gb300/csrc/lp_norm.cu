@@ -49,7 +49,8 @@ __global__ void __maxnreg__((kRegisters<CPL, BRANCH>)) norm_kernel(const __grid_
   const int stage_units = at_gate + (kFull ? room * kUnits<YF> : 0);
   auto fetch = [&](uint32_t row, int stage) {
     const uint32_t bytes_h = groups * kUnits<HF> * 16, bytes_y = groups * kUnits<YF> * 16;
-    if (tid != 0 || row >= T || !ring.begin(stage, bytes_h + (kHasY ? bytes_y : 0) + (kFull ? bytes_y : 0))) return;
+    if (tid != 0 || row >= T || !ring.may_copy(p, row, 0, groups, stage, stage_units)) return;
+    if (!ring.begin(stage, bytes_h + (kHasY ? bytes_y : 0) + (kFull ? bytes_y : 0))) return;
     uint4* const to = stages + stage * stage_units;
     copy_bulk(to, h.at<HF>(row, 0), bytes_h, &ring.full[stage]);
     if constexpr (kHasY) copy_bulk(to + at_y, y.at<YF>(row, 0), bytes_y, &ring.full[stage]);
@@ -189,7 +190,8 @@ __global__ void __maxnreg__((kRegisters<CPL, BRANCH>)) norm_kernel(const __grid_
         if constexpr (kFull) b = b * (kCta ? Group<YF>::read(at + at_gate + g * kUnits<YF>) : raw_z[kCta ? 0 : c]).unpack();
         if (drop) keep8(bits[c], p.drop.limit, b);
         u[c] = fma8(u[c], p.scale, b);
-        if (g < groups) store_group<HF>(to_h + c * width * kUnits<HF>, u[c]);
+        uint4* const at_u = to_h + c * width * kUnits<HF>;
+        if (g < groups && is_at<HF>(p, at_u, p.h_out, p.ld_h_out, row, g)) store_group<HF>(at_u, u[c]);
       }
       dot8(square, u[c], u[c]);
     }
@@ -214,8 +216,11 @@ __global__ void __maxnreg__((kRegisters<CPL, BRANCH>)) norm_kernel(const __grid_
     if (wanted) {
       const float r = rsqrtf(__fmaf_rn(s[0], p.inv_width, p.eps));
 #pragma unroll
-      for (int c = 0; c < CPL; ++c)
-        if (here && lane + c * width < groups) store_group<YF>(to_norm + c * width * kUnits<YF>, u[c] * (w[c] * r));
+      for (int c = 0; c < CPL; ++c) {
+        const int g = lane + c * width;
+        uint4* const at_n = to_norm + c * width * kUnits<YF>;
+        if (here && g < groups && is_at<YF>(p, at_n, p.norm, p.ld_norm, row, g)) store_group<YF>(at_n, u[c] * (w[c] * r));
+      }
     }
     if (next == 0) parity ^= 1u;
     stage = next;
@@ -290,15 +295,18 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
   const int64_t base = int64_t(blockIdx.x) * (kDropThreads * kDropGroups) + threadIdx.x;
   const Rows x{(char*)p.x, p.ld_x}, out{(char*)p.out, p.ld_out};
   Group<F32> v[kDropGroups];
+  auto row_of = [&](int64_t i) {
+    return n <= int64_t(UINT32_MAX) ? int64_t(uint32_t(i) / uint32_t(p.groups)) : i / p.groups;
+  };
   auto place = [&](const Rows& m, int64_t i) {
     if constexpr (LINEAR) return reinterpret_cast<uint4*>(m.base) + i * kUnits<F32>;
-    const int64_t row = n <= int64_t(UINT32_MAX) ? int64_t(uint32_t(i) / uint32_t(p.groups)) : i / p.groups;
+    const int64_t row = row_of(i);
     return m.at<F32>(row, int(i - row * p.groups));
   };
 #pragma unroll
   for (int k = 0; k < kDropGroups; ++k) {
     const int64_t i = base + k * kDropThreads;
-    if (i >= n) continue;
+    if (i >= n || !in_bounds(row_of(i) < p.T, p.err)) continue;
     const uint4* from = place(x, i);
 #pragma unroll
     for (int j = 0; j < kUnits<F32>; ++j) v[k].v[j] = from[j];
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
 #pragma unroll
   for (int k = 0; k < kDropGroups; ++k) {
     const int64_t i = base + k * kDropThreads;
-    if (i >= n) continue;
+    if (i >= n || !in_bounds(row_of(i) < p.T, p.err)) continue;
     Eight e = v[k].unpack();
     if (p.drop.threshold > 0) {
       e = e * p.drop.factor;

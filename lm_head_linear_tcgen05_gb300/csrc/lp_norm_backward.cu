@@ -105,7 +105,8 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
   auto fetch = [&](uint32_t row, int stage) {
     const uint32_t bytes_h = span * kUnits<HF> * 16, bytes_y = span * kUnits<YF> * 16;
     const uint32_t parts_h = 1 + has_d, parts_y = has_n + kHasY + kFull;
-    if (tid != 0 || row >= T || !ring.begin(stage, parts_h * bytes_h + parts_y * bytes_y)) return;
+    if (tid != 0 || row >= T || !ring.may_copy(p.f, row, cta_g0, cta_g0 + span, stage, stage_units)) return;
+    if (!ring.begin(stage, parts_h * bytes_h + parts_y * bytes_y)) return;
     uint4* const to = stages + stage * stage_units;
     uint64_t* const bar = &ring.full[stage];
     copy_bulk(to, h.at<HF>(row, cta_g0), bytes_h, bar);
@@ -259,7 +260,8 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
         D = fma8(u, k, fma8(n, w[c], D));
         dw[c] = fma8(n, u, dw[c]);
       }
-      if (there) store_group<HF>(to_h + c * width * kUnits<HF>, D * p.f.scale);
+      uint4* const at_h = to_h + c * width * kUnits<HF>;
+      if (there && is_at<HF>(p.f, at_h, p.d_h, p.ld_d_h, row, g)) store_group<HF>(at_h, D * p.f.scale);
       if constexpr (kHasY) {
         kept_y[c] = kCta ? in_y(at, at_y, c) : now.y[kCta ? 0 : c];
         Eight b = kept_y[c].unpack();
@@ -267,7 +269,7 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
         if constexpr (kFull) {
           Eight x = (kCta ? in_y(at, at_gate, c) : now.z[kCta ? 0 : c]).unpack();
           if (drop) keep8(bits[c], p.f.drop.limit, D, b, x);
-          if (there && p.d_gate != nullptr)
+          if (there && p.d_gate != nullptr && in_bounds(row < T, p.f.err))
             store_group<YF>(Rows{(char*)p.d_gate, p.ld_d_gate}.template at<YF>(row, g), D * b * (before[c] * ry));
           D = D * x;
         }
@@ -276,7 +278,8 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
         S[c] = fma8(by, of_S, S[c]);
         dot8(cy, by, before[c]);
         e[c] = D * before[c];
-        if (!post && there) store_group<YF>(to_y + c * width * kUnits<YF>, e[c] * token);
+        uint4* const at_dy = to_y + c * width * kUnits<YF>;
+        if (!post && there && is_at<YF>(p.f, at_dy, p.d_y, p.ld_d_y, row, g)) store_group<YF>(at_dy, e[c] * token);
       }
     }
     float after = 0.f;  // the sum of cy
@@ -303,9 +306,9 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
           const int g = g0 + c * width;
-          if (here && g < groups)
-            store_group<YF>(to_y + c * width * kUnits<YF>,
-                            fma8(kept_y[c].unpack(), ky, e[c] * (ry * token)));
+          uint4* const at_dy = to_y + c * width * kUnits<YF>;
+          if (here && g < groups && is_at<YF>(p.f, at_dy, p.d_y, p.ld_d_y, row, g))
+            store_group<YF>(at_dy, fma8(kept_y[c].unpack(), ky, e[c] * (ry * token)));
         }
       }
     }
@@ -324,6 +327,11 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
     const bool one = kAny && !PAIR && p.one_cluster;
     float* const out = one ? own : p.partials + int64_t(unit) * kSums * H;
     if (kCta && one) __syncthreads();  // the stages have been read
+    // whether a sum's columns [from, to) have their place: in the workspace, or in shared memory
+    auto has_place = [&](int which, int64_t from, int64_t to) {
+      if (one) return in_shared((reinterpret_cast<char*>(own + which * H + to) - reinterpret_cast<char*>(stages)), p.f.err);
+      return in_buffer(p.partials, p.ws_bytes, out + which * H + from, (to - from) * sizeof(float), p.f.err);
+    };
     auto write = [&](int which, const Eight (&v)[CPL]) {
       if constexpr (LANES > 0) {
         // the CTA's rows' sums are added in their order, through shared memory
@@ -336,13 +344,14 @@ __global__ void __maxnreg__(kRegisters) norm_grad_kernel(const __grid_constant__
         for (int col = tid; col < H; col += kSmallThreads) {
           float x = sum[col];
           for (int i = 1; i < per_cta; ++i) x = __fadd_rn(x, sum[i * CPL * width * 8 + col]);
-          out[which * H + col] = x;
+          if (has_place(which, col, col + 1)) out[which * H + col] = x;
         }
       } else {
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
           const int g = g0 + c * width;
-          if (g < groups) store_group<true>(reinterpret_cast<uint4*>(out + which * H) + 2 * g, v[c]);
+          if (g < groups && has_place(which, g * 8, g * 8 + 8))
+            store_group<true>(reinterpret_cast<uint4*>(out + which * H) + 2 * g, v[c]);
         }
       }
     };
@@ -383,8 +392,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   float x = 0.f;
   if (col < H) {
 #pragma unroll 8
-    for (int i = j; i < parts; i += kJoinParts)
-      x = __fadd_rn(x, __ldcg(p.partials + (int64_t(i) * kSums + blockIdx.y) * H + col));
+    for (int i = j; i < parts; i += kJoinParts) {
+      const float* const from = p.partials + (int64_t(i) * kSums + blockIdx.y) * H + col;
+      if (in_buffer(p.partials, p.ws_bytes, from, sizeof(float), p.f.err)) x = __fadd_rn(x, __ldcg(from));
+    }
   }
   scratch[j][threadIdx.x % kJoinCols] = x;
   __syncthreads();

@@ -108,6 +108,12 @@ struct Rows {
   }
 };
 
+// Whether `at`, which was stepped from row to row, is where group g of row `row` goes.
+template <bool F32>
+__device__ __forceinline__ bool is_at(const NormParams& p, const uint4* at, const void* base, int64_t ld, uint32_t row, int g) {
+  return in_bounds(row < uint32_t(p.T) && g < p.groups && at == Rows{(char*)base, ld}.template at<F32>(row, g), p.err);
+}
+
 template <bool F32>
 __device__ __forceinline__ void store_group(uint4* p, const Eight& e) {
   Group<F32> g;
@@ -180,6 +186,12 @@ struct RowRing {
     }
     abort = 0;
     fence_barrier_init();
+  }
+  // Whether groups [from, to) of row `row` are there to be copied, and the stage to copy them to.
+  static __device__ __forceinline__ bool may_copy(const NormParams& p, uint32_t row, int from, int to, int stage,
+                                                  int stage_units) {
+    return in_bounds(row < uint32_t(p.T) && from >= 0 && from < to && to <= p.groups, p.err) &&
+           in_shared(int64_t(stage + 1) * stage_units * 16, p.err);
   }
   // announces copies of so many bytes in all; false after a wait has given up: then none may follow
   __device__ __forceinline__ bool begin(int stage, uint32_t bytes) {
