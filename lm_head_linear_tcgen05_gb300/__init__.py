@@ -817,7 +817,7 @@ _SAME_DEVICE = contextlib.nullcontext()
 
 
 def _on(dev: torch.device):
-    return _SAME_DEVICE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    return _SAME_DEVICE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _raw_stream(dev: torch.device) -> int:
