@@ -306,8 +306,9 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
     int c = 0;
 #pragma unroll
     for (uint32_t r = 0; r < kCluster; ++r) c += e < p.E ? of_cta(all, r)[e] : *of_cta(&kept, r);
-    int32_t* const to = ws.experts + cluster * (p.E + 1) + e;
-    if (in_bounds(cluster < kCountClusters, p.err) && in_workspace(p, to, sizeof(int32_t))) *to = c;
+    if (in_bounds(cluster < kCountClusters, p.err) &&
+        in_workspace(p, ws.experts + cluster * (p.E + 1) + e, sizeof(int32_t)))
+      ws.experts[cluster * (p.E + 1) + e] = c;
   }
   cluster_sync();
 }
