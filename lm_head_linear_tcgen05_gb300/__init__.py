@@ -1169,6 +1169,8 @@ def lp_dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, row_start:
     are dropped as in one call. ``rng`` (int64 [2] on the GPU) is added to seed and offset when the kernel
     runs. ``out`` may be x; row strides may be any multiple of 16 bytes."""
     T, H, dtype, ld = _matrix(x, "x")
+    if not -(1 << 63) <= row_start < 1 << 63:            # ctypes would take it modulo 2^64
+        raise TypeError(f"row_start must be in [0, 2^63), got {row_start}")
     d, dev = x.get_device(), x.device
     if out is None:
         out, ld_out = torch.empty((T, H), dtype=x.dtype, device=dev), H
