@@ -1260,6 +1260,9 @@ def lp_residual_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, weight: 
         raise TypeError(f"the norm has y's type, {y_dtype}")
     dev, h_out, n, ld_h_out, ld_n = h.device, None, None, H, H
     given = _NOTHING if out is None else out
+    for name in given:
+        if name not in ("h_out", "norm"):
+            raise ValueError(f"out[{name!r}] is not an output of this call")
     if y is not None:
         h_out = given.get("h_out")
         if h_out is None:

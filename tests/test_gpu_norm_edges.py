@@ -25,3 +25,10 @@ def test_a_first_row_past_63_bits_is_refused(lp, start):
     for call in (lambda: lp.lp_dropout(x, 0.5, 1, row_start=start), lambda: lp.lp_residual_norm(x, x, dropout=0.5, row_start=start)):
         with pytest.raises((TypeError, lp.LPError)):
             call()
+
+
+def test_an_output_of_another_name_is_refused(lp):
+    h = torch.ones(4, 64, device="cuda")
+    for name in ("d_h", "hout", "y"):
+        with pytest.raises(ValueError):
+            lp.lp_residual_norm(h, h, out={name: torch.empty_like(h)})
