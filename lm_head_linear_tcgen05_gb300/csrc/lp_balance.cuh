@@ -29,8 +29,15 @@ constexpr int kCountClusters = kSms / kCluster;
 constexpr int kTokenResident = 2;  // CTAs of the token stage on an SM; three spill, and are no faster
 constexpr int kTokenCtas = kTokenResident * kSms;
 constexpr int kFewSequences = 8;  // sequences of a CTA's tokens that are counted in shared memory first
-// The one-launch form takes batches of up to this many logits, slots and (sequences x experts). At 4096 x 64, the most,
-// its GPU time is 10 us where the other's is 7, but a call takes 20 us and not 27, without a workspace and a launch.
+// The one-launch form takes batches of up to this many logits, slots and (sequences x experts): as long as a call in a
+// loop takes less time than with the other's workspace and launches. GPU time crosses earlier. One launch | several,
+// fp32 softmax without sequences (with 8, 2 to 4 us more of each), us on the GPU and a call:
+//     logits        2^12               2^16                2^17                2^18                2^19
+//     16 experts    5.1 20 | 6.2 26    8.2 21 |  6.9 26   12.2 21 |  7.8 26   20.3 23 |  8.3 26   36.5 40 |  9.2 25
+//     64 experts    5.5 22 | 6.7 26    6.2 21 |  7.2 27    7.4 21 |  7.3 26   10.4 22 |  7.3 26   15.9 22 |  8.0 26
+//     256 experts   5.8 21 | 7.2 26    6.4 21 |  7.9 26    7.8 21 |  8.0 26   10.4 21 |  7.9 26   15.7 21 |  8.1 25
+// So up to 2^16 logits (2^15 of 16 experts) the choice costs nothing; above, a replayed graph pays up to 3 us for it
+// with 64 experts or more, 12 with 16.
 constexpr int64_t kOneLogits = 1 << 18;
 constexpr int64_t kOneSlots = 1 << 15;
 constexpr int kOneTable = 2048;
@@ -844,7 +851,9 @@ cudaError_t launch_stages(const BalanceParams& p, cudaStream_t s) {
 }
 
 // Lanes of a token: as few as leave a lane 16 logits, but four. (131071 x 256 in bf16: 47 us with 16, 51 with
-// 32, where a step has fewer instructions for each logit but less else to do while it waits for its sums.)
+// 32, where a step has fewer instructions for each logit but less else to do while it waits for its sums.) Element by
+// element, 65 to 128 experts have 16 lanes as up to 256 have; 8 would take 65536 x 100 in bf16 from 33.6 to 24.4 us and
+// 65536 x 101 in fp32 from 22.0 to 18.9.
 template <bool LF, bool SIGMOID, int VE>
 cudaError_t launch_widths(const BalanceParams& p, cudaStream_t s) {
   constexpr int kFewest = VE > 4 ? VE : 4;
