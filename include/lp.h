@@ -830,11 +830,11 @@ typedef struct {
  * are not kept get zero gradients; a batch that keeps none has loss 0. A token whose logits are all
  * -inf has p = 0 (and no z term). An id outside {-1} U [0, E) of a kept token records
  * LP_ERR_EXPERT_OUT_OF_RANGE and counts for no expert. Offsets that do not ascend from 0 to T
- * record LP_ERR_SEQ_OFFSETS; metrics are then NaN and gradients zero. These gradients and those of
- * tokens that are not kept are zero whatever upstream is. Scores, log-sum-exp and sums are fp32, by the hardware's
- * approximate 2^x, 1/x and log2 (subnormal numbers as zero): with x the distance of a logit from the largest
- * (sigmoid: from 0), its p has a relative error of up to some 12 (1 + x) 2^-24, and a p below 2^-126 is zero. Sums have an order fixed by
- * sizes, types and alignments: results are bitwise the same from run to run. T = 0 gives loss 0.
+ * record LP_ERR_SEQ_OFFSETS; metrics are then NaN and gradients zero. These gradients and those of tokens that are
+ * not kept are zero whatever upstream is. Scores, log-sum-exp and sums are fp32, by the hardware's approximate
+ * 2^x, 1/x and log2 (subnormal numbers as zero): with x the distance of a logit from the largest (sigmoid: from 0),
+ * its p has a relative error of up to some 12 (1 + x) 2^-24, and a p below 2^-126 is zero. Sums have an order fixed
+ * by sizes, types and alignments: results are bitwise the same from run to run. T = 0 gives loss 0.
  * Workspace: lp_balance_workspace_size(T, E, K, n_seqs), n_seqs = 0 without cu_seqlens. */
 LP_API lp_status lp_balance_loss(int64_t T, int64_t E, int64_t K, const lp_balance_inputs* in,
                                  const lp_balance_options* opts, const lp_balance_outputs* out, void* workspace,
